@@ -535,6 +535,138 @@ ss_status ss_cosine_chunk_noalloc(const ss_csr *queries, const ss_csr *items, in
                                   int64_t row_end, int64_t chunk_nnz, float *out, int64_t ld_out,
                                   int32_t *device_status, void *stream);
 
+/*
+ * Dense operators: what trains and serves a dense student of the exact top-k
+ * lists (the lists of ss_topk_all are the teacher of ss_distill), and makes
+ * the rows that are scored (ss_linear with SS_ACT_LOG1P_RELU is a sparse
+ * embedding's head).  Common to all of them:
+ *  - A matrix is row-major in device memory: value (r, c) at data[r * ld + c],
+ *    ld >= n_cols, any alignment of its rows (16-byte aligned rows run
+ *    fastest), n_rows and n_cols below SS_DENSE_MAX.  A vector is a matrix of
+ *    one row, or a float array where so declared.
+ *  - Sums, norms and softmax statistics are float32, each output is rounded
+ *    once; results are the same bit for bit on every call.
+ *  - Outputs must not overlap inputs, except where stated.
+ *  - `scratch` is device memory of at least the stated bytes, aligned to
+ *    SS_SCRATCH_ALIGN, free for the call's use until its work on `stream` is
+ *    done (NULL when 0 bytes are needed).  No call allocates or synchronises:
+ *    all of them may be captured into a graph (after one call of the same
+ *    kind outside a capture, which loads the kernels).
+ *  - No rows: SS_OK, no work (gradients that are sums over rows are zeroed).
+ * Errors: SS_ERR_INVALID_ARG (null pointers, shapes, types, ld, pointers not
+ * aligned to their type), SS_ERR_LIMIT, SS_ERR_CUDA; no work is queued then.
+ */
+#define SS_VALUES_F8 3 /* e4m3: 4 bits of exponent, 3 of fraction, largest 448 */
+#define SS_DENSE_MAX ((int64_t)1 << 30)
+#define SS_SCRATCH_ALIGN 256
+
+typedef struct ss_dense {
+  void *data;
+  int64_t n_rows;
+  int64_t n_cols;
+  int64_t ld;   /* values from one row to the next */
+  int32_t type; /* SS_VALUES_* */
+} ss_dense;
+
+/*
+ * Root-mean-square norm with the residual's addition.  Per row:
+ *   s = x + residual,  rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * weight
+ * x, residual (or NULL: s = x), total: float32, bfloat16 or float16, one type.
+ * weight: 1 x n_cols of that type or float32.  total (or NULL; only with a
+ * residual): s rounded; may be x or residual itself.  rstd: float[n_rows] or
+ * NULL.  y: x's type with scale NULL, or SS_VALUES_F8 with scale
+ * float[n_rows]: then scale = max|y| / 448 of the row and y holds y / scale
+ * to the nearest (a row of zeros: scale 0 and zeros).  A row that holds an
+ * infinity or a NaN has NaN where the formula has.
+ */
+ss_status ss_rms_norm(ss_handle *h, const ss_dense *x, const ss_dense *residual, const ss_dense *weight, float eps,
+                      const ss_dense *total, const ss_dense *y, float *scale, float *rstd, void *stream);
+
+/*
+ * Its gradient.  With xh = total * rstd and g = grad_y * weight:
+ *   grad_x = rstd * (g - xh * mean(g * xh)) + grad_total   (also the residual's)
+ *   grad_weight = sum over rows of grad_y * xh
+ * total: the summed input as kept by the forward call (x without a residual);
+ * rstd: as kept; grad_total: the gradient that reaches total past the norm,
+ * or NULL.  All of total's type, weight and grad_weight of one type.
+ * scratch: ss_rms_norm_backward_scratch bytes.
+ */
+int64_t ss_rms_norm_backward_scratch(const ss_handle *h, int64_t n_rows, int64_t n_cols);
+ss_status ss_rms_norm_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *total, const ss_dense *weight,
+                               const float *rstd, const ss_dense *grad_total, const ss_dense *grad_x,
+                               const ss_dense *grad_weight, void *scratch, int64_t scratch_bytes, void *stream);
+
+/* Activations of ss_linear: z; max(z, 0); z Phi(z) (with erf); its tanh
+ * approximation; z / (1 + exp(-z)); log(1 + max(z, 0)). */
+#define SS_ACT_NONE 0
+#define SS_ACT_RELU 1
+#define SS_ACT_GELU 2
+#define SS_ACT_GELU_TANH 3
+#define SS_ACT_SILU 4
+#define SS_ACT_LOG1P_RELU 5
+
+/*
+ * Linear layer:  z = (x w^T) * x_scale * w_scale + bias,  y = act(z) + residual
+ * x: M x K and w: N x K, both bfloat16, both float16, or both SS_VALUES_F8
+ * with x_scale float[M] and w_scale float[N] (one scale a row, as ss_rms_norm
+ * writes them; NULL for the other types).  bias: float[N] or NULL.  y: M x N
+ * of x's type or float32 (8-bit inputs: any of float32, bfloat16, float16).
+ * residual and pre (or NULL): of y's type; pre receives z, for the gradient.
+ * Products are exact and summed in float32.  scratch: ss_linear_scratch bytes
+ * (0 when the rows of x and w start on 16-byte boundaries).
+ */
+int64_t ss_linear_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w);
+ss_status ss_linear(ss_handle *h, const ss_dense *x, const float *x_scale, const ss_dense *w, const float *w_scale,
+                    const float *bias, int32_t activation, const ss_dense *residual, const ss_dense *pre,
+                    const ss_dense *y, void *scratch, int64_t scratch_bytes, void *stream);
+
+/*
+ * Its gradient, for 16-bit x and w.  With gz = grad_y * act'(pre):
+ *   grad_x = gz w,  grad_w = gz^T x,  grad_bias = sum over rows of gz
+ * (the residual's gradient is grad_y itself).  pre: the z kept by the forward
+ * call (NULL for SS_ACT_NONE).  The rectified activations have slope 0 at 0.
+ * gz enters the products rounded to x's type; grad_bias sums it unrounded.
+ * grad_x (M x K) and grad_w (N x K): of x's type or float32; grad_bias:
+ * float[N]; each may be NULL.  scratch: ss_linear_backward_scratch bytes.
+ */
+int64_t ss_linear_backward_scratch(const ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_dense *w,
+                                   int32_t activation);
+ss_status ss_linear_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_dense *w,
+                             const ss_dense *pre, int32_t activation, const ss_dense *grad_x, const ss_dense *grad_w,
+                             float *grad_bias, void *scratch, int64_t scratch_bytes, void *stream);
+
+/*
+ * Distillation from a teacher's k listed scores a row (the lists of
+ * ss_topk_all), 1 <= k <= SS_DISTILL_LIST_MAX:
+ *   p = softmax(score / teacher_temperature) over the row's listed items
+ *   q = softmax(logits / temperature) over all n_cols items
+ *   loss = weight * temperature^2 * sum_j p_j (log p_j - log q[item_j])
+ *   grad_logits_v = grad_loss * weight * temperature * (q_v - sum of p_j with item_j = v)
+ * logits: float32, bfloat16 or float16.  scores: float[n_rows][k]; items:
+ * int64[n_rows][k].  An entry of a negative item, of score -INFINITY, or of
+ * an item whose logit is -INFINITY (the student masks it) is absent; an item
+ * at or beyond n_cols too, and the next ss_check_device reports it as
+ * SS_ERR_OUT_OF_RANGE.  A row without entries, or of weight 0, has loss 0 and
+ * gradient 0 whatever its logits are; a NaN logit makes a row's loss and
+ * gradient NaN.  weight, grad_loss: float[n_rows] or NULL (1).  Temperatures
+ * lie in [SS_DISTILL_TEMPERATURE_MIN, 1 / SS_DISTILL_TEMPERATURE_MIN].
+ * ss_distill keeps stats (float[n_rows][2]: the row's largest logit and the
+ * sum of exp((logit - it) / temperature)) for ss_distill_backward, which
+ * takes the same lists, temperatures and weight.  ss_distill_step gives loss
+ * and gradient in one launch; its grad_logits may be the logits themselves.
+ */
+#define SS_DISTILL_LIST_MAX 256
+#define SS_DISTILL_TEMPERATURE_MIN 1e-6f
+ss_status ss_distill(ss_handle *h, const ss_dense *logits, const float *scores, const int64_t *items, int32_t k,
+                     float temperature, float teacher_temperature, const float *weight, float *loss, float *stats,
+                     void *stream);
+ss_status ss_distill_backward(ss_handle *h, const float *grad_loss, const ss_dense *logits, const float *scores,
+                              const int64_t *items, int32_t k, float temperature, float teacher_temperature,
+                              const float *weight, const float *stats, const ss_dense *grad_logits, void *stream);
+ss_status ss_distill_step(ss_handle *h, const float *grad_loss, const ss_dense *logits, const float *scores,
+                          const int64_t *items, int32_t k, float temperature, float teacher_temperature,
+                          const float *weight, float *loss, const ss_dense *grad_logits, void *stream);
+
 /* Number of kernels this handle has launched so far (every call that
  * queues kernels adds the number it queued).  Host-side count; no sync; 0
  * for a null handle. */

@@ -14,6 +14,10 @@ of the matrix) and ``bulk_cosine_host`` (host buffers in, result streamed
 back chunk by chunk; ``set_device_limit`` bounds its device memory, with
 item batches streamed and queries tiled, see ``plan_host_pass``; 16-bit
 host values with ``host_values="bf16"`` or ``"f16"``).
+
+The dense operators train and serve a dense student of the exact lists:
+``rms_norm``, ``linear`` and ``distill`` with their gradients, and
+``rms_norm_quantized`` for 8-bit layers (``dense.py``).
 """
 from __future__ import annotations
 
@@ -26,6 +30,7 @@ import torch
 
 from . import _abi
 from ._abi import SparseCosError, SS_VALIDATE  # noqa: F401
+from .dense import DenseOperators
 
 DEFAULT_CHUNK_ROWS = 8192
 
@@ -88,7 +93,7 @@ def _host_csr(batch, host_values="f32"):
     return m, (indptr, indices, values)
 
 
-class SparseCosine:
+class SparseCosine(DenseOperators):
     """One library handle: a device, a dimension and a chunk size."""
 
     ALGORITHMS = ("auto", "hybrid", "posting", "tensor")

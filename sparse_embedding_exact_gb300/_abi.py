@@ -29,7 +29,16 @@ SS_MAX_CHUNK_ROWS = 65536
 SS_VALUES_F32 = 0
 SS_VALUES_BF16 = 1
 SS_VALUES_F16 = 2
+SS_VALUES_F8 = 3
 SS_EXPORT_HOT_MAX = 160
+SS_SCRATCH_ALIGN = 256
+SS_DISTILL_LIST_MAX = 256
+SS_ACT_NONE = 0
+SS_ACT_RELU = 1
+SS_ACT_GELU = 2
+SS_ACT_GELU_TANH = 3
+SS_ACT_SILU = 4
+SS_ACT_LOG1P_RELU = 5
 SS_DEVICE_OK = 0
 SS_DEVICE_UNSORTED = 1
 SS_DEVICE_OUT_OF_RANGE = 2
@@ -49,12 +58,24 @@ class ss_csr(ctypes.Structure):
     ]
 
 
+class ss_dense(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int64),
+        ("n_cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("type", ctypes.c_int32),
+    ]
+
+
 ss_chunk_consumer = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                      ctypes.c_int64, ctypes.POINTER(ctypes.c_float), ctypes.c_int64,
                                      ctypes.c_int64)
 
 _P = ctypes.c_void_p
 _CSR = ctypes.POINTER(ss_csr)
+_DENSE = ctypes.POINTER(ss_dense)
+_F32 = ctypes.c_float
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 
@@ -85,6 +106,16 @@ SIGNATURES = {
     "ss_index_export": (_I32, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, ctypes.POINTER(_I64), _P]),
     "ss_lists_export": (_I32, [_P, ctypes.POINTER(_I64), _P, _P, _P, _P, _I64, ctypes.POINTER(_I64), _P]),
     "ss_cosine_chunk_noalloc": (_I32, [_CSR, _CSR, _I64, _I64, _I64, _P, _I64, _P, _P]),
+    "ss_rms_norm": (_I32, [_P, _DENSE, _DENSE, _DENSE, _F32, _DENSE, _DENSE, _P, _P, _P]),
+    "ss_rms_norm_backward_scratch": (_I64, [_P, _I64, _I64]),
+    "ss_rms_norm_backward": (_I32, [_P, _DENSE, _DENSE, _DENSE, _P, _DENSE, _DENSE, _DENSE, _P, _I64, _P]),
+    "ss_linear_scratch": (_I64, [_P, _DENSE, _DENSE]),
+    "ss_linear": (_I32, [_P, _DENSE, _P, _DENSE, _P, _P, _I32, _DENSE, _DENSE, _DENSE, _P, _I64, _P]),
+    "ss_linear_backward_scratch": (_I64, [_P, _DENSE, _DENSE, _DENSE, _I32]),
+    "ss_linear_backward": (_I32, [_P, _DENSE, _DENSE, _DENSE, _DENSE, _I32, _DENSE, _DENSE, _P, _P, _I64, _P]),
+    "ss_distill": (_I32, [_P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _P, _P]),
+    "ss_distill_backward": (_I32, [_P, _P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _DENSE, _P]),
+    "ss_distill_step": (_I32, [_P, _P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _DENSE, _P]),
     "ss_kernel_launches": (ctypes.c_uint64, [_P]),
     "ss_inject_alloc_failure": (_I64, [_I64]),
     "ss_profile_scorer": (_I32, [_P, _I32]),

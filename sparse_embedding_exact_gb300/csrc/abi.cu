@@ -49,6 +49,21 @@ bool injected_failure() {
   return false;
 }
 
+}  // namespace
+
+ss_status report_cuda(ss_handle *h, cudaError_t e, const char *what) { return cuda_fail(h, e, what); }
+
+ss_status report(ss_handle *h, ss_status st, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(h, st, "%s", buf);
+}
+
+namespace {
+
 #define SS_CUDA(h, call)                                  \
   do {                                                    \
     cudaError_t e_ = (call);                              \

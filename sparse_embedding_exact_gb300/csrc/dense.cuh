@@ -1,0 +1,160 @@
+// Shared by the dense operators (rmsnorm.cu, linear.cu, distill.cu): value
+// types, vector loads and stores, reductions, and the launchers the ABI calls.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.cuh"
+
+namespace dense {
+
+constexpr float kF8Max = 448.0f;  // largest finite e4m3 value
+
+// ---------------------------------------------------------------- values
+template <typename T>
+struct Type;
+template <>
+struct Type<float> {
+  static constexpr int kVec = 4;  // values in 16 bytes
+  static __device__ __forceinline__ float up(float v) { return v; }
+  static __device__ __forceinline__ float down(float v) { return v; }
+};
+template <>
+struct Type<__nv_bfloat16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float up(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Type<__half> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float up(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
+};
+
+// kN consecutive values read as one access of kN * sizeof(T) bytes, and their
+// float32 values.
+template <typename T, int kN>
+struct alignas(sizeof(T) * kN) Pack {
+  T v[kN];
+};
+template <typename T, int kN>
+__device__ __forceinline__ void widen(const Pack<T, kN> &p, float (&f)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) f[i] = Type<T>::up(p.v[i]);
+}
+// Each value rounded once, to the nearest (ties to even).
+template <typename T, int kN>
+__device__ __forceinline__ Pack<T, kN> narrow(const float (&f)[kN]) {
+  Pack<T, kN> p;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) p.v[i] = Type<T>::down(f[i]);
+  return p;
+}
+template <typename T, int kN>
+__device__ __forceinline__ Pack<T, kN> load_pack(const T *p) {
+  return *reinterpret_cast<const Pack<T, kN> *>(p);
+}
+template <typename T, int kN>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, kN> &v) {
+  *reinterpret_cast<Pack<T, kN> *>(p) = v;
+}
+// kN values rounded to e4m3 (to the nearest, beyond 448 to 448; NaN kept).
+template <int kN>
+__device__ __forceinline__ void store_f8(uint8_t *p, const float (&f)[kN]) {
+  if constexpr (kN == 1) {
+    *p = (uint8_t)__nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
+  } else {
+    Pack<uint16_t, kN / 2> q;
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i)
+      q.v[i] = (uint16_t)__nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<Pack<uint16_t, kN / 2> *>(p) = q;
+  }
+}
+
+// The larger of two values, NaN when either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+__device__ __forceinline__ void flag(int32_t *status, int32_t code) { atomicCAS(status, DEV_OK, code); }
+
+inline int64_t size_of(int32_t type) {
+  return type == SS_VALUES_F32 ? 4 : type == SS_VALUES_F8 ? 1 : 2;
+}
+// Whether the rows of m can be read in aligned units of `unit` bytes.
+inline bool rows_aligned(const ss_dense &m, int64_t unit) {
+  return (reinterpret_cast<uintptr_t>(m.data) % (uintptr_t)unit) == 0 &&
+         (m.n_rows <= 1 || (m.ld * size_of(m.type)) % unit == 0);
+}
+
+}  // namespace dense
+
+// Launchers (all asynchronous on `s`; *queued gets the kernels queued).  The
+// matrices have been checked; absent ones have a null data pointer.
+struct rms_args {
+  ss_dense x, residual, weight, total, y;
+  float *scale;  // with y in 8 bits: one scale a row
+  float *rstd;   // or null
+  float eps;
+};
+cudaError_t launch_rms_norm(ss_handle *h, const rms_args &a, cudaStream_t s, int *queued);
+
+struct rms_grad_args {
+  ss_dense grad_y, total, weight, grad_total, grad_x, grad_weight;
+  const float *rstd;
+  float *scratch;  // rms_grad_scratch bytes
+};
+int64_t rms_grad_scratch(const ss_handle *h, int64_t rows, int64_t cols);
+cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &a, cudaStream_t s, int *queued);
+
+struct distill_args {
+  ss_dense logits, grad_logits;
+  const float *scores;   // [rows][k]
+  const int64_t *items;  // [rows][k]
+  int32_t k;
+  float temperature, teacher_temperature;
+  const float *weight;     // [rows] or null: 1
+  const float *grad_loss;  // [rows] or null: 1
+  float *loss;             // [rows]
+  float *stats;            // [rows][2]: {max, sum of exp((z - max) / T)}
+};
+enum : int32_t { DISTILL_FORWARD = 0, DISTILL_BACKWARD = 1, DISTILL_STEP = 2 };
+cudaError_t launch_distill(ss_handle *h, const distill_args &a, int32_t mode, cudaStream_t s, int *queued);
+
+struct linear_args {
+  ss_dense x, w, residual, pre, y;
+  const float *x_scale, *w_scale, *bias;
+  int32_t activation;
+  unsigned char *scratch;  // linear_scratch bytes
+};
+int64_t linear_scratch(const ss_handle *h, const ss_dense &x, const ss_dense &w);
+cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, int *queued);
+
+struct linear_grad_args {
+  ss_dense grad_y, x, w, pre, grad_x, grad_w;  // grad_x, grad_w: or null
+  float *grad_bias;                            // or null
+  int32_t activation;
+  unsigned char *scratch;  // linear_grad_scratch bytes
+};
+int64_t linear_grad_scratch(const ss_handle *h, const ss_dense &grad_y, const ss_dense &x, const ss_dense &w,
+                            int32_t activation);
+cudaError_t launch_linear_grad(ss_handle *h, const linear_grad_args &a, cudaStream_t s, int *queued);

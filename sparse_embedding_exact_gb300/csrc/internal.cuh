@@ -345,6 +345,11 @@ cudaError_t host_alloc(T **p, size_t bytes) {
 // a clean workspace.
 void reset_after_oom(ss_handle *h);
 
+// Sets the handle's last error and returns `st` (of a CUDA error: the status
+// that stands for it, the handle's buffers freed after a failed allocation).
+ss_status report(ss_handle *h, ss_status st, const char *fmt, ...);
+ss_status report_cuda(ss_handle *h, cudaError_t e, const char *what);
+
 // Forgets what was prepared from the current query matrix (its caches are
 // keyed on the arrays' addresses, which a host pass reuses for new contents).
 void invalidate_queries(ss_handle *h);

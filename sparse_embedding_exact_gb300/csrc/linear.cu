@@ -1,0 +1,748 @@
+// Linear layers: y = act((x w^T) sx sw^T + b) + r, and their gradients.
+//
+//   z = (x w^T) sx[m] sw[n] + b[n],   y = act(z) + r,   pre = z if kept
+//   gz = grad_y act'(pre),  grad_x = gz w,  grad_w = gz^T x,  grad_b = sum gz
+//
+// x [M, K] and w [N, K] hold bf16, fp16 or e4m3 values (one scale a row then);
+// products are exact and summed in float32, the epilogue is float32, and each
+// output is rounded once.  gz is rounded to the inputs' type, as the tensor
+// cores take it.
+//
+// Many rows (k_product): bound by the tensor cores.  D = A B^T by tiles of 128
+// x kBN in tensor memory, operands by tensor copies in the 128-byte swizzle
+// through a ring of shared-memory stages; one warp copies, one thread issues
+// the products, four warps run the epilogue.  The three products of a layer
+// differ in which operand runs along the summed dimension: x w^T has both
+// rows contiguous in it (K-major), gz w has w contiguous across it, and
+// gz^T x both (MN-major); the copies and descriptors take either, so nothing
+// is transposed in memory.
+//
+// Up to 256 rows: bound by reading w.  The same kernel with the sides
+// swapped, A = w and B = x, so that 128 features fill the tile's rows and few
+// columns are spent on rows that do not exist; where the tiles are fewer than
+// the SMs the summed dimension is split over a cluster of up to 8 blocks,
+// which add their tiles through each other's shared memory in a fixed order.
+//
+// Up to 4 rows (k_rows): a warp takes whole rows of w with 16-byte loads and
+// ordinary multiply-adds, no tile to fill.
+//
+// Rows that do not start on 16-byte boundaries, which tensor copies cannot
+// take, are first copied into scratch with padded rows.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "tc.cuh"
+
+namespace {
+
+using namespace dense;
+
+constexpr int kTileM = 128;       // rows of A a tile
+constexpr int kRowBytes = 128;    // of the summed dimension a stage, both operands
+constexpr int kThreads = 192;     // copy warp, product warp, four epilogue warps
+constexpr int kSmemMost = 227 * 1024;
+
+enum : int { kMajorK = 0, kMajorMN = 1 };
+
+// ---------------------------------------------------------------- activations
+template <int kAct>
+__device__ __forceinline__ float act_of(float z) {
+  if (kAct == SS_ACT_RELU) return z > 0.0f ? z : (z == z ? 0.0f : z);
+  if (kAct == SS_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if (kAct == SS_ACT_GELU_TANH) return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+  if (kAct == SS_ACT_SILU) return z / (1.0f + expf(-z));
+  if (kAct == SS_ACT_LOG1P_RELU) return z > 0.0f ? log1pf(z) : (z == z ? 0.0f : z);
+  return z;
+}
+__device__ __forceinline__ float act_any(int32_t act, float z) {
+  switch (act) {
+    case SS_ACT_RELU: return act_of<SS_ACT_RELU>(z);
+    case SS_ACT_GELU: return act_of<SS_ACT_GELU>(z);
+    case SS_ACT_GELU_TANH: return act_of<SS_ACT_GELU_TANH>(z);
+    case SS_ACT_SILU: return act_of<SS_ACT_SILU>(z);
+    case SS_ACT_LOG1P_RELU: return act_of<SS_ACT_LOG1P_RELU>(z);
+    default: return z;
+  }
+}
+// act'(z); 0 at the kink of the rectified ones.
+__device__ __forceinline__ float act_slope(int32_t act, float z) {
+  switch (act) {
+    case SS_ACT_RELU: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
+    case SS_ACT_GELU:
+      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    case SS_ACT_GELU_TANH: {
+      if (fabsf(z) > 1e4f) return z > 0.0f ? 1.0f : 0.0f;  // where z^2 could overflow
+      const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
+      return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456080286536f * (1.0f + 0.134145f * z * z);
+    }
+    case SS_ACT_SILU: {
+      const float s = 1.0f / (1.0f + expf(-z));
+      return s * (1.0f + z * (1.0f - s));
+    }
+    case SS_ACT_LOG1P_RELU: return z > 0.0f ? 1.0f / (1.0f + z) : (z == z ? 0.0f : z);
+    default: return 1.0f;
+  }
+}
+
+// ---------------------------------------------------------------- epilogue
+// What follows the product, for output rows m and features n.
+struct Epilogue {
+  ss_dense y, pre, residual;
+  const float *row_scale, *col_scale, *bias;
+  int32_t act;
+  int32_t vec;  // y, pre and residual rows start on 16-byte boundaries
+};
+__device__ __forceinline__ float read_any(const ss_dense &m, int64_t i) {
+  return m.type == SS_VALUES_F32    ? static_cast<const float *>(m.data)[i]
+         : m.type == SS_VALUES_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(m.data)[i])
+                                    : __half2float(static_cast<const __half *>(m.data)[i]);
+}
+__device__ __forceinline__ void write_any(const ss_dense &m, int64_t i, float v) {
+  if (m.type == SS_VALUES_F32)
+    static_cast<float *>(m.data)[i] = v;
+  else if (m.type == SS_VALUES_BF16)
+    static_cast<__nv_bfloat16 *>(m.data)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half *>(m.data)[i] = __float2half_rn(v);
+}
+__device__ __forceinline__ void finish_one(const Epilogue &ep, int64_t m, int64_t n, float v) {
+  if (ep.row_scale) v *= ep.row_scale[m] * ep.col_scale[n];
+  if (ep.bias) v += ep.bias[n];
+  if (ep.pre.data) write_any(ep.pre, m * ep.pre.ld + n, v);
+  v = act_any(ep.act, v);
+  if (ep.residual.data) v += read_any(ep.residual, m * ep.residual.ld + n);
+  write_any(ep.y, m * ep.y.ld + n, v);
+}
+template <typename T>
+__device__ __forceinline__ void write16(T *p, const float (&v)[16]) {
+  constexpr int kV = Type<T>::kVec;
+#pragma unroll
+  for (int q = 0; q < 16 / kV; ++q) {
+    float f[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) f[i] = v[q * kV + i];
+    store_pack(p + q * kV, narrow<T, kV>(f));
+  }
+}
+__device__ __forceinline__ void write16_any(const ss_dense &m, int64_t i, const float (&v)[16]) {
+  if (m.type == SS_VALUES_F32)
+    write16(static_cast<float *>(m.data) + i, v);
+  else if (m.type == SS_VALUES_BF16)
+    write16(static_cast<__nv_bfloat16 *>(m.data) + i, v);
+  else
+    write16(static_cast<__half *>(m.data) + i, v);
+}
+// 16 features n .. n + 15 of row m.
+__device__ __forceinline__ void finish16(const Epilogue &ep, int64_t m, int64_t n, float (&v)[16]) {
+  if (m >= ep.y.n_rows || n >= ep.y.n_cols) return;
+  if (!ep.vec || n + 16 > ep.y.n_cols) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (n + i < ep.y.n_cols) finish_one(ep, m, n + i, v[i]);
+    return;
+  }
+  if (ep.row_scale) {
+    const float s = ep.row_scale[m];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= s * ep.col_scale[n + i];
+  }
+  if (ep.bias) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += ep.bias[n + i];
+  }
+  if (ep.pre.data) write16_any(ep.pre, m * ep.pre.ld + n, v);
+  if (ep.act != SS_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_any(ep.act, v[i]);
+  }
+  if (ep.residual.data) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += read_any(ep.residual, m * ep.residual.ld + n + i);
+  }
+  write16_any(ep.y, m * ep.y.ld + n, v);
+}
+
+// ---------------------------------------------------------------- products
+struct Product {
+  CUtensorMap a, b;
+  Epilogue ep;
+  int64_t rows_a, rows_b;
+  int32_t blocks_k;   // stages of the summed dimension
+  int32_t tiles_a, tiles_b;
+  int32_t swapped;    // A holds the features, B the rows
+  uint32_t idesc;
+  int32_t *status;
+};
+
+template <int kBN>
+struct Ring {
+  static constexpr int kBytesA = kTileM * kRowBytes, kBytesB = kBN * kRowBytes;
+  static constexpr int kStage = kBytesA + kBytesB;
+  static constexpr int kStages = (kSmemMost - 2048) / kStage < 8 ? (kSmemMost - 2048) / kStage : 8;
+  static constexpr int kSmem = kStages * kStage + 1024;  // + alignment to 1024
+  static_assert(kBN * kTileM * 4 <= kStages * kStage, "a tile to exchange fits the ring");
+};
+
+// One tile a cluster; its blocks take equal shares of the summed dimension.
+template <int kBN, int kMajA, int kMajB, bool kF8>
+__global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Product a) {
+  using R = Ring<kBN>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t bars[2 * R::kStages + 1];
+  __shared__ uint32_t tmem_slot;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = (tc::smem_u32(raw) + 1023u) & ~1023u;
+  auto full = [&](int s) { return tc::smem_u32(&bars[s]); };
+  auto empty = [&](int s) { return tc::smem_u32(&bars[R::kStages + s]); };
+  const uint32_t done = tc::smem_u32(&bars[2 * R::kStages]);
+  constexpr uint32_t kCols = kBN < 32 ? 32 : kBN;
+  if (tid == 0) {
+    for (int i = 0; i < 2 * R::kStages + 1; ++i) tc::bar_init(tc::smem_u32(&bars[i]), 1);
+    tc::bar_init_fence();
+    tc::prefetch_map(&a.a);
+    tc::prefetch_map(&a.b);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_slot)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  uint32_t split;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
+  const uint32_t rank = split > 1 ? tc::cluster_rank() : 0;
+  const int64_t tile = blockIdx.x / split;
+  // Tiles go down groups of 8 tile rows of A, so that the blocks of a wave
+  // share both operands in L2.
+  const int64_t group = 8ll * a.tiles_b, g0 = tile / group * 8, gh = min((int64_t)8, (int64_t)a.tiles_a - g0);
+  const int64_t ta = g0 + (tile % group) % gh, tb = (tile % group) / gh;
+  const int32_t row_a = (int32_t)(ta * kTileM), row_b = (int32_t)(tb * kBN);
+  const int k0 = (int)((int64_t)a.blocks_k * rank / split), k1 = (int)((int64_t)a.blocks_k * (rank + 1) / split);
+  const int n = k1 - k0;
+  constexpr int kUnit = kF8 ? kRowBytes : kRowBytes / 2;  // values of the summed dimension a stage
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (; issued < n; ++issued) {
+        const int s = issued % R::kStages, turn = issued / R::kStages;
+        if (turn > 0 && !tc::bar_wait(empty(s), (uint32_t)((turn - 1) & 1), a.status)) break;
+        tc::bar_expect(full(s), R::kStage);
+        const int32_t k = (k0 + issued) * kUnit;
+        const uint32_t sa = ring + (uint32_t)(s * R::kStage), sb = sa + R::kBytesA;
+        if (kMajA == kMajorK) {
+          tc::load_2d(sa, &a.a, k, row_a, full(s));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTileM / 64; ++i) tc::load_2d(sa + i * 8192, &a.a, row_a + 64 * i, k, full(s));
+        }
+        if (kMajB == kMajorK) {
+          tc::load_2d(sb, &a.b, k, row_b, full(s));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kBN / 64; ++i) tc::load_2d(sb + i * 8192, &a.b, row_b + 64 * i, k, full(s));
+        }
+      }
+      // Every copy issued lands before the block goes on, also after a wait
+      // that gave up: a stage's next copy is issued only once its previous
+      // one was read, so at most the last copy of each stage is in flight.
+      for (int s = 0; s < R::kStages; ++s) {
+        const int m = (issued + R::kStages - 1 - s) / R::kStages;
+        if (m > 0) tc::bar_wait(full(s), (uint32_t)((m - 1) & 1), a.status);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < n; ++i) {
+        const int s = i % R::kStages;
+        if (!tc::bar_wait(full(s), (uint32_t)((i / R::kStages) & 1), a.status)) break;
+        tc::fence_after();
+        const uint32_t sa = ring + (uint32_t)(s * R::kStage), sb = sa + R::kBytesA;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t da = kMajA == kMajorK ? tc::desc_128b(sa + 32 * j, 16, 1024) : tc::desc_128b(sa + 2048 * j, 8192, 1024);
+          const uint64_t db = kMajB == kMajorK ? tc::desc_128b(sb + 32 * j, 16, 1024) : tc::desc_128b(sb + 2048 * j, 8192, 1024);
+          tc::mma<kF8>(tmem, da, db, a.idesc, (i > 0 || j > 0) ? 1u : 0u);
+        }
+        tc::commit(empty(s));
+      }
+      tc::commit(done);
+    }
+  }
+  __syncwarp();
+  // All warps wait: shared memory is free for the exchange once the products
+  // are done (they read every copy that landed).
+  const bool ok = tc::bar_wait(done, 0, a.status);
+  __syncthreads();
+  tc::fence_after();
+
+  const int64_t base = a.swapped ? tb * kBN : ta * kTileM;  // first output row
+  if (split == 1) {
+    if (warp >= 2 && ok) {
+      const int q = warp & 3;  // tensor-memory lanes 32 q .. 32 q + 31
+      const int r = q * 32 + lane;
+      for (int c = 0; c < kBN; c += 16) {
+        float v[16];
+        tc::load_acc16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+        if (n == 0) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        }
+        if (!a.swapped) {
+          finish16(a.ep, row_a + r, (int64_t)row_b + c, v);
+        } else if ((int64_t)row_a + r < a.rows_a) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (base + c + i < a.rows_b) finish_one(a.ep, base + c + i, row_a + r, v[i]);
+        }
+      }
+    }
+  } else {
+    // tile[column][row of A] of this block's share
+    if (warp >= 2) {
+      const int q = warp & 3, r = q * 32 + lane;
+      for (int c = 0; c < kBN; c += 16) {
+        float v[16];
+        tc::load_acc16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(ring + (uint32_t)((c + i) * kTileM + r) * 4), "f"(n > 0 ? v[i] : 0.0f)
+                       : "memory");
+      }
+    }
+    tc::cluster_sync();
+    if (warp >= 2 && ok) {
+      const int q = warp & 3, r = q * 32 + lane;
+      const int c0 = (int)(kBN * rank / split), c1 = (int)(kBN * (rank + 1) / split);
+      for (int c = c0; c < c1; ++c) {
+        float v = 0.0f;
+        for (uint32_t p = 0; p < split; ++p) v += tc::load_remote(ring + (uint32_t)(c * kTileM + r) * 4, p);
+        const int64_t ra = (int64_t)row_a + r, rb = (int64_t)row_b + c;
+        if (ra < a.rows_a && rb < a.rows_b) a.swapped ? finish_one(a.ep, rb, ra, v) : finish_one(a.ep, ra, rb, v);
+      }
+    }
+    tc::cluster_sync();  // no block leaves while another reads its tile
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+template <typename T, int kN>
+__device__ __forceinline__ void read_vec(const T *p, float (&f)[kN]) {
+  if constexpr (sizeof(T) == 1) {
+    const Pack<uint8_t, kN> q = *reinterpret_cast<const Pack<uint8_t, kN> *>(p);
+    if constexpr (kN == 1) {
+      f[0] = __half2float(__half(__nv_cvt_fp8_to_halfraw(q.v[0], __NV_E4M3)));
+    } else {
+      Pack<uint16_t, kN / 2> two;
+      memcpy(&two, &q, sizeof(two));
+#pragma unroll
+      for (int i = 0; i < kN / 2; ++i) {
+        const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two.v[i], __NV_E4M3)));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  } else {
+    widen(load_pack<T, kN>(p), f);
+  }
+}
+
+constexpr int kRowWarps = 8;
+// A warp takes kW features and, in turns, kM rows of x; kN values a load.
+template <typename T, int kM, int kW, int kN>
+__global__ void __launch_bounds__(32 * kRowWarps) k_rows(const ss_dense x, const ss_dense w, const Epilogue ep) {
+  const int lane = threadIdx.x & 31;
+  const int64_t n0 = ((int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * kW;
+  const int64_t N = w.n_rows, M = x.n_rows, K = x.n_cols;
+  if (n0 >= N) return;
+  const T *xp = static_cast<const T *>(x.data), *wp = static_cast<const T *>(w.data);
+  for (int64_t m0 = (int64_t)blockIdx.y * kM; m0 < M; m0 += (int64_t)gridDim.y * kM) {
+    float sum[kW][kM];
+#pragma unroll
+    for (int j = 0; j < kW; ++j)
+#pragma unroll
+      for (int m = 0; m < kM; ++m) sum[j][m] = 0.0f;
+#pragma unroll 2
+    for (int64_t k = (int64_t)lane * kN; k < K; k += 32 * kN) {
+      float xv[kM][kN], wv[kW][kN];
+#pragma unroll
+      for (int j = 0; j < kW; ++j) read_vec<T, kN>(wp + min(n0 + j, N - 1) * w.ld + k, wv[j]);
+#pragma unroll
+      for (int m = 0; m < kM; ++m) read_vec<T, kN>(xp + min(m0 + m, M - 1) * x.ld + k, xv[m]);
+#pragma unroll
+      for (int j = 0; j < kW; ++j)
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int i = 0; i < kN; ++i) sum[j][m] = fmaf(wv[j][i], xv[m][i], sum[j][m]);
+    }
+    float mine = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kW; ++j)
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const float v = warp_sum(sum[j][m]);
+        if (lane == j * kM + m) mine = v;
+      }
+    if (lane < kW * kM) {
+      const int64_t n = n0 + lane / kM, m = m0 + lane % kM;
+      if (n < N && m < M) finish_one(ep, m, n, mine);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+// gz = grad_y act'(pre) into gz[M][ld] (or nowhere), and the sums of its
+// columns over the block's rows into part[blockIdx.y][N] (or nowhere).
+template <typename T, int kN>
+__global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, int32_t act, T *gz,
+                                                  int64_t ld, float *part) {
+  __shared__ float sm[8][32 * kN + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t M = grad_y.n_rows, N = grad_y.n_cols, c = ((int64_t)blockIdx.x * 32 + lane) * kN;
+  float sum[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) sum[i] = 0.0f;
+  if (c < N)
+    for (int64_t m = (int64_t)blockIdx.y * 8 + warp; m < M; m += (int64_t)gridDim.y * 8) {
+      float g[kN], z[kN];
+      read_vec<T, kN>(static_cast<const T *>(grad_y.data) + m * grad_y.ld + c, g);
+      if (act != SS_ACT_NONE) {
+        read_vec<T, kN>(static_cast<const T *>(pre.data) + m * pre.ld + c, z);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) g[i] *= act_slope(act, z[i]);
+      }
+      if (gz) store_pack(gz + m * ld + c, narrow<T, kN>(g));
+#pragma unroll
+      for (int i = 0; i < kN; ++i) sum[i] += g[i];
+    }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) sm[warp][i * 32 + lane] = sum[i];
+  __syncthreads();
+  for (int t = threadIdx.x; t < 32 * kN; t += 256) {
+    float v = 0.0f;
+    for (int k = 0; k < 8; ++k) v += sm[k][t];
+    const int64_t col = ((int64_t)blockIdx.x * 32 + t % 32) * kN + t / 32;
+    if (col < N) part[(int64_t)blockIdx.y * N + col] = v;
+  }
+}
+
+// out[c] = sum over the n rows of part, in a fixed order.
+__global__ void __launch_bounds__(256) k_sum_parts(const float *part, int64_t n, int64_t N, float *out) {
+  __shared__ float sm[8][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float sum = 0.0f;
+  if (c < N)
+    for (int64_t k = warp; k < n; k += 8) sum += part[k * N + c];
+  sm[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && c < N) {
+    for (int k = 1; k < 8; ++k) sum += sm[k][lane];
+    out[c] = sum;
+  }
+}
+
+// Copies the rows of src (values of kSize bytes) to dst with rows of ld values.
+template <typename T>
+__global__ void __launch_bounds__(256) k_copy_rows(const ss_dense src, T *dst, int64_t ld) {
+  for (int64_t r = blockIdx.x; r < src.n_rows; r += gridDim.x)
+    for (int64_t c = threadIdx.x; c < src.n_cols; c += 256) dst[r * ld + c] = static_cast<const T *>(src.data)[r * src.ld + c];
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    cudaGetLastError();
+  });
+  return fn;
+}
+
+// A map of m (rows on 16-byte boundaries) for boxes of `inner` values x
+// `outer` rows in the 128-byte swizzle; parts outside the matrix read as 0.
+cudaError_t encode(CUtensorMap *map, const ss_dense &m, int inner, int outer) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
+  if (!fn) return cudaErrorNotSupported;
+  const int64_t size = size_of(m.type);
+  const cuuint64_t dims[2] = {(cuuint64_t)m.n_cols, (cuuint64_t)m.n_rows};
+  // one row: its stride is never used, and any ld is allowed for it
+  const cuuint64_t strides[1] = {(cuuint64_t)(m.n_rows > 1 ? m.ld * size : (m.n_cols * size + 15) / 16 * 16)};
+  const cuuint32_t box[2] = {(cuuint32_t)inner, (cuuint32_t)outer}, elem[2] = {1, 1};
+  return fn(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, m.data, dims, strides,
+            box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+int64_t padded_ld(const ss_dense &m) { return (m.n_cols + 15) / 16 * 16; }
+int64_t align_up(int64_t b) { return (b + SS_SCRATCH_ALIGN - 1) / SS_SCRATCH_ALIGN * SS_SCRATCH_ALIGN; }
+int64_t copy_bytes(const ss_dense &m) {
+  return rows_aligned(m, 16) ? 0 : align_up(m.n_rows * padded_ld(m) * size_of(m.type));
+}
+// m itself, or its copy with padded rows at *scratch (advanced past it).
+cudaError_t aligned_rows(ss_handle *h, ss_dense *m, unsigned char **scratch, cudaStream_t s, int *queued) {
+  if (rows_aligned(*m, 16)) return cudaSuccess;
+  const int64_t ld = padded_ld(*m);
+  const unsigned grid = (unsigned)std::min<int64_t>(m->n_rows, 8 * std::max(1, h->sm_count));
+  if (size_of(m->type) == 1)
+    k_copy_rows<uint8_t><<<grid, 256, 0, s>>>(*m, *scratch, ld);
+  else
+    k_copy_rows<uint16_t><<<grid, 256, 0, s>>>(*m, reinterpret_cast<uint16_t *>(*scratch), ld);
+  *queued += 1;
+  m->data = *scratch;
+  *scratch += align_up(m->n_rows * ld * size_of(m->type));
+  m->ld = ld;
+  return cudaGetLastError();
+}
+
+template <int kBN, int kMajA, int kMajB, bool kF8>
+cudaError_t run_product(Product &p, int split, cudaStream_t s) {
+  auto kernel = k_product<kBN, kMajA, kMajB, kF8>;
+  cudaError_t e = ensure_dyn_smem(kernel, Ring<kBN>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.tiles_a * p.tiles_b * split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Ring<kBN>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// ep.y = the product of A and B over their summed dimension; A and B are
+// [rows][summed] (kMajorK) or [summed][rows] (kMajorMN), rows aligned.
+cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B, int majB, bool swapped,
+                    const Epilogue &ep, cudaStream_t s, int *queued) {
+  const bool f8 = A.type == SS_VALUES_F8;
+  Product p = {};
+  p.rows_a = majA == kMajorK ? A.n_rows : A.n_cols;
+  p.rows_b = majB == kMajorK ? B.n_rows : B.n_cols;
+  const int64_t K = majA == kMajorK ? A.n_cols : A.n_rows;
+  p.ep = ep;
+  p.swapped = swapped ? 1 : 0;
+  p.status = h->d_status;
+  const int unit = f8 ? kRowBytes : kRowBytes / 2;
+  p.blocks_k = (int32_t)((K + unit - 1) / unit);
+  const int64_t sms = std::max(1, h->sm_count);
+  p.tiles_a = (int32_t)((p.rows_a + kTileM - 1) / kTileM);
+  // Columns a tile: as few as hold B's rows, at most 256 (64 at least for
+  // MN-major operands, whose copies are 64 rows wide), halved while the tiles
+  // would leave half of the SMs idle.
+  const int least = majB == kMajorK ? 16 : 64;
+  int bn = 256;
+  while (bn > least && bn / 2 >= p.rows_b) bn /= 2;
+  while (bn > 64 && (int64_t)p.tiles_a * ((p.rows_b + bn - 1) / bn) * 2 <= sms) bn /= 2;
+  p.tiles_b = (int32_t)((p.rows_b + bn - 1) / bn);
+  if ((int64_t)p.tiles_a * p.tiles_b > INT32_MAX) return cudaErrorInvalidConfiguration;
+  int split = 1;
+  if (bn <= 128)
+    while (split < 8 && (int64_t)p.tiles_a * p.tiles_b * split * 2 <= sms && p.blocks_k / (split * 2) >= 4) split *= 2;
+  const int type = A.type == SS_VALUES_BF16 ? 1 : 0;  // f8: 0 is e4m3
+  p.idesc = (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | ((uint32_t)majA << 15) |
+            ((uint32_t)majB << 16) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+  cudaError_t e;
+  e = majA == kMajorK ? encode(&p.a, A, unit, kTileM) : encode(&p.a, A, 64, unit);
+  if (e != cudaSuccess) return e;
+  e = majB == kMajorK ? encode(&p.b, B, unit, bn) : encode(&p.b, B, 64, unit);
+  if (e != cudaSuccess) return e;
+  *queued += 1;
+  if (f8) {
+    switch (bn) {
+      case 16: return run_product<16, kMajorK, kMajorK, true>(p, split, s);
+      case 32: return run_product<32, kMajorK, kMajorK, true>(p, split, s);
+      case 64: return run_product<64, kMajorK, kMajorK, true>(p, split, s);
+      case 128: return run_product<128, kMajorK, kMajorK, true>(p, split, s);
+      default: return run_product<256, kMajorK, kMajorK, true>(p, split, s);
+    }
+  }
+  if (majA == kMajorK && majB == kMajorK) {
+    switch (bn) {
+      case 16: return run_product<16, kMajorK, kMajorK, false>(p, split, s);
+      case 32: return run_product<32, kMajorK, kMajorK, false>(p, split, s);
+      case 64: return run_product<64, kMajorK, kMajorK, false>(p, split, s);
+      case 128: return run_product<128, kMajorK, kMajorK, false>(p, split, s);
+      default: return run_product<256, kMajorK, kMajorK, false>(p, split, s);
+    }
+  }
+  if (majA == kMajorK) {
+    switch (bn) {
+      case 64: return run_product<64, kMajorK, kMajorMN, false>(p, split, s);
+      case 128: return run_product<128, kMajorK, kMajorMN, false>(p, split, s);
+      default: return run_product<256, kMajorK, kMajorMN, false>(p, split, s);
+    }
+  }
+  switch (bn) {
+    case 64: return run_product<64, kMajorMN, kMajorMN, false>(p, split, s);
+    case 128: return run_product<128, kMajorMN, kMajorMN, false>(p, split, s);
+    default: return run_product<256, kMajorMN, kMajorMN, false>(p, split, s);
+  }
+}
+
+constexpr int64_t kFewRows = 4;     // k_rows up to this many rows
+constexpr int64_t kSwapRows = 256;  // features as A up to this many rows
+
+template <typename T, int kN>
+cudaError_t rows_typed(const ss_dense &x, const ss_dense &w, const Epilogue &ep, cudaStream_t s) {
+  const int64_t M = x.n_rows, N = w.n_rows;
+  auto run = [&](auto kernel, int m, int wide) {
+    kernel<<<dim3((unsigned)((N + kRowWarps * wide - 1) / (kRowWarps * wide)), (unsigned)std::min<int64_t>(65535, (M + m - 1) / m)), 32 * kRowWarps, 0,
+             s>>>(x, w, ep);
+  };
+  if (M == 1)
+    run(k_rows<T, 1, 4, kN>, 1, 4);
+  else if (M == 2)
+    run(k_rows<T, 2, 2, kN>, 2, 2);
+  else
+    run(k_rows<T, 4, 2, kN>, 4, 2);
+  return cudaGetLastError();
+}
+
+bool few_rows(const ss_dense &x) { return x.n_rows <= kFewRows || x.n_cols == 0; }
+
+int64_t grad_parts(const ss_handle *h, int64_t M, int64_t N) {
+  const int64_t slabs = (N + 255) / 256;
+  return std::max<int64_t>(1, std::min<int64_t>((M + 63) / 64, 8 * (int64_t)std::max(1, h->sm_count) / slabs));
+}
+
+}  // namespace
+
+int64_t linear_scratch(const ss_handle *, const ss_dense &x, const ss_dense &w) {
+  return few_rows(x) ? 0 : copy_bytes(x) + copy_bytes(w);
+}
+
+int64_t linear_grad_scratch(const ss_handle *h, const ss_dense &grad_y, const ss_dense &x, const ss_dense &w,
+                            int32_t act) {
+  const int64_t M = grad_y.n_rows, N = grad_y.n_cols;
+  const bool own = act != SS_ACT_NONE || !rows_aligned(grad_y, 16);
+  return copy_bytes(x) + copy_bytes(w) + (own ? align_up(M * padded_ld(grad_y) * size_of(grad_y.type)) : 0) +
+         align_up(grad_parts(h, M, N) * N * (int64_t)sizeof(float));
+}
+
+cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, int *queued) {
+  *queued = 0;
+  if (a.y.n_rows == 0 || a.y.n_cols == 0) return cudaSuccess;
+  Epilogue ep = {a.y, a.pre, a.residual, a.x_scale, a.w_scale, a.bias, a.activation, 0};
+  auto aligned = [](const ss_dense &m) { return !m.data || rows_aligned(m, 16); };
+  ep.vec = aligned(a.y) && aligned(a.pre) && aligned(a.residual);
+  if (few_rows(a.x)) {
+    *queued = 1;
+    const int v = a.x.type == SS_VALUES_F8 ? 16 : 8;
+    const bool vec = a.x.n_cols % v == 0 && rows_aligned(a.x, 16) && rows_aligned(a.w, 16);
+    switch (a.x.type) {
+      case SS_VALUES_F8:
+        return vec ? rows_typed<uint8_t, 16>(a.x, a.w, ep, s) : rows_typed<uint8_t, 1>(a.x, a.w, ep, s);
+      case SS_VALUES_BF16:
+        return vec ? rows_typed<__nv_bfloat16, 8>(a.x, a.w, ep, s) : rows_typed<__nv_bfloat16, 1>(a.x, a.w, ep, s);
+      default:
+        return vec ? rows_typed<__half, 8>(a.x, a.w, ep, s) : rows_typed<__half, 1>(a.x, a.w, ep, s);
+    }
+  }
+  ss_dense x = a.x, w = a.w;
+  unsigned char *scratch = a.scratch;
+  cudaError_t e;
+  if ((e = aligned_rows(h, &x, &scratch, s, queued)) != cudaSuccess) return e;
+  if ((e = aligned_rows(h, &w, &scratch, s, queued)) != cudaSuccess) return e;
+  const bool swapped = x.n_rows <= kSwapRows;
+  return swapped ? product(h, w, kMajorK, x, kMajorK, true, ep, s, queued)
+                 : product(h, x, kMajorK, w, kMajorK, false, ep, s, queued);
+}
+
+namespace {
+template <typename T>
+cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, int *queued) {
+  const int64_t M = a.grad_y.n_rows, N = a.grad_y.n_cols;
+  cudaError_t e;
+  unsigned char *scratch = a.scratch;
+  ss_dense gz = a.grad_y, x = a.x, w = a.w;
+  const bool own = a.activation != SS_ACT_NONE || !rows_aligned(a.grad_y, 16);
+  if (own) {
+    gz.ld = padded_ld(a.grad_y);
+    gz.data = scratch;
+    scratch += align_up(M * gz.ld * (int64_t)sizeof(T));
+  }
+  float *part = reinterpret_cast<float *>(scratch);
+  const int64_t parts = grad_parts(h, M, N);
+  scratch += align_up(parts * N * (int64_t)sizeof(float));
+  if (own || a.grad_bias) {
+    T *to = own ? static_cast<T *>(gz.data) : nullptr;
+    float *sums = a.grad_bias ? part : nullptr;
+    const bool vec = N % 8 == 0 && rows_aligned(a.grad_y, 16) && (!a.pre.data || rows_aligned(a.pre, 16));
+    if (vec)
+      k_act_grad<T, 8><<<dim3((unsigned)((N + 255) / 256), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, a.activation, to,
+                                                                                      gz.ld, sums);
+    else
+      k_act_grad<T, 1><<<dim3((unsigned)((N + 31) / 32), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, a.activation, to,
+                                                                                    gz.ld, sums);
+    *queued += 1;
+    if (sums) {
+      k_sum_parts<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(part, parts, N, a.grad_bias);
+      *queued += 1;
+    }
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  auto out = [](const ss_dense &m) {
+    Epilogue ep = {};
+    ep.y = m;
+    ep.vec = rows_aligned(m, 16);
+    return ep;
+  };
+  if (a.grad_x.data) {
+    if ((e = aligned_rows(h, &w, &scratch, s, queued)) != cudaSuccess) return e;
+    if ((e = product(h, gz, kMajorK, w, kMajorMN, false, out(a.grad_x), s, queued)) != cudaSuccess) return e;
+  }
+  if (a.grad_w.data) {
+    if ((e = aligned_rows(h, &x, &scratch, s, queued)) != cudaSuccess) return e;
+    if ((e = product(h, gz, kMajorMN, x, kMajorMN, false, out(a.grad_w), s, queued)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// Zeroes the rows of m (a sum over nothing).
+cudaError_t zero(const ss_dense &m, cudaStream_t s) {
+  if (!m.data || m.n_rows == 0 || m.n_cols == 0) return cudaSuccess;
+  const size_t size = (size_t)size_of(m.type);
+  return cudaMemset2DAsync(m.data, (size_t)m.ld * size, 0, (size_t)m.n_cols * size, (size_t)m.n_rows, s);
+}
+}  // namespace
+
+cudaError_t launch_linear_grad(ss_handle *h, const linear_grad_args &a, cudaStream_t s, int *queued) {
+  *queued = 0;
+  const int64_t M = a.grad_y.n_rows, N = a.grad_y.n_cols, K = a.x.n_cols;
+  if (M == 0 || N == 0) {
+    cudaError_t e = zero(a.grad_x, s);
+    if (e == cudaSuccess) e = zero(a.grad_w, s);
+    if (e == cudaSuccess && a.grad_bias && N > 0) e = cudaMemsetAsync(a.grad_bias, 0, sizeof(float) * (size_t)N, s);
+    return e;
+  }
+  linear_grad_args b = a;
+  if (K == 0) b.grad_x.data = b.grad_w.data = nullptr;
+  return a.x.type == SS_VALUES_BF16 ? grad_typed<__nv_bfloat16>(h, b, s, queued) : grad_typed<__half>(h, b, s, queued);
+}
