@@ -74,7 +74,7 @@ ss_chunk_consumer = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int
 
 _P = ctypes.c_void_p
 _CSR = ctypes.POINTER(ss_csr)
-_DENSE = ctypes.POINTER(ss_dense)
+_DENSE = _P  # ss_dense *: the address of a record
 _F32 = ctypes.c_float
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32

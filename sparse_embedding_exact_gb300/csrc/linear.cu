@@ -339,6 +339,308 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
   }
 }
 
+// ---------------------------------------------------------------- products by pairs of blocks
+constexpr int kEpiWarps = 8;                    // two for each 32 tensor-memory lanes, half of the columns each
+constexpr int kPairThreads = 64 + 32 * kEpiWarps;
+constexpr int kStaging = 32 * 128;              // an epilogue warp's box: 32 rows of 128 bytes
+
+struct PairProduct {
+  CUtensorMap a, b, y, pre;
+  Epilogue ep;
+  int32_t blocks_k, tiles_a, tiles_b;
+  uint32_t idesc;
+  int32_t *status;
+};
+
+template <int kBN>
+struct PairRing {
+  static constexpr int kBytesA = kTileM * kRowBytes, kBytesB = kBN / 2 * kRowBytes;
+  static constexpr int kStage = kBytesA + kBytesB;  // a block's part
+  static constexpr int kBoxes = kEpiWarps * 2 * kStaging;
+  static constexpr int kStages = (kSmemMost - 2048 - kBoxes) / kStage;
+  static constexpr int kSmem = kStages * kStage + kBoxes + 1024;
+};
+
+// One output box: 64 values of 16 bits or 32 of 32 bits a row, this thread's
+// row `lane`, in the 128-byte swizzle (chunk j of row r at j ^ (r % 8): no
+// bank is met twice by eight lanes).
+template <typename T, int kN>
+__device__ __forceinline__ void put_row(uint32_t box, int lane, const float *v) {
+  constexpr int kV = Type<T>::kVec;
+#pragma unroll
+  for (int j = 0; j < kN / kV; ++j) {
+    float f[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) f[i] = v[j * kV + i];
+    const Pack<T, kV> p = narrow<T, kV>(f);
+    uint4 q;
+    memcpy(&q, &p, 16);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))),
+                 "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                 : "memory");
+  }
+}
+
+// Writes 64 values of each lane's row (rows m0 + lane, columns n0 ..) to the
+// matrix of `map`, through the warp's two boxes in turn.
+__device__ __forceinline__ void put64(const ss_dense &out, const CUtensorMap *map, bool vec, uint32_t boxes, int &turn,
+                                      int lane, int64_t m0, int64_t n0, const float (&v)[64]) {
+  const bool wide = out.type == SS_VALUES_F32;
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    if (part && !wide) break;
+    const uint32_t box = boxes + (uint32_t)(turn & 1) * kStaging;
+    ++turn;
+    const int64_t n = n0 + 32 * part;
+    if (lane == 0) tc::store_wait_read1();
+    __syncwarp();
+    if (wide)
+      put_row<float, 32>(box, lane, v + 32 * part);
+    else if (out.type == SS_VALUES_BF16)
+      put_row<__nv_bfloat16, 64>(box, lane, v);
+    else
+      put_row<__half, 64>(box, lane, v);
+    if (vec) {
+      tc::fence_async();
+      __syncwarp();
+      if (lane == 0 && n < out.n_cols && m0 < out.n_rows) tc::store_2d(map, box, (int)n, (int)m0);
+      if (lane == 0) tc::store_commit();
+    } else {  // rows that start anywhere: row after row, the lanes along it
+      __syncwarp();
+      const int cols = wide ? 32 : 64;
+      for (int r = 0; r < 32 && m0 + r < out.n_rows; ++r)
+        for (int c = lane; c < cols && n + c < out.n_cols; c += 32) {
+          const int at = wide ? c * 4 : c * 2;
+          const uint32_t from = box + (uint32_t)(r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
+          const int64_t to = (m0 + r) * out.ld + n + c;
+          if (wide) {
+            uint32_t x;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
+            static_cast<uint32_t *>(out.data)[to] = x;
+          } else {
+            uint16_t x;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(from) : "memory");
+            static_cast<uint16_t *>(out.data)[to] = x;
+          }
+        }
+      __syncwarp();
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void add_row64(const T *p, float (&v)[64]) {
+  constexpr int kV = Type<T>::kVec;
+  Pack<T, kV> q[64 / kV];
+#pragma unroll
+  for (int j = 0; j < 64 / kV; ++j) q[j] = load_pack<T, kV>(p + j * kV);
+#pragma unroll
+  for (int j = 0; j < 64 / kV; ++j) {
+    float f[kV];
+    widen(q[j], f);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[j * kV + i] += f[i];
+  }
+}
+template <int kAct>
+__device__ __forceinline__ void act64(float (&v)[64]) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = act_of<kAct>(v[i]);
+}
+
+// 64 columns n .. of row m0 + lane: everything that follows the product.
+__device__ __forceinline__ void finish64(const PairProduct &a, uint32_t boxes, int &turn, int lane, int64_t m0, int64_t n0,
+                                         float (&v)[64]) {
+  const Epilogue &ep = a.ep;
+  const int64_t m = m0 + lane, M = ep.y.n_rows, N = ep.y.n_cols;
+  const bool whole = n0 + 64 <= N;
+  if (ep.row_scale) {
+    const float s = m < M ? ep.row_scale[m] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] *= s * (whole || n0 + i < N ? __ldg(ep.col_scale + n0 + i) : 0.0f);
+  }
+  if (ep.bias) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] += whole || n0 + i < N ? __ldg(ep.bias + n0 + i) : 0.0f;
+  }
+  if (ep.pre.data) put64(ep.pre, &a.pre, ep.vec, boxes, turn, lane, m0, n0, v);
+  switch (ep.act) {
+    case SS_ACT_RELU: act64<SS_ACT_RELU>(v); break;
+    case SS_ACT_GELU: act64<SS_ACT_GELU>(v); break;
+    case SS_ACT_GELU_TANH: act64<SS_ACT_GELU_TANH>(v); break;
+    case SS_ACT_SILU: act64<SS_ACT_SILU>(v); break;
+    case SS_ACT_LOG1P_RELU: act64<SS_ACT_LOG1P_RELU>(v); break;
+    default: break;
+  }
+  if (ep.residual.data && m < M) {
+    const int64_t at = m * ep.residual.ld + n0;
+    if (ep.vec && whole) {
+      if (ep.residual.type == SS_VALUES_F32)
+        add_row64(static_cast<const float *>(ep.residual.data) + at, v);
+      else if (ep.residual.type == SS_VALUES_BF16)
+        add_row64(static_cast<const __nv_bfloat16 *>(ep.residual.data) + at, v);
+      else
+        add_row64(static_cast<const __half *>(ep.residual.data) + at, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        if (n0 + i < N) v[i] += read_any(ep.residual, at + i);
+    }
+  }
+  put64(ep.y, &a.y, ep.vec, boxes, turn, lane, m0, n0, v);
+}
+
+// Persistent: each pair of blocks takes every n-th tile of 256 x kBN.
+template <int kBN, int kMajA, int kMajB, bool kF8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    k_product_pair(const __grid_constant__ PairProduct a) {
+  using R = PairRing<kBN>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t bars[2 * R::kStages + 4];
+  __shared__ uint32_t tmem_slot;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = (tc::smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t rank = tc::cluster_rank();
+  auto full = [&](int s) { return tc::smem_u32(&bars[s]); };
+  auto empty = [&](int s) { return tc::smem_u32(&bars[R::kStages + s]); };
+  auto acc_full = [&](int b) { return tc::smem_u32(&bars[2 * R::kStages + b]); };
+  auto acc_free = [&](int b) { return tc::smem_u32(&bars[2 * R::kStages + 2 + b]); };
+  constexpr uint32_t kCols = 2 * kBN;
+  if (tid == 0) {
+    for (int i = 0; i < 2 * R::kStages + 2; ++i) tc::bar_init(tc::smem_u32(&bars[i]), 1);
+    for (int b = 0; b < 2; ++b) tc::bar_init(acc_free(b), 2 * kEpiWarps);
+    tc::bar_init_fence();
+    tc::prefetch_map(&a.a);
+    tc::prefetch_map(&a.b);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_slot)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::cluster_sync();  // both blocks' barriers exist before either is signalled
+  tc::fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  const int n_pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int64_t tiles = (int64_t)a.tiles_a * a.tiles_b, group = 8ll * a.tiles_b;
+  const int kb = a.blocks_k;
+  constexpr int kUnit = kF8 ? kRowBytes : kRowBytes / 2;
+  // Down groups of 8 tile rows, so that the tiles in flight share both
+  // operands in L2.
+  auto place = [&](int64_t tile, int64_t &ta, int64_t &tb) {
+    const int64_t g0 = tile / group * 8, gh = min((int64_t)8, (int64_t)a.tiles_a - g0);
+    ta = g0 + (tile % group) % gh;
+    tb = (tile % group) / gh;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t tile = pair; tile < tiles && ok; tile += n_pairs) {
+        int64_t ta, tb;
+        place(tile, ta, tb);
+        const int32_t row_a = (int32_t)(ta * 2 * kTileM + rank * kTileM), row_b = (int32_t)(tb * kBN + rank * (kBN / 2));
+        for (int k = 0; k < kb; ++k, ++issued) {
+          const int s = (int)(issued % R::kStages);
+          const int64_t turn = issued / R::kStages;
+          if (turn > 0 && !(ok = tc::bar_wait(empty(s), (uint32_t)((turn - 1) & 1), a.status))) break;
+          if (rank == 0) tc::bar_expect(full(s), 2 * R::kStage);
+          const uint32_t bar = tc::map_rank(full(s), 0);
+          const uint32_t sa = ring + (uint32_t)(s * R::kStage), sb = sa + R::kBytesA;
+          if (kMajA == kMajorK) {
+            tc::load_2d_pair(sa, &a.a, k * kUnit, row_a, bar);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kTileM / 64; ++i) tc::load_2d_pair(sa + i * 8192, &a.a, row_a + 64 * i, k * kUnit, bar);
+          }
+          if (kMajB == kMajorK) {
+            tc::load_2d_pair(sb, &a.b, k * kUnit, row_b, bar);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kBN / 128; ++i) tc::load_2d_pair(sb + i * 8192, &a.b, row_b + 64 * i, k * kUnit, bar);
+          }
+        }
+      }
+      // The first block, whose barriers count both blocks' copies, waits for
+      // the last one into each stage; neither block leaves before that.
+      if (rank == 0)
+        for (int s = 0; s < R::kStages; ++s) {
+          const int64_t m = (issued + R::kStages - 1 - s) / R::kStages;
+          if (m > 0) tc::bar_wait(full(s), (uint32_t)((m - 1) & 1), a.status);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int64_t i = 0;
+      int t = 0;
+      bool ok = true;
+      for (int64_t tile = pair; tile < tiles && ok; tile += n_pairs, ++t) {
+        const int b = t & 1;
+        if (t >= 2 && !(ok = tc::bar_wait(acc_free(b), (uint32_t)(((t - 2) >> 1) & 1), a.status))) break;
+        tc::fence_after();
+        const uint32_t d = tmem + (uint32_t)(b * kBN);
+        for (int k = 0; k < kb; ++k, ++i) {
+          const int s = (int)(i % R::kStages);
+          if (!(ok = tc::bar_wait(full(s), (uint32_t)((i / R::kStages) & 1), a.status))) break;
+          tc::fence_after();
+          const uint32_t sa = ring + (uint32_t)(s * R::kStage), sb = sa + R::kBytesA;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t da = kMajA == kMajorK ? tc::desc_128b(sa + 32 * j, 16, 1024) : tc::desc_128b(sa + 2048 * j, 8192, 1024);
+            const uint64_t db = kMajB == kMajorK ? tc::desc_128b(sb + 32 * j, 16, 1024) : tc::desc_128b(sb + 2048 * j, 8192, 1024);
+            tc::mma_pair<kF8>(d, da, db, a.idesc, (k > 0 || j > 0) ? 1u : 0u);
+          }
+          tc::commit_pair(empty(s));
+        }
+        tc::commit_pair(acc_full(b));
+      }
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t boxes = ring + (uint32_t)(R::kStages * R::kStage + (warp - 2) * 2 * kStaging);
+    int t = 0, turn = 0;
+    for (int64_t tile = pair; tile < tiles; tile += n_pairs, ++t) {
+      const int b = t & 1;
+      if (!tc::bar_wait(acc_full(b), (uint32_t)((t >> 1) & 1), a.status)) break;
+      tc::fence_after();
+      int64_t ta, tb;
+      place(tile, ta, tb);
+      const int64_t m0 = ta * 2 * kTileM + rank * kTileM + q * 32;
+#pragma unroll 1
+      for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 64) {
+        uint32_t r[64];
+        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kBN + c);
+        tc::load_acc32(at, r);
+        tc::load_acc32(at + 32, r + 32);
+        tc::load_acc_wait();
+        if (c + 64 == (half + 1) * (kBN / 2)) {  // read out: the products may write it again
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::arrive_remote(tc::map_rank(acc_free(b), 0));
+        }
+        float v[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+        finish64(a, boxes, turn, lane, m0, tb * kBN + c, v);
+      }
+    }
+    if (lane == 0) tc::store_wait_all();
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();  // no block leaves while the other signals it or reads its operands
+  if (warp == 1) {
+    tc::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
+  }
+}
+
 // ---------------------------------------------------------------- few rows
 template <typename T, int kN>
 __device__ __forceinline__ void read_vec(const T *p, float (&f)[kN]) {
@@ -537,6 +839,61 @@ cudaError_t run_product(Product &p, int split, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// A map of an output for boxes of 128 bytes x 32 rows.
+cudaError_t encode_out(CUtensorMap *map, const ss_dense &m) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
+  if (!fn) return cudaErrorNotSupported;
+  const int64_t size = size_of(m.type);
+  const cuuint64_t dims[2] = {(cuuint64_t)m.n_cols, (cuuint64_t)m.n_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(m.n_rows > 1 ? m.ld * size : (m.n_cols * size + 15) / 16 * 16)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32}, elem[2] = {1, 1};
+  return fn(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, m.data, dims, strides,
+            box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int kBN, int kMajA, int kMajB, bool kF8>
+cudaError_t run_pair(ss_handle *h, PairProduct &p, cudaStream_t s) {
+  auto kernel = k_product_pair<kBN, kMajA, kMajB, kF8>;
+  cudaError_t e = ensure_dyn_smem(kernel, PairRing<kBN>::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)p.tiles_a * p.tiles_b;
+  const int64_t pairs = std::min<int64_t>(tiles, std::max(1, h->sm_count / 2));
+  kernel<<<(unsigned)(2 * pairs), kPairThreads, PairRing<kBN>::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+uint32_t idesc_of(const ss_dense &A, int majA, int majB, int m, int n) {
+  const uint32_t type = A.type == SS_VALUES_BF16 ? 1 : 0;  // fp16 and e4m3: 0
+  return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)majA << 15) | ((uint32_t)majB << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+template <int kBN>
+cudaError_t product_pair(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B, int majB, const Epilogue &ep,
+                         int64_t rows_a, int64_t rows_b, int64_t K, cudaStream_t s) {
+  const bool f8 = A.type == SS_VALUES_F8;
+  const int unit = f8 ? kRowBytes : kRowBytes / 2;
+  PairProduct p = {};
+  p.ep = ep;
+  p.status = h->d_status;
+  p.blocks_k = (int32_t)((K + unit - 1) / unit);
+  p.tiles_a = (int32_t)((rows_a + 2 * kTileM - 1) / (2 * kTileM));
+  p.tiles_b = (int32_t)((rows_b + kBN - 1) / kBN);
+  p.idesc = idesc_of(A, majA, majB, 2 * kTileM, kBN);
+  cudaError_t e = majA == kMajorK ? encode(&p.a, A, unit, kTileM) : encode(&p.a, A, 64, unit);
+  if (e == cudaSuccess) e = majB == kMajorK ? encode(&p.b, B, unit, kBN / 2) : encode(&p.b, B, 64, unit);
+  if (e == cudaSuccess && ep.vec) e = encode_out(&p.y, ep.y);
+  if (e == cudaSuccess && ep.vec && ep.pre.data) e = encode_out(&p.pre, ep.pre);
+  if (e != cudaSuccess) return e;
+  if (f8) return run_pair<kBN, kMajorK, kMajorK, true>(h, p, s);
+  if (majA == kMajorK && majB == kMajorK) return run_pair<kBN, kMajorK, kMajorK, false>(h, p, s);
+  if (majA == kMajorK) return run_pair<kBN, kMajorK, kMajorMN, false>(h, p, s);
+  return run_pair<kBN, kMajorMN, kMajorMN, false>(h, p, s);
+}
+
 // ep.y = the product of A and B over their summed dimension; A and B are
 // [rows][summed] (kMajorK) or [summed][rows] (kMajorMN), rows aligned.
 cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B, int majB, bool swapped,
@@ -552,6 +909,10 @@ cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B
   const int unit = f8 ? kRowBytes : kRowBytes / 2;
   p.blocks_k = (int32_t)((K + unit - 1) / unit);
   const int64_t sms = std::max(1, h->sm_count);
+  if (!swapped && ((p.rows_a + 255) / 256) * ((p.rows_b + 255) / 256) * 2 >= sms) {
+    *queued += 1;
+    return product_pair<256>(h, A, majA, B, majB, ep, p.rows_a, p.rows_b, K, s);
+  }
   p.tiles_a = (int32_t)((p.rows_a + kTileM - 1) / kTileM);
   // Columns a tile: as few as hold B's rows, at most 256 (64 at least for
   // MN-major operands, whose copies are 64 rows wide), halved while the tiles
@@ -565,9 +926,7 @@ cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B
   int split = 1;
   if (bn <= 128)
     while (split < 8 && (int64_t)p.tiles_a * p.tiles_b * split * 2 <= sms && p.blocks_k / (split * 2) >= 4) split *= 2;
-  const int type = A.type == SS_VALUES_BF16 ? 1 : 0;  // f8: 0 is e4m3
-  p.idesc = (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | ((uint32_t)majA << 15) |
-            ((uint32_t)majB << 16) | ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(kTileM >> 4) << 24);
+  p.idesc = idesc_of(A, majA, majB, kTileM, bn);
   cudaError_t e;
   e = majA == kMajorK ? encode(&p.a, A, unit, kTileM) : encode(&p.a, A, 64, unit);
   if (e != cudaSuccess) return e;

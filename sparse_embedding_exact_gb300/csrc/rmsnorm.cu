@@ -365,15 +365,9 @@ Shape shape_for(int64_t D, int n, int most_per) {
   return {kWideThreads, 0};
 }
 
-// Blocks that fill the GPU with `kernel` at `threads` a block, at most `rows`.
-template <typename K>
-int64_t fill(const ss_handle *h, K kernel, int threads, int64_t rows) {
-  int per_sm = 1;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) != cudaSuccess || per_sm < 1) {
-    cudaGetLastError();
-    per_sm = 1;
-  }
-  return std::min<int64_t>(rows, (int64_t)per_sm * std::max(1, h->sm_count));
+// Blocks that fill the GPU at `threads` a block, at most `rows`.
+int64_t fill(const ss_handle *h, int threads, int64_t rows) {
+  return std::min<int64_t>(rows, (int64_t)std::max(1, h->sm_count) * std::min(32, 2048 / threads));
 }
 
 template <typename T, bool kF8>
@@ -385,7 +379,7 @@ cudaError_t rms_norm_typed(ss_handle *h, const rms_args &a, cudaStream_t s) {
                    aligned(a.y, kF8 ? kV : 16);
   const Shape sh = shape_for(D, vec ? kV : 1, vec ? 4 : 16);
   auto run = [&](auto kernel) {
-    kernel<<<(unsigned)fill(h, kernel, sh.threads, R), sh.threads, 0, s>>>(a);
+    kernel<<<(unsigned)fill(h, sh.threads, R), sh.threads, 0, s>>>(a);
   };
   if (sh.per == 0)
     vec ? run(k_rms_norm_wide<T, kF8, kV>) : run(k_rms_norm_wide<T, kF8, 1>);
@@ -415,7 +409,7 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
   const Shape sh = shape_for(D, vec ? kV : 1, vec ? 4 : 16);
   int64_t n = most_parts(h, R, D);
   auto run = [&](auto kernel, int64_t blocks) {
-    blocks = std::min(blocks, fill(h, kernel, sh.threads, R));
+    blocks = std::min(blocks, fill(h, sh.threads, R));
     kernel<<<(unsigned)blocks, sh.threads, 0, s>>>(a);
     return blocks;
   };

@@ -5,6 +5,7 @@ e = 2^-24: a value that is a few float32 operations and a sum of n terms of
 size S is within u |value| + c e S of the exact one, c counting the roundings
 along the longest chain of additions.
 """
+import ctypes
 import math
 
 import pytest
@@ -583,13 +584,16 @@ def test_refusals(h):
     # the C calls check their own scratch and places
     lib, a = h._lib, sec._abi
     odd = _randn(8, 65, dtype=bf)[:, :63]
-    m = [h._matrix(t, "m") for t in (odd, _randn(32, 63, dtype=bf), torch.empty(8, 32, dtype=bf, device="cuda"))]
+    record = lambda t: a.ss_dense(*h._matrix(t, "m"))  # noqa: E731
+    ref_of = ctypes.addressof
+    keep = [record(t) for t in (odd, _randn(32, 63, dtype=bf), torch.empty(8, 32, dtype=bf, device="cuda"), x, g, g[:63])]
+    m = [ref_of(t) for t in keep]
     assert lib.ss_linear_scratch(h._h, m[0], m[1]) > 0
     assert lib.ss_linear(h._h, m[0], None, m[1], None, None, 0, None, None, m[2], None, 0, None) == a.SS_ERR_INVALID_ARG
-    z = h._matrix(x, "logits")
+    z = m[3]
     assert lib.ss_distill_backward(h._h, None, z, scores.data_ptr(), items.data_ptr(), 4, 1.0, 1.0, None,
                                    scores.data_ptr(), z, None) == a.SS_ERR_INVALID_ARG
     low = a.ss_dense(x.data_ptr(), 8, 64, 63, a.SS_VALUES_BF16)
-    assert lib.ss_rms_norm(h._h, low, None, h._matrix(g, "g"), 1e-6, None, z, None, None, None) == a.SS_ERR_INVALID_ARG
+    assert lib.ss_rms_norm(h._h, ref_of(low), None, m[4], 1e-6, None, z, None, None, None) == a.SS_ERR_INVALID_ARG
     off = a.ss_dense(x.data_ptr() + 1, 8, 63, 64, a.SS_VALUES_BF16)
-    assert lib.ss_rms_norm(h._h, off, None, h._matrix(g[:63], "g"), 1e-6, None, off, None, None, None) == a.SS_ERR_INVALID_ARG
+    assert lib.ss_rms_norm(h._h, ref_of(off), None, m[5], 1e-6, None, ref_of(off), None, None, None) == a.SS_ERR_INVALID_ARG
