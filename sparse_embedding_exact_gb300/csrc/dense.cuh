@@ -126,6 +126,10 @@ struct rms_grad_args {
 int64_t rms_grad_scratch(const ss_handle *h, int64_t rows, int64_t cols);
 cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &a, cudaStream_t s, int *queued);
 
+// out[c] = the sum of column c over the n rows of part (one kernel; a fixed
+// order), rounded to `type`.
+cudaError_t launch_sum_rows(const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s);
+
 struct distill_args {
   ss_dense logits, grad_logits;
   const float *scores;   // [rows][k]

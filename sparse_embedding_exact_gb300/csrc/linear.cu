@@ -33,6 +33,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "tc.cuh"
 
@@ -48,12 +49,30 @@ constexpr int kSmemMost = 227 * 1024;
 enum : int { kMajorK = 0, kMajorMN = 1 };
 
 // ---------------------------------------------------------------- activations
+// The normal distribution function and exp(-z^2 / 2), by Abramowitz and Stegun
+// 7.1.26: erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) with t = 1 / (1 + p x), off
+// by at most 1.5e-7; one exponential serves the gelu's slope as well, which
+// took twice the time with erff and expf (the gradient's pass over 8192 x 4096
+// values: 72 us, then 41 us).  Small values are not differences of large ones.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, x, 1.0f)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * x * -1.4426950408889634f));
+  const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  const float tail = 0.5f * poly * e;
+  return z > 0.0f ? 1.0f - tail : tail;
+}
+
 template <int kAct>
 __device__ __forceinline__ float act_of(float z) {
   if (kAct == SS_ACT_RELU) return z > 0.0f ? z : (z == z ? 0.0f : z);
-  if (kAct == SS_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if (kAct == SS_ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   if (kAct == SS_ACT_GELU_TANH) return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-  if (kAct == SS_ACT_SILU) return z / (1.0f + expf(-z));
+  if (kAct == SS_ACT_SILU) return z / (1.0f + __expf(-z));
   if (kAct == SS_ACT_LOG1P_RELU) return z > 0.0f ? log1pf(z) : (z == z ? 0.0f : z);
   return z;
 }
@@ -68,23 +87,25 @@ __device__ __forceinline__ float act_any(int32_t act, float z) {
   }
 }
 // act'(z); 0 at the kink of the rectified ones.
-__device__ __forceinline__ float act_slope(int32_t act, float z) {
-  switch (act) {
-    case SS_ACT_RELU: return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
-    case SS_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-    case SS_ACT_GELU_TANH: {
-      if (fabsf(z) > 1e4f) return z > 0.0f ? 1.0f : 0.0f;  // where z^2 could overflow
-      const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-      return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456080286536f * (1.0f + 0.134145f * z * z);
-    }
-    case SS_ACT_SILU: {
-      const float s = 1.0f / (1.0f + expf(-z));
-      return s * (1.0f + z * (1.0f - s));
-    }
-    case SS_ACT_LOG1P_RELU: return z > 0.0f ? 1.0f / (1.0f + z) : (z == z ? 0.0f : z);
-    default: return 1.0f;
+template <int kAct>
+__device__ __forceinline__ float act_slope(float z) {
+  if (kAct == SS_ACT_RELU) return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
+  if (kAct == SS_ACT_GELU) {
+    float e;
+    const float cdf = normal_cdf(z, e);
+    return fmaf(z * 0.39894228040143268f, e, cdf);
   }
+  if (kAct == SS_ACT_GELU_TANH) {
+    if (fabsf(z) > 1e4f) return z > 0.0f ? 1.0f : 0.0f;  // where z^2 could overflow
+    const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
+    return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456080286536f * (1.0f + 0.134145f * z * z);
+  }
+  if (kAct == SS_ACT_SILU) {
+    const float s = 1.0f / (1.0f + __expf(-z));
+    return s * (1.0f + z * (1.0f - s));
+  }
+  if (kAct == SS_ACT_LOG1P_RELU) return z > 0.0f ? 1.0f / (1.0f + z) : (z == z ? 0.0f : z);
+  return 1.0f;
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -709,28 +730,41 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_rows(const ss_dense x, const
 
 // ---------------------------------------------------------------- gradients
 // gz = grad_y act'(pre) into gz[M][ld] (or nowhere), and the sums of its
-// columns over the block's rows into part[blockIdx.y][N] (or nowhere).
-template <typename T, int kN>
-__global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, int32_t act, T *gz,
-                                                  int64_t ld, float *part) {
+// columns over the block's rows into part[blockIdx.y][N] (or nowhere).  A warp
+// takes every eighth row of the block's share, two of them at a time.
+template <typename T, int kN, int kAct>
+__global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, T *gz, int64_t ld, float *part) {
   __shared__ float sm[8][32 * kN + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t M = grad_y.n_rows, N = grad_y.n_cols, c = ((int64_t)blockIdx.x * 32 + lane) * kN;
+  const int64_t step = (int64_t)gridDim.y * 8;
+  const T *gp = static_cast<const T *>(grad_y.data) + c, *zp = static_cast<const T *>(pre.data) + c;
   float sum[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) sum[i] = 0.0f;
   if (c < N)
-    for (int64_t m = (int64_t)blockIdx.y * 8 + warp; m < M; m += (int64_t)gridDim.y * 8) {
-      float g[kN], z[kN];
-      read_vec<T, kN>(static_cast<const T *>(grad_y.data) + m * grad_y.ld + c, g);
-      if (act != SS_ACT_NONE) {
-        read_vec<T, kN>(static_cast<const T *>(pre.data) + m * pre.ld + c, z);
+    for (int64_t m = (int64_t)blockIdx.y * 8 + warp; m < M; m += 2 * step) {
+      Pack<T, kN> gv[2], zv[2];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) g[i] *= act_slope(act, z[i]);
-      }
-      if (gz) store_pack(gz + m * ld + c, narrow<T, kN>(g));
+      for (int u = 0; u < 2; ++u)
+        if (m + u * step < M) {
+          gv[u] = load_pack<T, kN>(gp + (m + u * step) * grad_y.ld);
+          if (kAct != SS_ACT_NONE) zv[u] = load_pack<T, kN>(zp + (m + u * step) * pre.ld);
+        }
 #pragma unroll
-      for (int i = 0; i < kN; ++i) sum[i] += g[i];
+      for (int u = 0; u < 2; ++u)
+        if (m + u * step < M) {
+          float g[kN], z[kN];
+          widen(gv[u], g);
+          if (kAct != SS_ACT_NONE) {
+            widen(zv[u], z);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) g[i] *= act_slope<kAct>(z[i]);
+          }
+          if (gz) store_pack(gz + (m + u * step) * ld + c, narrow<T, kN>(g));
+#pragma unroll
+          for (int i = 0; i < kN; ++i) sum[i] += g[i];
+        }
     }
   if (!part) return;
 #pragma unroll
@@ -741,22 +775,6 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
     for (int k = 0; k < 8; ++k) v += sm[k][t];
     const int64_t col = ((int64_t)blockIdx.x * 32 + t % 32) * kN + t / 32;
     if (col < N) part[(int64_t)blockIdx.y * N + col] = v;
-  }
-}
-
-// out[c] = sum over the n rows of part, in a fixed order.
-__global__ void __launch_bounds__(256) k_sum_parts(const float *part, int64_t n, int64_t N, float *out) {
-  __shared__ float sm[8][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float sum = 0.0f;
-  if (c < N)
-    for (int64_t k = warp; k < n; k += 8) sum += part[k * N + c];
-  sm[warp][lane] = sum;
-  __syncthreads();
-  if (warp == 0 && c < N) {
-    for (int k = 1; k < 8; ++k) sum += sm[k][lane];
-    out[c] = sum;
   }
 }
 
@@ -1054,18 +1072,27 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
     T *to = own ? static_cast<T *>(gz.data) : nullptr;
     float *sums = a.grad_bias ? part : nullptr;
     const bool vec = N % 8 == 0 && rows_aligned(a.grad_y, 16) && (!a.pre.data || rows_aligned(a.pre, 16));
-    if (vec)
-      k_act_grad<T, 8><<<dim3((unsigned)((N + 255) / 256), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, a.activation, to,
-                                                                                      gz.ld, sums);
-    else
-      k_act_grad<T, 1><<<dim3((unsigned)((N + 31) / 32), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, a.activation, to,
-                                                                                    gz.ld, sums);
+    auto run = [&](auto act) {
+      constexpr int kAct = decltype(act)::value;
+      if (vec)
+        k_act_grad<T, 8, kAct><<<dim3((unsigned)((N + 255) / 256), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, to, gz.ld, sums);
+      else
+        k_act_grad<T, 1, kAct><<<dim3((unsigned)((N + 31) / 32), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, to, gz.ld, sums);
+    };
+    switch (a.activation) {
+      case SS_ACT_RELU: run(std::integral_constant<int, SS_ACT_RELU>()); break;
+      case SS_ACT_GELU: run(std::integral_constant<int, SS_ACT_GELU>()); break;
+      case SS_ACT_GELU_TANH: run(std::integral_constant<int, SS_ACT_GELU_TANH>()); break;
+      case SS_ACT_SILU: run(std::integral_constant<int, SS_ACT_SILU>()); break;
+      case SS_ACT_LOG1P_RELU: run(std::integral_constant<int, SS_ACT_LOG1P_RELU>()); break;
+      default: run(std::integral_constant<int, SS_ACT_NONE>()); break;
+    }
     *queued += 1;
     if (sums) {
-      k_sum_parts<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(part, parts, N, a.grad_bias);
       *queued += 1;
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (sums && (e = launch_sum_rows(part, parts, N, a.grad_bias, SS_VALUES_F32, s)) != cudaSuccess) return e;
   }
   auto out = [](const ss_dense &m) {
     Epilogue ep = {};

@@ -13,33 +13,58 @@
 // Both are bound by memory: every value is read once, held in registers
 // across the row's reduction, and written once.  A block takes a row at a
 // time, every thread the same columns of each row, so the weights (and the
-// gradient's sums over rows) stay in registers; the next row is loaded before
-// the current row's reduction, which hides the reduction's barrier.  The sums
-// over a block's rows go to scratch, one row of it a block, and a second
-// kernel adds them in a fixed order: no atomics, the same bits every time.
+// gradient's sums over rows) stay in registers.  Rows arrive by bulk copies in
+// a ring of shared-memory slots, the next rows while one is worked on: with
+// plain loads into registers too few bytes were in flight (16,384 rows of 4096
+// bf16 with residual to 8 bits: 113 us, 4.2 TB/s).  A bulk copy moves whole
+// 16-byte units; where a row starts or ends inside one, the few values there
+// are read by ordinary loads.  The sums over a block's rows go to scratch, one
+// row of it a block, and a second kernel adds them in a fixed order: no
+// atomics, the same bits every time.
 #include <algorithm>
 
-#include "dense.cuh"
+#include "tc.cuh"
 
 namespace {
 
 using namespace dense;
 
 constexpr int kWideThreads = 1024;
-constexpr int kMostThreads = 512;  // of a block that holds its row in registers (up to 128 a thread)
+constexpr int64_t kRingBytes = 200 << 10;  // of an SM's shared memory, for the rings of its blocks
+constexpr int kMostThreads = 512;  // of a block that holds its rows in registers, up to 128 a thread
 
-// Sum of a and maximum of b over the block, in every thread.  `sm` holds two
-// sets of 32 pairs; consecutive calls alternate `set`, so that one barrier a
-// call is enough.
-__device__ __forceinline__ float2 block_sum_max(float a, float b, float2 (*sm)[32], int set) {
+// Threads of a block that work on one row: `index` of them in the block's
+// order, each of `threads` threads.
+struct Group {
+  int index, threads, lane;  // lane: this thread within its group
+  __device__ explicit Group(int t) : index(threadIdx.x / t), threads(t), lane(threadIdx.x % t) {}
+  __device__ void sync() const {
+    if (threads == 32)
+      __syncwarp();
+    else
+      tc::named_sync(1 + index, threads);
+  }
+};
+
+// Sum of a and maximum of b over the group, in every thread.  `sm` holds two
+// sets of 32 pairs, a group's at its first warp's number; consecutive calls
+// alternate `set`, so that one barrier a call is enough.
+__device__ __forceinline__ float2 group_sum_max(const Group &gr, float a, float b, float2 (*sm)[32], int set) {
   a = warp_sum(a);
   b = warp_max_nan(b);
-  const int n_warps = blockDim.x >> 5;
-  if (n_warps == 1) return make_float2(a, b);
-  const int lane = threadIdx.x & 31;
+  const int n_warps = gr.threads >> 5;
+  if (n_warps == 1) {
+    __syncwarp();
+    return make_float2(a, b);
+  }
+  const int lane = threadIdx.x & 31, first = gr.index * n_warps;
   if (lane == 0) sm[set][threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  const float2 v = lane < n_warps ? sm[set][lane] : make_float2(0.0f, 0.0f);
+  gr.sync();
+  if (n_warps == 4) {  // the usual width: no shuffles
+    const float2 v0 = sm[set][first], v1 = sm[set][first + 1], v2 = sm[set][first + 2], v3 = sm[set][first + 3];
+    return make_float2((v0.x + v1.x) + (v2.x + v3.x), max_nan(max_nan(v0.y, v1.y), max_nan(v2.y, v3.y)));
+  }
+  const float2 v = lane < n_warps ? sm[set][first + lane] : make_float2(0.0f, 0.0f);
   return make_float2(warp_sum(v.x), warp_max_nan(v.y));
 }
 
@@ -59,46 +84,113 @@ __device__ __forceinline__ float2 f8_factors(float most) {
   return make_float2(pre, most > 0.0f ? kF8Max / (most * pre) : (most == 0.0f ? 0.0f : most));
 }
 
+// A group's ring of rows in shared memory: slot s holds the current row of kRows
+// matrices.  Value c of a row lies at the same place within 16 bytes as in
+// global memory.
+template <typename T, int kRows>
+struct Ring {
+  uint32_t base, pitch;  // bytes of a row's place
+  uint32_t n;            // matrices present (the absent ones come last)
+  uint32_t bars;
+
+  static __host__ __device__ uint32_t pitch_for(int64_t D) { return (uint32_t)((D * (int64_t)sizeof(T) + 15) / 16 * 16 + 16); }
+
+  // By one thread: copies row `row` of each matrix (null: none) into a slot.
+  __device__ void fetch(int slot, const T *const (&p)[kRows], const int64_t (&ld)[kRows], int64_t row, int64_t D) const {
+    uint32_t bytes = 0;
+    const uint32_t bar = bars + 8u * slot;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (p[k]) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p[k] + row * ld[k]);
+        const uintptr_t b = (at + 15) & ~(uintptr_t)15, e = (at + D * sizeof(T)) & ~(uintptr_t)15;
+        if (e > b) bytes += (uint32_t)(e - b);
+      }
+    tc::bar_expect(bar, bytes);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+      if (p[k]) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p[k] + row * ld[k]);
+        const uintptr_t b = (at + 15) & ~(uintptr_t)15, e = (at + D * sizeof(T)) & ~(uintptr_t)15;
+        if (e > b)
+          tc::load_bulk(base + ((uint32_t)slot * n + k) * pitch + (uint32_t)(b - (at & ~(uintptr_t)15)),
+                        reinterpret_cast<const void *>(b), (uint32_t)(e - b), bar);
+      }
+  }
+  // Values c .. c + kN - 1 of the row of matrix k in `slot` (at `p` in global memory).
+  template <int kN>
+  __device__ __forceinline__ Pack<T, kN> read(int slot, int k, const T *p, int64_t c, int64_t D) const {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (kN == 1) {
+      const uintptr_t v = at + c * sizeof(T);
+      if (v < ((at + 15) & ~(uintptr_t)15) || v >= ((at + D * sizeof(T)) & ~(uintptr_t)15)) return load_pack<T, kN>(p + c);
+    }
+    return tc::read_shared<Pack<T, kN>>(base + ((uint32_t)slot * n + k) * pitch + (uint32_t)(at & 15) + (uint32_t)(c * sizeof(T)));
+  }
+};
+
+// Barriers and place of this group's ring in dynamic shared memory (the
+// barriers of 16 groups of 4 slots come first); the first rows' copies are
+// under way on return.  Row `first` and every `step`-th after it are the
+// group's.
+constexpr int kBarBytes = 16 * 4 * 8;
+template <typename T, int kRows>
+__device__ __forceinline__ Ring<T, kRows> open_ring(unsigned char *raw, const Group &gr, int slots, const T *const (&p)[kRows],
+                                                    const int64_t (&ld)[kRows], int64_t first, int64_t step, int64_t R,
+                                                    int64_t D) {
+  Ring<T, kRows> ring;
+  ring.pitch = Ring<T, kRows>::pitch_for(D);
+  ring.bars = tc::smem_u32(raw) + 32u * gr.index;
+  ring.n = 0;
+  for (int k = 0; k < kRows; ++k) ring.n += p[k] != nullptr;
+  ring.base = tc::smem_u32(raw) + kBarBytes + (uint32_t)(gr.index * slots) * ring.n * ring.pitch;
+  if (gr.lane == 0) {
+    for (int k = 0; k < slots; ++k) tc::bar_init(ring.bars + 8u * k, 1);
+    tc::bar_init_fence();
+    for (int k = 0; k < slots; ++k)
+      if (first + k * step < R) ring.fetch(k, p, ld, first + k * step, D);
+  }
+  __syncthreads();
+  return ring;
+}
+
 // kN values a vector (16 bytes of them, or 1), kPer vectors a thread: columns
-// (p * blockDim.x + tid) * kN + i.
+// (p * threads + lane) * kN + i of the group's row.
 template <typename T, bool kF8, int kN, int kPer>
-__global__ void __launch_bounds__(kMostThreads) k_rms_norm(const rms_args a) {
+__global__ void __launch_bounds__(kMostThreads) k_rms_norm(const rms_args a, int threads, int slots, int32_t *status) {
+  extern __shared__ __align__(16) unsigned char raw[];
   __shared__ float2 sm[2][32];
+  __shared__ int stalled;
+  if (threadIdx.x == 0) stalled = 0;
+  const Group gr(threads);
   const int64_t D = a.x.n_cols, R = a.x.n_rows;
-  const T *x = static_cast<const T *>(a.x.data), *r = static_cast<const T *>(a.residual.data);
+  const T *const src[2] = {static_cast<const T *>(a.x.data), static_cast<const T *>(a.residual.data)};
+  const int64_t ld[2] = {a.x.ld, a.residual.ld};
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / threads);
+  const int64_t first = (int64_t)gr.index * gridDim.x + blockIdx.x;
+  const Ring<T, 2> ring = open_ring<T, 2>(raw, gr, slots, src, ld, first, step, R, D);
   T *total = static_cast<T *>(a.total.data);
   float w[kPer][kN];
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
+    const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
     if (c < D) load_weights<kN>(a.weight, c, w[p]);
   }
-  Pack<T, kN> xv[kPer], rv[kPer];
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
-      if (c < D) {
-        xv[p] = load_pack<T, kN>(x + row * a.x.ld + c);
-        if (r) rv[p] = load_pack<T, kN>(r + row * a.residual.ld + c);
-      }
-    }
-  };
-  int set = 0;
-  if (blockIdx.x < R) fetch(blockIdx.x);
-  for (int64_t row = blockIdx.x; row < R; row += gridDim.x, set ^= 1) {
+  int set = 0, slot = 0;
+  uint32_t phase = 0;
+  for (int64_t row = first; row < R; row += step, set ^= 1) {
+    tc::bar_wait_on(ring.bars + 8u * slot, phase, status, &stalled);
     float s[kPer][kN], sq = 0.0f, most = 0.0f;
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
+      const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
       if (c < D) {
-        widen(xv[p], s[p]);
-        if (r) {
+        widen(ring.template read<kN>(slot, 0, src[0] + row * ld[0], c, D), s[p]);
+        if (src[1]) {
           float f[kN];
-          widen(rv[p], f);
+          widen(ring.template read<kN>(slot, 1, src[1] + row * ld[1], c, D), f);
 #pragma unroll
           for (int i = 0; i < kN; ++i) s[p][i] += f[i];
-          if (total) store_pack(total + row * a.total.ld + c, narrow<T, kN>(s[p]));
         }
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
@@ -107,18 +199,25 @@ __global__ void __launch_bounds__(kMostThreads) k_rms_norm(const rms_args a) {
         }
       }
     }
-    if (row + gridDim.x < R) fetch(row + gridDim.x);
-    const float2 red = block_sum_max(sq, most, sm, set);
+    const float2 red = group_sum_max(gr, sq, most, sm, set);
+    // every thread has read the slot: the row that comes `slots` turns later
+    const int64_t later = row + slots * step;
+    if (gr.lane == 0 && later < R) ring.fetch(slot, src, ld, later, D);
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
     const float rstd = 1.0f / sqrtf(red.x / (float)D + a.eps);
-    if (threadIdx.x == 0) {
+    if (gr.lane == 0) {
       if (a.rstd) a.rstd[row] = rstd;
       if (kF8) a.scale[row] = red.y * rstd / kF8Max;
     }
     const float2 to8 = f8_factors(red.y);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
+      const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
       if (c < D) {
+        if (total && src[1]) store_pack(total + row * a.total.ld + c, narrow<T, kN>(s[p]));
         float y[kN];
         if (kF8) {
 #pragma unroll
@@ -142,6 +241,7 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_norm_wide(const rms_args a
   const int64_t D = a.x.n_cols, R = a.x.n_rows;
   const T *x = static_cast<const T *>(a.x.data), *r = static_cast<const T *>(a.residual.data);
   T *total = static_cast<T *>(a.total.data);
+  const Group gr(blockDim.x);
   int set = 0;
   for (int64_t row = blockIdx.x; row < R; row += gridDim.x, set ^= 1) {
     auto values = [&](int64_t c, float (&s)[kN]) {
@@ -164,7 +264,7 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_norm_wide(const rms_args a
         if (kF8) most = max_nan(most, fabsf(s[i] * w[i]));
       }
     }
-    const float2 red = block_sum_max(sq, most, sm, set);
+    const float2 red = group_sum_max(gr, sq, most, sm, set);
     const float rstd = 1.0f / sqrtf(red.x / (float)D + a.eps);
     if (threadIdx.x == 0) {
       if (a.rstd) a.rstd[row] = rstd;
@@ -190,76 +290,102 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_norm_wide(const rms_args a
 // grad_x of the block's rows, and the block's part of grad_w into
 // scratch[blockIdx.x][D].
 template <typename T, int kN, int kPer>
-__global__ void __launch_bounds__(kMostThreads) k_rms_grad(const rms_grad_args a) {
+__global__ void __launch_bounds__(kMostThreads) k_rms_grad(const rms_grad_args a, int threads, int slots, int32_t *status) {
+  extern __shared__ __align__(16) unsigned char raw[];
   __shared__ float2 sm[2][32];
+  __shared__ int stalled;
+  if (threadIdx.x == 0) stalled = 0;
+  const Group gr(threads);
   const int64_t D = a.total.n_cols, R = a.total.n_rows;
-  const T *gy = static_cast<const T *>(a.grad_y.data), *x = static_cast<const T *>(a.total.data);
-  const T *gt = static_cast<const T *>(a.grad_total.data);
+  const T *const src[3] = {static_cast<const T *>(a.grad_y.data), static_cast<const T *>(a.total.data),
+                           static_cast<const T *>(a.grad_total.data)};
+  const int64_t ld[3] = {a.grad_y.ld, a.total.ld, a.grad_total.ld};
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / threads);
+  const int64_t first = (int64_t)gr.index * gridDim.x + blockIdx.x;
+  const Ring<T, 3> ring = open_ring<T, 3>(raw, gr, slots, src, ld, first, step, R, D);
   float w[kPer][kN], gw[kPer][kN];
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
+    const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
     if (c < D) load_weights<kN>(a.weight, c, w[p]);
 #pragma unroll
     for (int i = 0; i < kN; ++i) gw[p][i] = 0.0f;
   }
-  Pack<T, kN> gv[kPer], xv[kPer], tv[kPer];
-  float rstd_next = 0.0f;
-  auto fetch = [&](int64_t row) {
-    rstd_next = a.rstd[row];
-#pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
-      if (c < D) {
-        gv[p] = load_pack<T, kN>(gy + row * a.grad_y.ld + c);
-        xv[p] = load_pack<T, kN>(x + row * a.total.ld + c);
-        if (gt) tv[p] = load_pack<T, kN>(gt + row * a.grad_total.ld + c);
-      }
-    }
-  };
-  int set = 0;
-  if (blockIdx.x < R) fetch(blockIdx.x);
-  for (int64_t row = blockIdx.x; row < R; row += gridDim.x, set ^= 1) {
-    float g[kPer][kN], xh[kPer][kN], t[kPer][kN], dot = 0.0f;
+  int set = 0, slot = 0;
+  uint32_t phase = 0;
+  float rstd_next = first < R ? a.rstd[first] : 0.0f;
+  for (int64_t row = first; row < R; row += step, set ^= 1) {
     const float rstd = rstd_next;
+    if (row + step < R) rstd_next = a.rstd[row + step];
+    tc::bar_wait_on(ring.bars + 8u * slot, phase, status, &stalled);
+    // held as read, and widened again after the reduction: half the registers
+    Pack<T, kN> gv[kPer], xv[kPer], tv[kPer];
+    float dot = 0.0f;
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
+      const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
       if (c < D) {
-        widen(gv[p], g[p]);
-        widen(xv[p], xh[p]);
-        if (gt) widen(tv[p], t[p]);
+        gv[p] = ring.template read<kN>(slot, 0, src[0] + row * ld[0], c, D);
+        xv[p] = ring.template read<kN>(slot, 1, src[1] + row * ld[1], c, D);
+        if (src[2]) tv[p] = ring.template read<kN>(slot, 2, src[2] + row * ld[2], c, D);
+        float g[kN], xh[kN];
+        widen(gv[p], g);
+        widen(xv[p], xh);
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          xh[p][i] *= rstd;
-          gw[p][i] = fmaf(g[p][i], xh[p][i], gw[p][i]);
-          g[p][i] *= w[p][i];
-          dot = fmaf(g[p][i], xh[p][i], dot);
+          xh[i] *= rstd;
+          gw[p][i] = fmaf(g[i], xh[i], gw[p][i]);
+          dot = fmaf(g[i] * w[p][i], xh[i], dot);
         }
       }
     }
-    if (row + gridDim.x < R) fetch(row + gridDim.x);
-    const float mean = block_sum_max(dot, 0.0f, sm, set).x / (float)D;
+    const float mean = group_sum_max(gr, dot, 0.0f, sm, set).x / (float)D;
+    const int64_t later = row + slots * step;
+    if (gr.lane == 0 && later < R) ring.fetch(slot, src, ld, later, D);
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
+      const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
       if (c < D) {
-        float y[kN];
+        float g[kN], xh[kN], t[kN], y[kN];
+        widen(gv[p], g);
+        widen(xv[p], xh);
+        if (src[2]) widen(tv[p], t);
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          y[i] = rstd * (g[p][i] - xh[p][i] * mean);
-          if (gt) y[i] += t[p][i];
+          y[i] = rstd * (g[i] * w[p][i] - xh[i] * rstd * mean);
+          if (src[2]) y[i] += t[i];
         }
         store_pack(static_cast<T *>(a.grad_x.data) + row * a.grad_x.ld + c, narrow<T, kN>(y));
       }
     }
   }
+  // The groups' sums in their order, through the rings (whose copies have all
+  // been read).
+  const int groups = blockDim.x / threads;
+  float *mine = a.scratch + (int64_t)blockIdx.x * D;
+  float *place = reinterpret_cast<float *>(raw + kBarBytes);
+  if (groups > 1) {
+    __syncthreads();
+    mine = place + gr.index * D;
+  }
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * blockDim.x + threadIdx.x) * kN;
+    const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      if (c < D) a.scratch[(int64_t)blockIdx.x * D + c + i] = gw[p][i];
+      if (c < D) mine[c + i] = gw[p][i];
+  }
+  if (groups > 1) {
+    __syncthreads();
+    for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
+      float v = place[c];
+      for (int g = 1; g < groups; ++g) v += place[g * D + c];
+      a.scratch[(int64_t)blockIdx.x * D + c] = v;
+    }
   }
 }
 
@@ -270,6 +396,7 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_grad_wide(const rms_grad_a
   const int64_t D = a.total.n_cols, R = a.total.n_rows;
   const T *gy = static_cast<const T *>(a.grad_y.data), *x = static_cast<const T *>(a.total.data);
   const T *gt = static_cast<const T *>(a.grad_total.data);
+  const Group gr(blockDim.x);
   int set = 0;
   for (int64_t row = blockIdx.x; row < R; row += gridDim.x, set ^= 1) {
     const float rstd = a.rstd[row];
@@ -290,7 +417,7 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_grad_wide(const rms_grad_a
 #pragma unroll
       for (int i = 0; i < kN; ++i) dot = fmaf(g[i], xh[i], dot);
     }
-    const float mean = block_sum_max(dot, 0.0f, sm, set).x / (float)D;
+    const float mean = group_sum_max(gr, dot, 0.0f, sm, set).x / (float)D;
     for (int64_t c = (int64_t)threadIdx.x * kN; c < D; c += (int64_t)blockDim.x * kN) {
       float y[kN], t[kN];
       values(c, g, xh);
@@ -326,48 +453,69 @@ __global__ void __launch_bounds__(256) k_rms_grad_cols(const rms_grad_args a) {
   }
 }
 
-// grad_w[c] = sum over the n rows of part, in a fixed order: eight warps take
-// every eighth row of 32 columns each.
-__global__ void __launch_bounds__(256) k_sum_rows(const float *part, int64_t n, int64_t D, void *out, int32_t type) {
-  __shared__ float sm[8][33];
+// out[c] = sum over the n rows of part, in a fixed order: 32 warps take every
+// 32nd row of 32 columns each, four at a time.
+__global__ void __launch_bounds__(1024) k_sum_rows(const float *part, int64_t n, int64_t D, void *out, int32_t type) {
+  __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
-  float sum = 0.0f;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < D)
-    for (int64_t k = warp; k < n; k += 8) sum += part[k * D + c];
-  sm[warp][lane] = sum;
-  __syncthreads();
-  if (warp == 0 && c < D) {
-    for (int k = 1; k < 8; ++k) sum += sm[k][lane];
-    if (type == SS_VALUES_F32)
-      static_cast<float *>(out)[c] = sum;
-    else if (type == SS_VALUES_BF16)
-      static_cast<__nv_bfloat16 *>(out)[c] = __float2bfloat16_rn(sum);
-    else
-      static_cast<__half *>(out)[c] = __float2half_rn(sum);
-  }
-}
-
-// Threads and vectors a thread for D columns in vectors of n values: one
-// vector a thread where kMostThreads threads allow it (a row is then one load
-// a thread), else 4, else most_per; 0 vectors: too wide for registers.
-struct Shape {
-  int threads, per;
-};
-Shape shape_for(int64_t D, int n, int most_per) {
-  const int64_t vecs = (D + n - 1) / n;
-  for (int per = 1; per <= most_per; per *= 4) {
-    if (vecs <= (int64_t)per * kMostThreads) {
-      const int64_t t = (vecs + per - 1) / per;
-      return {(int)((t + 31) / 32 * 32), per};
+    for (int64_t k = warp; k < n; k += 128) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k + 32 * u < n) sum[u] += part[(k + 32 * u) * D + c];
     }
+  sm[warp][lane] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  __syncthreads();
+  const float v = warp_sum(sm[lane][warp]);  // of column blockIdx.x * 32 + warp
+  const int64_t col = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && col < D) {
+    if (type == SS_VALUES_F32)
+      static_cast<float *>(out)[col] = v;
+    else if (type == SS_VALUES_BF16)
+      static_cast<__nv_bfloat16 *>(out)[col] = __float2bfloat16_rn(v);
+    else
+      static_cast<__half *>(out)[col] = __float2half_rn(v);
   }
-  return {kWideThreads, 0};
 }
 
-// Blocks that fill the GPU at `threads` a block, at most `rows`.
-int64_t fill(const ss_handle *h, int threads, int64_t rows) {
-  return std::min<int64_t>(rows, (int64_t)std::max(1, h->sm_count) * std::min(32, 2048 / threads));
+// How rows of D columns in vectors of n values are worked on: `per` vectors a
+// thread of `threads` a row, `groups` rows a block, `slots` rows of the ring a
+// group, `blocks` an SM.  per = 0: too wide for registers.
+//
+// Many rows: the most of `pers`, 16 to 32 values a thread.  What a thread spends on a row besides its values (the reduction's shuffles and
+// barrier, the root) is as much as 8 values cost, and with 8 values a thread
+// the norm of 16,384 x 4096 bf16 rows to 8 bits was bound by instructions (94
+// us).  Rows for every SM or fewer: one vector a thread, for the time of one
+// row.
+constexpr int kVecPers[3] = {1, 4, 4}, kOnePers[3] = {1, 4, 16};
+constexpr int kGradPers[3] = {1, 2, 4};  // the gradient's 16-bit vectors: 4 only beyond 8192 columns, where 2 do not reach
+struct Shape {
+  int per, threads, groups, slots, blocks, smem;
+};
+Shape shape_for(const ss_handle *h, int64_t R, int64_t D, int n, const int (&pers)[3], int64_t row_bytes) {
+  const int64_t vecs = (D + n - 1) / n;
+  Shape sh = {0, kWideThreads, 1, 0, 2, 0};
+  for (int k = 0; k < 3; ++k) {
+    const int per = pers[k];
+    const int64_t t = ((vecs + per - 1) / per + 31) / 32 * 32;
+    if (t > kMostThreads || row_bytes > kRingBytes) continue;
+    if (sh.per && (vecs < 32 * per || R <= h->sm_count)) break;
+    if (sh.per == 2) break;
+    sh.per = per;
+    sh.threads = (int)t;
+  }
+  if (!sh.per) return sh;
+  const bool many = R > h->sm_count;
+  sh.groups = many ? std::max(1, 256 / sh.threads) : 1;
+  sh.blocks = std::max(1, (sh.per * n > 8 ? 512 : 1024) / (sh.groups * sh.threads));
+  // up to four slots a group within the SM's ring bytes
+  while (sh.blocks > 1 && sh.blocks * sh.groups * row_bytes > kRingBytes) sh.blocks /= 2;
+  while (sh.groups > 1 && sh.groups * row_bytes > kRingBytes) sh.groups /= 2;
+  sh.slots = (int)std::min<int64_t>(4, kRingBytes / (sh.blocks * sh.groups * row_bytes));
+  sh.smem = (int)(kBarBytes + sh.groups * sh.slots * row_bytes);
+  return sh;
 }
 
 template <typename T, bool kF8>
@@ -377,25 +525,29 @@ cudaError_t rms_norm_typed(ss_handle *h, const rms_args &a, cudaStream_t s) {
   auto aligned = [&](const ss_dense &m, int64_t unit) { return !m.data || rows_aligned(m, unit); };
   const bool vec = D % kV == 0 && aligned(a.x, 16) && aligned(a.residual, 16) && aligned(a.total, 16) &&
                    aligned(a.y, kF8 ? kV : 16);
-  const Shape sh = shape_for(D, vec ? kV : 1, vec ? 4 : 16);
-  auto run = [&](auto kernel) {
-    kernel<<<(unsigned)fill(h, sh.threads, R), sh.threads, 0, s>>>(a);
+  const Shape sh = shape_for(h, R, D, vec ? kV : 1, vec ? kVecPers : kOnePers, (a.residual.data ? 2 : 1) * (int64_t)Ring<T, 2>::pitch_for(D));
+  const unsigned grid = (unsigned)std::min<int64_t>((R + sh.groups - 1) / sh.groups, (int64_t)std::max(1, h->sm_count) * sh.blocks);
+  auto run = [&](auto kernel) -> cudaError_t {
+    const cudaError_t e = ensure_dyn_smem(kernel, sh.smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, sh.groups * sh.threads, sh.smem, s>>>(a, sh.threads, sh.slots, h->d_status);
+    return cudaGetLastError();
   };
-  if (sh.per == 0)
-    vec ? run(k_rms_norm_wide<T, kF8, kV>) : run(k_rms_norm_wide<T, kF8, 1>);
-  else if (vec)
-    sh.per == 1 ? run(k_rms_norm<T, kF8, kV, 1>) : run(k_rms_norm<T, kF8, kV, 4>);
-  else
-    sh.per == 1   ? run(k_rms_norm<T, kF8, 1, 1>)
-    : sh.per == 4 ? run(k_rms_norm<T, kF8, 1, 4>)
-                  : run(k_rms_norm<T, kF8, 1, 16>);
-  return cudaGetLastError();
+  if (sh.per == 0) {
+    if (vec)
+      k_rms_norm_wide<T, kF8, kV><<<grid, sh.threads, 0, s>>>(a);
+    else
+      k_rms_norm_wide<T, kF8, 1><<<grid, sh.threads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  if (vec) return sh.per == 1 ? run(k_rms_norm<T, kF8, kV, 1>) : run(k_rms_norm<T, kF8, kV, 4>);
+  return sh.per == 1 ? run(k_rms_norm<T, kF8, 1, 1>) : sh.per == 4 ? run(k_rms_norm<T, kF8, 1, 4>) : run(k_rms_norm<T, kF8, 1, 16>);
 }
 
-// Most blocks of a gradient launch: enough to fill the GPU, while the rows of
-// partial sums stay a few megabytes.
-int64_t most_parts(const ss_handle *h, int64_t R, int64_t D) {
-  return std::min<int64_t>(R, std::max<int64_t>(std::max(1, h->sm_count), (int64_t)(5 << 18) / D));
+// Most rows of partial sums of a gradient: its blocks, at most four an SM.
+constexpr int kGradBlocks = 4;
+int64_t most_parts(const ss_handle *h, int64_t R) {
+  return std::min<int64_t>(R, (int64_t)kGradBlocks * std::max(1, h->sm_count));
 }
 
 template <typename T>
@@ -406,28 +558,33 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
     return cudaMemsetAsync(a.grad_weight.data, 0, (size_t)(D * size_of(a.grad_weight.type)), s);
   auto aligned = [&](const ss_dense &m) { return !m.data || rows_aligned(m, 16); };
   const bool vec = D % kV == 0 && aligned(a.grad_y) && aligned(a.total) && aligned(a.grad_total) && aligned(a.grad_x);
-  const Shape sh = shape_for(D, vec ? kV : 1, vec ? 4 : 16);
-  int64_t n = most_parts(h, R, D);
-  auto run = [&](auto kernel, int64_t blocks) {
-    blocks = std::min(blocks, fill(h, sh.threads, R));
-    kernel<<<(unsigned)blocks, sh.threads, 0, s>>>(a);
-    return blocks;
+  const Shape sh = shape_for(h, R, D, vec ? kV : 1, vec ? (kV == 8 ? kGradPers : kVecPers) : kOnePers, (a.grad_total.data ? 3 : 2) * (int64_t)Ring<T, 3>::pitch_for(D));
+  int64_t n = std::min<int64_t>(most_parts(h, (R + sh.groups - 1) / sh.groups), (int64_t)std::max(1, h->sm_count) * sh.blocks);
+  auto run = [&](auto kernel) -> cudaError_t {
+    const cudaError_t e = ensure_dyn_smem(kernel, sh.smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)n, sh.groups * sh.threads, sh.smem, s>>>(a, sh.threads, sh.slots, h->d_status);
+    return cudaGetLastError();
   };
+  cudaError_t e = cudaSuccess;
   if (sh.per == 0) {
-    vec ? run(k_rms_grad_wide<T, kV>, R) : run(k_rms_grad_wide<T, 1>, R);
+    const unsigned grid = (unsigned)std::min<int64_t>(R, (int64_t)std::max(1, h->sm_count) * sh.blocks);
+    if (vec)
+      k_rms_grad_wide<T, kV><<<grid, sh.threads, 0, s>>>(a);
+    else
+      k_rms_grad_wide<T, 1><<<grid, sh.threads, 0, s>>>(a);
     n = std::min<int64_t>(n, 32);
     k_rms_grad_cols<T><<<dim3((unsigned)((D + 31) / 32), (unsigned)n), 256, 0, s>>>(a);
     *queued += 1;
+    e = cudaGetLastError();
   } else if (vec) {
-    n = sh.per == 1 ? run(k_rms_grad<T, kV, 1>, n) : run(k_rms_grad<T, kV, 4>, n);
+    e = sh.per == 1 ? run(k_rms_grad<T, kV, 1>) : sh.per == 2 ? run(k_rms_grad<T, kV, 2>) : run(k_rms_grad<T, kV, 4>);
   } else {
-    n = sh.per == 1   ? run(k_rms_grad<T, 1, 1>, n)
-        : sh.per == 4 ? run(k_rms_grad<T, 1, 4>, n)
-                      : run(k_rms_grad<T, 1, 16>, n);
+    e = sh.per == 1 ? run(k_rms_grad<T, 1, 1>) : sh.per == 4 ? run(k_rms_grad<T, 1, 4>) : run(k_rms_grad<T, 1, 16>);
   }
-  k_sum_rows<<<(unsigned)((D + 31) / 32), 256, 0, s>>>(a.scratch, n, D, a.grad_weight.data, a.grad_weight.type);
+  if (e != cudaSuccess) return e;
   *queued += 2;
-  return cudaGetLastError();
+  return launch_sum_rows(a.scratch, n, D, a.grad_weight.data, a.grad_weight.type, s);
 }
 
 }  // namespace
@@ -445,8 +602,13 @@ cudaError_t launch_rms_norm(ss_handle *h, const rms_args &a, cudaStream_t s, int
   }
 }
 
+cudaError_t launch_sum_rows(const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s) {
+  k_sum_rows<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(part, n, cols, out, type);
+  return cudaGetLastError();
+}
+
 int64_t rms_grad_scratch(const ss_handle *h, int64_t R, int64_t D) {
-  return R > 0 ? most_parts(h, R, D) * D * (int64_t)sizeof(float) : 0;
+  return R > 0 ? most_parts(h, R) * D * (int64_t)sizeof(float) : 0;
 }
 
 cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &a, cudaStream_t s, int *queued) {

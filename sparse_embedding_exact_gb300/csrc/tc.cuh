@@ -1,11 +1,12 @@
-// Tensor-core (tcgen05), tensor-copy (TMA) and mbarrier instructions as used
-// by linear.cu.
+// Tensor-core (tcgen05), asynchronous copy and mbarrier instructions of the
+// dense operators.
 #pragma once
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "dense.cuh"
 
@@ -50,6 +51,28 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int32_t 
     }
   }
 }
+// The same for code that must not leave its path when a wait runs out (the
+// block's other barriers count on every thread): waits until the phase
+// completes, kWaitNs pass (which flags DEV_STALL and sets *stalled) or
+// *stalled is set, and returns either way.
+__device__ __forceinline__ void bar_wait_on(uint32_t bar, uint32_t parity, int32_t *status, volatile int *stalled) {
+  if (bar_try(bar, parity)) return;
+  const long long t0 = global_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (bar_try(bar, parity)) return;
+    if (*stalled) return;
+    if (global_ns() - t0 > kWaitNs) {
+      dense::flag(status, DEV_STALL);
+      *stalled = 1;
+      return;
+    }
+  }
+}
+// The barrier `id` (1 to 15) of `threads` threads of the block.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -64,7 +87,33 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *map, in
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-// The same into this block's shared memory, counted on barrier `bar` (a
+// Plain bytes: both addresses 16-byte aligned, a multiple of 16 of them.
+__device__ __forceinline__ void load_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// A value of 2, 4 or 16 bytes at a shared address aligned to its size.
+template <typename P>
+__device__ __forceinline__ P read_shared(uint32_t at) {
+  P v;
+  if constexpr (sizeof(P) == 16) {
+    uint4 q;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
+    memcpy(&v, &q, 16);
+  } else if constexpr (sizeof(P) == 4) {
+    uint32_t q;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q) : "r"(at) : "memory");
+    memcpy(&v, &q, 4);
+  } else {
+    static_assert(sizeof(P) == 2, "16, 4 or 2 bytes");
+    uint16_t q;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(q) : "r"(at) : "memory");
+    memcpy(&v, &q, 2);
+  }
+  return v;
+}
+// A box into this block's shared memory, counted on barrier `bar` (a
 // cluster address) of either block of the pair.
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
   asm volatile(
@@ -179,6 +228,30 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Asks for the work of a cluster of this grid that has not started: the 16-byte
+// answer goes to shared address `at` of every block of this cluster and counts
+// on the barrier at `bar` there.
+__device__ __forceinline__ void ask_for_cluster(uint32_t at, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], [%1];" ::"r"(at),
+      "r"(bar)
+      : "memory");
+}
+// The first block's x of the cluster that an answer gives, or -1: none left.
+__device__ __forceinline__ int64_t cluster_given(uint32_t at) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.b32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}\n"
+      : "=r"(ok), "=r"(x)
+      : "r"(at)
+      : "memory");
+  return ok ? (int64_t)x : -1;
+}
 // The address in the cluster of shared address `addr` of block `rank`.
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   uint32_t a;
@@ -188,6 +261,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 // Arrives on a barrier given by its address in the cluster.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Two floats to shared memory of a block of the cluster, counted as 8 bytes on
+// barrier `bar` there (both cluster addresses).  Unlike an arrival that
+// releases to the cluster it does not wait for this thread's earlier stores.
+__device__ __forceinline__ void send_remote(uint32_t at, float x, float y, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at), "f"(x), "f"(y), "r"(bar)
+               : "memory");
 }
 // The float at shared address `addr` of block `rank` of the cluster.
 __device__ __forceinline__ float load_remote(uint32_t addr, uint32_t rank) {
