@@ -297,7 +297,7 @@ ss_status ss_distill_step(ss_handle *h, const float *grad_loss, const ss_dense *
   SS_TRY(check(h, grad_logits, logits->n_rows, logits->n_cols, F32 | HALVES, call, "grad_logits"));
   SS_TRY(same_type(h, grad_logits, logits->type, call, "grad_logits"));
   if (logits->n_rows > 0 && !loss) return report(h, SS_ERR_INVALID_ARG, "%s: null loss", call);
-  if (grad_logits->data == logits->data && grad_logits->ld != logits->ld && logits->n_rows > 1)
+  if (grad_logits->data == logits->data && grad_logits->ld != logits->ld && logits->n_rows > 1 && logits->n_cols > 0)
     return report(h, SS_ERR_INVALID_ARG, "%s: grad_logits in the logits' place with another ld", call);
   distill_args a = distill_of(logits, scores, items, k, temperature, teacher_temperature, weight);
   a.grad_loss = grad_loss;

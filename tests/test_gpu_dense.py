@@ -584,7 +584,12 @@ def test_refusals(h):
     # the C calls check their own scratch and places
     lib, a = h._lib, sec._abi
     odd = _randn(8, 65, dtype=bf)[:, :63]
-    record = lambda t: a.ss_dense(*h._matrix(t, "m"))  # noqa: E731
+    code = {torch.float32: a.SS_VALUES_F32, bf: a.SS_VALUES_BF16}
+
+    def record(t):
+        rows = t.shape[0] if t.dim() == 2 else 1
+        return a.ss_dense(t.data_ptr(), rows, t.shape[-1], t.stride(0) if rows > 1 else t.shape[-1], code[t.dtype])
+
     ref_of = ctypes.addressof
     keep = [record(t) for t in (odd, _randn(32, 63, dtype=bf), torch.empty(8, 32, dtype=bf, device="cuda"), x, g, g[:63])]
     m = [ref_of(t) for t in keep]
