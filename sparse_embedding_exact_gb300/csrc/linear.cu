@@ -109,6 +109,8 @@ __device__ __forceinline__ float act_slope(float z) {
 }
 
 // ---------------------------------------------------------------- epilogue
+constexpr int kStaging = 32 * 128;  // an epilogue warp's box: 32 rows of 128 bytes
+
 // What follows the product, for output rows m and features n.
 struct Epilogue {
   ss_dense y, pre, residual;
@@ -186,9 +188,208 @@ __device__ __forceinline__ void finish16(const Epilogue &ep, int64_t m, int64_t 
   write16_any(ep.y, m * ep.y.ld + n, v);
 }
 
+// One output box: 64 values of 16 bits or 32 of 32 bits a row, this thread's
+// row `lane`, in the 128-byte swizzle (chunk j of row r at j ^ (r % 8): no
+// bank is met twice by eight lanes).
+template <typename T, int kN>
+__device__ __forceinline__ void put_row(uint32_t box, int lane, const float *v) {
+  constexpr int kV = Type<T>::kVec;
+#pragma unroll
+  for (int j = 0; j < kN / kV; ++j) {
+    float f[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) f[i] = v[j * kV + i];
+    const Pack<T, kV> p = narrow<T, kV>(f);
+    uint4 q;
+    memcpy(&q, &p, 16);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))),
+                 "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                 : "memory");
+  }
+}
+
+// Writes 64 values of each lane's row (rows m0 + lane, columns n0 ..) to the
+// matrix of `map`, through the warp's box.
+__device__ __forceinline__ void put64(const ss_dense &out, const CUtensorMap *map, bool vec, uint32_t box, int lane, int64_t m0,
+                                      int64_t n0, const float (&v)[64]) {
+  const bool wide = out.type == SS_VALUES_F32;
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    if (part && !wide) break;
+    const int64_t n = n0 + 32 * part;
+    if (lane == 0) tc::store_wait_read();  // the box's last copy out
+    __syncwarp();
+    if (wide)
+      put_row<float, 32>(box, lane, v + 32 * part);
+    else if (out.type == SS_VALUES_BF16)
+      put_row<__nv_bfloat16, 64>(box, lane, v);
+    else
+      put_row<__half, 64>(box, lane, v);
+    if (vec) {
+      tc::fence_async();
+      __syncwarp();
+      if (lane == 0 && n < out.n_cols && m0 < out.n_rows) tc::store_2d(map, box, (int)n, (int)m0);
+      if (lane == 0) tc::store_commit();
+    } else {  // rows that start anywhere: row after row, the lanes along it
+      __syncwarp();
+      const int cols = wide ? 32 : 64;
+      for (int r = 0; r < 32 && m0 + r < out.n_rows; ++r)
+        for (int c = lane; c < cols && n + c < out.n_cols; c += 32) {
+          const int at = wide ? c * 4 : c * 2;
+          const uint32_t from = box + (uint32_t)(r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
+          const int64_t to = (m0 + r) * out.ld + n + c;
+          if (wide) {
+            uint32_t x;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
+            static_cast<uint32_t *>(out.data)[to] = x;
+          } else {
+            uint16_t x;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(from) : "memory");
+            static_cast<uint16_t *>(out.data)[to] = x;
+          }
+        }
+      __syncwarp();
+    }
+  }
+}
+
+// A box of 16-bit values, rows m0 .. m0 + 31 and columns n0 .. n0 + 63 of m: 16
+// bytes a lane, eight lanes along a row.  (A row a lane, though it needs no
+// box to change over, reads 16 bytes of each of 32 lines at a time: a residual
+// then cost 13 us of 170 at 8192 x 4096 x 4096.)
+struct Box64 {
+  uint4 q[8];
+};
+__device__ __forceinline__ Box64 load_box(const ss_dense &m, int64_t m0, int64_t n0, int lane) {
+  Box64 b;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t row = min(m0 + 4 * j + lane / 8, m.n_rows - 1);  // rows past the end are not used
+    b.q[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(m.data) + row * m.ld + n0 + lane % 8 * 8);
+  }
+  return b;
+}
+// Adds the box's row `lane` to v, through shared memory.
+template <typename T>
+__device__ __forceinline__ void add_box(const Box64 &b, uint32_t box, int lane, float (&v)[64]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int row = 4 * j + lane / 8, c = lane % 8;
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4))),
+                 "r"(b.q[j].x), "r"(b.q[j].y), "r"(b.q[j].z), "r"(b.q[j].w)
+                 : "memory");
+  }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float f[8];
+    widen(tc::read_shared<Pack<T, 8>>(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))), f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];
+  }
+  __syncwarp();
+}
+// The same for 16-bit rows that start anywhere or end within the box: row
+// after row, the lanes along it.
+template <typename T>
+__device__ __forceinline__ void add_ragged(const ss_dense &m, int64_t m0, int64_t n0, uint32_t box, int lane, float (&v)[64]) {
+  for (int r = 0; r < 32 && m0 + r < m.n_rows; ++r)
+    for (int c = lane; c < 64 && n0 + c < m.n_cols; c += 32) {
+      const uint16_t x = static_cast<const uint16_t *>(m.data)[(m0 + r) * m.ld + n0 + c];
+      asm volatile("st.shared.b16 [%0], %1;" ::"r"(box + (uint32_t)(r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2)), "h"(x)
+                   : "memory");
+    }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float f[8];
+    widen(tc::read_shared<Pack<T, 8>>(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))), f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];  // of columns that exist; the others are not stored
+  }
+  __syncwarp();
+}
+template <int kAct>
+__device__ __forceinline__ void act64(float (&v)[64]) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = act_of<kAct>(v[i]);
+}
+
+// Calls f(i, p[i]) for 64 columns (`n` of them exist): the same addresses in
+// every lane, four at a time where they are aligned.
+template <typename F>
+__device__ __forceinline__ void along64(const float *p, bool whole, int n, F f) {
+  if (whole && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float4 q = __ldg(reinterpret_cast<const float4 *>(p) + j);
+      f(4 * j, q.x);
+      f(4 * j + 1, q.y);
+      f(4 * j + 2, q.z);
+      f(4 * j + 3, q.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) f(i, i < n ? __ldg(p + i) : 0.0f);
+  }
+}
+
+// 64 columns n0 .. of rows m0 + lane: everything that follows the product,
+// from the accumulators at `acc`; `done` is called once they are read.  The
+// warp's boxes: one for what goes out, one for the residual.
+template <typename F>
+__device__ __forceinline__ void finish64(const Epilogue &ep, const CUtensorMap *map_y, const CUtensorMap *map_pre, uint32_t boxes,
+                                         int lane, int64_t m0, int64_t n0, uint32_t acc, F done) {
+  const int64_t m = m0 + lane, M = ep.y.n_rows, N = ep.y.n_cols;
+  const bool whole = n0 + 64 <= N, halves = ep.residual.data && ep.residual.type != SS_VALUES_F32;
+  const bool by_box = halves && ep.vec && whole && m0 < M;
+  Box64 res;
+  if (by_box) res = load_box(ep.residual, m0, n0, lane);  // asked for early: the rest hides the wait
+  float v[64];
+  {
+    uint32_t r[64];
+    tc::load_acc32(acc, r);
+    tc::load_acc32(acc + 32, r + 32);
+    tc::load_acc_wait();
+    done();
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+  }
+  if (ep.row_scale) {
+    const float s = m < M ? ep.row_scale[m] : 0.0f;
+    along64(ep.col_scale + n0, whole, (int)min((int64_t)64, N - n0), [&](int i, float f) { v[i] *= s * f; });
+  }
+  if (ep.bias) along64(ep.bias + n0, whole, (int)min((int64_t)64, N - n0), [&](int i, float f) { v[i] += f; });
+  if (ep.pre.data) put64(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);
+  switch (ep.act) {
+    case SS_ACT_RELU: act64<SS_ACT_RELU>(v); break;
+    case SS_ACT_GELU: act64<SS_ACT_GELU>(v); break;
+    case SS_ACT_GELU_TANH: act64<SS_ACT_GELU_TANH>(v); break;
+    case SS_ACT_SILU: act64<SS_ACT_SILU>(v); break;
+    case SS_ACT_LOG1P_RELU: act64<SS_ACT_LOG1P_RELU>(v); break;
+    default: break;
+  }
+  if (by_box) {
+    if (ep.residual.type == SS_VALUES_BF16)
+      add_box<__nv_bfloat16>(res, boxes + kStaging, lane, v);
+    else
+      add_box<__half>(res, boxes + kStaging, lane, v);
+  } else if (halves && m0 < M) {
+    if (ep.residual.type == SS_VALUES_BF16)
+      add_ragged<__nv_bfloat16>(ep.residual, m0, n0, boxes + kStaging, lane, v);
+    else
+      add_ragged<__half>(ep.residual, m0, n0, boxes + kStaging, lane, v);
+  } else if (ep.residual.data && m < M) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      if (n0 + i < N) v[i] += read_any(ep.residual, m * ep.residual.ld + n0 + i);
+  }
+  put64(ep.y, map_y, ep.vec, boxes, lane, m0, n0, v);
+}
+
 // ---------------------------------------------------------------- products
 struct Product {
-  CUtensorMap a, b;
+  CUtensorMap a, b, y, pre;
   Epilogue ep;
   int64_t rows_a, rows_b;
   int32_t blocks_k;   // stages of the summed dimension
@@ -204,7 +405,8 @@ struct Ring {
   static constexpr int kStage = kBytesA + kBytesB;
   static constexpr int kStages = (kSmemMost - 2048) / kStage < 8 ? (kSmemMost - 2048) / kStage : 8;
   static constexpr int kSmem = kStages * kStage + 1024;  // + alignment to 1024
-  static_assert(kBN * kTileM * 4 <= kStages * kStage, "a tile to exchange fits the ring");
+  static_assert((kBN + 1) * kTileM * 4 <= kStages * kStage, "a tile to exchange fits the ring");
+  static_assert(8 * kStaging <= kStages * kStage, "and so do four warps' boxes");
 };
 
 // One tile a cluster; its blocks take equal shares of the summed dimension.
@@ -305,49 +507,72 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
   __syncthreads();
   tc::fence_after();
 
-  const int64_t base = a.swapped ? tb * kBN : ta * kTileM;  // first output row
+  const int q = warp & 3, r = q * 32 + lane;  // epilogue: tensor-memory lane, row of A in the tile
+  const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
   if (split == 1) {
     if (warp >= 2 && ok) {
-      const int q = warp & 3;  // tensor-memory lanes 32 q .. 32 q + 31
-      const int r = q * 32 + lane;
-      for (int c = 0; c < kBN; c += 16) {
-        float v[16];
-        tc::load_acc16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
-        if (n == 0) {
+      if (a.swapped) {  // the lanes along the features
+        for (int c = 0; c < kBN; c += 16) {
+          float v[16];
+          tc::load_acc16(lanes + (uint32_t)c, v);
+          if ((int64_t)row_a + r < a.rows_a) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+            for (int i = 0; i < 16; ++i)
+              if ((int64_t)row_b + c + i < a.rows_b) finish_one(a.ep, (int64_t)row_b + c + i, row_a + r, v[i]);
+          }
         }
-        if (!a.swapped) {
+      } else if constexpr (kBN < 64) {
+        for (int c = 0; c < kBN; c += 16) {
+          float v[16];
+          tc::load_acc16(lanes + (uint32_t)c, v);
           finish16(a.ep, row_a + r, (int64_t)row_b + c, v);
-        } else if ((int64_t)row_a + r < a.rows_a) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (base + c + i < a.rows_b) finish_one(a.ep, base + c + i, row_a + r, v[i]);
         }
+      } else {
+        const uint32_t boxes = ring + (uint32_t)((warp - 2) * 2 * kStaging);
+#pragma unroll 1
+        for (int c = 0; c < kBN && (int64_t)row_b + c < a.rows_b; c += 64)
+          finish64(a.ep, &a.y, &a.pre, boxes, lane, (int64_t)row_a + q * 32, (int64_t)row_b + c, lanes + (uint32_t)c, [] {});
+        if (lane == 0) tc::store_wait_all();
       }
     }
   } else {
-    // tile[column][row of A] of this block's share
+    // This block's share of the sum to shared memory, [column][row of A]
+    // where the features are the rows of A, else [row of A][column + 1 pad]:
+    // either way the features lie along the lanes below.
+    constexpr int kPitch = kBN + 1;
     if (warp >= 2) {
-      const int q = warp & 3, r = q * 32 + lane;
       for (int c = 0; c < kBN; c += 16) {
         float v[16];
-        tc::load_acc16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+        tc::load_acc16(lanes + (uint32_t)c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(ring + (uint32_t)((c + i) * kTileM + r) * 4), "f"(n > 0 ? v[i] : 0.0f)
-                       : "memory");
+        for (int i = 0; i < 16; ++i) {
+          const int at = a.swapped ? (c + i) * kTileM + r : r * kPitch + c + i;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(ring + (uint32_t)at * 4), "f"(n > 0 ? v[i] : 0.0f) : "memory");
+        }
       }
     }
     tc::cluster_sync();
     if (warp >= 2 && ok) {
-      const int q = warp & 3, r = q * 32 + lane;
-      const int c0 = (int)(kBN * rank / split), c1 = (int)(kBN * (rank + 1) / split);
-      for (int c = c0; c < c1; ++c) {
-        float v = 0.0f;
-        for (uint32_t p = 0; p < split; ++p) v += tc::load_remote(ring + (uint32_t)(c * kTileM + r) * 4, p);
-        const int64_t ra = (int64_t)row_a + r, rb = (int64_t)row_b + c;
-        if (ra < a.rows_a && rb < a.rows_b) a.swapped ? finish_one(a.ep, rb, ra, v) : finish_one(a.ep, ra, rb, v);
+      if (a.swapped) {
+        const int c0 = (int)(kBN * rank / split), c1 = (int)(kBN * (rank + 1) / split);
+        for (int c = c0; c < c1; ++c) {
+          const int64_t ra = (int64_t)row_a + r, rb = (int64_t)row_b + c;
+          if (rb >= a.rows_b) break;
+          float v = 0.0f;
+          for (uint32_t p = 0; p < split; ++p) v += tc::load_remote(ring + (uint32_t)(c * kTileM + r) * 4, p);
+          if (ra < a.rows_a) finish_one(a.ep, rb, ra, v);
+        }
+      } else {
+        const int rows = kTileM / (int)split;
+        for (int i = q; i < rows; i += 4) {
+          const int row = rows * (int)rank + i;
+          if ((int64_t)row_a + row >= a.rows_a) break;
+          for (int c = lane; c < kBN && (int64_t)row_b + c < a.rows_b; c += 32) {
+            float v = 0.0f;
+            for (uint32_t p = 0; p < split; ++p) v += tc::load_remote(ring + (uint32_t)(row * kPitch + c) * 4, p);
+            finish_one(a.ep, (int64_t)row_a + row, (int64_t)row_b + c, v);
+          }
+        }
       }
     }
     tc::cluster_sync();  // no block leaves while another reads its tile
@@ -363,7 +588,6 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
 // ---------------------------------------------------------------- products by pairs of blocks
 constexpr int kEpiWarps = 8;                    // two for each 32 tensor-memory lanes, half of the columns each
 constexpr int kPairThreads = 64 + 32 * kEpiWarps;
-constexpr int kStaging = 32 * 128;              // an epilogue warp's box: 32 rows of 128 bytes
 
 struct PairProduct {
   CUtensorMap a, b, y, pre;
@@ -381,135 +605,6 @@ struct PairRing {
   static constexpr int kStages = (kSmemMost - 2048 - kBoxes) / kStage;
   static constexpr int kSmem = kStages * kStage + kBoxes + 1024;
 };
-
-// One output box: 64 values of 16 bits or 32 of 32 bits a row, this thread's
-// row `lane`, in the 128-byte swizzle (chunk j of row r at j ^ (r % 8): no
-// bank is met twice by eight lanes).
-template <typename T, int kN>
-__device__ __forceinline__ void put_row(uint32_t box, int lane, const float *v) {
-  constexpr int kV = Type<T>::kVec;
-#pragma unroll
-  for (int j = 0; j < kN / kV; ++j) {
-    float f[kV];
-#pragma unroll
-    for (int i = 0; i < kV; ++i) f[i] = v[j * kV + i];
-    const Pack<T, kV> p = narrow<T, kV>(f);
-    uint4 q;
-    memcpy(&q, &p, 16);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))),
-                 "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
-                 : "memory");
-  }
-}
-
-// Writes 64 values of each lane's row (rows m0 + lane, columns n0 ..) to the
-// matrix of `map`, through the warp's two boxes in turn.
-__device__ __forceinline__ void put64(const ss_dense &out, const CUtensorMap *map, bool vec, uint32_t boxes, int &turn,
-                                      int lane, int64_t m0, int64_t n0, const float (&v)[64]) {
-  const bool wide = out.type == SS_VALUES_F32;
-#pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    if (part && !wide) break;
-    const uint32_t box = boxes + (uint32_t)(turn & 1) * kStaging;
-    ++turn;
-    const int64_t n = n0 + 32 * part;
-    if (lane == 0) tc::store_wait_read1();
-    __syncwarp();
-    if (wide)
-      put_row<float, 32>(box, lane, v + 32 * part);
-    else if (out.type == SS_VALUES_BF16)
-      put_row<__nv_bfloat16, 64>(box, lane, v);
-    else
-      put_row<__half, 64>(box, lane, v);
-    if (vec) {
-      tc::fence_async();
-      __syncwarp();
-      if (lane == 0 && n < out.n_cols && m0 < out.n_rows) tc::store_2d(map, box, (int)n, (int)m0);
-      if (lane == 0) tc::store_commit();
-    } else {  // rows that start anywhere: row after row, the lanes along it
-      __syncwarp();
-      const int cols = wide ? 32 : 64;
-      for (int r = 0; r < 32 && m0 + r < out.n_rows; ++r)
-        for (int c = lane; c < cols && n + c < out.n_cols; c += 32) {
-          const int at = wide ? c * 4 : c * 2;
-          const uint32_t from = box + (uint32_t)(r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
-          const int64_t to = (m0 + r) * out.ld + n + c;
-          if (wide) {
-            uint32_t x;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
-            static_cast<uint32_t *>(out.data)[to] = x;
-          } else {
-            uint16_t x;
-            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(from) : "memory");
-            static_cast<uint16_t *>(out.data)[to] = x;
-          }
-        }
-      __syncwarp();
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void add_row64(const T *p, float (&v)[64]) {
-  constexpr int kV = Type<T>::kVec;
-  Pack<T, kV> q[64 / kV];
-#pragma unroll
-  for (int j = 0; j < 64 / kV; ++j) q[j] = load_pack<T, kV>(p + j * kV);
-#pragma unroll
-  for (int j = 0; j < 64 / kV; ++j) {
-    float f[kV];
-    widen(q[j], f);
-#pragma unroll
-    for (int i = 0; i < kV; ++i) v[j * kV + i] += f[i];
-  }
-}
-template <int kAct>
-__device__ __forceinline__ void act64(float (&v)[64]) {
-#pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = act_of<kAct>(v[i]);
-}
-
-// 64 columns n .. of row m0 + lane: everything that follows the product.
-__device__ __forceinline__ void finish64(const PairProduct &a, uint32_t boxes, int &turn, int lane, int64_t m0, int64_t n0,
-                                         float (&v)[64]) {
-  const Epilogue &ep = a.ep;
-  const int64_t m = m0 + lane, M = ep.y.n_rows, N = ep.y.n_cols;
-  const bool whole = n0 + 64 <= N;
-  if (ep.row_scale) {
-    const float s = m < M ? ep.row_scale[m] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] *= s * (whole || n0 + i < N ? __ldg(ep.col_scale + n0 + i) : 0.0f);
-  }
-  if (ep.bias) {
-#pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] += whole || n0 + i < N ? __ldg(ep.bias + n0 + i) : 0.0f;
-  }
-  if (ep.pre.data) put64(ep.pre, &a.pre, ep.vec, boxes, turn, lane, m0, n0, v);
-  switch (ep.act) {
-    case SS_ACT_RELU: act64<SS_ACT_RELU>(v); break;
-    case SS_ACT_GELU: act64<SS_ACT_GELU>(v); break;
-    case SS_ACT_GELU_TANH: act64<SS_ACT_GELU_TANH>(v); break;
-    case SS_ACT_SILU: act64<SS_ACT_SILU>(v); break;
-    case SS_ACT_LOG1P_RELU: act64<SS_ACT_LOG1P_RELU>(v); break;
-    default: break;
-  }
-  if (ep.residual.data && m < M) {
-    const int64_t at = m * ep.residual.ld + n0;
-    if (ep.vec && whole) {
-      if (ep.residual.type == SS_VALUES_F32)
-        add_row64(static_cast<const float *>(ep.residual.data) + at, v);
-      else if (ep.residual.type == SS_VALUES_BF16)
-        add_row64(static_cast<const __nv_bfloat16 *>(ep.residual.data) + at, v);
-      else
-        add_row64(static_cast<const __half *>(ep.residual.data) + at, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (n0 + i < N) v[i] += read_any(ep.residual, at + i);
-    }
-  }
-  put64(ep.y, &a.y, ep.vec, boxes, turn, lane, m0, n0, v);
-}
 
 // Persistent: each pair of blocks takes every n-th tile of 256 x kBN.
 template <int kBN, int kMajA, int kMajB, bool kF8>
@@ -624,7 +719,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t boxes = ring + (uint32_t)(R::kStages * R::kStage + (warp - 2) * 2 * kStaging);
-    int t = 0, turn = 0;
+    int t = 0;
     for (int64_t tile = pair; tile < tiles; tile += n_pairs, ++t) {
       const int b = t & 1;
       if (!tc::bar_wait(acc_full(b), (uint32_t)((t >> 1) & 1), a.status)) break;
@@ -634,20 +729,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int64_t m0 = ta * 2 * kTileM + rank * kTileM + q * 32;
 #pragma unroll 1
       for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 64) {
-        uint32_t r[64];
-        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kBN + c);
-        tc::load_acc32(at, r);
-        tc::load_acc32(at + 32, r + 32);
-        tc::load_acc_wait();
-        if (c + 64 == (half + 1) * (kBN / 2)) {  // read out: the products may write it again
-          tc::fence_before();
+        const bool last = c + 64 == (half + 1) * (kBN / 2);
+        finish64(a.ep, &a.y, &a.pre, boxes, lane, m0, tb * kBN + c, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kBN + c), [&] {
+          if (!last) return;
+          tc::fence_before();  // read out: the products may write it again
           __syncwarp();
           if (lane == 0) tc::arrive_remote(tc::map_rank(acc_free(b), 0));
-        }
-        float v[64];
-#pragma unroll
-        for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
-        finish64(a, boxes, turn, lane, m0, tb * kBN + c, v);
+        });
       }
     }
     if (lane == 0) tc::store_wait_all();
@@ -949,6 +1037,10 @@ cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B
   e = majA == kMajorK ? encode(&p.a, A, unit, kTileM) : encode(&p.a, A, 64, unit);
   if (e != cudaSuccess) return e;
   e = majB == kMajorK ? encode(&p.b, B, unit, bn) : encode(&p.b, B, 64, unit);
+  if (!swapped && split == 1 && bn >= 64 && ep.vec) {  // the epilogue that stores by tensor copies
+    if (e == cudaSuccess) e = encode_out(&p.y, ep.y);
+    if (e == cudaSuccess && ep.pre.data) e = encode_out(&p.pre, ep.pre);
+  }
   if (e != cudaSuccess) return e;
   *queued += 1;
   if (f8) {
