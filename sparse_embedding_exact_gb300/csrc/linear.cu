@@ -43,7 +43,8 @@ using namespace dense;
 
 constexpr int kTileM = 128;       // rows of A a tile
 constexpr int kRowBytes = 128;    // of the summed dimension a stage, both operands
-constexpr int kThreads = 192;     // copy warp, product warp, four epilogue warps
+constexpr int kEpiFew = 8;        // epilogue warps of a block on its own, two for each 32 tensor-memory lanes
+constexpr int kThreads = 64 + 32 * kEpiFew;  // copy warp, product warp, epilogue
 constexpr int kSmemMost = 227 * 1024;
 
 enum : int { kMajorK = 0, kMajorMN = 1 };
@@ -72,7 +73,7 @@ __device__ __forceinline__ float act_of(float z) {
     return z * normal_cdf(z, e);
   }
   if (kAct == SS_ACT_GELU_TANH) return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-  if (kAct == SS_ACT_SILU) return z / (1.0f + __expf(-z));
+  if (kAct == SS_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));  // an IEEE quotient's slow path orders the values: 128 cycles each
   if (kAct == SS_ACT_LOG1P_RELU) return z > 0.0f ? log1pf(z) : (z == z ? 0.0f : z);
   return z;
 }
@@ -109,7 +110,7 @@ __device__ __forceinline__ float act_slope(float z) {
 }
 
 // ---------------------------------------------------------------- epilogue
-constexpr int kStaging = 32 * 128;  // an epilogue warp's box: 32 rows of 128 bytes
+constexpr int kStaging = 32 * 64;  // an epilogue warp's box: 32 rows of 64 bytes
 
 // What follows the product, for output rows m and features n.
 struct Epilogue {
@@ -188,9 +189,15 @@ __device__ __forceinline__ void finish16(const Epilogue &ep, int64_t m, int64_t 
   write16_any(ep.y, m * ep.y.ld + n, v);
 }
 
-// One output box: 64 values of 16 bits or 32 of 32 bits a row, this thread's
-// row `lane`, in the 128-byte swizzle (chunk j of row r at j ^ (r % 8): no
-// bank is met twice by eight lanes).
+// An epilogue warp takes 32 rows x 32 columns at a time.  Its boxes in shared
+// memory have 32 rows of 64 bytes in the 64-byte swizzle of tensor copies
+// (16-byte unit j of row r at j ^ (r / 2 % 4)): eight lanes with a row each, or
+// four with a row's units, meet no bank twice.
+__device__ __forceinline__ uint32_t unit_at(uint32_t box, int row, int unit) {
+  return box + (uint32_t)(row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
+}
+
+// Writes kN values of 64 bytes together, this lane's row.
 template <typename T, int kN>
 __device__ __forceinline__ void put_row(uint32_t box, int lane, const float *v) {
   constexpr int kV = Type<T>::kVec;
@@ -202,126 +209,128 @@ __device__ __forceinline__ void put_row(uint32_t box, int lane, const float *v) 
     const Pack<T, kV> p = narrow<T, kV>(f);
     uint4 q;
     memcpy(&q, &p, 16);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))),
-                 "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(unit_at(box, lane, j)), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
                  : "memory");
   }
 }
-
-// Writes 64 values of each lane's row (rows m0 + lane, columns n0 ..) to the
+// The box's values to rows that start anywhere: row after row, the lanes along it.
+template <typename U>
+__device__ __forceinline__ void store_ragged(const ss_dense &out, uint32_t box, int lane, int64_t m0, int64_t n) {
+  constexpr int kCols = 64 / (int)sizeof(U), kPer = 16 / (int)sizeof(U);
+  U *to = static_cast<U *>(out.data) + m0 * out.ld + n + lane % kCols;
+#pragma unroll 8
+  for (int r = lane / kCols; r < 32; r += 32 / kCols) {
+    const int c = lane % kCols;
+    if (m0 + r < out.n_rows && n + c < out.n_cols)
+      to[r * out.ld] = tc::read_shared<U>(unit_at(box, r, c / kPer) + (uint32_t)(c % kPer * sizeof(U)));
+  }
+}
+// Writes 32 values of each lane's row (rows m0 + lane, columns n0 ..) to the
 // matrix of `map`, through the warp's box.
-__device__ __forceinline__ void put64(const ss_dense &out, const CUtensorMap *map, bool vec, uint32_t box, int lane, int64_t m0,
-                                      int64_t n0, const float (&v)[64]) {
+__device__ __forceinline__ void put32(const ss_dense &out, const CUtensorMap *map, bool vec, uint32_t box, int lane, int64_t m0,
+                                      int64_t n0, const float (&v)[32]) {
   const bool wide = out.type == SS_VALUES_F32;
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
     if (part && !wide) break;
-    const int64_t n = n0 + 32 * part;
+    const int64_t n = n0 + 16 * part;
     if (lane == 0) tc::store_wait_read();  // the box's last copy out
     __syncwarp();
     if (wide)
-      put_row<float, 32>(box, lane, v + 32 * part);
+      put_row<float, 16>(box, lane, v + 16 * part);
     else if (out.type == SS_VALUES_BF16)
-      put_row<__nv_bfloat16, 64>(box, lane, v);
+      put_row<__nv_bfloat16, 32>(box, lane, v);
     else
-      put_row<__half, 64>(box, lane, v);
+      put_row<__half, 32>(box, lane, v);
     if (vec) {
       tc::fence_async();
       __syncwarp();
-      if (lane == 0 && n < out.n_cols && m0 < out.n_rows) tc::store_2d(map, box, (int)n, (int)m0);
-      if (lane == 0) tc::store_commit();
-    } else {  // rows that start anywhere: row after row, the lanes along it
+      if (lane == 0) {
+        if (n < out.n_cols && m0 < out.n_rows) tc::store_2d(map, box, (int)n, (int)m0);
+        tc::store_commit();
+      }
+    } else {
       __syncwarp();
-      const int cols = wide ? 32 : 64;
-      for (int r = 0; r < 32 && m0 + r < out.n_rows; ++r)
-        for (int c = lane; c < cols && n + c < out.n_cols; c += 32) {
-          const int at = wide ? c * 4 : c * 2;
-          const uint32_t from = box + (uint32_t)(r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
-          const int64_t to = (m0 + r) * out.ld + n + c;
-          if (wide) {
-            uint32_t x;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(from) : "memory");
-            static_cast<uint32_t *>(out.data)[to] = x;
-          } else {
-            uint16_t x;
-            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(from) : "memory");
-            static_cast<uint16_t *>(out.data)[to] = x;
-          }
-        }
+      if (wide)
+        store_ragged<uint32_t>(out, box, lane, m0, n);
+      else
+        store_ragged<uint16_t>(out, box, lane, m0, n);
       __syncwarp();
     }
   }
 }
 
-// A box of 16-bit values, rows m0 .. m0 + 31 and columns n0 .. n0 + 63 of m: 16
-// bytes a lane, eight lanes along a row.  (A row a lane, though it needs no
-// box to change over, reads 16 bytes of each of 32 lines at a time: a residual
-// then cost 13 us of 170 at 8192 x 4096 x 4096.)
-struct Box64 {
-  uint4 q[8];
+// A box of 16-bit values, rows m0 .. m0 + 31 and columns n0 .. n0 + 31 of m, by
+// loads of 16 bytes, four lanes along a row, or of one value, a row at a time,
+// for rows that start anywhere or end in the box.  (A row a lane, though it
+// needs no shared memory to change over, reads 16 bytes of each of 32 lines at
+// a time: a residual then cost 13 us of 170 at 8192 x 4096 x 4096.)
+struct Box {
+  uint4 q[4];
 };
-__device__ __forceinline__ Box64 load_box(const ss_dense &m, int64_t m0, int64_t n0, int lane) {
-  Box64 b;
+__device__ __forceinline__ Box load_box(const ss_dense &m, bool whole, int64_t m0, int64_t n0, int lane) {
+  Box b;
+  const uint16_t *p = static_cast<const uint16_t *>(m.data) + n0;
+  if (whole) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t row = min(m0 + 4 * j + lane / 8, m.n_rows - 1);  // rows past the end are not used
-    b.q[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(m.data) + row * m.ld + n0 + lane % 8 * 8);
+    for (int j = 0; j < 4; ++j) {
+      const int64_t row = min(m0 + 8 * j + lane / 4, m.n_rows - 1);  // rows past the end are not used
+      b.q[j] = *reinterpret_cast<const uint4 *>(p + row * m.ld + lane % 4 * 8);
+    }
+  } else {
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const bool in = n0 + lane < m.n_cols;
+      const uint32_t lo = in && m0 + 2 * k < m.n_rows ? p[(m0 + 2 * k) * m.ld + lane] : 0;
+      const uint32_t hi = in && m0 + 2 * k + 1 < m.n_rows ? p[(m0 + 2 * k + 1) * m.ld + lane] : 0;
+      w[k] = lo | hi << 16;  // column `lane` of rows 2 k and 2 k + 1
+    }
+    memcpy(b.q, w, sizeof(w));
   }
   return b;
 }
 // Adds the box's row `lane` to v, through shared memory.
 template <typename T>
-__device__ __forceinline__ void add_box(const Box64 &b, uint32_t box, int lane, float (&v)[64]) {
+__device__ __forceinline__ void add_box(const Box &b, bool whole, uint32_t box, int lane, float (&v)[32]) {
+  if (whole) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int row = 4 * j + lane / 8, c = lane % 8;
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4))),
-                 "r"(b.q[j].x), "r"(b.q[j].y), "r"(b.q[j].z), "r"(b.q[j].w)
-                 : "memory");
+    for (int j = 0; j < 4; ++j)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(unit_at(box, 8 * j + lane / 4, lane % 4)), "r"(b.q[j].x),
+                   "r"(b.q[j].y), "r"(b.q[j].z), "r"(b.q[j].w)
+                   : "memory");
+  } else {
+    uint32_t w[16];
+    memcpy(w, b.q, sizeof(w));
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+      asm volatile("st.shared.b16 [%0], %1;" ::"r"(unit_at(box, r, lane / 8) + (uint32_t)(lane % 8 * 2)),
+                   "h"((uint16_t)(w[r / 2] >> r % 2 * 16))
+                   : "memory");
   }
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     float f[8];
-    widen(tc::read_shared<Pack<T, 8>>(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))), f);
+    widen(tc::read_shared<Pack<T, 8>>(unit_at(box, lane, j)), f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];
   }
   __syncwarp();
 }
-// The same for 16-bit rows that start anywhere or end within the box: row
-// after row, the lanes along it.
-template <typename T>
-__device__ __forceinline__ void add_ragged(const ss_dense &m, int64_t m0, int64_t n0, uint32_t box, int lane, float (&v)[64]) {
-  for (int r = 0; r < 32 && m0 + r < m.n_rows; ++r)
-    for (int c = lane; c < 64 && n0 + c < m.n_cols; c += 32) {
-      const uint16_t x = static_cast<const uint16_t *>(m.data)[(m0 + r) * m.ld + n0 + c];
-      asm volatile("st.shared.b16 [%0], %1;" ::"r"(box + (uint32_t)(r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2)), "h"(x)
-                   : "memory");
-    }
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float f[8];
-    widen(tc::read_shared<Pack<T, 8>>(box + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4))), f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[8 * j + i] += f[i];  // of columns that exist; the others are not stored
-  }
-  __syncwarp();
-}
 template <int kAct>
-__device__ __forceinline__ void act64(float (&v)[64]) {
+__device__ __forceinline__ void act32(float (&v)[32]) {
 #pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = act_of<kAct>(v[i]);
+  for (int i = 0; i < 32; ++i) v[i] = act_of<kAct>(v[i]);
 }
 
-// Calls f(i, p[i]) for 64 columns (`n` of them exist): the same addresses in
+// Calls f(i, p[i]) for 32 columns (`n` of them exist): the same addresses in
 // every lane, four at a time where they are aligned.
 template <typename F>
-__device__ __forceinline__ void along64(const float *p, bool whole, int n, F f) {
-  if (whole && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+__device__ __forceinline__ void along32(const float *p, int64_t n, F f) {
+  if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const float4 q = __ldg(reinterpret_cast<const float4 *>(p) + j);
       f(4 * j, q.x);
       f(4 * j + 1, q.y);
@@ -330,61 +339,56 @@ __device__ __forceinline__ void along64(const float *p, bool whole, int n, F f) 
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) f(i, i < n ? __ldg(p + i) : 0.0f);
+    for (int i = 0; i < 32; ++i) f(i, i < n ? __ldg(p + i) : 0.0f);
   }
 }
 
-// 64 columns n0 .. of rows m0 + lane: everything that follows the product,
+// 32 columns n0 .. of rows m0 + lane: everything that follows the product,
 // from the accumulators at `acc`; `done` is called once they are read.  The
 // warp's boxes: one for what goes out, one for the residual.
 template <typename F>
-__device__ __forceinline__ void finish64(const Epilogue &ep, const CUtensorMap *map_y, const CUtensorMap *map_pre, uint32_t boxes,
+__device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *map_y, const CUtensorMap *map_pre, uint32_t boxes,
                                          int lane, int64_t m0, int64_t n0, uint32_t acc, F done) {
   const int64_t m = m0 + lane, M = ep.y.n_rows, N = ep.y.n_cols;
-  const bool whole = n0 + 64 <= N, halves = ep.residual.data && ep.residual.type != SS_VALUES_F32;
-  const bool by_box = halves && ep.vec && whole && m0 < M;
-  Box64 res;
-  if (by_box) res = load_box(ep.residual, m0, n0, lane);  // asked for early: the rest hides the wait
-  float v[64];
+  const bool there = m0 < M && n0 < N, whole = ep.vec && n0 + 32 <= N;
+  const bool by_box = there && ep.residual.data && ep.residual.type != SS_VALUES_F32;
+  Box res;
+  if (by_box) res = load_box(ep.residual, whole, m0, n0, lane);  // asked for early: the rest hides the wait
+  float v[32];
   {
-    uint32_t r[64];
+    uint32_t r[32];
     tc::load_acc32(acc, r);
-    tc::load_acc32(acc + 32, r + 32);
     tc::load_acc_wait();
     done();
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
   }
+  if (!there) return;
   if (ep.row_scale) {
     const float s = m < M ? ep.row_scale[m] : 0.0f;
-    along64(ep.col_scale + n0, whole, (int)min((int64_t)64, N - n0), [&](int i, float f) { v[i] *= s * f; });
+    along32(ep.col_scale + n0, N - n0, [&](int i, float f) { v[i] *= s * f; });
   }
-  if (ep.bias) along64(ep.bias + n0, whole, (int)min((int64_t)64, N - n0), [&](int i, float f) { v[i] += f; });
-  if (ep.pre.data) put64(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);
+  if (ep.bias) along32(ep.bias + n0, N - n0, [&](int i, float f) { v[i] += f; });
+  if (ep.pre.data) put32(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);
   switch (ep.act) {
-    case SS_ACT_RELU: act64<SS_ACT_RELU>(v); break;
-    case SS_ACT_GELU: act64<SS_ACT_GELU>(v); break;
-    case SS_ACT_GELU_TANH: act64<SS_ACT_GELU_TANH>(v); break;
-    case SS_ACT_SILU: act64<SS_ACT_SILU>(v); break;
-    case SS_ACT_LOG1P_RELU: act64<SS_ACT_LOG1P_RELU>(v); break;
+    case SS_ACT_RELU: act32<SS_ACT_RELU>(v); break;
+    case SS_ACT_GELU: act32<SS_ACT_GELU>(v); break;
+    case SS_ACT_GELU_TANH: act32<SS_ACT_GELU_TANH>(v); break;
+    case SS_ACT_SILU: act32<SS_ACT_SILU>(v); break;
+    case SS_ACT_LOG1P_RELU: act32<SS_ACT_LOG1P_RELU>(v); break;
     default: break;
   }
   if (by_box) {
     if (ep.residual.type == SS_VALUES_BF16)
-      add_box<__nv_bfloat16>(res, boxes + kStaging, lane, v);
+      add_box<__nv_bfloat16>(res, whole, boxes + kStaging, lane, v);
     else
-      add_box<__half>(res, boxes + kStaging, lane, v);
-  } else if (halves && m0 < M) {
-    if (ep.residual.type == SS_VALUES_BF16)
-      add_ragged<__nv_bfloat16>(ep.residual, m0, n0, boxes + kStaging, lane, v);
-    else
-      add_ragged<__half>(ep.residual, m0, n0, boxes + kStaging, lane, v);
+      add_box<__half>(res, whole, boxes + kStaging, lane, v);
   } else if (ep.residual.data && m < M) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < 32; ++i)
       if (n0 + i < N) v[i] += read_any(ep.residual, m * ep.residual.ld + n0 + i);
   }
-  put64(ep.y, map_y, ep.vec, boxes, lane, m0, n0, v);
+  put32(ep.y, map_y, ep.vec, boxes, lane, m0, n0, v);
 }
 
 // ---------------------------------------------------------------- products
@@ -406,7 +410,7 @@ struct Ring {
   static constexpr int kStages = (kSmemMost - 2048) / kStage < 8 ? (kSmemMost - 2048) / kStage : 8;
   static constexpr int kSmem = kStages * kStage + 1024;  // + alignment to 1024
   static_assert((kBN + 1) * kTileM * 4 <= kStages * kStage, "a tile to exchange fits the ring");
-  static_assert(8 * kStaging <= kStages * kStage, "and so do four warps' boxes");
+  static_assert(2 * kEpiFew * kStaging <= kStages * kStage, "and so do the epilogue's boxes");
 };
 
 // One tile a cluster; its blocks take equal shares of the summed dimension.
@@ -508,11 +512,14 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
   tc::fence_after();
 
   const int q = warp & 3, r = q * 32 + lane;  // epilogue: tensor-memory lane, row of A in the tile
+  const int half = (warp - 2) >> 2;           // which columns of it
   const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+  constexpr int kSlice = kBN / 2 < 16 ? 16 : kBN / 2;
+  const int slice0 = half * kSlice, slice1 = min(kBN, slice0 + kSlice);  // none for the second of 16 columns
   if (split == 1) {
     if (warp >= 2 && ok) {
       if (a.swapped) {  // the lanes along the features
-        for (int c = 0; c < kBN; c += 16) {
+        for (int c = slice0; c < slice1; c += 16) {
           float v[16];
           tc::load_acc16(lanes + (uint32_t)c, v);
           if ((int64_t)row_a + r < a.rows_a) {
@@ -522,7 +529,7 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
           }
         }
       } else if constexpr (kBN < 64) {
-        for (int c = 0; c < kBN; c += 16) {
+        for (int c = slice0; c < slice1; c += 16) {
           float v[16];
           tc::load_acc16(lanes + (uint32_t)c, v);
           finish16(a.ep, row_a + r, (int64_t)row_b + c, v);
@@ -530,8 +537,8 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
       } else {
         const uint32_t boxes = ring + (uint32_t)((warp - 2) * 2 * kStaging);
 #pragma unroll 1
-        for (int c = 0; c < kBN && (int64_t)row_b + c < a.rows_b; c += 64)
-          finish64(a.ep, &a.y, &a.pre, boxes, lane, (int64_t)row_a + q * 32, (int64_t)row_b + c, lanes + (uint32_t)c, [] {});
+        for (int c = slice0; c < slice1; c += 32)
+          finish32(a.ep, &a.y, &a.pre, boxes, lane, (int64_t)row_a + q * 32, (int64_t)row_b + c, lanes + (uint32_t)c, [] {});
         if (lane == 0) tc::store_wait_all();
       }
     }
@@ -541,7 +548,7 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
     // either way the features lie along the lanes below.
     constexpr int kPitch = kBN + 1;
     if (warp >= 2) {
-      for (int c = 0; c < kBN; c += 16) {
+      for (int c = slice0; c < slice1; c += 16) {
         float v[16];
         tc::load_acc16(lanes + (uint32_t)c, v);
 #pragma unroll
@@ -555,7 +562,7 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
     if (warp >= 2 && ok) {
       if (a.swapped) {
         const int c0 = (int)(kBN * rank / split), c1 = (int)(kBN * (rank + 1) / split);
-        for (int c = c0; c < c1; ++c) {
+        for (int c = c0 + half; c < c1; c += 2) {
           const int64_t ra = (int64_t)row_a + r, rb = (int64_t)row_b + c;
           if (rb >= a.rows_b) break;
           float v = 0.0f;
@@ -564,7 +571,7 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
         }
       } else {
         const int rows = kTileM / (int)split;
-        for (int i = q; i < rows; i += 4) {
+        for (int i = warp - 2; i < rows; i += kEpiFew) {
           const int row = rows * (int)rank + i;
           if ((int64_t)row_a + row >= a.rows_a) break;
           for (int c = lane; c < kBN && (int64_t)row_b + c < a.rows_b; c += 32) {
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
 }
 
 // ---------------------------------------------------------------- products by pairs of blocks
-constexpr int kEpiWarps = 8;                    // two for each 32 tensor-memory lanes, half of the columns each
+constexpr int kEpiWarps = 16;                   // four for each 32 tensor-memory lanes, a quarter of the columns each
 constexpr int kPairThreads = 64 + 32 * kEpiWarps;
 
 struct PairProduct {
@@ -717,7 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int q = warp & 3, quarter = (warp - 2) >> 2;
     const uint32_t boxes = ring + (uint32_t)(R::kStages * R::kStage + (warp - 2) * 2 * kStaging);
     int t = 0;
     for (int64_t tile = pair; tile < tiles; tile += n_pairs, ++t) {
@@ -728,9 +735,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       place(tile, ta, tb);
       const int64_t m0 = ta * 2 * kTileM + rank * kTileM + q * 32;
 #pragma unroll 1
-      for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 64) {
-        const bool last = c + 64 == (half + 1) * (kBN / 2);
-        finish64(a.ep, &a.y, &a.pre, boxes, lane, m0, tb * kBN + c, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kBN + c), [&] {
+      for (int c = quarter * (kBN / 4); c < (quarter + 1) * (kBN / 4); c += 32) {
+        const bool last = c + 32 == (quarter + 1) * (kBN / 4);
+        finish32(a.ep, &a.y, &a.pre, boxes, lane, m0, tb * kBN + c, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kBN + c), [&] {
           if (!last) return;
           tc::fence_before();  // read out: the products may write it again
           __syncwarp();
@@ -945,16 +952,16 @@ cudaError_t run_product(Product &p, int split, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// A map of an output for boxes of 128 bytes x 32 rows.
+// A map of an output for boxes of 64 bytes x 32 rows.
 cudaError_t encode_out(CUtensorMap *map, const ss_dense &m) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const int64_t size = size_of(m.type);
   const cuuint64_t dims[2] = {(cuuint64_t)m.n_cols, (cuuint64_t)m.n_rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(m.n_rows > 1 ? m.ld * size : (m.n_cols * size + 15) / 16 * 16)};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32}, elem[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)(64 / size), 32}, elem[2] = {1, 1};
   return fn(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, m.data, dims, strides,
-            box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
