@@ -77,6 +77,46 @@ __device__ __forceinline__ void store_f8(uint8_t *p, const float (&f)[kN]) {
   }
 }
 
+// Two float32 values in one register pair: one instruction for both.
+struct Two {
+  unsigned long long v;
+};
+__device__ __forceinline__ Two two(float x, float y) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma_of(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// Values 2 i and 2 i + 1 of a vector.
+__device__ __forceinline__ Two pair_of(const Pack<float, 4> &p, int i) { return two(p.v[2 * i], p.v[2 * i + 1]); }
+__device__ __forceinline__ Two pair_of(const Pack<__nv_bfloat16, 8> &p, int i) {
+  const float2 f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162 *>(p.v)[i]);
+  return two(f.x, f.y);
+}
+__device__ __forceinline__ Two pair_of(const Pack<__half, 8> &p, int i) {
+  const float2 f = __half22float2(reinterpret_cast<const __half2 *>(p.v)[i]);
+  return two(f.x, f.y);
+}
 // The larger of two values, NaN when either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;

@@ -55,48 +55,14 @@ __device__ __forceinline__ void join(Run &a, float m, float s, float c) {
   a.s = a.s * exp2_fast((a.m - o) * c) + s * exp2_fast((m - o) * c);
   a.m = M;
 }
-// Two float32 lanes in one register pair: one instruction for both.  With
-// them a step takes about 10 instructions a bf16 value, of the 21 that its
-// share of the memory's time allows.
-struct Two {
-  unsigned long long v;
-};
-__device__ __forceinline__ Two two(float x, float y) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 both(Two a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ Two operator+(Two a, Two b) {
-  Two r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Two operator*(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-// 2^((z - o) c) of both, with `minus` = -o twice.
+// 2^((z - o) c) of both, with `minus` = -o twice.  In pairs of values a step
+// takes about 10 instructions a bf16 value, of the 21 that its share of the
+// memory's time allows.
 __device__ __forceinline__ Two exp_of(Two z, Two minus, Two c) {
   const float2 x = both((z + minus) * c);
   return two(exp2_fast(x.x), exp2_fast(x.y));
 }
 
-// Values 2 i and 2 i + 1 of a vector.
-__device__ __forceinline__ Two pair_of(const Pack<float, 4> &p, int i) { return two(p.v[2 * i], p.v[2 * i + 1]); }
-__device__ __forceinline__ Two pair_of(const Pack<__nv_bfloat16, 8> &p, int i) {
-  const float2 f = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162 *>(p.v)[i]);
-  return two(f.x, f.y);
-}
-__device__ __forceinline__ Two pair_of(const Pack<__half, 8> &p, int i) {
-  const float2 f = __half22float2(reinterpret_cast<const __half2 *>(p.v)[i]);
-  return two(f.x, f.y);
-}
 __device__ __forceinline__ float max_of(const Pack<float, 4> &p) { return fmaxf(fmaxf(p.v[0], p.v[1]), fmaxf(p.v[2], p.v[3])); }
 __device__ __forceinline__ float max_of(const Pack<__nv_bfloat16, 8> &p) {
   const __nv_bfloat162 *q = reinterpret_cast<const __nv_bfloat162 *>(p.v);

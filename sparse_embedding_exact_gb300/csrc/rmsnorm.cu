@@ -22,6 +22,7 @@
 // row of it a block, and a second kernel adds them in a fixed order: no
 // atomics, the same bits every time.
 #include <algorithm>
+#include <initializer_list>
 
 #include "tc.cuh"
 
@@ -46,12 +47,13 @@ struct Group {
   }
 };
 
-// Sum of a and maximum of b over the group, in every thread.  `sm` holds two
-// sets of 32 pairs, a group's at its first warp's number; consecutive calls
-// alternate `set`, so that one barrier a call is enough.
-__device__ __forceinline__ float2 group_sum_max(const Group &gr, float a, float b, float2 (*sm)[32], int set) {
+// Sum of a (and, with kMax, maximum of b) over the group, in every thread.  `sm`
+// holds two sets of 32 pairs, a group's at its first warp's number;
+// consecutive calls alternate `set`, so that one barrier a call is enough.
+template <bool kMax>
+__device__ __forceinline__ float2 group_reduce(const Group &gr, float a, float b, float2 (*sm)[32], int set) {
   a = warp_sum(a);
-  b = warp_max_nan(b);
+  if (kMax) b = warp_max_nan(b);
   const int n_warps = gr.threads >> 5;
   if (n_warps == 1) {
     __syncwarp();
@@ -60,19 +62,27 @@ __device__ __forceinline__ float2 group_sum_max(const Group &gr, float a, float 
   const int lane = threadIdx.x & 31, first = gr.index * n_warps;
   if (lane == 0) sm[set][threadIdx.x >> 5] = make_float2(a, b);
   gr.sync();
-  if (n_warps == 4) {  // the usual width: no shuffles
-    const float2 v0 = sm[set][first], v1 = sm[set][first + 1], v2 = sm[set][first + 2], v3 = sm[set][first + 3];
-    return make_float2((v0.x + v1.x) + (v2.x + v3.x), max_nan(max_nan(v0.y, v1.y), max_nan(v2.y, v3.y)));
+  if (n_warps == 2 || n_warps == 4) {  // the usual widths: no shuffles
+    const float2 v0 = sm[set][first], v1 = sm[set][first + 1];
+    float2 r = make_float2(v0.x + v1.x, kMax ? max_nan(v0.y, v1.y) : 0.0f);
+    if (n_warps == 4) {
+      const float2 v2 = sm[set][first + 2], v3 = sm[set][first + 3];
+      r.x += v2.x + v3.x;
+      if (kMax) r.y = max_nan(r.y, max_nan(v2.y, v3.y));
+    }
+    return r;
   }
   const float2 v = lane < n_warps ? sm[set][first + lane] : make_float2(0.0f, 0.0f);
-  return make_float2(warp_sum(v.x), warp_max_nan(v.y));
+  return make_float2(warp_sum(v.x), kMax ? warp_max_nan(v.y) : 0.0f);
 }
 
+// Weights c .. c + kN - 1, 0 where the row has none.
 template <int kN>
 __device__ __forceinline__ void load_weights(const ss_dense &w, int64_t c, float (&f)[kN]) {
 #pragma unroll
   for (int i = 0; i < kN; ++i)
-    f[i] = w.type == SS_VALUES_F32    ? static_cast<const float *>(w.data)[c + i]
+    f[i] = c + i < 0 || c + i >= w.n_cols ? 0.0f
+           : w.type == SS_VALUES_F32    ? static_cast<const float *>(w.data)[c + i]
            : w.type == SS_VALUES_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w.data)[c + i])
                                       : __half2float(static_cast<const __half *>(w.data)[c + i]);
 }
@@ -92,41 +102,129 @@ struct Ring {
   uint32_t base, pitch;  // bytes of a row's place
   uint32_t n;            // matrices present (the absent ones come last)
   uint32_t bars;
+  int64_t R, D;
 
   static __host__ __device__ uint32_t pitch_for(int64_t D) { return (uint32_t)((D * (int64_t)sizeof(T) + 15) / 16 * 16 + 16); }
-
+  // What a bulk copy of row `row` at p takes: whole 16-byte units, those that
+  // the row shares with the rows before and after it included where these are
+  // there (and a unit long).
+  __device__ __forceinline__ void span(const T *p, int64_t row, uintptr_t &b, uintptr_t &e) const {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), end = at + D * sizeof(T);
+    const bool lengthy = D * (int64_t)sizeof(T) >= 16;
+    b = lengthy && row > 0 ? at & ~(uintptr_t)15 : (at + 15) & ~(uintptr_t)15;
+    e = lengthy && row < R - 1 ? (end + 15) & ~(uintptr_t)15 : end & ~(uintptr_t)15;
+    if (e < b) e = b;
+  }
   // By one thread: copies row `row` of each matrix (null: none) into a slot.
-  __device__ void fetch(int slot, const T *const (&p)[kRows], const int64_t (&ld)[kRows], int64_t row, int64_t D) const {
+  // The few values outside whole units, of the first and the last row or of
+  // rows shorter than a unit, it copies itself.
+  __device__ void fetch(int slot, const T *const (&p)[kRows], const int64_t (&ld)[kRows], int64_t row) const {
     uint32_t bytes = 0;
     const uint32_t bar = bars + 8u * slot;
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
       if (p[k]) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p[k] + row * ld[k]);
-        const uintptr_t b = (at + 15) & ~(uintptr_t)15, e = (at + D * sizeof(T)) & ~(uintptr_t)15;
-        if (e > b) bytes += (uint32_t)(e - b);
+        const T *q = p[k] + row * ld[k];
+        uintptr_t b, e;
+        span(q, row, b, e);
+        bytes += (uint32_t)(e - b);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(q), end = at + D * sizeof(T);
+        const uint32_t to = place(slot, k, q);
+        if (b > at || e < end)
+          for (uintptr_t v = at; v < end; v += sizeof(T)) {
+            if (v >= b && v < e) v = e;
+            if (v < end) tc::write_shared(to + (uint32_t)(v - at), *reinterpret_cast<const T *>(v));
+          }
       }
     tc::bar_expect(bar, bytes);
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
       if (p[k]) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(p[k] + row * ld[k]);
-        const uintptr_t b = (at + 15) & ~(uintptr_t)15, e = (at + D * sizeof(T)) & ~(uintptr_t)15;
+        const T *q = p[k] + row * ld[k];
+        uintptr_t b, e;
+        span(q, row, b, e);
         if (e > b)
-          tc::load_bulk(base + ((uint32_t)slot * n + k) * pitch + (uint32_t)(b - (at & ~(uintptr_t)15)),
+          tc::load_bulk(place(slot, k, q) + (uint32_t)(int32_t)(int64_t)(b - reinterpret_cast<uintptr_t>(q)),
                         reinterpret_cast<const void *>(b), (uint32_t)(e - b), bar);
       }
   }
-  // Values c .. c + kN - 1 of the row of matrix k in `slot` (at `p` in global memory).
-  template <int kN>
-  __device__ __forceinline__ Pack<T, kN> read(int slot, int k, const T *p, int64_t c, int64_t D) const {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    if (kN == 1) {
-      const uintptr_t v = at + c * sizeof(T);
-      if (v < ((at + 15) & ~(uintptr_t)15) || v >= ((at + D * sizeof(T)) & ~(uintptr_t)15)) return load_pack<T, kN>(p + c);
-    }
-    return tc::read_shared<Pack<T, kN>>(base + ((uint32_t)slot * n + k) * pitch + (uint32_t)(at & 15) + (uint32_t)(c * sizeof(T)));
+  // Where value 0 of the row at p lies in `slot`.
+  __device__ __forceinline__ uint32_t place(int slot, int k, const T *p) const {
+    return base + ((uint32_t)slot * n + k) * pitch + (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
   }
+  // Values c .. c + kN - 1 of the row of matrix k in `slot` (at `p` in global
+  // memory), 0 where the row has none.  kN > 1: whole 16-byte units.
+  template <int kN>
+  __device__ __forceinline__ Pack<T, kN> read(int slot, int k, const T *p, int64_t c) const {
+    Pack<T, kN> v = tc::read_shared<Pack<T, kN>>(place(slot, k, p) + (uint32_t)(int32_t)(c * (int64_t)sizeof(T)));
+    if (kN > 1 && (c < 0 || c + kN > D)) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (c + i < 0 || c + i >= D) v.v[i] = Type<T>::down(0.0f);
+    }
+    return v;
+  }
+};
+
+// Values c .. c + kN - 1 of a row at p, those that it has.
+template <typename T, int kN>
+__device__ __forceinline__ void write(T *p, int64_t c, int64_t D, const float (&f)[kN]) {
+  const Pack<T, kN> v = narrow<T, kN>(f);
+  if (kN == 1 || (c >= 0 && c + kN <= D)) {
+    store_pack(p + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (c + i >= 0 && c + i < D) p[c + i] = v.v[i];
+  }
+}
+template <int kN>
+__device__ __forceinline__ void write_f8(uint8_t *p, int64_t c, int64_t D, const float (&f)[kN]) {
+  if (kN == 1 || (c >= 0 && c + kN <= D)) {
+    store_f8<kN>(p + c, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float one[1] = {f[i]};
+      if (c + i >= 0 && c + i < D) store_f8<1>(p + c + i, one);
+    }
+  }
+}
+
+// kN values worked on in pairs, or one alone.
+template <typename T, int kN>
+struct Work {
+  using V = Two;
+  static constexpr int kM = kN / 2;
+  static __device__ __forceinline__ V get(const Pack<T, kN> &p, int i) { return pair_of(p, i); }
+  static __device__ __forceinline__ V all(float x) { return two(x, x); }
+  static __device__ __forceinline__ V of(const float (&f)[kN], int i) { return two(f[2 * i], f[2 * i + 1]); }
+  static __device__ __forceinline__ void put(float (&f)[kN], int i, V v) {
+    const float2 q = both(v);
+    f[2 * i] = q.x;
+    f[2 * i + 1] = q.y;
+  }
+  static __device__ __forceinline__ float sum(V v) {
+    const float2 q = both(v);
+    return q.x + q.y;
+  }
+  static __device__ __forceinline__ float most(float m, V v) {
+    const float2 q = both(v);
+    return max_nan(m, max_nan(fabsf(q.x), fabsf(q.y)));
+  }
+};
+__device__ __forceinline__ float fma_of(float a, float b, float c) { return fmaf(a, b, c); }
+using dense::fma_of;
+template <typename T>
+struct Work<T, 1> {
+  using V = float;
+  static constexpr int kM = 1;
+  static __device__ __forceinline__ V get(const Pack<T, 1> &p, int) { return Type<T>::up(p.v[0]); }
+  static __device__ __forceinline__ V all(float x) { return x; }
+  static __device__ __forceinline__ V of(const float (&f)[1], int) { return f[0]; }
+  static __device__ __forceinline__ void put(float (&f)[1], int, V v) { f[0] = v; }
+  static __device__ __forceinline__ float sum(V v) { return v; }
+  static __device__ __forceinline__ float most(float m, V v) { return max_nan(m, fabsf(v)); }
 };
 
 // Barriers and place of this group's ring in dynamic shared memory (the
@@ -139,6 +237,8 @@ __device__ __forceinline__ Ring<T, kRows> open_ring(unsigned char *raw, const Gr
                                                     const int64_t (&ld)[kRows], int64_t first, int64_t step, int64_t R,
                                                     int64_t D) {
   Ring<T, kRows> ring;
+  ring.R = R;
+  ring.D = D;
   ring.pitch = Ring<T, kRows>::pitch_for(D);
   ring.bars = tc::smem_u32(raw) + 32u * gr.index;
   ring.n = 0;
@@ -148,16 +248,26 @@ __device__ __forceinline__ Ring<T, kRows> open_ring(unsigned char *raw, const Gr
     for (int k = 0; k < slots; ++k) tc::bar_init(ring.bars + 8u * k, 1);
     tc::bar_init_fence();
     for (int k = 0; k < slots; ++k)
-      if (first + k * step < R) ring.fetch(k, p, ld, first + k * step, D);
+      if (first + k * step < R) ring.fetch(k, p, ld, first + k * step);
   }
   __syncthreads();
   return ring;
 }
 
-// kN values a vector (16 bytes of them, or 1), kPer vectors a thread: columns
-// (p * threads + lane) * kN + i of the group's row.
+// Values by which the rows of a group start past a 16-byte boundary: the same
+// for all of them, as `step` is a multiple of the values in 16 bytes where
+// that is not the same for all rows.
+template <typename T, int kN>
+__device__ __forceinline__ int shift_of(const T *p, int64_t ld, int64_t row) {
+  return kN == 1 ? 0 : (int)(reinterpret_cast<uintptr_t>(p + row * ld) / sizeof(T) % kN);
+}
+
+// kN values a vector (a 16-byte unit of them, or 1), kPer vectors a thread:
+// columns (p * threads + lane) * kN - shift + i of the group's row, those that
+// it has.
 template <typename T, bool kF8, int kN, int kPer>
-__global__ void __launch_bounds__(kMostThreads) k_rms_norm(const rms_args a, int threads, int slots, int32_t *status) {
+__global__ void __launch_bounds__(kMostThreads, 1) k_rms_norm(const rms_args a, int threads, int slots, int32_t *status) {
+  using W = Work<T, kN>;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ float2 sm[2][32];
   __shared__ int stalled;
@@ -169,65 +279,76 @@ __global__ void __launch_bounds__(kMostThreads) k_rms_norm(const rms_args a, int
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / threads);
   const int64_t first = (int64_t)gr.index * gridDim.x + blockIdx.x;
   const Ring<T, 2> ring = open_ring<T, 2>(raw, gr, slots, src, ld, first, step, R, D);
+  const int shift = shift_of<T, kN>(src[0], ld[0], first);
+  const float inv_d = 1.0f / (float)D;
   T *total = static_cast<T *>(a.total.data);
-  float w[kPer][kN];
+  typename W::V w[kPer][W::kM];
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
-    if (c < D) load_weights<kN>(a.weight, c, w[p]);
+    const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
+    if (c < D) {
+      float f[kN];
+      load_weights<kN>(a.weight, c, f);
+#pragma unroll
+      for (int i = 0; i < W::kM; ++i) w[p][i] = W::of(f, i);
+    }
   }
   int set = 0, slot = 0;
   uint32_t phase = 0;
   for (int64_t row = first; row < R; row += step, set ^= 1) {
     tc::bar_wait_on(ring.bars + 8u * slot, phase, status, &stalled);
-    float s[kPer][kN], sq = 0.0f, most = 0.0f;
+    typename W::V s[kPer][W::kM], sq = W::all(0.0f);
+    float most = 0.0f;
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
+      const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
       if (c < D) {
-        widen(ring.template read<kN>(slot, 0, src[0] + row * ld[0], c, D), s[p]);
-        if (src[1]) {
-          float f[kN];
-          widen(ring.template read<kN>(slot, 1, src[1] + row * ld[1], c, D), f);
+        const Pack<T, kN> x = ring.template read<kN>(slot, 0, src[0] + row * ld[0], c);
 #pragma unroll
-          for (int i = 0; i < kN; ++i) s[p][i] += f[i];
+        for (int i = 0; i < W::kM; ++i) s[p][i] = W::get(x, i);
+        if (src[1]) {
+          const Pack<T, kN> r = ring.template read<kN>(slot, 1, src[1] + row * ld[1], c);
+#pragma unroll
+          for (int i = 0; i < W::kM; ++i) s[p][i] = s[p][i] + W::get(r, i);
         }
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          sq = fmaf(s[p][i], s[p][i], sq);
-          if (kF8) most = max_nan(most, fabsf(s[p][i] * w[p][i]));
+        for (int i = 0; i < W::kM; ++i) {
+          sq = fma_of(s[p][i], s[p][i], sq);
+          if (kF8) most = W::most(most, s[p][i] * w[p][i]);
         }
       }
     }
-    const float2 red = group_sum_max(gr, sq, most, sm, set);
+    const float2 red = group_reduce<kF8>(gr, W::sum(sq), most, sm, set);
     // every thread has read the slot: the row that comes `slots` turns later
     const int64_t later = row + slots * step;
-    if (gr.lane == 0 && later < R) ring.fetch(slot, src, ld, later, D);
+    if (gr.lane == 0 && later < R) ring.fetch(slot, src, ld, later);
     if (++slot == slots) {
       slot = 0;
       phase ^= 1;
     }
-    const float rstd = 1.0f / sqrtf(red.x / (float)D + a.eps);
+    const float rstd = 1.0f / sqrtf(red.x * inv_d + a.eps);
     if (gr.lane == 0) {
       if (a.rstd) a.rstd[row] = rstd;
       if (kF8) a.scale[row] = red.y * rstd / kF8Max;
     }
-    const float2 to8 = f8_factors(red.y);
+    const float2 to8 = kF8 ? f8_factors(red.y) : make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
+      const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
       if (c < D) {
-        if (total && src[1]) store_pack(total + row * a.total.ld + c, narrow<T, kN>(s[p]));
-        float y[kN];
-        if (kF8) {
+        float f[kN];
+        if (total && src[1]) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) y[i] = s[p][i] * w[p][i] * to8.x * to8.y;
-          store_f8<kN>(static_cast<uint8_t *>(a.y.data) + row * a.y.ld + c, y);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kN; ++i) y[i] = s[p][i] * rstd * w[p][i];
-          store_pack(static_cast<T *>(a.y.data) + row * a.y.ld + c, narrow<T, kN>(y));
+          for (int i = 0; i < W::kM; ++i) W::put(f, i, s[p][i]);
+          write<T, kN>(total + row * a.total.ld, c, D, f);
         }
+#pragma unroll
+        for (int i = 0; i < W::kM; ++i)
+          W::put(f, i, kF8 ? s[p][i] * w[p][i] * W::all(to8.x) * W::all(to8.y) : s[p][i] * W::all(rstd) * w[p][i]);
+        if (kF8)
+          write_f8<kN>(static_cast<uint8_t *>(a.y.data) + row * a.y.ld, c, D, f);
+        else
+          write<T, kN>(static_cast<T *>(a.y.data) + row * a.y.ld, c, D, f);
       }
     }
   }
@@ -264,7 +385,7 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_norm_wide(const rms_args a
         if (kF8) most = max_nan(most, fabsf(s[i] * w[i]));
       }
     }
-    const float2 red = group_sum_max(gr, sq, most, sm, set);
+    const float2 red = group_reduce<kF8>(gr, sq, most, sm, set);
     const float rstd = 1.0f / sqrtf(red.x / (float)D + a.eps);
     if (threadIdx.x == 0) {
       if (a.rstd) a.rstd[row] = rstd;
@@ -290,7 +411,8 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_norm_wide(const rms_args a
 // grad_x of the block's rows, and the block's part of grad_w into
 // scratch[blockIdx.x][D].
 template <typename T, int kN, int kPer>
-__global__ void __launch_bounds__(kMostThreads) k_rms_grad(const rms_grad_args a, int threads, int slots, int32_t *status) {
+__global__ void __launch_bounds__(kMostThreads, 1) k_rms_grad(const rms_grad_args a, int threads, int slots, int32_t *status) {
+  using W = Work<T, kN>;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ float2 sm[2][32];
   __shared__ int stalled;
@@ -303,13 +425,19 @@ __global__ void __launch_bounds__(kMostThreads) k_rms_grad(const rms_grad_args a
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / threads);
   const int64_t first = (int64_t)gr.index * gridDim.x + blockIdx.x;
   const Ring<T, 3> ring = open_ring<T, 3>(raw, gr, slots, src, ld, first, step, R, D);
-  float w[kPer][kN], gw[kPer][kN];
+  const int shift = shift_of<T, kN>(src[0], ld[0], first);
+  const float inv_d = 1.0f / (float)D;
+  typename W::V w[kPer][W::kM], gw[kPer][W::kM];
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
-    if (c < D) load_weights<kN>(a.weight, c, w[p]);
+    const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
+    float f[kN];
+    if (c < D) load_weights<kN>(a.weight, c, f);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) gw[p][i] = 0.0f;
+    for (int i = 0; i < W::kM; ++i) {
+      if (c < D) w[p][i] = W::of(f, i);
+      gw[p][i] = W::all(0.0f);
+    }
   }
   int set = 0, slot = 0;
   uint32_t phase = 0;
@@ -320,46 +448,42 @@ __global__ void __launch_bounds__(kMostThreads) k_rms_grad(const rms_grad_args a
     tc::bar_wait_on(ring.bars + 8u * slot, phase, status, &stalled);
     // held as read, and widened again after the reduction: half the registers
     Pack<T, kN> gv[kPer], xv[kPer], tv[kPer];
-    float dot = 0.0f;
+    typename W::V dot = W::all(0.0f);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
+      const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
       if (c < D) {
-        gv[p] = ring.template read<kN>(slot, 0, src[0] + row * ld[0], c, D);
-        xv[p] = ring.template read<kN>(slot, 1, src[1] + row * ld[1], c, D);
-        if (src[2]) tv[p] = ring.template read<kN>(slot, 2, src[2] + row * ld[2], c, D);
-        float g[kN], xh[kN];
-        widen(gv[p], g);
-        widen(xv[p], xh);
+        gv[p] = ring.template read<kN>(slot, 0, src[0] + row * ld[0], c);
+        xv[p] = ring.template read<kN>(slot, 1, src[1] + row * ld[1], c);
+        if (src[2]) tv[p] = ring.template read<kN>(slot, 2, src[2] + row * ld[2], c);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          xh[i] *= rstd;
-          gw[p][i] = fmaf(g[i], xh[i], gw[p][i]);
-          dot = fmaf(g[i] * w[p][i], xh[i], dot);
+        for (int i = 0; i < W::kM; ++i) {
+          const typename W::V g = W::get(gv[p], i), xh = W::get(xv[p], i) * W::all(rstd);
+          gw[p][i] = fma_of(g, xh, gw[p][i]);
+          dot = fma_of(g * w[p][i], xh, dot);
         }
       }
     }
-    const float mean = group_sum_max(gr, dot, 0.0f, sm, set).x / (float)D;
+    const float mean = group_reduce<false>(gr, W::sum(dot), 0.0f, sm, set).x * inv_d;
     const int64_t later = row + slots * step;
-    if (gr.lane == 0 && later < R) ring.fetch(slot, src, ld, later, D);
+    if (gr.lane == 0 && later < R) ring.fetch(slot, src, ld, later);
     if (++slot == slots) {
       slot = 0;
       phase ^= 1;
     }
+    // rstd (g w - xh mean) + t = g w rstd + (x (-rstd^2 mean) + t)
+    const typename W::V fx = W::all(-rstd * rstd * mean), fg = W::all(rstd);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
+      const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
       if (c < D) {
-        float g[kN], xh[kN], t[kN], y[kN];
-        widen(gv[p], g);
-        widen(xv[p], xh);
-        if (src[2]) widen(tv[p], t);
+        float y[kN];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          y[i] = rstd * (g[i] * w[p][i] - xh[i] * rstd * mean);
-          if (src[2]) y[i] += t[i];
+        for (int i = 0; i < W::kM; ++i) {
+          const typename W::V t = src[2] ? W::get(tv[p], i) : W::all(0.0f);
+          W::put(y, i, fma_of(W::get(gv[p], i) * w[p][i], fg, fma_of(W::get(xv[p], i), fx, t)));
         }
-        store_pack(static_cast<T *>(a.grad_x.data) + row * a.grad_x.ld + c, narrow<T, kN>(y));
+        write<T, kN>(static_cast<T *>(a.grad_x.data) + row * a.grad_x.ld, c, D, y);
       }
     }
   }
@@ -374,10 +498,13 @@ __global__ void __launch_bounds__(kMostThreads) k_rms_grad(const rms_grad_args a
   }
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * threads + gr.lane) * kN;
+    const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
+    float f[kN];
+#pragma unroll
+    for (int i = 0; i < W::kM; ++i) W::put(f, i, gw[p][i]);
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      if (c < D) mine[c + i] = gw[p][i];
+      if (c + i >= 0 && c + i < D) mine[c + i] = f[i];
   }
   if (groups > 1) {
     __syncthreads();
@@ -417,7 +544,7 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_grad_wide(const rms_grad_a
 #pragma unroll
       for (int i = 0; i < kN; ++i) dot = fmaf(g[i], xh[i], dot);
     }
-    const float mean = group_sum_max(gr, dot, 0.0f, sm, set).x / (float)D;
+    const float mean = group_reduce<false>(gr, dot, 0.0f, sm, set).x / (float)D;
     for (int64_t c = (int64_t)threadIdx.x * kN; c < D; c += (int64_t)blockDim.x * kN) {
       float y[kN], t[kN];
       values(c, g, xh);
@@ -502,7 +629,7 @@ Shape shape_for(const ss_handle *h, int64_t R, int64_t D, int n, const int (&per
     const int64_t t = ((vecs + per - 1) / per + 31) / 32 * 32;
     if (t > kMostThreads || row_bytes > kRingBytes) continue;
     if (sh.per && (vecs < 32 * per || R <= h->sm_count)) break;
-    if (sh.per == 2) break;
+    if (sh.per && (sh.per == 2 || per == 16)) break;  // 4 and 16: where the ones before do not reach
     sh.per = per;
     sh.threads = (int)t;
   }
@@ -518,28 +645,54 @@ Shape shape_for(const ss_handle *h, int64_t R, int64_t D, int n, const int (&per
   return sh;
 }
 
+// Whether rows of these matrices (those present) can be worked on in 16-byte
+// units of n values of the first: each row starts as many values past such a
+// unit in all of them.  *shifting: not the same number in every row.
+bool in_units(std::initializer_list<ss_dense> ms, int n, int64_t D, bool *shifting) {
+  int64_t start = -1, ld = -1;
+  for (const ss_dense &m : ms) {
+    if (!m.data) continue;
+    const int64_t s = (int64_t)(reinterpret_cast<uintptr_t>(m.data) / (uintptr_t)size_of(m.type) % (uintptr_t)n);
+    const int64_t l = m.n_rows > 1 ? m.ld % n : 0;
+    if (start >= 0 && (s != start || l != ld)) return false;
+    start = s;
+    ld = l;
+  }
+  *shifting = ld != 0;
+  return D >= n || (start == 0 && ld == 0 && D % n == 0);
+}
+// A grid of `blocks` at most whose groups' step keeps a row's shift: a multiple
+// of n rows.
+int64_t keep_shift(int64_t blocks, int groups, int64_t R, int n, bool shifting) {
+  if (!shifting || blocks * groups >= R) return blocks;
+  while (blocks > 1 && blocks * groups % n != 0) --blocks;
+  return blocks;
+}
+
 template <typename T, bool kF8>
 cudaError_t rms_norm_typed(ss_handle *h, const rms_args &a, cudaStream_t s) {
   constexpr int kV = Type<T>::kVec;
-  const int64_t R = a.x.n_rows, D = a.x.n_cols;
-  auto aligned = [&](const ss_dense &m, int64_t unit) { return !m.data || rows_aligned(m, unit); };
-  const bool vec = D % kV == 0 && aligned(a.x, 16) && aligned(a.residual, 16) && aligned(a.total, 16) &&
-                   aligned(a.y, kF8 ? kV : 16);
-  const Shape sh = shape_for(h, R, D, vec ? kV : 1, vec ? kVecPers : kOnePers, (a.residual.data ? 2 : 1) * (int64_t)Ring<T, 2>::pitch_for(D));
-  const unsigned grid = (unsigned)std::min<int64_t>((R + sh.groups - 1) / sh.groups, (int64_t)std::max(1, h->sm_count) * sh.blocks);
-  auto run = [&](auto kernel) -> cudaError_t {
-    const cudaError_t e = ensure_dyn_smem(kernel, sh.smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, sh.groups * sh.threads, sh.smem, s>>>(a, sh.threads, sh.slots, h->d_status);
-    return cudaGetLastError();
-  };
+  const int64_t R = a.x.n_rows, D = a.x.n_cols, sms = std::max(1, h->sm_count);
+  bool shifting = false;
+  const bool vec = in_units({a.x, a.residual, a.total, a.y}, kV, D, &shifting);
+  const bool aligned = vec && !shifting && reinterpret_cast<uintptr_t>(a.x.data) % 16 == 0 && D % kV == 0;
+  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? kVecPers : kOnePers,
+                             (a.residual.data ? 2 : 1) * (int64_t)Ring<T, 2>::pitch_for(D));
   if (sh.per == 0) {
-    if (vec)
+    const unsigned grid = (unsigned)std::min<int64_t>(R, sms * sh.blocks);
+    if (aligned)
       k_rms_norm_wide<T, kF8, kV><<<grid, sh.threads, 0, s>>>(a);
     else
       k_rms_norm_wide<T, kF8, 1><<<grid, sh.threads, 0, s>>>(a);
     return cudaGetLastError();
   }
+  const int64_t grid = keep_shift(std::min<int64_t>((R + sh.groups - 1) / sh.groups, sms * sh.blocks), sh.groups, R, kV, shifting && vec);
+  auto run = [&](auto kernel) -> cudaError_t {
+    const cudaError_t e = ensure_dyn_smem(kernel, sh.smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)grid, sh.groups * sh.threads, sh.smem, s>>>(a, sh.threads, sh.slots, h->d_status);
+    return cudaGetLastError();
+  };
   if (vec) return sh.per == 1 ? run(k_rms_norm<T, kF8, kV, 1>) : run(k_rms_norm<T, kF8, kV, 4>);
   return sh.per == 1 ? run(k_rms_norm<T, kF8, 1, 1>) : sh.per == 4 ? run(k_rms_norm<T, kF8, 1, 4>) : run(k_rms_norm<T, kF8, 1, 16>);
 }
@@ -556,10 +709,13 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
   const int64_t R = a.total.n_rows, D = a.total.n_cols;
   if (R == 0)  // the sum over no rows
     return cudaMemsetAsync(a.grad_weight.data, 0, (size_t)(D * size_of(a.grad_weight.type)), s);
-  auto aligned = [&](const ss_dense &m) { return !m.data || rows_aligned(m, 16); };
-  const bool vec = D % kV == 0 && aligned(a.grad_y) && aligned(a.total) && aligned(a.grad_total) && aligned(a.grad_x);
-  const Shape sh = shape_for(h, R, D, vec ? kV : 1, vec ? (kV == 8 ? kGradPers : kVecPers) : kOnePers, (a.grad_total.data ? 3 : 2) * (int64_t)Ring<T, 3>::pitch_for(D));
+  bool shifting = false;
+  const bool vec = in_units({a.grad_y, a.total, a.grad_total, a.grad_x}, kV, D, &shifting);
+  const bool aligned = vec && !shifting && reinterpret_cast<uintptr_t>(a.total.data) % 16 == 0 && D % kV == 0;
+  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? (kV == 8 ? kGradPers : kVecPers) : kOnePers,
+                             (a.grad_total.data ? 3 : 2) * (int64_t)Ring<T, 3>::pitch_for(D));
   int64_t n = std::min<int64_t>(most_parts(h, (R + sh.groups - 1) / sh.groups), (int64_t)std::max(1, h->sm_count) * sh.blocks);
+  if (sh.per) n = keep_shift(n, sh.groups, R, kV, shifting && vec);
   auto run = [&](auto kernel) -> cudaError_t {
     const cudaError_t e = ensure_dyn_smem(kernel, sh.smem);
     if (e != cudaSuccess) return e;
@@ -569,7 +725,7 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
   cudaError_t e = cudaSuccess;
   if (sh.per == 0) {
     const unsigned grid = (unsigned)std::min<int64_t>(R, (int64_t)std::max(1, h->sm_count) * sh.blocks);
-    if (vec)
+    if (aligned)
       k_rms_grad_wide<T, kV><<<grid, sh.threads, 0, s>>>(a);
     else
       k_rms_grad_wide<T, 1><<<grid, sh.threads, 0, s>>>(a);

@@ -113,6 +113,20 @@ __device__ __forceinline__ P read_shared(uint32_t at) {
   }
   return v;
 }
+// Writes a value of 2 or 4 bytes.
+template <typename P>
+__device__ __forceinline__ void write_shared(uint32_t at, P v) {
+  if constexpr (sizeof(P) == 4) {
+    uint32_t q;
+    memcpy(&q, &v, 4);
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(q) : "memory");
+  } else {
+    static_assert(sizeof(P) == 2, "4 or 2 bytes");
+    uint16_t q;
+    memcpy(&q, &v, 2);
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(q) : "memory");
+  }
+}
 // A box into this block's shared memory, counted on barrier `bar` (a
 // cluster address) of either block of the pair.
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
