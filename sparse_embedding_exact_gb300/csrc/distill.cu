@@ -65,12 +65,14 @@ __device__ __forceinline__ Two exp_of(Two z, Two minus, Two c) {
 
 __device__ __forceinline__ float max_of(const Pack<float, 4> &p) { return fmaxf(fmaxf(p.v[0], p.v[1]), fmaxf(p.v[2], p.v[3])); }
 __device__ __forceinline__ float max_of(const Pack<__nv_bfloat16, 8> &p) {
-  const __nv_bfloat162 *q = reinterpret_cast<const __nv_bfloat162 *>(p.v);
+  __nv_bfloat162 q[4];
+  memcpy(q, p.w, 16);
   const float2 f = __bfloat1622float2(__hmax2(__hmax2(q[0], q[1]), __hmax2(q[2], q[3])));
   return fmaxf(f.x, f.y);
 }
 __device__ __forceinline__ float max_of(const Pack<__half, 8> &p) {
-  const __half2 *q = reinterpret_cast<const __half2 *>(p.v);
+  __half2 q[4];
+  memcpy(q, p.w, 16);
   const float2 f = __half22float2(__hmax2(__hmax2(q[0], q[1]), __hmax2(q[2], q[3])));
   return fmaxf(f.x, f.y);
 }
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) k_distill(const distill_args a, int 
               store_pack(to, out);
             } else {
 #pragma unroll
-              for (int i = 0; i < kV; ++i) to[i] = out.v[i];
+              for (int i = 0; i < kV; ++i) to[i] = item(out, i);
             }
           }
         },
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
           store_pack(to, out);
         } else {
 #pragma unroll
-          for (int i = 0; i < kV; ++i) to[i] = out.v[i];
+          for (int i = 0; i < kV; ++i) to[i] = item(out, i);
         }
       };
       for (int j = 0; j < p.chunks; j += 2) {

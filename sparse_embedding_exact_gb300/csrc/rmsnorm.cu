@@ -34,6 +34,10 @@ constexpr int kWideThreads = 1024;
 constexpr int64_t kRingBytes = 200 << 10;  // of an SM's shared memory, for the rings of its blocks
 constexpr int kMostThreads = 512;  // of a block that holds its rows in registers, up to 128 a thread
 
+// Threads of a block of the gradient: 16 values a thread leave room for three
+// blocks of 256.
+constexpr int grad_threads(int n, int per) { return n * per == 16 ? 256 : kMostThreads; }
+
 // Threads of a block that work on one row: `index` of them in the block's
 // order, each of `threads` threads.
 struct Group {
@@ -152,35 +156,41 @@ struct Ring {
   __device__ __forceinline__ uint32_t place(int slot, int k, const T *p) const {
     return base + ((uint32_t)slot * n + k) * pitch + (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
   }
-  // Values c .. c + kN - 1 of the row of matrix k in `slot` (at `p` in global
-  // memory), 0 where the row has none.  kN > 1: whole 16-byte units.
-  template <int kN>
-  __device__ __forceinline__ Pack<T, kN> read(int slot, int k, const T *p, int64_t c) const {
-    Pack<T, kN> v = tc::read_shared<Pack<T, kN>>(place(slot, k, p) + (uint32_t)(int32_t)(c * (int64_t)sizeof(T)));
-    if (kN > 1 && (c < 0 || c + kN > D)) {
+  // Values c .. c + kN - 1 of the row of matrix k in `slot`, 0 where the row
+  // has none; `at`: their place from the row's (for kN > 1 a 16-byte unit's,
+  // the same for every row).
+  template <int kN, bool kEdges>
+  __device__ __forceinline__ Pack<T, kN> read(int slot, int k, uint32_t at, int c) const {
+    Pack<T, kN> v = tc::read_shared<Pack<T, kN>>(base + ((uint32_t)slot * n + k) * pitch + at);
+    if (kEdges && (c < 0 || c + kN > (int)D)) {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
-        if (c + i < 0 || c + i >= D) v.v[i] = Type<T>::down(0.0f);
+        if (c + i < 0 || c + i >= (int)D) clear_item(v, i);
     }
     return v;
+  }
+  // That place: units count from the 16 bytes that the row starts in.
+  template <int kN>
+  __device__ __forceinline__ uint32_t at_of(const T *p, int unit) const {
+    return kN > 1 ? 16u * unit : (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15) + (uint32_t)(unit * sizeof(T));
   }
 };
 
 // Values c .. c + kN - 1 of a row at p, those that it has.
-template <typename T, int kN>
-__device__ __forceinline__ void write(T *p, int64_t c, int64_t D, const float (&f)[kN]) {
+template <typename T, int kN, bool kEdges>
+__device__ __forceinline__ void write(T *p, int c, int D, const float (&f)[kN]) {
   const Pack<T, kN> v = narrow<T, kN>(f);
-  if (kN == 1 || (c >= 0 && c + kN <= D)) {
+  if (!kEdges || (c >= 0 && c + kN <= D)) {
     store_pack(p + c, v);
   } else {
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      if (c + i >= 0 && c + i < D) p[c + i] = v.v[i];
+      if (c + i >= 0 && c + i < D) p[c + i] = item(v, i);
   }
 }
-template <int kN>
-__device__ __forceinline__ void write_f8(uint8_t *p, int64_t c, int64_t D, const float (&f)[kN]) {
-  if (kN == 1 || (c >= 0 && c + kN <= D)) {
+template <int kN, bool kEdges>
+__device__ __forceinline__ void write_f8(uint8_t *p, int c, int D, const float (&f)[kN]) {
+  if (!kEdges || (c >= 0 && c + kN <= D)) {
     store_f8<kN>(p + c, f);
   } else {
 #pragma unroll
@@ -264,8 +274,9 @@ __device__ __forceinline__ int shift_of(const T *p, int64_t ld, int64_t row) {
 
 // kN values a vector (a 16-byte unit of them, or 1), kPer vectors a thread:
 // columns (p * threads + lane) * kN - shift + i of the group's row, those that
-// it has.
-template <typename T, bool kF8, int kN, int kPer>
+// it has.  kEdges: units of several values, some of which have values before
+// or after the row's.
+template <typename T, bool kF8, int kN, int kPer, bool kEdges>
 __global__ void __launch_bounds__(kMostThreads, 1) k_rms_norm(const rms_args a, int threads, int slots, int32_t *status) {
   using W = Work<T, kN>;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -279,14 +290,14 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_rms_norm(const rms_args a, 
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / threads);
   const int64_t first = (int64_t)gr.index * gridDim.x + blockIdx.x;
   const Ring<T, 2> ring = open_ring<T, 2>(raw, gr, slots, src, ld, first, step, R, D);
-  const int shift = shift_of<T, kN>(src[0], ld[0], first);
+  const int shift = kEdges ? shift_of<T, kN>(src[0], ld[0], first) : 0;
   const float inv_d = 1.0f / (float)D;
   T *total = static_cast<T *>(a.total.data);
   typename W::V w[kPer][W::kM];
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
-    if (c < D) {
+    const int unit = p * threads + gr.lane, c = unit * kN - shift;
+    if (c < (int)D) {
       float f[kN];
       load_weights<kN>(a.weight, c, f);
 #pragma unroll
@@ -301,13 +312,13 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_rms_norm(const rms_args a, 
     float most = 0.0f;
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
-      if (c < D) {
-        const Pack<T, kN> x = ring.template read<kN>(slot, 0, src[0] + row * ld[0], c);
+      const int unit = p * threads + gr.lane, c = unit * kN - shift;
+      if (c < (int)D) {
+        const Pack<T, kN> x = ring.template read<kN, kEdges>(slot, 0, ring.template at_of<kN>(src[0] + row * ld[0], unit), c);
 #pragma unroll
         for (int i = 0; i < W::kM; ++i) s[p][i] = W::get(x, i);
         if (src[1]) {
-          const Pack<T, kN> r = ring.template read<kN>(slot, 1, src[1] + row * ld[1], c);
+          const Pack<T, kN> r = ring.template read<kN, kEdges>(slot, 1, ring.template at_of<kN>(src[1] + row * ld[1], unit), c);
 #pragma unroll
           for (int i = 0; i < W::kM; ++i) s[p][i] = s[p][i] + W::get(r, i);
         }
@@ -334,21 +345,21 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_rms_norm(const rms_args a, 
     const float2 to8 = kF8 ? f8_factors(red.y) : make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
-      if (c < D) {
+      const int unit = p * threads + gr.lane, c = unit * kN - shift;
+      if (c < (int)D) {
         float f[kN];
         if (total && src[1]) {
 #pragma unroll
           for (int i = 0; i < W::kM; ++i) W::put(f, i, s[p][i]);
-          write<T, kN>(total + row * a.total.ld, c, D, f);
+          write<T, kN, kEdges>(total + row * a.total.ld, c, (int)D, f);
         }
 #pragma unroll
         for (int i = 0; i < W::kM; ++i)
           W::put(f, i, kF8 ? s[p][i] * w[p][i] * W::all(to8.x) * W::all(to8.y) : s[p][i] * W::all(rstd) * w[p][i]);
         if (kF8)
-          write_f8<kN>(static_cast<uint8_t *>(a.y.data) + row * a.y.ld, c, D, f);
+          write_f8<kN, kEdges>(static_cast<uint8_t *>(a.y.data) + row * a.y.ld, c, (int)D, f);
         else
-          write<T, kN>(static_cast<T *>(a.y.data) + row * a.y.ld, c, D, f);
+          write<T, kN, kEdges>(static_cast<T *>(a.y.data) + row * a.y.ld, c, (int)D, f);
       }
     }
   }
@@ -410,8 +421,8 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_norm_wide(const rms_args a
 
 // grad_x of the block's rows, and the block's part of grad_w into
 // scratch[blockIdx.x][D].
-template <typename T, int kN, int kPer>
-__global__ void __launch_bounds__(kMostThreads, 1) k_rms_grad(const rms_grad_args a, int threads, int slots, int32_t *status) {
+template <typename T, int kN, int kPer, bool kEdges>
+__global__ void __launch_bounds__(grad_threads(kN, kPer), kN * kPer == 16 ? 3 : 1) k_rms_grad(const rms_grad_args a, int threads, int slots, int32_t *status) {
   using W = Work<T, kN>;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ float2 sm[2][32];
@@ -425,17 +436,17 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_rms_grad(const rms_grad_arg
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / threads);
   const int64_t first = (int64_t)gr.index * gridDim.x + blockIdx.x;
   const Ring<T, 3> ring = open_ring<T, 3>(raw, gr, slots, src, ld, first, step, R, D);
-  const int shift = shift_of<T, kN>(src[0], ld[0], first);
+  const int shift = kEdges ? shift_of<T, kN>(src[0], ld[0], first) : 0;
   const float inv_d = 1.0f / (float)D;
   typename W::V w[kPer][W::kM], gw[kPer][W::kM];
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
+    const int unit = p * threads + gr.lane, c = unit * kN - shift;
     float f[kN];
-    if (c < D) load_weights<kN>(a.weight, c, f);
+    if (c < (int)D) load_weights<kN>(a.weight, c, f);
 #pragma unroll
     for (int i = 0; i < W::kM; ++i) {
-      if (c < D) w[p][i] = W::of(f, i);
+      if (c < (int)D) w[p][i] = W::of(f, i);
       gw[p][i] = W::all(0.0f);
     }
   }
@@ -446,45 +457,53 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_rms_grad(const rms_grad_arg
     const float rstd = rstd_next;
     if (row + step < R) rstd_next = a.rstd[row + step];
     tc::bar_wait_on(ring.bars + 8u * slot, phase, status, &stalled);
-    // held as read, and widened again after the reduction: half the registers
-    Pack<T, kN> gv[kPer], xv[kPer], tv[kPer];
     typename W::V dot = W::all(0.0f);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
-      if (c < D) {
-        gv[p] = ring.template read<kN>(slot, 0, src[0] + row * ld[0], c);
-        xv[p] = ring.template read<kN>(slot, 1, src[1] + row * ld[1], c);
-        if (src[2]) tv[p] = ring.template read<kN>(slot, 2, src[2] + row * ld[2], c);
+      const int unit = p * threads + gr.lane, c = unit * kN - shift;
+      if (c < (int)D) {
+        const Pack<T, kN> gv = ring.template read<kN, kEdges>(slot, 0, ring.template at_of<kN>(src[0] + row * ld[0], unit), c);
+        const Pack<T, kN> xv = ring.template read<kN, kEdges>(slot, 1, ring.template at_of<kN>(src[1] + row * ld[1], unit), c);
 #pragma unroll
         for (int i = 0; i < W::kM; ++i) {
-          const typename W::V g = W::get(gv[p], i), xh = W::get(xv[p], i) * W::all(rstd);
+          const typename W::V g = W::get(gv, i), xh = W::get(xv, i) * W::all(rstd);
           gw[p][i] = fma_of(g, xh, gw[p][i]);
           dot = fma_of(g * w[p][i], xh, dot);
         }
       }
     }
     const float mean = group_reduce<false>(gr, W::sum(dot), 0.0f, sm, set).x * inv_d;
-    const int64_t later = row + slots * step;
-    if (gr.lane == 0 && later < R) ring.fetch(slot, src, ld, later);
-    if (++slot == slots) {
-      slot = 0;
-      phase ^= 1;
-    }
+    // Every thread is through with the row before: its slot's next row.  (The
+    // row itself is read again below, rather than kept: half the registers,
+    // half again as many blocks on an SM.)
+    if (gr.lane == 0 && slots > 1 && row != first && row + (slots - 1) * step < R)
+      ring.fetch(slot == 0 ? slots - 1 : slot - 1, src, ld, row + (slots - 1) * step);
     // rstd (g w - xh mean) + t = g w rstd + (x (-rstd^2 mean) + t)
     const typename W::V fx = W::all(-rstd * rstd * mean), fg = W::all(rstd);
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
-      const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
-      if (c < D) {
+      const int unit = p * threads + gr.lane, c = unit * kN - shift;
+      if (c < (int)D) {
+        const Pack<T, kN> gv = ring.template read<kN, kEdges>(slot, 0, ring.template at_of<kN>(src[0] + row * ld[0], unit), c);
+        const Pack<T, kN> xv = ring.template read<kN, kEdges>(slot, 1, ring.template at_of<kN>(src[1] + row * ld[1], unit), c);
+        Pack<T, kN> tv;
+        if (src[2]) tv = ring.template read<kN, kEdges>(slot, 2, ring.template at_of<kN>(src[2] + row * ld[2], unit), c);
         float y[kN];
 #pragma unroll
         for (int i = 0; i < W::kM; ++i) {
-          const typename W::V t = src[2] ? W::get(tv[p], i) : W::all(0.0f);
-          W::put(y, i, fma_of(W::get(gv[p], i) * w[p][i], fg, fma_of(W::get(xv[p], i), fx, t)));
+          const typename W::V t = src[2] ? W::get(tv, i) : W::all(0.0f);
+          W::put(y, i, fma_of(W::get(gv, i) * w[p][i], fg, fma_of(W::get(xv, i), fx, t)));
         }
-        write<T, kN>(static_cast<T *>(a.grad_x.data) + row * a.grad_x.ld, c, D, y);
+        write<T, kN, kEdges>(static_cast<T *>(a.grad_x.data) + row * a.grad_x.ld, c, (int)D, y);
       }
+    }
+    if (slots == 1) {
+      gr.sync();
+      if (gr.lane == 0 && row + step < R) ring.fetch(0, src, ld, row + step);
+    }
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
     }
   }
   // The groups' sums in their order, through the rings (whose copies have all
@@ -498,7 +517,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_rms_grad(const rms_grad_arg
   }
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    const int64_t c = ((int64_t)p * threads + gr.lane) * kN - shift;
+    const int c = (p * threads + gr.lane) * kN - shift;
     float f[kN];
 #pragma unroll
     for (int i = 0; i < W::kM; ++i) W::put(f, i, gw[p][i]);
@@ -611,34 +630,33 @@ __global__ void __launch_bounds__(1024) k_sum_rows(const float *part, int64_t n,
 // thread of `threads` a row, `groups` rows a block, `slots` rows of the ring a
 // group, `blocks` an SM.  per = 0: too wide for registers.
 //
-// Many rows: the most of `pers`, 16 to 32 values a thread.  What a thread spends on a row besides its values (the reduction's shuffles and
+// Many rows: 4 vectors a thread, 16 to 32 values of it.  What a thread spends on a row besides its values (the reduction's shuffles and
 // barrier, the root) is as much as 8 values cost, and with 8 values a thread
 // the norm of 16,384 x 4096 bf16 rows to 8 bits was bound by instructions (94
 // us).  Rows for every SM or fewer: one vector a thread, for the time of one
 // row.
 constexpr int kVecPers[3] = {1, 4, 4}, kOnePers[3] = {1, 4, 16};
-constexpr int kGradPers[3] = {1, 2, 4};  // the gradient's 16-bit vectors: 4 only beyond 8192 columns, where 2 do not reach
 struct Shape {
   int per, threads, groups, slots, blocks, smem;
 };
-Shape shape_for(const ss_handle *h, int64_t R, int64_t D, int n, const int (&pers)[3], int64_t row_bytes) {
+Shape shape_for(const ss_handle *h, int64_t R, int64_t D, int n, const int (&pers)[3], bool grad, int64_t row_bytes) {
   const int64_t vecs = (D + n - 1) / n;
   Shape sh = {0, kWideThreads, 1, 0, 2, 0};
-  for (int k = 0; k < 3; ++k) {
-    const int per = pers[k];
+  for (const int per : pers) {
     const int64_t t = ((vecs + per - 1) / per + 31) / 32 * 32;
-    if (t > kMostThreads || row_bytes > kRingBytes) continue;
+    if (t > (grad ? grad_threads(n, per) : kMostThreads) || row_bytes > kRingBytes) continue;
     if (sh.per && (vecs < 32 * per || R <= h->sm_count)) break;
-    if (sh.per && (sh.per == 2 || per == 16)) break;  // 4 and 16: where the ones before do not reach
+    if (sh.per && per == 16) break;  // where 4 do not reach
     sh.per = per;
     sh.threads = (int)t;
   }
   if (!sh.per) return sh;
   const bool many = R > h->sm_count;
+  const int values = sh.per * n;
   sh.groups = many ? std::max(1, 256 / sh.threads) : 1;
-  sh.blocks = std::max(1, (sh.per * n > 8 ? 512 : 1024) / (sh.groups * sh.threads));
+  sh.blocks = std::max(1, (values <= 8 ? 1024 : grad && values == 16 ? 768 : 512) / (sh.groups * sh.threads));
   // up to four slots a group within the SM's ring bytes
-  while (sh.blocks > 1 && sh.blocks * sh.groups * row_bytes > kRingBytes) sh.blocks /= 2;
+  while (sh.blocks > 1 && sh.blocks * sh.groups * row_bytes > kRingBytes) --sh.blocks;
   while (sh.groups > 1 && sh.groups * row_bytes > kRingBytes) sh.groups /= 2;
   sh.slots = (int)std::min<int64_t>(4, kRingBytes / (sh.blocks * sh.groups * row_bytes));
   sh.smem = (int)(kBarBytes + sh.groups * sh.slots * row_bytes);
@@ -676,7 +694,7 @@ cudaError_t rms_norm_typed(ss_handle *h, const rms_args &a, cudaStream_t s) {
   bool shifting = false;
   const bool vec = in_units({a.x, a.residual, a.total, a.y}, kV, D, &shifting);
   const bool aligned = vec && !shifting && reinterpret_cast<uintptr_t>(a.x.data) % 16 == 0 && D % kV == 0;
-  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? kVecPers : kOnePers,
+  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? kVecPers : kOnePers, false,
                              (a.residual.data ? 2 : 1) * (int64_t)Ring<T, 2>::pitch_for(D));
   if (sh.per == 0) {
     const unsigned grid = (unsigned)std::min<int64_t>(R, sms * sh.blocks);
@@ -693,8 +711,11 @@ cudaError_t rms_norm_typed(ss_handle *h, const rms_args &a, cudaStream_t s) {
     kernel<<<(unsigned)grid, sh.groups * sh.threads, sh.smem, s>>>(a, sh.threads, sh.slots, h->d_status);
     return cudaGetLastError();
   };
-  if (vec) return sh.per == 1 ? run(k_rms_norm<T, kF8, kV, 1>) : run(k_rms_norm<T, kF8, kV, 4>);
-  return sh.per == 1 ? run(k_rms_norm<T, kF8, 1, 1>) : sh.per == 4 ? run(k_rms_norm<T, kF8, 1, 4>) : run(k_rms_norm<T, kF8, 1, 16>);
+  if (aligned) return sh.per == 1 ? run(k_rms_norm<T, kF8, kV, 1, false>) : run(k_rms_norm<T, kF8, kV, 4, false>);
+  if (vec) return sh.per == 1 ? run(k_rms_norm<T, kF8, kV, 1, true>) : run(k_rms_norm<T, kF8, kV, 4, true>);
+  return sh.per == 1   ? run(k_rms_norm<T, kF8, 1, 1, false>)
+         : sh.per == 4 ? run(k_rms_norm<T, kF8, 1, 4, false>)
+                       : run(k_rms_norm<T, kF8, 1, 16, false>);
 }
 
 // Most rows of partial sums of a gradient: its blocks, at most four an SM.
@@ -712,7 +733,7 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
   bool shifting = false;
   const bool vec = in_units({a.grad_y, a.total, a.grad_total, a.grad_x}, kV, D, &shifting);
   const bool aligned = vec && !shifting && reinterpret_cast<uintptr_t>(a.total.data) % 16 == 0 && D % kV == 0;
-  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? (kV == 8 ? kGradPers : kVecPers) : kOnePers,
+  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? kVecPers : kOnePers, true,
                              (a.grad_total.data ? 3 : 2) * (int64_t)Ring<T, 3>::pitch_for(D));
   int64_t n = std::min<int64_t>(most_parts(h, (R + sh.groups - 1) / sh.groups), (int64_t)std::max(1, h->sm_count) * sh.blocks);
   if (sh.per) n = keep_shift(n, sh.groups, R, kV, shifting && vec);
@@ -734,9 +755,14 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
     *queued += 1;
     e = cudaGetLastError();
   } else if (vec) {
-    e = sh.per == 1 ? run(k_rms_grad<T, kV, 1>) : sh.per == 2 ? run(k_rms_grad<T, kV, 2>) : run(k_rms_grad<T, kV, 4>);
+    if (aligned)
+      e = sh.per == 1 ? run(k_rms_grad<T, kV, 1, false>) : run(k_rms_grad<T, kV, 4, false>);
+    else
+      e = sh.per == 1 ? run(k_rms_grad<T, kV, 1, true>) : run(k_rms_grad<T, kV, 4, true>);
   } else {
-    e = sh.per == 1 ? run(k_rms_grad<T, 1, 1>) : sh.per == 4 ? run(k_rms_grad<T, 1, 4>) : run(k_rms_grad<T, 1, 16>);
+    e = sh.per == 1   ? run(k_rms_grad<T, 1, 1, false>)
+        : sh.per == 4 ? run(k_rms_grad<T, 1, 4, false>)
+                      : run(k_rms_grad<T, 1, 16, false>);
   }
   if (e != cudaSuccess) return e;
   *queued += 2;
