@@ -1007,9 +1007,46 @@ cudaError_t product_pair(ss_handle *h, const ss_dense &A, int majA, const ss_den
   return run_pair<kBN, kMajorMN, kMajorMN, false>(h, p, s);
 }
 
+// How a product is cut: a tile's columns, the blocks that share its sum, and
+// whether pairs of blocks take tiles of 256 x 256.
+struct Cut {
+  int bn, split;
+  bool pair;
+  double clocks;
+};
+// The cut of the least estimated time.  A stage of the summed dimension takes
+// a pair 600 clocks (512 are the tensor cores' own), measured over 8192 x 4096
+// x 4096, and a tile as long as its epilogue, 7,000, at least, as the next
+// one's products run beside it; a block on its own takes its bytes at 85 a
+// clock (128 x 256: 520 measured with rows along the sum, 610 across it), one
+// after the other with its set-up, its epilogue and, for a split sum, the
+// exchange.
+Cut cut_of(const ss_handle *h, int64_t rows_a, int64_t rows_b, int64_t blocks_k, int least, bool pairs) {
+  const int64_t sms = std::max(1, h->sm_count);
+  auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  Cut best = {256, 1, false, 0.0};
+  best.pair = pairs;
+  best.clocks = pairs ? 18e3 + (double)up(up(rows_a, 256) * up(rows_b, 256), std::max<int64_t>(1, sms / 2)) * std::max(600.0 * (double)blocks_k, 7e3) : 1e30;
+  for (int bn = 256; bn >= least; bn /= 2) {
+    if (bn < 256 && bn < 64 && rows_b > bn) break;  // narrow tiles: where they hold all of B's rows
+    for (int split = 1; split <= (bn <= 128 ? 8 : 1) && (split == 1 || blocks_k / split >= 2); split *= 2) {
+      // blocks at a time: clusters stay within a group of SMs, and of 152 SMs 36
+      // of 4 blocks and 15 of 8 run at once
+      const int64_t at_once = split == 8 ? sms * 15 / 19 : split == 4 ? sms * 18 / 19 : sms;
+      // a matrix that one row of tiles reads once comes from memory, not L2
+      const double rate = up(rows_a, kTileM) == 1 || up(rows_b, bn) == 1 ? 40.0 : 85.0;
+      const double turns = (double)up(up(rows_a, kTileM) * up(rows_b, bn) * split, at_once);
+      const double each = 5e3 + (split > 1 ? 5e3 + 80.0 * bn : 0.0) + 30.0 * bn / split + (double)up(blocks_k, split) * (kTileM + bn) * kRowBytes / rate;
+      const double clocks = 4e3 + turns * each;
+      if (clocks < best.clocks) best = {bn, split, false, clocks};
+    }
+  }
+  return best;
+}
+
 // ep.y = the product of A and B over their summed dimension; A and B are
 // [rows][summed] (kMajorK) or [summed][rows] (kMajorMN), rows aligned.
-cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B, int majB, bool swapped,
+cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B, int majB, bool swapped, const Cut &cut,
                     const Epilogue &ep, cudaStream_t s, int *queued) {
   const bool f8 = A.type == SS_VALUES_F8;
   Product p = {};
@@ -1021,24 +1058,14 @@ cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B
   p.status = h->d_status;
   const int unit = f8 ? kRowBytes : kRowBytes / 2;
   p.blocks_k = (int32_t)((K + unit - 1) / unit);
-  const int64_t sms = std::max(1, h->sm_count);
-  if (!swapped && ((p.rows_a + 255) / 256) * ((p.rows_b + 255) / 256) * 2 >= sms) {
+  if (cut.pair) {
     *queued += 1;
     return product_pair<256>(h, A, majA, B, majB, ep, p.rows_a, p.rows_b, K, s);
   }
+  const int bn = cut.bn, split = cut.split;
   p.tiles_a = (int32_t)((p.rows_a + kTileM - 1) / kTileM);
-  // Columns a tile: as few as hold B's rows, at most 256 (64 at least for
-  // MN-major operands, whose copies are 64 rows wide), halved while the tiles
-  // would leave half of the SMs idle.
-  const int least = majB == kMajorK ? 16 : 64;
-  int bn = 256;
-  while (bn > least && bn / 2 >= p.rows_b) bn /= 2;
-  while (bn > 64 && (int64_t)p.tiles_a * ((p.rows_b + bn - 1) / bn) * 2 <= sms) bn /= 2;
   p.tiles_b = (int32_t)((p.rows_b + bn - 1) / bn);
-  if ((int64_t)p.tiles_a * p.tiles_b > INT32_MAX) return cudaErrorInvalidConfiguration;
-  int split = 1;
-  if (bn <= 128)
-    while (split < 8 && (int64_t)p.tiles_a * p.tiles_b * split * 2 <= sms && p.blocks_k / (split * 2) >= 4) split *= 2;
+  if ((int64_t)p.tiles_a * p.tiles_b * split > INT32_MAX) return cudaErrorInvalidConfiguration;
   p.idesc = idesc_of(A, majA, majB, kTileM, bn);
   cudaError_t e;
   e = majA == kMajorK ? encode(&p.a, A, unit, kTileM) : encode(&p.a, A, 64, unit);
@@ -1083,7 +1110,7 @@ cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B
 }
 
 constexpr int64_t kFewRows = 4;     // k_rows up to this many rows
-constexpr int64_t kSwapRows = 256;  // features as A up to this many rows
+constexpr int64_t kSwapRows = 256;  // features as A is looked at up to this many rows
 
 template <typename T, int kN>
 cudaError_t rows_typed(const ss_dense &x, const ss_dense &w, const Epilogue &ep, cudaStream_t s) {
@@ -1099,6 +1126,12 @@ cudaError_t rows_typed(const ss_dense &x, const ss_dense &w, const Epilogue &ep,
   else
     run(k_rows<T, 4, 2, kN>, 4, 2);
   return cudaGetLastError();
+}
+
+// Stages of a summed dimension of K values of m's type.
+int64_t stages_of(const ss_dense &m, int64_t K) {
+  const int unit = m.type == SS_VALUES_F8 ? kRowBytes : kRowBytes / 2;
+  return (K + unit - 1) / unit;
 }
 
 bool few_rows(const ss_dense &x) { return x.n_rows <= kFewRows || x.n_cols == 0; }
@@ -1146,9 +1179,13 @@ cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, in
   cudaError_t e;
   if ((e = aligned_rows(h, &x, &scratch, s, queued)) != cudaSuccess) return e;
   if ((e = aligned_rows(h, &w, &scratch, s, queued)) != cudaSuccess) return e;
-  const bool swapped = x.n_rows <= kSwapRows;
-  return swapped ? product(h, w, kMajorK, x, kMajorK, true, ep, s, queued)
-                 : product(h, x, kMajorK, w, kMajorK, false, ep, s, queued);
+  const int64_t M = x.n_rows, N = w.n_rows, kb = stages_of(x, x.n_cols);
+  const Cut cut = cut_of(h, M, N, kb, 16, true);
+  if (M <= kSwapRows) {
+    const Cut other = cut_of(h, N, M, kb, 16, false);
+    if (other.clocks <= cut.clocks) return product(h, w, kMajorK, x, kMajorK, true, other, ep, s, queued);
+  }
+  return product(h, x, kMajorK, w, kMajorK, false, cut, ep, s, queued);
 }
 
 namespace {
@@ -1201,11 +1238,11 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
   };
   if (a.grad_x.data) {
     if ((e = aligned_rows(h, &w, &scratch, s, queued)) != cudaSuccess) return e;
-    if ((e = product(h, gz, kMajorK, w, kMajorMN, false, out(a.grad_x), s, queued)) != cudaSuccess) return e;
+    if ((e = product(h, gz, kMajorK, w, kMajorMN, false, cut_of(h, M, x.n_cols, stages_of(gz, N), 64, true), out(a.grad_x), s, queued)) != cudaSuccess) return e;
   }
   if (a.grad_w.data) {
     if ((e = aligned_rows(h, &x, &scratch, s, queued)) != cudaSuccess) return e;
-    if ((e = product(h, gz, kMajorMN, x, kMajorMN, false, out(a.grad_w), s, queued)) != cudaSuccess) return e;
+    if ((e = product(h, gz, kMajorMN, x, kMajorMN, false, cut_of(h, N, x.n_cols, stages_of(gz, M), 64, true), out(a.grad_w), s, queued)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
