@@ -32,6 +32,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 
@@ -873,11 +874,18 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
   }
 }
 
-// Copies the rows of src (values of kSize bytes) to dst with rows of ld values.
+// Copies of matrices with rows of ld values, one of them each blockIdx.y.
+struct Copies {
+  ss_dense src[2];
+  void *dst[2];
+  int64_t ld[2];
+};
 template <typename T>
-__global__ void __launch_bounds__(256) k_copy_rows(const ss_dense src, T *dst, int64_t ld) {
+__global__ void __launch_bounds__(256) k_copy_rows(const Copies a) {
+  const ss_dense &src = a.src[blockIdx.y];
+  T *dst = static_cast<T *>(a.dst[blockIdx.y]);
   for (int64_t r = blockIdx.x; r < src.n_rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < src.n_cols; c += 256) dst[r * ld + c] = static_cast<const T *>(src.data)[r * src.ld + c];
+    for (int64_t c = threadIdx.x; c < src.n_cols; c += 256) dst[r * a.ld[blockIdx.y] + c] = static_cast<const T *>(src.data)[r * src.ld + c];
 }
 
 // ---------------------------------------------------------------- host side
@@ -917,19 +925,31 @@ int64_t align_up(int64_t b) { return (b + SS_SCRATCH_ALIGN - 1) / SS_SCRATCH_ALI
 int64_t copy_bytes(const ss_dense &m) {
   return rows_aligned(m, 16) ? 0 : align_up(m.n_rows * padded_ld(m) * size_of(m.type));
 }
-// m itself, or its copy with padded rows at *scratch (advanced past it).
-cudaError_t aligned_rows(ss_handle *h, ss_dense *m, unsigned char **scratch, cudaStream_t s, int *queued) {
-  if (rows_aligned(*m, 16)) return cudaSuccess;
-  const int64_t ld = padded_ld(*m);
-  const unsigned grid = (unsigned)std::min<int64_t>(m->n_rows, 8 * std::max(1, h->sm_count));
-  if (size_of(m->type) == 1)
-    k_copy_rows<uint8_t><<<grid, 256, 0, s>>>(*m, *scratch, ld);
+// Each matrix itself, or its copy with padded rows at *scratch (advanced past
+// it); one launch.
+cudaError_t aligned_rows(ss_handle *h, std::initializer_list<ss_dense *> ms, unsigned char **scratch, cudaStream_t s, int *queued) {
+  Copies a = {};
+  int n = 0;
+  int64_t rows = 0;
+  bool bytes = false;
+  for (ss_dense *m : ms) {
+    if (rows_aligned(*m, 16)) continue;
+    a.src[n] = *m;
+    a.dst[n] = *scratch;
+    a.ld[n] = padded_ld(*m);
+    bytes = size_of(m->type) == 1;
+    rows = std::max(rows, m->n_rows);
+    m->data = *scratch;
+    m->ld = a.ld[n++];
+    *scratch += align_up(m->n_rows * m->ld * size_of(m->type));
+  }
+  if (n == 0) return cudaSuccess;
+  const dim3 grid((unsigned)std::min<int64_t>(rows, 8 * std::max(1, h->sm_count)), (unsigned)n);
+  if (bytes)
+    k_copy_rows<uint8_t><<<grid, 256, 0, s>>>(a);
   else
-    k_copy_rows<uint16_t><<<grid, 256, 0, s>>>(*m, reinterpret_cast<uint16_t *>(*scratch), ld);
+    k_copy_rows<uint16_t><<<grid, 256, 0, s>>>(a);
   *queued += 1;
-  m->data = *scratch;
-  *scratch += align_up(m->n_rows * ld * size_of(m->type));
-  m->ld = ld;
   return cudaGetLastError();
 }
 
@@ -1177,8 +1197,7 @@ cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, in
   ss_dense x = a.x, w = a.w;
   unsigned char *scratch = a.scratch;
   cudaError_t e;
-  if ((e = aligned_rows(h, &x, &scratch, s, queued)) != cudaSuccess) return e;
-  if ((e = aligned_rows(h, &w, &scratch, s, queued)) != cudaSuccess) return e;
+  if ((e = aligned_rows(h, {&x, &w}, &scratch, s, queued)) != cudaSuccess) return e;
   const int64_t M = x.n_rows, N = w.n_rows, kb = stages_of(x, x.n_cols);
   const Cut cut = cut_of(h, M, N, kb, 16, true);
   if (M <= kSwapRows) {
@@ -1237,11 +1256,11 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
     return ep;
   };
   if (a.grad_x.data) {
-    if ((e = aligned_rows(h, &w, &scratch, s, queued)) != cudaSuccess) return e;
+    if ((e = aligned_rows(h, {&w}, &scratch, s, queued)) != cudaSuccess) return e;
     if ((e = product(h, gz, kMajorK, w, kMajorMN, false, cut_of(h, M, x.n_cols, stages_of(gz, N), 64, true), out(a.grad_x), s, queued)) != cudaSuccess) return e;
   }
   if (a.grad_w.data) {
-    if ((e = aligned_rows(h, &x, &scratch, s, queued)) != cudaSuccess) return e;
+    if ((e = aligned_rows(h, {&x}, &scratch, s, queued)) != cudaSuccess) return e;
     if ((e = product(h, gz, kMajorMN, x, kMajorMN, false, cut_of(h, N, x.n_cols, stages_of(gz, M), 64, true), out(a.grad_w), s, queued)) != cudaSuccess) return e;
   }
   return cudaSuccess;
