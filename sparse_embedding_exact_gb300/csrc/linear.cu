@@ -882,10 +882,24 @@ struct Copies {
 };
 template <typename T>
 __global__ void __launch_bounds__(256) k_copy_rows(const Copies a) {
-  const ss_dense &src = a.src[blockIdx.y];
-  T *dst = static_cast<T *>(a.dst[blockIdx.y]);
-  for (int64_t r = blockIdx.x; r < src.n_rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < src.n_cols; c += 256) dst[r * a.ld[blockIdx.y] + c] = static_cast<const T *>(src.data)[r * src.ld + c];
+  const bool second = blockIdx.y == 1;
+  const ss_dense src = second ? a.src[1] : a.src[0];
+  const int64_t ld = second ? a.ld[1] : a.ld[0];
+  T *dst = static_cast<T *>(second ? a.dst[1] : a.dst[0]);
+  const int n = (int)src.n_cols;
+  for (int64_t r = blockIdx.x; r < src.n_rows; r += gridDim.x) {
+    const T *p = static_cast<const T *>(src.data) + r * src.ld;
+    T *q = dst + r * ld;
+    for (int c = threadIdx.x; c < n; c += 4 * 256) {  // four loads under way at a time
+      T v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c + u * 256 < n) v[u] = p[c + u * 256];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c + u * 256 < n) q[c + u * 256] = v[u];
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host side
