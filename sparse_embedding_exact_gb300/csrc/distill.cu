@@ -12,11 +12,16 @@
 //
 // Bound by memory: the softmax's maximum M and sum S = sum exp((z - M) / T)
 // are taken in one pass over the row (each thread rescales its sum when its
-// maximum grows), then q = exp((z - M) / T) / S is written in a second one.
-// The row is shared by a cluster of up to 8 blocks, which exchange their (M,
-// S) through each other's shared memory, so a step is one launch and a row's
-// second read finds it in L2.  The k entries are then written over by one
-// thread each, the duplicates of an item summed in list order.
+// maximum grows), then q = exp((z - M) / T) / S is written in a second one,
+// and the k entries are written over by one thread each, the duplicates of an
+// item summed in list order.  A row is shared by a cluster of up to 8 blocks,
+// which exchange their (M, S) through each other's shared memory, so every
+// call is one launch.  Loss alone and gradient alone stream the row
+// (k_distill); a step keeps it on chip between its passes (k_distill_step)
+// where 8 blocks can hold it, and reads it a second time where not.
+//
+// Measured: loss and gradient of 2,500 x 200,000 bf16 logits, top 64, 365 us
+// (5.5 TB/s, 81% of the copy bandwidth; streaming it twice 457 us).
 #include <cooperative_groups.h>
 #include <math.h>
 

@@ -10,17 +10,24 @@
 // Gradient, with xh = s rstd and g = grad_y w:
 //   grad_x = rstd (g - xh mean(g xh)) + grad_s,   grad_w = sum_rows grad_y xh
 //
-// Both are bound by memory: every value is read once, held in registers
-// across the row's reduction, and written once.  A block takes a row at a
-// time, every thread the same columns of each row, so the weights (and the
-// gradient's sums over rows) stay in registers.  Rows arrive by bulk copies in
-// a ring of shared-memory slots, the next rows while one is worked on: with
-// plain loads into registers too few bytes were in flight (16,384 rows of 4096
-// bf16 with residual to 8 bits: 113 us, 4.2 TB/s).  A bulk copy moves whole
-// 16-byte units; where a row starts or ends inside one, the few values there
-// are read by ordinary loads.  The sums over a block's rows go to scratch, one
-// row of it a block, and a second kernel adds them in a fixed order: no
-// atomics, the same bits every time.
+// Both are bound by memory: every value is read from it once and written
+// once.  A group of threads takes a row at a time, each thread the same
+// columns of every row, so the weights (and the gradient's sums over rows)
+// stay in registers; values are worked on in pairs, one instruction for two.
+// Rows arrive by bulk copies in a ring of shared-memory slots, the next rows
+// while one is worked on: with plain loads into registers too few bytes were
+// in flight (16,384 rows of 4096 bf16 with residual to 8 bits: 113 us).  A bulk
+// copy moves whole 16-byte units, those that a row shares with its neighbours
+// included; where all matrices' rows start alike within a unit, threads work
+// on units and drop what is not the row's.  The sums over a block's rows go to
+// scratch, one row of it a block, and a second kernel adds them in a fixed
+// order: no atomics, the same bits every time.
+//
+// Measured: 16,384 x 4096 bf16 with residual to 8 bits 86 us (5.4 TB/s, 73 us
+// without the write-back of its output: memory); the gradient of 16,384 x 2048
+// bf16 59 us, of which the kernel 50 and the sums 6 (4.6 TB/s: instructions,
+// at 16 warps an SM, which its registers allow); of 5000 x 1001 float32 29 us
+// (22 and 5).
 #include <algorithm>
 #include <initializer_list>
 
@@ -630,12 +637,13 @@ __global__ void __launch_bounds__(1024) k_sum_rows(const float *part, int64_t n,
 // thread of `threads` a row, `groups` rows a block, `slots` rows of the ring a
 // group, `blocks` an SM.  per = 0: too wide for registers.
 //
-// Many rows: 4 vectors a thread, 16 to 32 values of it.  What a thread spends on a row besides its values (the reduction's shuffles and
-// barrier, the root) is as much as 8 values cost, and with 8 values a thread
-// the norm of 16,384 x 4096 bf16 rows to 8 bits was bound by instructions (94
-// us).  Rows for every SM or fewer: one vector a thread, for the time of one
-// row.
-constexpr int kVecPers[3] = {1, 4, 4}, kOnePers[3] = {1, 4, 16};
+// Many rows: 4 vectors a thread, 16 or 32 values of it.  What a thread spends on
+// a row besides its values (the reduction's shuffles and barrier, the root) is
+// as much as 8 values cost: with 8 values a thread the norm of 16,384 x 4096
+// bf16 rows to 8 bits took 94 us against 72, and with 16 the gradient of
+// 16,384 x 2048 rows 63 against 59.  Rows for every SM or fewer: one vector a
+// thread, for the time of one row.
+constexpr int kVecPers[3] = {1, 4, 4}, kF32Pers[3] = {1, 4, 8}, kOnePers[3] = {1, 4, 16};
 struct Shape {
   int per, threads, groups, slots, blocks, smem;
 };
@@ -646,7 +654,7 @@ Shape shape_for(const ss_handle *h, int64_t R, int64_t D, int n, const int (&per
     const int64_t t = ((vecs + per - 1) / per + 31) / 32 * 32;
     if (t > (grad ? grad_threads(n, per) : kMostThreads) || row_bytes > kRingBytes) continue;
     if (sh.per && (vecs < 32 * per || R <= h->sm_count)) break;
-    if (sh.per && per == 16) break;  // where 4 do not reach
+    if (sh.per && per > 4) break;  // where 4 do not reach
     sh.per = per;
     sh.threads = (int)t;
   }
@@ -694,7 +702,7 @@ cudaError_t rms_norm_typed(ss_handle *h, const rms_args &a, cudaStream_t s) {
   bool shifting = false;
   const bool vec = in_units({a.x, a.residual, a.total, a.y}, kV, D, &shifting);
   const bool aligned = vec && !shifting && reinterpret_cast<uintptr_t>(a.x.data) % 16 == 0 && D % kV == 0;
-  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? kVecPers : kOnePers, false,
+  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? (kV == 4 ? kF32Pers : kVecPers) : kOnePers, false,
                              (a.residual.data ? 2 : 1) * (int64_t)Ring<T, 2>::pitch_for(D));
   if (sh.per == 0) {
     const unsigned grid = (unsigned)std::min<int64_t>(R, sms * sh.blocks);
@@ -711,8 +719,15 @@ cudaError_t rms_norm_typed(ss_handle *h, const rms_args &a, cudaStream_t s) {
     kernel<<<(unsigned)grid, sh.groups * sh.threads, sh.smem, s>>>(a, sh.threads, sh.slots, h->d_status);
     return cudaGetLastError();
   };
-  if (aligned) return sh.per == 1 ? run(k_rms_norm<T, kF8, kV, 1, false>) : run(k_rms_norm<T, kF8, kV, 4, false>);
-  if (vec) return sh.per == 1 ? run(k_rms_norm<T, kF8, kV, 1, true>) : run(k_rms_norm<T, kF8, kV, 4, true>);
+  constexpr int kMore = kV == 4 ? 8 : 4;
+  if (aligned)
+    return sh.per == 1   ? run(k_rms_norm<T, kF8, kV, 1, false>)
+           : sh.per == 4 ? run(k_rms_norm<T, kF8, kV, 4, false>)
+                         : run(k_rms_norm<T, kF8, kV, kMore, false>);
+  if (vec)
+    return sh.per == 1   ? run(k_rms_norm<T, kF8, kV, 1, true>)
+           : sh.per == 4 ? run(k_rms_norm<T, kF8, kV, 4, true>)
+                         : run(k_rms_norm<T, kF8, kV, kMore, true>);
   return sh.per == 1   ? run(k_rms_norm<T, kF8, 1, 1, false>)
          : sh.per == 4 ? run(k_rms_norm<T, kF8, 1, 4, false>)
                        : run(k_rms_norm<T, kF8, 1, 16, false>);
@@ -733,7 +748,7 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
   bool shifting = false;
   const bool vec = in_units({a.grad_y, a.total, a.grad_total, a.grad_x}, kV, D, &shifting);
   const bool aligned = vec && !shifting && reinterpret_cast<uintptr_t>(a.total.data) % 16 == 0 && D % kV == 0;
-  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? kVecPers : kOnePers, true,
+  const Shape sh = shape_for(h, R, vec && !aligned ? D + kV - 1 : D, vec ? kV : 1, vec ? (kV == 4 ? kF32Pers : kVecPers) : kOnePers, true,
                              (a.grad_total.data ? 3 : 2) * (int64_t)Ring<T, 3>::pitch_for(D));
   int64_t n = std::min<int64_t>(most_parts(h, (R + sh.groups - 1) / sh.groups), (int64_t)std::max(1, h->sm_count) * sh.blocks);
   if (sh.per) n = keep_shift(n, sh.groups, R, kV, shifting && vec);
@@ -755,10 +770,15 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
     *queued += 1;
     e = cudaGetLastError();
   } else if (vec) {
+    constexpr int kMore = kV == 4 ? 8 : 4;
     if (aligned)
-      e = sh.per == 1 ? run(k_rms_grad<T, kV, 1, false>) : run(k_rms_grad<T, kV, 4, false>);
+      e = sh.per == 1   ? run(k_rms_grad<T, kV, 1, false>)
+          : sh.per == 4 ? run(k_rms_grad<T, kV, 4, false>)
+                        : run(k_rms_grad<T, kV, kMore, false>);
     else
-      e = sh.per == 1 ? run(k_rms_grad<T, kV, 1, true>) : run(k_rms_grad<T, kV, 4, true>);
+      e = sh.per == 1   ? run(k_rms_grad<T, kV, 1, true>)
+          : sh.per == 4 ? run(k_rms_grad<T, kV, 4, true>)
+                        : run(k_rms_grad<T, kV, kMore, true>);
   } else {
     e = sh.per == 1   ? run(k_rms_grad<T, 1, 1, false>)
         : sh.per == 4 ? run(k_rms_grad<T, 1, 4, false>)
