@@ -35,7 +35,7 @@
 //
 // Up to 4 rows (k_rows): a warp takes whole rows of w with 16-byte loads and
 // ordinary multiply-adds, no tile to fill.  One row, 65,536 features of 1024
-// bf16: 28 us (4.8 TB/s; eight features a warp 31 us, two 29 us).
+// bf16: 25.7 us (5.2 TB/s).
 //
 // Rows that do not start on 16-byte boundaries, which tensor copies cannot
 // take, are first copied into scratch with padded rows.
@@ -791,10 +791,13 @@ __device__ __forceinline__ void read_vec(const T *p, float (&f)[kN]) {
   }
 }
 
-constexpr int kRowWarps = 8;
-// A warp takes kW features and, in turns, kM rows of x; kN values a load.
+constexpr int kRowWarps = 2;
+// A warp takes kW features and, in turns, kM rows of x; kN values a load.  Small
+// blocks, so that a finished warp's place is filled soon, and for one row 32
+// warps an SM (65,536 features of 1024 bf16: 25.7 us; blocks of eight warps
+// with the registers they like, 24 warps an SM, 28.5 us).
 template <typename T, int kM, int kW, int kN>
-__global__ void __launch_bounds__(32 * kRowWarps) k_rows(const ss_dense x, const ss_dense w, const Epilogue ep) {
+__global__ void __launch_bounds__(32 * kRowWarps, kM == 1 ? 16 : 1) k_rows(const ss_dense x, const ss_dense w, const Epilogue ep) {
   const int lane = threadIdx.x & 31;
   const int64_t n0 = ((int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * kW;
   const int64_t N = w.n_rows, M = x.n_rows, K = x.n_cols;
