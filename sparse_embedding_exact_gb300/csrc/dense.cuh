@@ -230,7 +230,7 @@ cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &a, cudaStrea
 
 // out[c] = the sum of column c over the n rows of part (one kernel; a fixed
 // order), rounded to `type`.
-cudaError_t launch_sum_rows(const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s);
+cudaError_t launch_sum_rows(const ss_handle *h, const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s);
 
 struct distill_args {
   ss_dense logits, grad_logits;

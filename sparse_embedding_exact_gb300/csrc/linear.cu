@@ -33,7 +33,7 @@
 // contiguous across it, and gz^T x both (MN-major); the copies and descriptors
 // take either, so nothing is transposed in memory.
 //
-// Up to 4 rows (k_rows): a warp takes whole rows of w with 16-byte loads and
+// One row, two of 16 bits (k_rows): a warp takes whole rows of w with 16-byte loads and
 // ordinary multiply-adds, no tile to fill.  One row, 65,536 features of 1024
 // bf16: 25.7 us (5.2 TB/s).
 //
@@ -419,7 +419,9 @@ template <int kBN>
 struct Ring {
   static constexpr int kBytesA = kTileM * kRowBytes, kBytesB = kBN * kRowBytes;
   static constexpr int kStage = kBytesA + kBytesB;
-  static constexpr int kStages = (kSmemMost - 2048) / kStage < 8 ? (kSmemMost - 2048) / kStage : 8;
+  // narrow tiles: short rings, so that two or three blocks an SM hide each
+  // other's set-up and epilogue
+  static constexpr int kStages = kBN == 16 ? 4 : kBN <= 64 ? 3 : (kSmemMost - 2048) / kStage;
   static constexpr int kSmem = kStages * kStage + 1024;  // + alignment to 1024
   static_assert((kBN + 1) * kTileM * 4 <= kStages * kStage, "a tile to exchange fits the ring");
   static_assert(2 * kEpiFew * kStaging <= kStages * kStage, "and so do the epilogue's boxes");
@@ -809,7 +811,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, kM == 1 ? 16 : 1) k_rows(const
     for (int j = 0; j < kW; ++j)
 #pragma unroll
       for (int m = 0; m < kM; ++m) sum[j][m] = 0.0f;
-#pragma unroll 2
+#pragma unroll(kW == 1 ? 8 : 2)
     for (int64_t k = (int64_t)lane * kN; k < K; k += 32 * kN) {
       float xv[kM][kN], wv[kW][kN];
 #pragma unroll
@@ -1079,13 +1081,16 @@ Cut cut_of(const ss_handle *h, int64_t rows_a, int64_t rows_b, int64_t blocks_k,
   for (int bn = 256; bn >= least; bn /= 2) {
     if (bn < 256 && bn < 64 && rows_b > bn) break;  // narrow tiles: where they hold all of B's rows
     for (int split = 1; split <= (bn <= 128 ? 8 : 1) && (split == 1 || blocks_k / split >= 2); split *= 2) {
-      // blocks at a time: clusters stay within a group of SMs, and of 152 SMs 36
-      // of 4 blocks and 15 of 8 run at once
-      const int64_t at_once = split == 8 ? sms * 15 / 19 : split == 4 ? sms * 18 / 19 : sms;
+      // Blocks at a time: clusters stay within a group of SMs, and of 152 SMs 36
+      // of 4 blocks and 15 of 8 run at once (of 456 places 110 and 51).
+      const int64_t an_sm = bn <= 32 ? 3 : bn == 64 ? 2 : 1, places = sms * an_sm;
+      const int64_t at_once = split == 8 ? places * (an_sm > 1 ? 17 : 15) / 19 : split == 4 ? places * 18 / 19 : places;
+      const int64_t blocks = up(rows_a, kTileM) * up(rows_b, bn) * split;
+      const double sharing = (double)std::min(an_sm, up(blocks, sms));
       // a matrix that one row of tiles reads once comes from memory, not L2
       const double rate = up(rows_a, kTileM) == 1 || up(rows_b, bn) == 1 ? 40.0 : 85.0;
-      const double turns = (double)up(up(rows_a, kTileM) * up(rows_b, bn) * split, at_once);
-      const double each = 5e3 + (split > 1 ? 5e3 + 80.0 * bn : 0.0) + 30.0 * bn / split + (double)up(blocks_k, split) * (kTileM + bn) * kRowBytes / rate;
+      const double turns = (double)up(blocks, at_once);
+      const double each = 5e3 + (split > 1 ? 5e3 + 80.0 * bn : 0.0) + 30.0 * bn / split + (double)up(blocks_k, split) * (kTileM + bn) * kRowBytes * sharing / rate;
       const double clocks = 4e3 + turns * each;
       if (clocks < best.clocks) best = {bn, split, false, clocks};
     }
@@ -1158,22 +1163,25 @@ cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B
   }
 }
 
-constexpr int64_t kFewRows = 4;     // k_rows up to this many rows
+// k_rows up to this many rows: two of 1024 bf16 against 65,536 take it 32 us and
+// tiles 41, three 43 and 41; two of e4m3 26 and 20.
+int64_t few_rows_of(const ss_dense &x) { return x.type == SS_VALUES_F8 ? 1 : 2; }
 constexpr int64_t kSwapRows = 256;  // features as A is looked at up to this many rows
 
 template <typename T, int kN>
-cudaError_t rows_typed(const ss_dense &x, const ss_dense &w, const Epilogue &ep, cudaStream_t s) {
+cudaError_t rows_typed(const ss_dense &x, const ss_dense &w, const Epilogue &ep, int sms, cudaStream_t s) {
   const int64_t M = x.n_rows, N = w.n_rows;
   auto run = [&](auto kernel, int m, int wide) {
     kernel<<<dim3((unsigned)((N + kRowWarps * wide - 1) / (kRowWarps * wide)), (unsigned)std::min<int64_t>(65535, (M + m - 1) / m)), 32 * kRowWarps, 0,
              s>>>(x, w, ep);
   };
-  if (M == 1)
+  // one feature a warp where four leave less than 16 warps an SM
+  if (M == 1 && N >= 64 * (int64_t)std::max(1, sms))
     run(k_rows<T, 1, 4, kN>, 1, 4);
-  else if (M == 2)
-    run(k_rows<T, 2, 2, kN>, 2, 2);
+  else if (M == 1)
+    run(k_rows<T, 1, 1, kN>, 1, 1);
   else
-    run(k_rows<T, 4, 2, kN>, 4, 2);
+    run(k_rows<T, 2, 2, kN>, 2, 2);
   return cudaGetLastError();
 }
 
@@ -1183,7 +1191,7 @@ int64_t stages_of(const ss_dense &m, int64_t K) {
   return (K + unit - 1) / unit;
 }
 
-bool few_rows(const ss_dense &x) { return x.n_rows <= kFewRows || x.n_cols == 0; }
+bool few_rows(const ss_dense &x) { return x.n_rows <= few_rows_of(x) || x.n_cols == 0; }
 
 int64_t grad_parts(const ss_handle *h, int64_t M, int64_t N) {
   const int64_t slabs = (N + 255) / 256;
@@ -1216,11 +1224,11 @@ cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, in
     const bool vec = a.x.n_cols % v == 0 && rows_aligned(a.x, 16) && rows_aligned(a.w, 16);
     switch (a.x.type) {
       case SS_VALUES_F8:
-        return vec ? rows_typed<uint8_t, 16>(a.x, a.w, ep, s) : rows_typed<uint8_t, 1>(a.x, a.w, ep, s);
+        return vec ? rows_typed<uint8_t, 16>(a.x, a.w, ep, h->sm_count, s) : rows_typed<uint8_t, 1>(a.x, a.w, ep, h->sm_count, s);
       case SS_VALUES_BF16:
-        return vec ? rows_typed<__nv_bfloat16, 8>(a.x, a.w, ep, s) : rows_typed<__nv_bfloat16, 1>(a.x, a.w, ep, s);
+        return vec ? rows_typed<__nv_bfloat16, 8>(a.x, a.w, ep, h->sm_count, s) : rows_typed<__nv_bfloat16, 1>(a.x, a.w, ep, h->sm_count, s);
       default:
-        return vec ? rows_typed<__half, 8>(a.x, a.w, ep, s) : rows_typed<__half, 1>(a.x, a.w, ep, s);
+        return vec ? rows_typed<__half, 8>(a.x, a.w, ep, h->sm_count, s) : rows_typed<__half, 1>(a.x, a.w, ep, h->sm_count, s);
     }
   }
   ss_dense x = a.x, w = a.w;
@@ -1276,7 +1284,7 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
       *queued += 1;
     }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (sums && (e = launch_sum_rows(part, parts, N, a.grad_bias, SS_VALUES_F32, s)) != cudaSuccess) return e;
+    if (sums && (e = launch_sum_rows(h, part, parts, N, a.grad_bias, SS_VALUES_F32, s)) != cudaSuccess) return e;
   }
   auto out = [](const ss_dense &m) {
     Epilogue ep = {};

@@ -606,27 +606,32 @@ __global__ void __launch_bounds__(256) k_rms_grad_cols(const rms_grad_args a) {
   }
 }
 
-// out[c] = sum over the n rows of part, in a fixed order: a block takes 8
-// columns, each thread every 128th row of one, four at a time (32 columns and
-// 32 rows a block left most SMs idle: 5 us against 3).
-constexpr int kSumCols = 8, kSumRows = 128;
-__global__ void __launch_bounds__(kSumCols *kSumRows) k_sum_rows(const float *part, int64_t n, int64_t D, void *out, int32_t type) {
-  __shared__ float sm[kSumRows][kSumCols + 1];
-  const int col = threadIdx.x % kSumCols, lane = threadIdx.x / kSumCols;
-  const int64_t c = (int64_t)blockIdx.x * kSumCols + col;
+// out[c] = sum over the n rows of part, in a fixed order: a block takes kCols
+// columns, each of its threads every (1024 / kCols)-th row of one, four at a
+// time.  8 columns where 32 would leave more than half of the SMs idle (456
+// rows of 1001: 5 us with 32, 3 with 8), else 32, a line a warp.
+template <int kCols>
+__global__ void __launch_bounds__(1024) k_sum_rows(const float *part, int64_t n, int64_t D, void *out, int32_t type) {
+  constexpr int kLanes = 1024 / kCols;
+  __shared__ float sm[kLanes][kCols + 1];
+  const int col = threadIdx.x % kCols, lane = threadIdx.x / kCols;
+  const int64_t c = (int64_t)blockIdx.x * kCols + col;
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < D)
-    for (int64_t k = lane; k < n; k += 4 * kSumRows) {
+    for (int64_t k = lane; k < n; k += 4 * kLanes) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (k + kSumRows * u < n) sum[u] += part[(k + kSumRows * u) * D + c];
+        if (k + kLanes * u < n) sum[u] += part[(k + kLanes * u) * D + c];
     }
   sm[lane][col] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   __syncthreads();
   const int warp = threadIdx.x >> 5, t = threadIdx.x & 31;
-  if (warp >= kSumCols) return;
-  const float v = warp_sum((sm[t][warp] + sm[t + 32][warp]) + (sm[t + 64][warp] + sm[t + 96][warp]));
-  const int64_t at = (int64_t)blockIdx.x * kSumCols + warp;
+  if (warp >= kCols) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kLanes; u += 32) v += sm[t + u][warp];
+  v = warp_sum(v);
+  const int64_t at = (int64_t)blockIdx.x * kCols + warp;
   if (t == 0 && at < D) {
     if (type == SS_VALUES_F32)
       static_cast<float *>(out)[at] = v;
@@ -790,7 +795,7 @@ cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s,
   }
   if (e != cudaSuccess) return e;
   *queued += 2;
-  return launch_sum_rows(a.scratch, n, D, a.grad_weight.data, a.grad_weight.type, s);
+  return launch_sum_rows(h, a.scratch, n, D, a.grad_weight.data, a.grad_weight.type, s);
 }
 
 }  // namespace
@@ -808,8 +813,11 @@ cudaError_t launch_rms_norm(ss_handle *h, const rms_args &a, cudaStream_t s, int
   }
 }
 
-cudaError_t launch_sum_rows(const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s) {
-  k_sum_rows<<<(unsigned)((cols + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, s>>>(part, n, cols, out, type);
+cudaError_t launch_sum_rows(const ss_handle *h, const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s) {
+  if (cols / 32 >= h->sm_count / 2)
+    k_sum_rows<32><<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(part, n, cols, out, type);
+  else
+    k_sum_rows<8><<<(unsigned)((cols + 7) / 8), 1024, 0, s>>>(part, n, cols, out, type);
   return cudaGetLastError();
 }
 
