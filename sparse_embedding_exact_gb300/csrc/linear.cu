@@ -25,7 +25,7 @@
 // memory in a fixed order.  With few rows the sides are swapped, A = w and B =
 // x, so that 128 features fill the tile's rows and few columns are spent on
 // rows that do not exist; then reading w is the bound.  16 x 4096 x 4096 e4m3:
-// 8.6 us, of which about 5 are latency (set-up, first copies, exchange).
+// 9.4 us a call, most of it latency (set-up, first copies, exchange).
 // cut_of chooses by estimated time.
 //
 // The three products of a layer differ in which operand runs along the summed
