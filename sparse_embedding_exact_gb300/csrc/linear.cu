@@ -1194,7 +1194,7 @@ int64_t stages_of(const ss_dense &m, int64_t K) {
 bool few_rows(const ss_dense &x) { return x.n_rows <= few_rows_of(x) || x.n_cols == 0; }
 
 int64_t grad_parts(const ss_handle *h, int64_t M, int64_t N) {
-  const int64_t slabs = (N + 255) / 256;
+  const int64_t slabs = std::max<int64_t>(1, (N + 255) / 256);
   return std::max<int64_t>(1, std::min<int64_t>((M + 63) / 64, 8 * (int64_t)std::max(1, h->sm_count) / slabs));
 }
 
@@ -1207,6 +1207,7 @@ int64_t linear_scratch(const ss_handle *, const ss_dense &x, const ss_dense &w) 
 int64_t linear_grad_scratch(const ss_handle *h, const ss_dense &grad_y, const ss_dense &x, const ss_dense &w,
                             int32_t act) {
   const int64_t M = grad_y.n_rows, N = grad_y.n_cols;
+  if (M == 0 || N == 0) return 0;  // the gradients are zeroed
   const bool own = act != SS_ACT_NONE || !rows_aligned(grad_y, 16);
   return copy_bytes(x) + copy_bytes(w) + (own ? align_up(M * padded_ld(grad_y) * size_of(grad_y.type)) : 0) +
          align_up(grad_parts(h, M, N) * N * (int64_t)sizeof(float));
