@@ -105,6 +105,10 @@ __device__ __forceinline__ float2 f8_factors(float most) {
   return make_float2(pre, most > 0.0f ? kF8Max / (most * pre) : (most == 0.0f ? 0.0f : most));
 }
 
+// A row's scale, max|y| / 448; 0 for a row of zeros, also where eps = 0 makes
+// its rstd infinite.
+__device__ __forceinline__ float scale_of(float most, float rstd) { return most == 0.0f ? 0.0f : most * rstd / kF8Max; }
+
 // A group's ring of rows in shared memory: slot s holds the current row of kRows
 // matrices.  Value c of a row lies at the same place within 16 bytes as in
 // global memory.
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kMostThreads, 1) k_rms_norm(const rms_args a, 
     const float rstd = 1.0f / sqrtf(red.x * inv_d + a.eps);
     if (gr.lane == 0) {
       if (a.rstd) a.rstd[row] = rstd;
-      if (kF8) a.scale[row] = red.y * rstd / kF8Max;
+      if (kF8) a.scale[row] = scale_of(red.y, rstd);
     }
     const float2 to8 = kF8 ? f8_factors(red.y) : make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(kWideThreads) k_rms_norm_wide(const rms_args a
     const float rstd = 1.0f / sqrtf(red.x / (float)D + a.eps);
     if (threadIdx.x == 0) {
       if (a.rstd) a.rstd[row] = rstd;
-      if (kF8) a.scale[row] = red.y * rstd / kF8Max;
+      if (kF8) a.scale[row] = scale_of(red.y, rstd);
     }
     const float2 to8 = f8_factors(red.y);
     for (int64_t c = (int64_t)threadIdx.x * kN; c < D; c += (int64_t)blockDim.x * kN) {
