@@ -145,7 +145,7 @@ __device__ __forceinline__ void write_any(const ss_dense &m, int64_t i, float v)
     static_cast<__half *>(m.data)[i] = __float2half_rn(v);
 }
 __device__ __forceinline__ void finish_one(const Epilogue &ep, int64_t m, int64_t n, float v) {
-  if (ep.row_scale) v *= ep.row_scale[m] * ep.col_scale[n];
+  if (ep.row_scale) v = v * ep.row_scale[m] * ep.col_scale[n];  // one after the other: their product may leave float32's range
   if (ep.bias) v += ep.bias[n];
   if (ep.pre.data) write_any(ep.pre, m * ep.pre.ld + n, v);
   v = act_any(ep.act, v);
@@ -183,7 +183,7 @@ __device__ __forceinline__ void finish16(const Epilogue &ep, int64_t m, int64_t 
   if (ep.row_scale) {
     const float s = ep.row_scale[m];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= s * ep.col_scale[n + i];
+    for (int i = 0; i < 16; ++i) v[i] = v[i] * s * ep.col_scale[n + i];
   }
   if (ep.bias) {
 #pragma unroll
@@ -378,7 +378,7 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *
   if (!there) return;
   if (ep.row_scale) {
     const float s = m < M ? ep.row_scale[m] : 0.0f;
-    along32(ep.col_scale + n0, N - n0, [&](int i, float f) { v[i] *= s * f; });
+    along32(ep.col_scale + n0, N - n0, [&](int i, float f) { v[i] = v[i] * s * f; });
   }
   if (ep.bias) along32(ep.bias + n0, N - n0, [&](int i, float f) { v[i] += f; });
   if (ep.pre.data) put32(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);

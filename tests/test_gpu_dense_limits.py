@@ -43,3 +43,35 @@ def test_zero_row_to_8_bits_without_eps(h, dtype, cols):
     assert float(scale[1]) == 0 and not y[1].float().any()
     assert torch.isfinite(scale).all() and (scale[[0, 2]] > 0).all()
     assert (y[[0, 2]].float().abs().amax(1) == 448).all()
+
+
+# ---------------------------------------------------------------- linear
+# One row; few rows (features along the tile's rows); one tile; many tiles, an
+# odd row length and rows of features off 16 bytes.
+SCALE_SHAPES = [(1, 64, 96), (16, 256, 300), (40, 4096, 256), (300, 256, 520), (300, 200, 333), (2600, 64, 4000)]
+
+
+@pytest.mark.parametrize("m,k,n", SCALE_SHAPES)
+@pytest.mark.parametrize("sx,sw,x", [(1e-25, 1e-20, 448.0), (1e25, 1e16, 2.0 ** -9), (1e-19, 1e-30, 448.0)])
+def test_row_scales_apply_one_after_the_other(h, m, k, n, sx, sw, x):
+    # Every sum is k x^2, exact in float32 (448^2 = 49 * 2^12, k below 2^13);
+    # the scales' product alone would be 0 or infinite.
+    one = torch.full((m, k), x, device="cuda")
+    one[m // 2] = 0  # a row of zeros: 0 whatever the scales are
+    a, b = one.to(F8), torch.full((n, k), x, device="cuda").to(F8)
+    vx, vw = torch.full((m,), sx, device="cuda"), torch.full((n,), sw, device="cuda")
+    y = h.linear(a, b, x_scale=vx, w_scale=vw, out_dtype=torch.float32)
+    want = (a.to(F64) @ b.to(F64).t() * vx.to(F64)[:, None] * vw.to(F64))
+    fits = want <= torch.finfo(torch.float32).max  # past it the float32 output is infinite
+    # two roundings, and results below 2^-126 keep a step of 2^-149
+    assert ((y.to(F64) - want).abs() <= 2 * E * want.abs() + 2.0 ** -149)[fits].all()
+    assert torch.isinf(y[~fits]).all() and not y[m // 2].any()
+
+
+@pytest.mark.parametrize("k", [64, 100])
+def test_row_scales_of_one_row(h, k):
+    x, w = torch.full((1, k), 448.0, device="cuda").to(F8), torch.full((77, k), 448.0, device="cuda").to(F8)
+    sx, sw = torch.full((1,), 1e-30, device="cuda"), torch.full((77,), 1e-19, device="cuda")
+    y = h.linear(x, w, x_scale=sx, w_scale=sw, out_dtype=torch.float32)
+    want = x.to(F64) @ w.to(F64).t() * sx.to(F64)[:, None] * sw.to(F64)
+    assert ((y.to(F64) - want).abs() <= 2 * E * want.abs() + 2.0 ** -149).all() and (y > 0).all()
