@@ -75,3 +75,43 @@ def test_row_scales_of_one_row(h, k):
     y = h.linear(x, w, x_scale=sx, w_scale=sw, out_dtype=torch.float32)
     want = x.to(F64) @ w.to(F64).t() * sx.to(F64)[:, None] * sw.to(F64)
     assert ((y.to(F64) - want).abs() <= 2 * E * want.abs() + 2.0 ** -149).all() and (y > 0).all()
+
+
+# ---------------------------------------------------------------- activations
+# In multiples of E, relative to the result; z reaches the activation exactly
+# (as the bias of rows of zeros).  An exponential of an argument of size a has
+# the argument's two or three roundings, 2.5 a E at most, and the instruction's
+# 4 E; the rest is a dozen roundings, their factors below 2, and the
+# polynomial's 3 E.
+TAILS = {
+    "gelu": (lambda z: 0.5 * torch.erfc(-z / 2 ** 0.5), lambda z: 1.25 * z * z + 24),
+    "gelu_tanh": (lambda z: 1 / (1 + torch.exp(-2 * (2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3))),
+                  lambda z: 6 * (2 / torch.pi) ** 0.5 * (z.abs() + 0.044715 * z.abs() ** 3) + 24),
+    "silu": (lambda z: 1 / (1 + torch.exp(-z)), lambda z: 3 * z.abs() + 24),
+}
+
+
+def _tail(name, m):
+    """act(z) of m rows for z from -8 to -2 and a few around 0, in 64 bits too."""
+    z = torch.cat([torch.linspace(-8, -2, 1200), torch.linspace(-2, 3, 336)]).cuda()
+    x, w = torch.zeros(m, 64, dtype=torch.bfloat16, device="cuda"), _randn(z.numel(), 64, dtype=torch.bfloat16)
+    share, units = TAILS[name]
+    return x, w, z, share(z.to(F64)), units(z.to(F64)) * E
+
+
+def _tail_of(h, name, m, dtype):
+    x, w, z, share, room = _tail(name, m)
+    want = z.to(F64) * share
+    y = h.linear(x.to(dtype) if dtype != torch.float32 else x, w.to(dtype) if dtype != torch.float32 else w, bias=z,
+                 activation=name, out_dtype=dtype)
+    return y.to(F64), want, room
+
+
+@pytest.mark.parametrize("m", [1, 40, 600])
+def test_gelu_of_negative_values(h, m):
+    y, want, room = _tail_of(h, "gelu", m, torch.float32)
+    assert ((y - want).abs() <= (room + E) * want.abs()).all()
+    y, want, room = _tail_of(h, "gelu", m, torch.bfloat16)
+    assert ((y - want).abs() <= (room + 2.0 ** -8) * want.abs()).all()
+    y, want, room = _tail_of(h, "gelu", m, torch.float16)
+    assert ((y - want).abs() <= (room + 2.0 ** -11) * want.abs() + 2.0 ** -25).all()
