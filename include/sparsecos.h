@@ -599,7 +599,9 @@ ss_status ss_rms_norm_backward(ss_handle *h, const ss_dense *grad_y, const ss_de
 /* Activations of ss_linear: z; max(z, 0); z Phi(z) (with erf); its tanh
  * approximation; z / (1 + exp(-z)); log(1 + max(z, 0)).  In float32, whose
  * error comes before the output's one rounding: the gelu's is at most
- * (1.25 z^2 + 24) 2^-24 of its value, also for negative z (0 past -13). */
+ * (1.25 z^2 + 24) 2^-24 of its value, also for negative z (0 past -13), its
+ * approximation's and z / (1 + exp(-z))'s at most (3 a + 24) 2^-24 for an
+ * exponential of size a (values below 2^-119 may come out 0). */
 #define SS_ACT_NONE 0
 #define SS_ACT_RELU 1
 #define SS_ACT_GELU 2

@@ -85,6 +85,14 @@ __device__ __forceinline__ float normal_cdf(float z, float &e) {
   return z > 0.0f ? 1.0f - tail : tail;
 }
 
+// (1 + tanh u) / 2 with u = sqrt(2 / pi) (z + 0.044715 z^3), as 1 / (1 + exp(-2 u)):
+// 1 + tanh u itself is the difference of two values near 1 where z is negative.
+__device__ __forceinline__ float tanh_share(float z) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-z * fmaf(z * z, 0.10294324f, 2.30220818f)));  // 2 log2(e) sqrt(2 / pi) = 2.3022
+  return __fdividef(1.0f, 1.0f + e);
+}
+
 template <int kAct>
 __device__ __forceinline__ float act_of(float z) {
   if (kAct == SS_ACT_RELU) return z > 0.0f ? z : (z == z ? 0.0f : z);
@@ -92,7 +100,7 @@ __device__ __forceinline__ float act_of(float z) {
     float e;
     return z * normal_cdf(z, e);
   }
-  if (kAct == SS_ACT_GELU_TANH) return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+  if (kAct == SS_ACT_GELU_TANH) return z * tanh_share(z);
   if (kAct == SS_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));  // an IEEE quotient's slow path orders the values: 128 cycles each
   if (kAct == SS_ACT_LOG1P_RELU) return z > 0.0f ? log1pf(z) : (z == z ? 0.0f : z);
   return z;
@@ -118,8 +126,8 @@ __device__ __forceinline__ float act_slope(float z) {
   }
   if (kAct == SS_ACT_GELU_TANH) {
     if (fabsf(z) > 1e4f) return z > 0.0f ? 1.0f : 0.0f;  // where z^2 could overflow
-    const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-    return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456080286536f * (1.0f + 0.134145f * z * z);
+    const float s = tanh_share(z);
+    return s + z * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
   }
   if (kAct == SS_ACT_SILU) {
     const float s = 1.0f / (1.0f + __expf(-z));

@@ -115,3 +115,28 @@ def test_gelu_of_negative_values(h, m):
     assert ((y - want).abs() <= (room + 2.0 ** -8) * want.abs()).all()
     y, want, room = _tail_of(h, "gelu", m, torch.float16)
     assert ((y - want).abs() <= (room + 2.0 ** -11) * want.abs() + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("m", [1, 40, 600])
+@pytest.mark.parametrize("name", ["gelu_tanh", "silu"])
+def test_gelu_tanh_and_silu_of_negative_values(h, name, m):
+    y, want, room = _tail_of(h, name, m, torch.float32)
+    assert ((y - want).abs() <= (room + E) * want.abs()).all()
+    y, want, room = _tail_of(h, name, m, torch.bfloat16)
+    assert ((y - want).abs() <= (room + 2.0 ** -8) * want.abs()).all()
+    y, want, room = _tail_of(h, name, m, torch.float16)
+    assert ((y - want).abs() <= (room + 2.0 ** -11) * want.abs() + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("name", ["gelu_tanh", "silu", "gelu"])
+def test_slopes_of_large_values(h, name):
+    # grad_bias of one row is grad_y act'(pre): 0 or 1 where the activation is
+    # flat or the identity, and finite everywhere
+    z = torch.tensor([-1e38, -1e20, -3e4, -300.0, -90.0, -88.0, 88.0, 300.0, 3e4, 1e38], device="cuda").to(torch.bfloat16)
+    n = z.numel()
+    gy = torch.ones(1, n, dtype=torch.bfloat16, device="cuda")
+    x, w = torch.ones(1, 16, dtype=torch.bfloat16, device="cuda"), torch.ones(n, 16, dtype=torch.bfloat16, device="cuda")
+    _, _, gb = h.linear_backward(gy, x, w, z[None], name)
+    assert ((gb - (z > 0).float()).abs() <= 1e-30).all()
+    y = h.linear(torch.zeros(1, 16, dtype=torch.bfloat16, device="cuda"), w, bias=z.float(), activation=name, out_dtype=torch.float32)
+    assert ((y[0] - torch.relu(z.float())).abs() <= 1e-30).all()
