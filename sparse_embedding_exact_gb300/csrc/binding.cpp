@@ -281,6 +281,8 @@ PyObject *distill_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const ss_dense mg = in_place ? l.logits : dense(g, l.logits.n_rows, l.logits.n_cols, l.logits.type);
     const ss_status st = ss_distill_step(c.h, gl, &l.logits, l.scores, l.items, l.k, l.t, l.u, l.weight, loss.data_ptr<float>(),
                                          &mg, c.stream());
+    // torch's record that the logits changed (tensors of its inference mode have none)
+    if (!st && in_place && !z.is_inference()) z.unsafeGetTensorImpl()->bump_version();
     return st ? status(st) : pack({loss, g});
   });
 }

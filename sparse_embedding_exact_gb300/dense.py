@@ -1,7 +1,10 @@
 """The dense operators of a handle: norm, linear layers and distillation.
 
-Matrices are 2-D with contiguous rows (any stride between rows); vectors are
-1-D and contiguous.  Outputs are new torch tensors on the call's stream.  The
+Matrices are 2-D with contiguous rows (any stride between rows that holds one);
+vectors are 1-D and contiguous.  Outputs are new torch tensors on the call's
+stream.  The calls stand outside of torch's autograd: inputs may require
+gradients, new outputs never do, and the ``_backward`` calls and ``distill_step``
+give the gradients (``logits.backward(grad)`` hands one on to torch).  The
 formulas stand in ``include/sparsecos.h``; the marshalling is native
 (``csrc/binding.cpp``), as a short call is mostly host time.
 """
@@ -133,6 +136,6 @@ class DenseOperators:
                      temperature: float = 1.0, teacher_temperature: Optional[float] = None, in_place: bool = False,
                      stream=None):
         """(loss, grad_logits) in one launch, the logits read once.  in_place:
-        the gradient replaces the logits."""
+        the gradient replaces the logits, and torch counts them as modified."""
         u = temperature if teacher_temperature is None else teacher_temperature
         return self._run("distill_step", stream, logits, scores, items, weight, temperature, u, grad_loss, in_place)
