@@ -41,71 +41,81 @@ def _binding_source():
     return os.path.join(CSRC, "binding.cpp")
 
 
-def _inputs():
-    return sources() + [_binding_source()] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+def _newer(target, inputs) -> bool:
+    """Whether `target` exists and no input changed after it was made."""
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in inputs)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _binding_up_to_date() -> bool:
+    return _newer(BINDING, [_binding_source()] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _library_up_to_date() and _binding_up_to_date()
+
+
+def _run(cmd, what: str, verbose: bool = False):
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout + r.stderr, file=sys.stderr)
+
+
+def _link(target: str, cmd, what: str):
+    """Runs a link command, whose output replaces `target` once it is whole."""
+    tmp = f"{target}.{os.getpid()}.tmp"
+    _run([cmd[0], "-shared", "-o", tmp] + cmd[1:], what)
+    os.replace(tmp, target)
+
+
+def _compile_binding():
+    """(object, torch's library folders) of the binding."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(BUILD, "binding.o")
+    include = [INCLUDE, CSRC, sysconfig.get_paths()["include"]] + cpp_extension.include_paths("cuda")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    _run([shutil.which("g++") or "g++", "-c", _binding_source(), "-o", obj, "-O2", "-std=c++17", "-fPIC",
+          "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}"] + ["-I" + i for i in include],
+         f"g++ failed on {_binding_source()}")
+    return obj, cpp_extension.library_paths("cuda")
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
+    """Builds what is not up to date.  The library needs nvcc alone and is
+    there also where the binding, which needs torch's C++ headers, fails; that
+    is raised afterwards."""
+    library, binding = force or not _library_up_to_date(), force or not _binding_up_to_date()
+    if not (library or binding):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    cc = nvcc()
-    objs = []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc, "-c", src, "-o", obj] + ARCH + NVCC_FLAGS + list(extra_flags)
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr, file=sys.stderr)
+        _run([nvcc(), "-c", src, "-o", obj] + ARCH + NVCC_FLAGS + list(extra_flags), f"nvcc failed on {src}", verbose)
         return obj
 
-    def compile_binding():
-        import sysconfig
-
-        import torch
-        from torch.utils import cpp_extension
-
-        obj = os.path.join(BUILD, "binding.o")
-        include = [INCLUDE, CSRC, sysconfig.get_paths()["include"]] + cpp_extension.include_paths("cuda")
-        abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
-        cmd = [shutil.which("g++") or "g++", "-c", _binding_source(), "-o", obj, "-O2", "-std=c++17", "-fPIC",
-               "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}"] + ["-I" + i for i in include]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on {_binding_source()}:\n{r.stdout}\n{r.stderr}")
-        return obj, cpp_extension.library_paths("cuda")
-
     with ThreadPoolExecutor(max_workers=max(1, min(16, len(sources()) + 1))) as ex:
-        binding = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, sources()))
-        binding_obj, torch_libs = binding.result()
-    tmp = f"{LIB}.{os.getpid()}.tmp"
-    cmd = [cc, "-shared", "-o", tmp] + objs + ARCH + ["-cudart", "static", "-Xcompiler", "-fPIC"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = f"{BINDING}.{os.getpid()}.tmp"
-    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, binding_obj, "-L" + BUILD, "-lsparsecos", "-Wl,-rpath,$ORIGIN"]
-    for d in torch_libs:
-        cmd += ["-L" + d, "-Wl,-rpath," + d]
-    cmd += ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"linking {BINDING} failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+        compiled = ex.submit(_compile_binding) if binding else None
+        if library:
+            objs = list(ex.map(compile_one, sources()))
+            _link(LIB, [nvcc()] + objs + ARCH + ["-cudart", "static", "-Xcompiler", "-fPIC"], "nvcc link failed")
+    if binding:
+        obj, torch_libs = compiled.result()
+        cmd = [shutil.which("g++") or "g++", obj, "-L" + BUILD, "-lsparsecos", "-Wl,-rpath,$ORIGIN"]
+        for d in torch_libs:
+            cmd += ["-L" + d, "-Wl,-rpath," + d]
+        _link(BINDING, cmd + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], f"linking {BINDING} failed")
     return LIB
 
 
