@@ -13,6 +13,7 @@ import shutil
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -50,8 +51,24 @@ def _library_up_to_date() -> bool:
     return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _torch() -> str:
+    import torch
+
+    return str(torch.__version__)
+
+
+def binding_torch() -> Optional[str]:
+    """The version of torch that the binding was built against (its C++
+    interface changes between versions); None: there is no binding."""
+    try:
+        with open(BINDING + ".torch") as f:
+            return f.read() if os.path.exists(BINDING) else None
+    except OSError:
+        return None
+
+
 def _binding_up_to_date() -> bool:
-    return _newer(BINDING, [_binding_source()] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    return binding_torch() == _torch() and _newer(BINDING, [_binding_source()] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:
@@ -116,6 +133,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         for d in torch_libs:
             cmd += ["-L" + d, "-Wl,-rpath," + d]
         _link(BINDING, cmd + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], f"linking {BINDING} failed")
+        with open(BINDING + ".torch", "w") as f:
+            f.write(_torch())
     return LIB
 
 

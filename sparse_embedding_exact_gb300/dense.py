@@ -26,10 +26,16 @@ _native = None
 
 
 def _load():
-    """The native binding, loaded once; raises if it has not been built."""
+    """The native binding, loaded once; raises if it has not been built, or
+    not for this torch."""
     global _native
     if _native is None:
         _abi.load()
+        built_for = _build.binding_torch()
+        if built_for != str(torch.__version__):
+            state = "is not built" if built_for is None else f"was built for torch {built_for}, this is {torch.__version__}"
+            raise ImportError(f"the binding of the dense operators ({_build.BINDING}) {state}; "
+                              "run python -m sparse_embedding_exact_gb300.build")
         spec = importlib.util.spec_from_file_location("_dense_binding", _build.BINDING)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -67,3 +67,26 @@ def test_library_failure_is_raised(compilers):
     with pytest.raises(RuntimeError, match="nvcc link failed"):
         build.build()
     assert not os.path.exists(build.LIB)
+
+
+def test_binding_of_another_torch_is_rebuilt(compilers, monkeypatch):
+    build.build()
+    compilers.commands.clear()
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert not build.up_to_date()
+    build.build()
+    assert build.up_to_date() and not compilers.of(".cu") and compilers.of("binding.cpp")
+
+
+def test_binding_of_another_torch_is_not_loaded(compilers, monkeypatch):
+    from sparse_embedding_exact_gb300 import _abi, dense
+
+    build.build()
+    monkeypatch.setattr(dense, "_native", None)
+    monkeypatch.setattr(_abi, "load", lambda: None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    with pytest.raises(ImportError, match="0.0.1"):
+        dense._load()
+    os.remove(build.BINDING)
+    with pytest.raises(ImportError, match="not built"):
+        dense._load()
