@@ -107,7 +107,7 @@ __device__ __forceinline__ float2 f8_factors(float most) {
 
 // A row's scale, max|y| / 448; 0 for a row of zeros, also where eps = 0 makes
 // its rstd infinite.
-__device__ __forceinline__ float scale_of(float most, float rstd) { return most == 0.0f ? 0.0f : most * rstd / kF8Max; }
+__device__ __forceinline__ float scale_of(float most, float rstd) { return most * (most == 0.0f ? 0.0f : rstd) / kF8Max; }
 
 // A group's ring of rows in shared memory: slot s holds the current row of kRows
 // matrices.  Value c of a row lies at the same place within 16 bytes as in
