@@ -376,24 +376,33 @@ constexpr int kStepSmem = kMostChunks * kChunk + 128;
 // the whole 16-byte units [in_lo, in_hi) of the row within it.
 struct Part {
   int64_t lo, hi, in_lo, in_hi, off;
-  int chunks;  // the same for every row, the last ones perhaps empty
+  int chunks;
   __device__ __forceinline__ int bytes(int j) const {
     const int64_t left = in_hi - in_lo - (int64_t)j * kChunk;
     return (int)max((int64_t)0, min((int64_t)kChunk, left));
   }
 };
+// Bytes and chunks of a part, the same for every row (the last chunks perhaps empty).
+template <typename T>
+__device__ __forceinline__ int64_t width_of(int64_t V, int n_part) {
+  return ((V * (int64_t)sizeof(T) + 15) / 16 + 1 + n_part - 1) / n_part * 16;
+}
+template <typename T>
+__device__ __forceinline__ int chunks_of(int64_t V, int n_part) {
+  return (int)((width_of<T>(V, n_part) + kChunk - 1) / kChunk);
+}
 template <typename T>
 __device__ __forceinline__ Part part_of(const T *z, int64_t V, int part, int n_part) {
   Part p;
   p.off = (int64_t)(reinterpret_cast<uintptr_t>(z) & 15);
   const int64_t end = p.off + V * (int64_t)sizeof(T);
-  const int64_t width = ((V * (int64_t)sizeof(T) + 15) / 16 + 1 + n_part - 1) / n_part * 16;
+  const int64_t width = width_of<T>(V, n_part);
   p.lo = min(end, part * width);
   p.hi = min(end, p.lo + width);
   p.in_lo = p.lo == 0 && p.off ? 16 : p.lo;
   p.in_hi = p.hi & ~(int64_t)15;
   if (p.in_hi < p.in_lo) p.in_hi = p.in_lo;
-  p.chunks = (int)((width + kChunk - 1) / kChunk);
+  p.chunks = chunks_of<T>(V, n_part);
   return p;
 }
 
@@ -439,17 +448,24 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
   const int64_t V = a.logits.n_cols;
   const int part = (int)(blockIdx.x % n_part);
   const float c = kLog2e / a.temperature;
+  // The long part of a wait out of line for 16-bit logits (2,500 x 200,000: 374 us,
+  // 379 in line), in line for float32 (660 us, 683 out of line, where the calls
+  // spill).
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    return sizeof(T) == 4 ? tc::bar_wait_on(bar, parity, status, &stalled) : tc::bar_wait_far(bar, parity, status, &stalled);
+  };
   // Row n of this cluster (-1: no more); its list's place, and the list's
   // barriers, are those of n & 1.
   auto row_at = [&](int64_t n) {
     const int i = (int)(n & 1);
-    tc::bar_wait_on(row_full(i), (uint32_t)((n >> 1) & 1), status, &stalled);
+    wait(row_full(i), (uint32_t)((n >> 1) & 1));
     return stalled ? (int64_t)-1 : row_of[i];
   };
 
   if (warp == kStepWarps) {
     // ---- copies: each chunk as the gradient's pass of the row before leaves it
     int64_t loaded = 0;  // rows of weight other than 0 so far
+    int issued = 0;      // chunks of the last of them (lane 0)
     for (int64_t n = 0;; ++n) {
       const int64_t row = row_at(n);
       if (row < 0) break;
@@ -458,9 +474,11 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
         const Part p = part_of(z, V, part, n_part);
         if (lane == 0) {
           const unsigned char *base = reinterpret_cast<const unsigned char *>(z) - p.off;
-          for (int j = 0; j < p.chunks; ++j) {
+          for (issued = 0; issued < p.chunks; ++issued) {
+            const int j = issued;
             const uint32_t bytes = (uint32_t)p.bytes(j);
-            if (loaded > 0) tc::bar_wait_on(used(j), (uint32_t)((loaded - 1) & 1), status, &stalled);
+            // (a place that may still be read is not written over)
+            if (loaded > 0 && !wait(used(j), (uint32_t)((loaded - 1) & 1))) break;
             tc::bar_expect(full(j), bytes);
             if (bytes) tc::load_bulk(ring + (uint32_t)j * kChunk, base + p.in_lo + (int64_t)j * kChunk, bytes, full(j));
           }
@@ -470,6 +488,13 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
       __syncwarp();
       if (lane == 0) tc::bar_arrive(list_free((int)(n & 1)));
     }
+    // After a wait that ran out the copies under way may not be read by anyone:
+    // the last one of each chunk lands before the block leaves.
+    if (stalled && lane == 0)
+      for (int j = 0; j < kMostChunks; ++j) {
+        const int64_t copies = loaded - (j < issued ? 0 : 1);
+        if (copies > 0 && j < chunks_of<T>(V, n_part)) wait(full(j), (uint32_t)((copies - 1) & 1));
+      }
   } else if (warp == kStepWarps + 1) {
     // ---- rows and lists, a row ahead of their use (the list's three loads
     // depend on each other: with the copies they held them up by 5 us a row),
@@ -481,7 +506,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
     // the next one may be written over that.
     auto finish = [&](int64_t m, bool more) {
       const int i = (int)(m & 1);
-      tc::bar_wait_on(list_free(i), (uint32_t)((m >> 1) & 1), status, &stalled);
+      wait(list_free(i), (uint32_t)((m >> 1) & 1));
       if (part != 0) return;
       if (more && lane == 0 && !stalled) {
         tc::fence_async();
@@ -498,7 +523,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
       const int q = (int)(n % kAsked);
       if (lane == 0) tc::bar_expect(answered(q), 16);
       __syncwarp();
-      tc::bar_wait_on(answered(q), (uint32_t)((n / kAsked - (q == 0)) & 1), status, &stalled);
+      wait(answered(q), (uint32_t)((n / kAsked - (q == 0)) & 1));
       return tc::cluster_given(tc::smem_u32(&answers[q]));
     };
     int64_t n = 0, asked = kAsked;  // answers asked for so far, with row 0
@@ -550,7 +575,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
             tc::send_remote(tc::map_rank(tc::smem_u32(&exchange[i][part]), (uint32_t)lane), r.m, r.s,
                             tc::map_rank(met(i), (uint32_t)lane));
         }
-        tc::bar_wait_on(met(i), (uint32_t)((n >> 1) & 1), status, &stalled);
+        wait(met(i), (uint32_t)((n >> 1) & 1));
       };
       const T *z = static_cast<const T *>(a.logits.data) + row * a.logits.ld;
       T *g = static_cast<T *>(a.grad_logits.data) + row * a.grad_logits.ld;
@@ -582,8 +607,8 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
       // two chunks at a time
       const int units = (int)((p.in_hi - p.in_lo) / 16);
       for (int j = 0; j < p.chunks; j += 2) {
-        tc::bar_wait_on(full(j), parity, status, &stalled);
-        if (j + 1 < p.chunks) tc::bar_wait_on(full(j + 1), parity, status, &stalled);
+        wait(full(j), parity);
+        if (j + 1 < p.chunks) wait(full(j + 1), parity);
         Pack<T, kV> q[kU];
         if ((j + 2) * kChunkUnits <= units) {
 #pragma unroll
@@ -604,7 +629,7 @@ __global__ void __launch_bounds__(kStepThreads, 2) k_distill_step(const distill_
       if (lane == 0) warp_run[warp] = r;
       // The list is read before this block lets the others go on: with the
       // gradient in the logits' place they would write over what it reads.
-      tc::bar_wait_on(list_full(i), (uint32_t)((lists_read >> i) & 1), status, &stalled);
+      wait(list_full(i), (uint32_t)((lists_read >> i) & 1));
       lists_read ^= 1u << i;
       const List &list = lists[i];
       tc::named_sync(1, kStepWorkers);

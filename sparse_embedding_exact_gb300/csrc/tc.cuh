@@ -52,22 +52,44 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int32_t 
   }
 }
 // The same for code that must not leave its path when a wait runs out (the
-// block's other barriers count on every thread): waits until the phase
-// completes, kWaitNs pass (which flags DEV_STALL and sets *stalled) or
-// *stalled is set, and returns either way.
-__device__ __forceinline__ void bar_wait_on(uint32_t bar, uint32_t parity, int32_t *status, volatile int *stalled) {
-  if (bar_try(bar, parity)) return;
+// block's other barriers count on every thread): after kWaitNs it flags
+// DEV_STALL and sets *stalled, to the time then in units of 2^20 ns (made odd,
+// so not 0).  From then on it and the block's other waits go on for another
+// kWaitNs together, so that copies under way land before the block leaves, and
+// return whether their phases complete or not: whether they did.
+__host__ __device__ constexpr int stall_time(long long ns) { return (int)(unsigned)(ns >> 20) | 1; }
+__host__ __device__ constexpr bool stall_over(int stalled, long long ns) {
+  return (int)((unsigned)(ns >> 20) - (unsigned)stalled) > (int)(kWaitNs >> 20);
+}
+static_assert(stall_time(0) != 0 && !stall_over(stall_time(5ll << 32), 5ll << 32) &&
+                  !stall_over(stall_time(5ll << 32), (5ll << 32) + kWaitNs) &&
+                  stall_over(stall_time(5ll << 32), (5ll << 32) + kWaitNs + (3ll << 20)) &&
+                  !stall_over(stall_time((1ll << 52) - 1), (1ll << 52) + kWaitNs - (3ll << 20)) &&
+                  stall_over(stall_time((1ll << 52) - 1), (1ll << 52) + kWaitNs + (3ll << 20)),
+              "a second limit of kWaitNs from the stall on");
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, int32_t *status, volatile int *stalled) {
   const long long t0 = global_ns();
   for (;;) {
     for (int i = 0; i < 64; ++i)
-      if (bar_try(bar, parity)) return;
-    if (*stalled) return;
-    if (global_ns() - t0 > kWaitNs) {
+      if (bar_try(bar, parity)) return true;
+    const long long now = global_ns();
+    if (const int s = *stalled) {
+      if (stall_over(s, now)) return false;
+    } else if (now - t0 > kWaitNs) {
       dense::flag(status, DEV_STALL);
-      *stalled = 1;
-      return;
+      *stalled = stall_time(now);
     }
   }
+}
+__device__ __forceinline__ bool bar_wait_on(uint32_t bar, uint32_t parity, int32_t *status, volatile int *stalled) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity, status, stalled);
+}
+// The same with the long wait out of line, for a kernel of many waits.
+static __device__ __noinline__ bool bar_wait_apart(uint32_t bar, uint32_t parity, int32_t *status, volatile int *stalled) {
+  return bar_wait_long(bar, parity, status, stalled);
+}
+__device__ __forceinline__ bool bar_wait_far(uint32_t bar, uint32_t parity, int32_t *status, volatile int *stalled) {
+  return bar_try(bar, parity) || bar_wait_apart(bar, parity, status, stalled);
 }
 // The barrier `id` (1 to 15) of `threads` threads of the block.
 __device__ __forceinline__ void named_sync(int id, int threads) {
