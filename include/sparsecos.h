@@ -537,9 +537,9 @@ ss_status ss_cosine_chunk_noalloc(const ss_csr *queries, const ss_csr *items, in
 
 /*
  * Dense operators: what trains and serves a dense student of the exact top-k
- * lists (the lists of ss_topk_all are the teacher of ss_distill), and makes
- * the rows that are scored (ss_linear with SS_ACT_LOG1P_RELU is a sparse
- * embedding's head).  Common to all of them:
+ * lists (the lists of ss_topk_all are the teacher of ss_distill).  ss_linear
+ * with SS_ACT_LOG1P_RELU computes a sparse embedding's head, as dense rows;
+ * making CSR rows of them is the caller's.  Common to all of them:
  *  - A matrix is row-major in device memory: value (r, c) at data[r * ld + c],
  *    ld >= n_cols, any alignment of its rows (16-byte aligned rows run
  *    fastest), n_rows and n_cols below SS_DENSE_MAX.  A vector is a matrix of
@@ -576,8 +576,9 @@ typedef struct ss_dense {
  * residual): s rounded; may be x or residual itself.  rstd: float[n_rows] or
  * NULL.  y: x's type with scale NULL, or SS_VALUES_F8 with scale
  * float[n_rows]: then scale = max|y| / 448 of the row and y holds y / scale
- * to the nearest (a row of zeros: scale 0 and zeros).  A row that holds an
- * infinity or a NaN has NaN where the formula has.
+ * to the nearest (a row of zeros: scale 0 and zeros, for every eps).  A row
+ * that holds an infinity or a NaN has NaN where the formula has; one whose
+ * squares pass float32's range (values beyond 1e19) has rstd 0.
  */
 ss_status ss_rms_norm(ss_handle *h, const ss_dense *x, const ss_dense *residual, const ss_dense *weight, float eps,
                       const ss_dense *total, const ss_dense *y, float *scale, float *rstd, void *stream);

@@ -20,8 +20,8 @@
 // (k_distill); a step keeps it on chip between its passes (k_distill_step)
 // where 8 blocks can hold it, and reads it a second time where not.
 //
-// Measured: loss and gradient of 2,500 x 200,000 bf16 logits, top 64, 365 us
-// (5.5 TB/s, 81% of the copy bandwidth; streaming it twice 457 us).
+// Measured: loss and gradient of 2,500 x 200,000 bf16 logits, top 64, 368 us
+// (5.4 TB/s, 80% of the copy bandwidth; streaming it twice 457 us).
 #include <cooperative_groups.h>
 #include <math.h>
 

@@ -14,10 +14,10 @@
 // one tile's epilogue runs beside the next one's products.  Operands arrive by
 // tensor copies in the 128-byte swizzle through a ring of stages; one warp
 // copies, one thread issues the products, sixteen warps run the epilogue and
-// store by tensor copies.  Measured, 8192 x 4096 x 4096 bf16: 157 us alone
-// (1750 TFLOP/s, 89% of cuBLAS on the same card), 182 us with bias, gelu,
-// residual and kept pre-activation (the last tiles' epilogue and the 200 MB of
-// it); 5000 x 10000 x 2048 e4m3: 87 us.
+// store by tensor copies.  Measured, 8192 x 4096 x 4096 bf16, ten calls after a
+// pause: 159 us alone (1,730 TFLOP/s; cuBLAS on the same card 144), 202 us with
+// bias, gelu, residual and kept pre-activation (the last tiles' epilogue and the
+// 200 MB of it); 5000 x 10000 x 2048 e4m3: 87 us.
 //
 // Fewer tiles than that fills (k_product): blocks on their own with tiles of
 // 128 x kBN, the summed dimension split over a cluster of up to 8 of them
@@ -68,8 +68,8 @@ enum : int { kMajorK = 0, kMajorMN = 1 };
 // 7, over x up to 9.4, past which e is 0; with the 1/2 of Phi in it) is within
 // 8.4e-8 of it.  So Phi of a negative z is accurate relative to itself, within
 // (1.25 z^2 + 24) 2^-24, most of it the rounding of z^2.  One exponential serves
-// the gelu's slope as well; erff and expf took the gradient's pass over 8192 x
-// 4096 values from 45 to 72 us.
+// the gelu's slope as well: with erff and expf the gradient's pass over 8192 x
+// 4096 values took 72 us where this form took 45 (36 with today's loads).
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
   float t;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.304055929f, fabsf(z), 1.0f)));
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, kM == 1 ? 16 : 1) k_rows(const
 // gz = grad_y act'(pre) into gz[M][ld] (or nowhere), and the sums of its
 // columns over the block's rows into part[blockIdx.y][N] (or nowhere).  A warp
 // takes every eighth row of the block's share, two of them at a time.  Bound
-// by memory and, with a gelu, by instructions: 8192 x 4096 bf16 34 us (5.8 TB/s).
+// by memory and, with a gelu, by instructions: 8192 x 4096 bf16 36 us (5.5 TB/s).
 template <typename T, int kN, int kAct>
 __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, T *gz, int64_t ld, float *part) {
   __shared__ float sm[8][32 * kN + 1];
@@ -1087,7 +1087,8 @@ struct Cut {
 // one's products run beside it; a block on its own takes its bytes at 85 a
 // clock (128 x 256: 520 measured with rows along the sum, 610 across it), one
 // after the other with its set-up, its epilogue and, for a split sum, the
-// exchange.
+// exchange.  It is an estimate: a tile of 5000 x 10000 x 2048 e4m3 takes 14,000
+// clocks where it counts 9,600.
 Cut cut_of(const ss_handle *h, int64_t rows_a, int64_t rows_b, int64_t blocks_k, int least, bool pairs) {
   const int64_t sms = std::max(1, h->sm_count);
   auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
@@ -1180,7 +1181,8 @@ cudaError_t product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B
 }
 
 // k_rows up to this many rows: two of 1024 bf16 against 65,536 take it 32 us and
-// tiles 41, three 43 and 41; two of e4m3 26 and 20.
+// tiles 41, three 43 and 41; two of e4m3 26 and 20.  Other lengths and rows that
+// start off 16 bytes go by the same rule, unmeasured.
 int64_t few_rows_of(const ss_dense &x) { return x.type == SS_VALUES_F8 ? 1 : 2; }
 constexpr int64_t kSwapRows = 256;  // features as A is looked at up to this many rows
 

@@ -23,11 +23,11 @@
 // scratch, one row of it a block, and a second kernel adds them in a fixed
 // order: no atomics, the same bits every time.
 //
-// Measured: 16,384 x 4096 bf16 with residual to 8 bits 86 us (5.4 TB/s, 73 us
-// without the write-back of its output: memory); the gradient of 16,384 x 2048
-// bf16 59 us, of which the kernel 50 and the sums 6 (4.6 TB/s: instructions,
-// at 16 warps an SM, which its registers allow); of 5000 x 1001 float32 27 us
-// (22 and 3 to 5).
+// Measured: 16,384 x 4096 bf16 with residual to 8 bits 86 us (5.4 TB/s: memory);
+// the gradient of 16,384 x 2048 bf16 59 us, of which the kernel 50 and the sums 6
+// to 7 (4.6 TB/s: waiting, at 1.8 of 4 instructions issued a clock by 16 warps an
+// SM, which its registers allow); of 5000 x 1001 float32 27 us (22 and 5, the
+// same at 23 warps).
 #include <algorithm>
 #include <initializer_list>
 
