@@ -69,7 +69,7 @@ enum : int { kMajorK = 0, kMajorMN = 1 };
 // 8.4e-8 of it.  So Phi of a negative z is accurate relative to itself, within
 // (1.25 z^2 + 24) 2^-24, most of it the rounding of z^2.  One exponential serves
 // the gelu's slope as well: with erff and expf the gradient's pass over 8192 x
-// 4096 values took 72 us where this form took 45 (36 with today's loads).
+// 4096 values took 72 us where one exponential took 45.
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
   float t;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.304055929f, fabsf(z), 1.0f)));
