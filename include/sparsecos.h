@@ -672,6 +672,46 @@ ss_status ss_distill_step(ss_handle *h, const float *grad_loss, const ss_dense *
                           const int64_t *items, int32_t k, float temperature, float teacher_temperature,
                           const float *weight, float *loss, const ss_dense *grad_logits, void *stream);
 
+/*
+ * Softmax cross entropy over every item, without the logits.  With
+ * z = (x w^T + bias) / temperature:
+ *   loss = weight * (log sum_v exp(z_v) - z_target)
+ *   gz_v = grad_loss * weight / temperature * (softmax(z)_v - [v = target])
+ *   grad_x = gz w,  grad_w = gz^T x,  grad_bias = sum over rows of gz
+ * x: M x K rows and w: V x K items (K, V >= 1), both bfloat16 or both float16,
+ * finite (an item masked by its bias included).  bias: float[V] or NULL;
+ * -INFINITY masks an item: its softmax and gradients are 0.  targets:
+ * int64[M].  A row of a negative target, of a masked one or of weight 0 is
+ * absent: loss 0, and no part in the gradients whatever its x holds; one at
+ * or beyond V too, and the next ss_check_device reports it as
+ * SS_ERR_OUT_OF_RANGE.  weight, grad_loss: float[M] or NULL (1).
+ * Temperatures as in ss_distill.  ss_cross_entropy keeps stats (float[M][2],
+ * 8-byte aligned: the row's largest x w^T + bias, and the sum of
+ * exp((x w^T + bias - it) / temperature); INFINITY for an absent row) for
+ * ss_cross_entropy_backward, which takes the same arguments.  grad_x (M x K)
+ * and grad_w (V x K): of x's type or float32; grad_bias: float[V]; each may
+ * be NULL.  The gradients are computed in pieces of the items, a piece's gz
+ * in scratch and rounded to x's type (float16: scaled by a power of two, so
+ * that the largest |weight grad_loss / temperature| is near 2^15).
+ * A softmax below 2^-126 of the largest counts as 0.  grad_bias sums gz
+ * unrounded.  ss_cross_entropy_step gives loss and
+ * gradients in one call.  scratch: bytes of the call's _scratch.
+ */
+int64_t ss_cross_entropy_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w);
+ss_status ss_cross_entropy(ss_handle *h, const ss_dense *x, const ss_dense *w, const float *bias, const int64_t *targets,
+                           float temperature, const float *weight, float *loss, float *stats, void *scratch,
+                           int64_t scratch_bytes, void *stream);
+int64_t ss_cross_entropy_backward_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w);
+ss_status ss_cross_entropy_backward(ss_handle *h, const float *grad_loss, const ss_dense *x, const ss_dense *w,
+                                    const float *bias, const int64_t *targets, float temperature, const float *weight,
+                                    const float *stats, const ss_dense *grad_x, const ss_dense *grad_w, float *grad_bias,
+                                    void *scratch, int64_t scratch_bytes, void *stream);
+int64_t ss_cross_entropy_step_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w);
+ss_status ss_cross_entropy_step(ss_handle *h, const float *grad_loss, const ss_dense *x, const ss_dense *w, const float *bias,
+                                const int64_t *targets, float temperature, const float *weight, float *loss,
+                                const ss_dense *grad_x, const ss_dense *grad_w, float *grad_bias, void *scratch,
+                                int64_t scratch_bytes, void *stream);
+
 /* Number of kernels this handle has launched so far (every call that
  * queues kernels adds the number it queued).  Host-side count; no sync; 0
  * for a null handle. */

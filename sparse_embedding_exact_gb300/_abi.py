@@ -116,6 +116,12 @@ SIGNATURES = {
     "ss_distill": (_I32, [_P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _P, _P]),
     "ss_distill_backward": (_I32, [_P, _P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _DENSE, _P]),
     "ss_distill_step": (_I32, [_P, _P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _DENSE, _P]),
+    "ss_cross_entropy_scratch": (_I64, [_P, _DENSE, _DENSE]),
+    "ss_cross_entropy": (_I32, [_P, _DENSE, _DENSE, _P, _P, _F32, _P, _P, _P, _P, _I64, _P]),
+    "ss_cross_entropy_backward_scratch": (_I64, [_P, _DENSE, _DENSE]),
+    "ss_cross_entropy_backward": (_I32, [_P, _P, _DENSE, _DENSE, _P, _P, _F32, _P, _P, _DENSE, _DENSE, _P, _P, _I64, _P]),
+    "ss_cross_entropy_step_scratch": (_I64, [_P, _DENSE, _DENSE]),
+    "ss_cross_entropy_step": (_I32, [_P, _P, _DENSE, _DENSE, _P, _P, _F32, _P, _P, _DENSE, _DENSE, _P, _P, _I64, _P]),
     "ss_kernel_launches": (ctypes.c_uint64, [_P]),
     "ss_inject_alloc_failure": (_I64, [_I64]),
     "ss_profile_scorer": (_I32, [_P, _I32]),

@@ -287,9 +287,84 @@ PyObject *distill_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// A cross entropy's common arguments: x, w, targets, bias or None, weight or None, T.
+struct Targets {
+  ss_dense x, w;
+  const int64_t *targets;
+  const float *bias, *weight;
+  float t;
+  Targets(const Call &c, PyObject *const *a) {
+    x = c.matrix(tensor(a[0], "x"), "x");
+    w = c.matrix(tensor(a[1], "w"), "w");
+    tensor(a[2], "targets");
+    targets = static_cast<const int64_t *>(c.array(a[2], "targets", x.n_rows, -1, at::kLong));
+    bias = c.floats(a[3], "bias", w.n_rows);
+    weight = c.floats(a[4], "weight", x.n_rows);
+    t = number(a[5]);
+  }
+};
+// The gradients of x, w and bias; code: of the first two, or -1 for x's.
+struct TargetGrads {
+  Tensor x, w, bias;
+  ss_dense mx, mw;
+  TargetGrads(const Call &c, const Targets &l, const Tensor &like_x, const Tensor &like_w, bool with_bias, PyObject *of) {
+    int64_t code = PyLong_AsLongLong(of);
+    if (code < 0) code = l.x.type;
+    const at::ScalarType type = type_of(code);
+    x = c.empty(like_x.sizes(), type);
+    w = c.empty(like_w.sizes(), type);
+    if (with_bias) bias = c.empty({l.w.n_rows}, at::kFloat);
+    mx = dense(x, l.x.n_rows, l.x.n_cols, (int32_t)code);
+    mw = dense(w, l.w.n_rows, l.w.n_cols, (int32_t)code);
+  }
+  float *sums() const { return bias.defined() ? bias.data_ptr<float>() : nullptr; }
+};
+
+// (handle, device, targets) -> loss, stats
+PyObject *cross_entropy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<8>(a, n, [&](Call c) -> PyObject * {
+    const Targets l(c, a + 2);
+    const Tensor loss = c.empty({l.x.n_rows}, at::kFloat), stats = c.empty({l.x.n_rows, 2}, at::kFloat);
+    const Tensor room = c.scratch(ss_cross_entropy_scratch(c.h, &l.x, &l.w));
+    const ss_status st = ss_cross_entropy(c.h, &l.x, &l.w, l.bias, l.targets, l.t, l.weight, loss.data_ptr<float>(),
+                                          stats.data_ptr<float>(), at_of(room), size_of(room), c.stream());
+    return st ? status(st) : pack({loss, stats});
+  });
+}
+
+// (handle, device, targets, grad_loss or None, stats, type of the gradients or -1) -> grad_x, grad_w, grad_bias or None
+PyObject *cross_entropy_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<11>(a, n, [&](Call c) -> PyObject * {
+    const Targets l(c, a + 2);
+    const float *gl = c.floats(a[8], "grad_loss", l.x.n_rows);
+    tensor(a[9], "stats");
+    const float *stats = c.floats(a[9], "stats", l.x.n_rows, 2);
+    const TargetGrads g(c, l, tensor(a[2], "x"), tensor(a[3], "w"), l.bias, a[10]);
+    const Tensor room = c.scratch(ss_cross_entropy_backward_scratch(c.h, &l.x, &l.w));
+    const ss_status st = ss_cross_entropy_backward(c.h, gl, &l.x, &l.w, l.bias, l.targets, l.t, l.weight, stats, &g.mx, &g.mw,
+                                                   g.sums(), at_of(room), size_of(room), c.stream());
+    return st ? status(st) : pack({g.x, g.w, g.bias});
+  });
+}
+
+// (handle, device, targets, grad_loss or None, type of the gradients or -1) -> loss, grad_x, grad_w, grad_bias or None
+PyObject *cross_entropy_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<10>(a, n, [&](Call c) -> PyObject * {
+    const Targets l(c, a + 2);
+    const float *gl = c.floats(a[8], "grad_loss", l.x.n_rows);
+    const Tensor loss = c.empty({l.x.n_rows}, at::kFloat);
+    const TargetGrads g(c, l, tensor(a[2], "x"), tensor(a[3], "w"), l.bias, a[9]);
+    const Tensor room = c.scratch(ss_cross_entropy_step_scratch(c.h, &l.x, &l.w));
+    const ss_status st = ss_cross_entropy_step(c.h, gl, &l.x, &l.w, l.bias, l.targets, l.t, l.weight, loss.data_ptr<float>(), &g.mx,
+                                               &g.mw, g.sums(), at_of(room), size_of(room), c.stream());
+    return st ? status(st) : pack({loss, g.x, g.w, g.bias});
+  });
+}
+
 #define SS_CALL(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SS_CALL(norm),    SS_CALL(norm_backward),    SS_CALL(linear),       SS_CALL(linear_backward),
-                         SS_CALL(distill), SS_CALL(distill_backward), SS_CALL(distill_step), {nullptr, nullptr, 0, nullptr}};
+                         SS_CALL(distill), SS_CALL(distill_backward), SS_CALL(distill_step),
+                         SS_CALL(cross_entropy), SS_CALL(cross_entropy_backward), SS_CALL(cross_entropy_step), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dense_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

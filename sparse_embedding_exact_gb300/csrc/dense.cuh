@@ -264,3 +264,29 @@ struct linear_grad_args {
 int64_t linear_grad_scratch(const ss_handle *h, const ss_dense &grad_y, const ss_dense &x, const ss_dense &w,
                             int32_t activation);
 cudaError_t launch_linear_grad(ss_handle *h, const linear_grad_args &a, cudaStream_t s, int *queued);
+
+// Each matrix itself, or its copy with padded rows at *scratch (advanced past
+// it, copy_bytes of each); `other` may be null.
+cudaError_t launch_aligned_rows(ss_handle *h, ss_dense *m, ss_dense *other, unsigned char **scratch, cudaStream_t s, int *queued);
+
+// y = factor A B + plus over the summed dimension; A and B are [rows][summed]
+// (kMajorK) or [summed][rows] (kMajorMN), 16-bit, their rows aligned.  plus: or
+// null data; float32 or y's type, and may be y.  factor: device float or null.
+cudaError_t launch_product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B, int majB, const ss_dense &y,
+                           const ss_dense &plus, const float *factor, cudaStream_t s, int *queued);
+
+struct xent_args {
+  ss_dense x, w, grad_x, grad_w;  // grad_x, grad_w: or null
+  const float *bias;              // [items] or null
+  const int64_t *targets;         // [rows]
+  const float *weight;            // [rows] or null: 1
+  const float *grad_loss;         // [rows] or null: 1
+  float *loss;                    // [rows]
+  float *stats;                   // [rows][2]: {largest logit, sum of exp((logit - it) / T)}
+  float *grad_bias;               // [items] or null
+  float temperature;
+  unsigned char *scratch;  // xent_scratch bytes
+};
+enum : int32_t { XENT_LOSS = 0, XENT_BACKWARD = 1, XENT_STEP = 2 };
+int64_t xent_scratch(const ss_handle *h, const ss_dense &x, const ss_dense &w, int32_t mode);
+cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStream_t s, int *queued);

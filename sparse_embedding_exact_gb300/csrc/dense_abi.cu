@@ -306,4 +306,89 @@ ss_status ss_distill_step(ss_handle *h, const float *grad_loss, const ss_dense *
   return run_distill(h, a, DISTILL_STEP, stream);
 }
 
+static ss_status check_xent(ss_handle *h, const ss_dense *x, const ss_dense *w, const int64_t *targets, float temperature,
+                            const char *call) {
+  if (!x || !w) return report(h, SS_ERR_INVALID_ARG, "%s: null %s", call, x ? "w" : "x");
+  SS_TRY(check(h, x, x->n_rows, x->n_cols, HALVES, call, "x"));
+  SS_TRY(check(h, w, w->n_rows, x->n_cols, HALVES, call, "w"));
+  SS_TRY(same_type(h, w, x->type, call, "w"));
+  if (x->n_cols < 1) return report(h, SS_ERR_INVALID_ARG, "%s: rows of no columns", call);
+  if (w->n_rows < 1) return report(h, SS_ERR_INVALID_ARG, "%s: no items", call);
+  if (x->n_rows > 0 && !targets) return report(h, SS_ERR_INVALID_ARG, "%s: null targets", call);
+  if (!(temperature >= SS_DISTILL_TEMPERATURE_MIN) || !(temperature <= 1.0f / SS_DISTILL_TEMPERATURE_MIN))
+    return report(h, SS_ERR_INVALID_ARG, "%s: temperature %g outside [%g, %g]", call, (double)temperature,
+                  (double)SS_DISTILL_TEMPERATURE_MIN, 1.0 / (double)SS_DISTILL_TEMPERATURE_MIN);
+  return SS_OK;
+}
+
+static ss_status run_xent(ss_handle *h, xent_args &a, int32_t mode, void *scratch, int64_t scratch_bytes, void *stream, const char *call) {
+  for (const ss_dense *g : {&a.grad_x, &a.grad_w}) {
+    if (!g->data && g->type == 0 && g->n_rows == 0) continue;
+    const char *name = g == &a.grad_x ? "grad_x" : "grad_w";
+    SS_TRY(check(h, g, g == &a.grad_x ? a.x.n_rows : a.w.n_rows, a.x.n_cols, F32 | HALVES, call, name));
+    if (g->type != SS_VALUES_F32) SS_TRY(same_type(h, g, a.x.type, call, name));
+  }
+  SS_TRY(check_scratch(h, scratch, scratch_bytes, xent_scratch(h, a.x, a.w, mode), call));
+  a.scratch = static_cast<unsigned char *>(scratch);
+  SS_RUN(h, cudaSetDevice(h->device));
+  int queued = 0;
+  SS_RUN(h, launch_xent(h, a, mode, as_stream(stream), &queued));
+  h->launches += queued;
+  return SS_OK;
+}
+
+static int64_t scratch_of_xent(const ss_handle *h, const ss_dense *x, const ss_dense *w, int32_t mode) {
+  const bool ok = h && x && w && x->n_rows >= 0 && x->n_rows < SS_DENSE_MAX && x->n_cols > 0 && x->n_cols < SS_DENSE_MAX &&
+                  w->n_rows > 0 && w->n_rows < SS_DENSE_MAX;
+  return ok ? xent_scratch(h, *x, *w, mode) : 0;
+}
+int64_t ss_cross_entropy_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w) {
+  return scratch_of_xent(h, x, w, XENT_LOSS);
+}
+int64_t ss_cross_entropy_backward_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w) {
+  return scratch_of_xent(h, x, w, XENT_BACKWARD);
+}
+int64_t ss_cross_entropy_step_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w) {
+  return scratch_of_xent(h, x, w, XENT_STEP);
+}
+
+ss_status ss_cross_entropy(ss_handle *h, const ss_dense *x, const ss_dense *w, const float *bias, const int64_t *targets,
+                           float temperature, const float *weight, float *loss, float *stats, void *scratch,
+                           int64_t scratch_bytes, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_cross_entropy";
+  SS_TRY(check_xent(h, x, w, targets, temperature, call));
+  if (x->n_rows > 0 && (!loss || !stats)) return report(h, SS_ERR_INVALID_ARG, "%s: null output", call);
+  if (reinterpret_cast<uintptr_t>(stats) % 8) return report(h, SS_ERR_INVALID_ARG, "%s: stats are not aligned to 8 bytes", call);
+  xent_args a = {*x, *w, {}, {}, bias, targets, weight, nullptr, loss, stats, nullptr, temperature, nullptr};
+  return run_xent(h, a, XENT_LOSS, scratch, scratch_bytes, stream, call);
+}
+
+ss_status ss_cross_entropy_backward(ss_handle *h, const float *grad_loss, const ss_dense *x, const ss_dense *w,
+                                    const float *bias, const int64_t *targets, float temperature, const float *weight,
+                                    const float *stats, const ss_dense *grad_x, const ss_dense *grad_w, float *grad_bias,
+                                    void *scratch, int64_t scratch_bytes, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_cross_entropy_backward";
+  SS_TRY(check_xent(h, x, w, targets, temperature, call));
+  if (x->n_rows > 0 && !stats) return report(h, SS_ERR_INVALID_ARG, "%s: null stats", call);
+  if (reinterpret_cast<uintptr_t>(stats) % 8) return report(h, SS_ERR_INVALID_ARG, "%s: stats are not aligned to 8 bytes", call);
+  xent_args a = {*x,        *w,      or_none(grad_x),             or_none(grad_w), bias,        targets, weight,
+                 grad_loss, nullptr, const_cast<float *>(stats), grad_bias,       temperature, nullptr};
+  return run_xent(h, a, XENT_BACKWARD, scratch, scratch_bytes, stream, call);
+}
+
+ss_status ss_cross_entropy_step(ss_handle *h, const float *grad_loss, const ss_dense *x, const ss_dense *w, const float *bias,
+                                const int64_t *targets, float temperature, const float *weight, float *loss,
+                                const ss_dense *grad_x, const ss_dense *grad_w, float *grad_bias, void *scratch,
+                                int64_t scratch_bytes, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_cross_entropy_step";
+  SS_TRY(check_xent(h, x, w, targets, temperature, call));
+  if (x->n_rows > 0 && !loss) return report(h, SS_ERR_INVALID_ARG, "%s: null loss", call);
+  xent_args a = {*x,        *w,   or_none(grad_x), or_none(grad_w), bias,        targets, weight,
+                 grad_loss, loss, nullptr,         grad_bias,       temperature, nullptr};
+  return run_xent(h, a, XENT_STEP, scratch, scratch_bytes, stream, call);
+}
+
 }  // extern "C"

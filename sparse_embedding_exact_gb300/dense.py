@@ -1,4 +1,5 @@
-"""The dense operators of a handle: norm, linear layers and distillation.
+"""The dense operators of a handle: norm, linear layers, distillation and cross
+entropy.
 
 Matrices are 2-D with contiguous rows (any stride between rows that holds one);
 vectors are 1-D and contiguous.  Outputs are new torch tensors on the call's
@@ -145,3 +146,33 @@ class DenseOperators:
         the gradient replaces the logits, and torch counts them as modified."""
         u = temperature if teacher_temperature is None else teacher_temperature
         return self._run("distill_step", stream, logits, scores, items, weight, temperature, u, grad_loss, in_place)
+
+    # -- cross entropy over every item
+    def cross_entropy(self, x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                      bias: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                      temperature: float = 1.0, stream=None):
+        """(loss, stats): per row weight * -log softmax((x w^T + bias) / T) at
+        its target, over every item, without the logits; x (M, K) and w (V, K)
+        in bfloat16 or float16, targets int64 (M,).  A row of a negative
+        target, of one whose bias is -inf, or of weight 0 has loss 0; a target
+        past the last item too, and ``check_device`` reports it.  stats are
+        what ``cross_entropy_backward`` takes."""
+        return self._run("cross_entropy", stream, x, w, targets, bias, weight, temperature)
+
+    def cross_entropy_backward(self, grad_loss: Optional[torch.Tensor], x: torch.Tensor, w: torch.Tensor,
+                               targets: torch.Tensor, stats: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                               weight: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                               grad_dtype: Optional[torch.dtype] = None, stream=None):
+        """(grad_x, grad_w, grad_bias); grad_loss: float32 of each row's loss
+        (None: 1).  grad_dtype: of grad_x and grad_w, x's type or float32;
+        grad_bias is float32 (None without a bias)."""
+        return self._run("cross_entropy_backward", stream, x, w, targets, bias, weight, temperature, grad_loss, stats,
+                         _type(grad_dtype))
+
+    def cross_entropy_step(self, x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                           grad_loss: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                           weight: Optional[torch.Tensor] = None, temperature: float = 1.0,
+                           grad_dtype: Optional[torch.dtype] = None, stream=None):
+        """(loss, grad_x, grad_w, grad_bias) in one call."""
+        return self._run("cross_entropy_step", stream, x, w, targets, bias, weight, temperature, grad_loss,
+                         _type(grad_dtype))
