@@ -673,6 +673,58 @@ ss_status ss_distill_step(ss_handle *h, const float *grad_loss, const ss_dense *
                           const float *weight, float *loss, const ss_dense *grad_logits, void *stream);
 
 /*
+ * Activations kept in 8 bits for the gradients: e4m3 codes, and a power of two
+ * for every SS_KEPT_GROUP values of a row (the last group may be shorter).
+ *   e = the smallest with max|x| <= 448 * 2^e over the group's finite values,
+ *       at least -126 (float32), -124 (bfloat16) or -15 (float16)
+ *   code = x * 2^-e to the nearest,  value = code * 2^e
+ * and scale holds e + 127 as a byte (an exponent-only 8-bit float: 255 is NaN).
+ * A value is off by at most 2^-4 of itself, or 2^(e - 10); one of 16 bits is
+ * exact in its type (beyond the type's largest: that).  An infinity or a NaN
+ * becomes NaN and leaves the others of its group as they are.
+ */
+#define SS_KEPT_GROUP 32
+typedef struct ss_kept {
+  void *codes;      /* n_rows x n_cols bytes; code (r, c) at r * ld + c */
+  uint8_t *scale;   /* n_rows x ceil(n_cols / 32) bytes; group g of row r at r * ld_scale + g */
+  int64_t n_rows;
+  int64_t n_cols;
+  int64_t ld;       /* >= n_cols; multiples of 16 run fastest */
+  int64_t ld_scale;
+} ss_kept;
+
+/* x (float32, bfloat16 or float16) to codes and scales, and their values to y
+ * (of any of the three; to the nearest, beyond its largest to that). */
+ss_status ss_compress(ss_handle *h, const ss_dense *x, const ss_kept *out, void *stream);
+ss_status ss_expand(ss_handle *h, const ss_kept *x, const ss_dense *y, void *stream);
+
+/* ss_linear with its z kept in 8 bits in pre's place (z unrounded; the least
+ * exponent is that of y's type).  K >= 1.  scratch: ss_linear_keep_scratch
+ * bytes. */
+int64_t ss_linear_keep_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w);
+ss_status ss_linear_keep(ss_handle *h, const ss_dense *x, const float *x_scale, const ss_dense *w, const float *w_scale,
+                         const float *bias, int32_t activation, const ss_dense *residual, const ss_kept *pre,
+                         const ss_dense *y, void *scratch, int64_t scratch_bytes, void *stream);
+
+/* ss_linear_backward from kept values: of x and x_kept one is given, and of
+ * pre and pre_kept one (none for SS_ACT_NONE).  x's values enter the product
+ * rounded to w's type (values of that type are exact).  scratch:
+ * ss_linear_kept_backward_scratch bytes. */
+int64_t ss_linear_kept_backward_scratch(const ss_handle *h, const ss_dense *grad_y, const ss_dense *w, int32_t activation);
+ss_status ss_linear_kept_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_kept *x_kept,
+                                  const ss_dense *w, const ss_dense *pre, const ss_kept *pre_kept, int32_t activation,
+                                  const ss_dense *grad_x, const ss_dense *grad_w, float *grad_bias, void *scratch,
+                                  int64_t scratch_bytes, void *stream);
+
+/* ss_rms_norm_backward from the kept total; grad_y, grad_total and grad_x of
+ * one type, to which total's values are rounded.  scratch:
+ * ss_rms_norm_kept_backward_scratch bytes. */
+int64_t ss_rms_norm_kept_backward_scratch(const ss_handle *h, int64_t n_rows, int64_t n_cols, int32_t type);
+ss_status ss_rms_norm_kept_backward(ss_handle *h, const ss_dense *grad_y, const ss_kept *total, const ss_dense *weight,
+                                    const float *rstd, const ss_dense *grad_total, const ss_dense *grad_x,
+                                    const ss_dense *grad_weight, void *scratch, int64_t scratch_bytes, void *stream);
+
+/*
  * Softmax cross entropy over every item, without the logits.  With
  * z = (x w^T + bias) / temperature:
  *   loss = weight * (log sum_v exp(z_v) - z_target)

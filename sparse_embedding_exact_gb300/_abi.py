@@ -68,6 +68,17 @@ class ss_dense(ctypes.Structure):
     ]
 
 
+class ss_kept(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int64),
+        ("n_cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("ld_scale", ctypes.c_int64),
+    ]
+
+
 ss_chunk_consumer = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                      ctypes.c_int64, ctypes.POINTER(ctypes.c_float), ctypes.c_int64,
                                      ctypes.c_int64)
@@ -75,6 +86,7 @@ ss_chunk_consumer = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_int
 _P = ctypes.c_void_p
 _CSR = ctypes.POINTER(ss_csr)
 _DENSE = _P  # ss_dense *: the address of a record
+_KEPT = _P  # ss_kept *
 _F32 = ctypes.c_float
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -116,6 +128,14 @@ SIGNATURES = {
     "ss_distill": (_I32, [_P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _P, _P]),
     "ss_distill_backward": (_I32, [_P, _P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _DENSE, _P]),
     "ss_distill_step": (_I32, [_P, _P, _DENSE, _P, _P, _I32, _F32, _F32, _P, _P, _DENSE, _P]),
+    "ss_compress": (_I32, [_P, _DENSE, _KEPT, _P]),
+    "ss_expand": (_I32, [_P, _KEPT, _DENSE, _P]),
+    "ss_linear_keep_scratch": (_I64, [_P, _DENSE, _DENSE]),
+    "ss_linear_keep": (_I32, [_P, _DENSE, _P, _DENSE, _P, _P, _I32, _DENSE, _KEPT, _DENSE, _P, _I64, _P]),
+    "ss_linear_kept_backward_scratch": (_I64, [_P, _DENSE, _DENSE, _I32]),
+    "ss_linear_kept_backward": (_I32, [_P, _DENSE, _DENSE, _KEPT, _DENSE, _DENSE, _KEPT, _I32, _DENSE, _DENSE, _P, _P, _I64, _P]),
+    "ss_rms_norm_kept_backward_scratch": (_I64, [_P, _I64, _I64, _I32]),
+    "ss_rms_norm_kept_backward": (_I32, [_P, _DENSE, _KEPT, _DENSE, _P, _DENSE, _DENSE, _DENSE, _P, _I64, _P]),
     "ss_cross_entropy_scratch": (_I64, [_P, _DENSE, _DENSE]),
     "ss_cross_entropy": (_I32, [_P, _DENSE, _DENSE, _P, _P, _F32, _P, _P, _P, _P, _I64, _P]),
     "ss_cross_entropy_backward_scratch": (_I64, [_P, _DENSE, _DENSE]),

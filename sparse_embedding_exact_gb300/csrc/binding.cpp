@@ -87,6 +87,23 @@ struct Call {
       throw Refused{PyExc_ValueError, std::string(name) + ": the values of a row must be contiguous"};
     return {t.data_ptr(), rows, cols, rows > 1 ? t.stride(0) : cols, code};
   }
+  // Values kept in 8 bits: codes (a matrix of e4m3) and their scales (one
+  // exponent-only byte for every 32 of a row).
+  ss_kept kept(const Tensor &codes, PyObject *s, const char *name) const {
+    const ss_dense m = matrix(codes, name);
+    const std::string what = std::string(name) + "_scale";
+    if (m.type != SS_VALUES_F8)
+      throw Refused{PyExc_TypeError, std::string(name) + " has type " + at::toString(codes.scalar_type()) + ", with scales it is Float8_e4m3fn"};
+    const Tensor &t = tensor(s, what.c_str());
+    here(t, what.c_str());
+    if (t.scalar_type() != at::kFloat8_e8m0fnu)
+      throw Refused{PyExc_TypeError, what + " has type " + at::toString(t.scalar_type()) + ", expected Float8_e8m0fnu"};
+    const int64_t groups = (m.n_cols + SS_KEPT_GROUP - 1) / SS_KEPT_GROUP, d = t.dim();
+    if (d != codes.dim() || (d == 2 && t.size(0) != m.n_rows) || t.size(d - 1) != groups || (groups > 1 && t.stride(d - 1) != 1))
+      throw Refused{PyExc_ValueError, what + ": expected " + std::to_string(groups) + " contiguous scales a row for " +
+                                          std::to_string(m.n_rows) + " rows"};
+    return {m.data, static_cast<uint8_t *>(t.data_ptr()), m.n_rows, m.n_cols, m.ld, m.n_rows > 1 ? t.stride(0) : groups};
+  }
   // The address of a contiguous array of the given shape and type, or null.
   void *array(PyObject *o, const char *name, int64_t rows, int64_t cols, at::ScalarType type) const {
     if (o == Py_None) return nullptr;
@@ -139,6 +156,48 @@ PyObject *guarded(PyObject *const *a, Py_ssize_t n, Body body) {
 }
 PyObject *status(ss_status st) { return PyLong_FromLong(st); }
 
+// Room for the values of a matrix kept in 8 bits: codes in rows that start on
+// 16-byte boundaries, and their scales.
+struct Codes {
+  Tensor codes, scale;
+  ss_kept m;
+  Codes(const Call &c, int64_t rows, int64_t cols, bool vector) {
+    const int64_t ld = (cols + 15) / 16 * 16, groups = (cols + SS_KEPT_GROUP - 1) / SS_KEPT_GROUP;
+    codes = c.empty({rows, ld}, at::kFloat8_e4m3fn);
+    if (ld != cols) codes = codes.narrow(1, 0, cols);
+    scale = c.empty({rows, groups}, at::kFloat8_e8m0fnu);
+    m = {codes.data_ptr(), static_cast<uint8_t *>(scale.data_ptr()), rows, cols, ld, groups};
+    if (vector) {
+      codes = codes.select(0, 0);
+      scale = scale.select(0, 0);
+    }
+  }
+};
+
+// (handle, device, x) -> codes, scale
+PyObject *compress(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<3>(a, n, [&](Call c) -> PyObject * {
+    const Tensor &x = tensor(a[2], "x");
+    const ss_dense mx = c.matrix(x, "x");
+    const Codes out(c, mx.n_rows, mx.n_cols, x.dim() == 1);
+    const ss_status st = ss_compress(c.h, &mx, &out.m, c.stream());
+    return st ? status(st) : pack({out.codes, out.scale});
+  });
+}
+
+// (handle, device, codes, scale, type) -> values
+PyObject *expand(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded<5>(a, n, [&](Call c) -> PyObject * {
+    const Tensor &codes = tensor(a[2], "codes");
+    const ss_kept m = c.kept(codes, a[3], "codes");
+    const int64_t code = PyLong_AsLongLong(a[4]);
+    const Tensor y = c.empty(codes.sizes(), type_of(code));
+    const ss_dense my = dense(y, m.n_rows, m.n_cols, (int32_t)code);
+    const ss_status st = ss_expand(c.h, &m, &my, c.stream());
+    return st ? status(st) : THPVariable_Wrap(y);
+  });
+}
+
 // (handle, device, x, weight, residual or None, eps, 8 bits) -> y, total, factor
 PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded<7>(a, n, [&](Call c) -> PyObject * {
@@ -161,24 +220,36 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// (handle, device, grad_y, total, weight, rstd, grad_total or None) -> grad_x, grad_weight
+// (handle, device, grad_y, total, weight, rstd, grad_total or None, total's scales or None) -> grad_x, grad_weight
 PyObject *norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded<7>(a, n, [&](Call c) -> PyObject * {
-    const Tensor &total = tensor(a[3], "total"), &weight = tensor(a[4], "weight");
-    const ss_dense mg = c.matrix(tensor(a[2], "grad_y"), "grad_y"), mt = c.matrix(total, "total"), mw = c.matrix(weight, "weight");
+  return guarded<8>(a, n, [&](Call c) -> PyObject * {
+    const Tensor &gy = tensor(a[2], "grad_y"), &total = tensor(a[3], "total"), &weight = tensor(a[4], "weight");
+    const bool kept = a[7] != Py_None;
+    const ss_dense mg = c.matrix(gy, "grad_y"), mw = c.matrix(weight, "weight");
+    ss_kept mk = {};
+    ss_dense mt;
+    if (kept) {
+      mk = c.kept(total, a[7], "total");
+      mt = {nullptr, mk.n_rows, mk.n_cols, mk.n_cols, mg.type};
+    } else {
+      mt = c.matrix(total, "total");
+    }
     const float *rstd = c.floats(a[5], "rstd", mt.n_rows);
     ss_dense mp = {};
     if (a[6] != Py_None) mp = c.matrix(tensor(a[6], "grad_total"), "grad_total");
-    const Tensor gx = c.empty(total.sizes(), total.scalar_type()), gw = c.empty(weight.sizes(), weight.scalar_type());
-    const Tensor room = c.scratch(ss_rms_norm_backward_scratch(c.h, mt.n_rows, mt.n_cols));
+    const ss_dense *past = a[6] != Py_None ? &mp : nullptr;
+    const Tensor gx = c.empty(total.sizes(), (kept ? gy : total).scalar_type()), gw = c.empty(weight.sizes(), weight.scalar_type());
+    const Tensor room = c.scratch(kept ? ss_rms_norm_kept_backward_scratch(c.h, mt.n_rows, mt.n_cols, mt.type)
+                                       : ss_rms_norm_backward_scratch(c.h, mt.n_rows, mt.n_cols));
     const ss_dense mx = dense(gx, mt.n_rows, mt.n_cols, mt.type), mv = dense(gw, mw.n_rows, mw.n_cols, mw.type);
-    const ss_status st = ss_rms_norm_backward(c.h, &mg, &mt, &mw, rstd, a[6] != Py_None ? &mp : nullptr, &mx, &mv, at_of(room),
-                                              size_of(room), c.stream());
+    const ss_status st = kept ? ss_rms_norm_kept_backward(c.h, &mg, &mk, &mw, rstd, past, &mx, &mv, at_of(room), size_of(room), c.stream())
+                              : ss_rms_norm_backward(c.h, &mg, &mt, &mw, rstd, past, &mx, &mv, at_of(room), size_of(room), c.stream());
     return st ? status(st) : pack({gx, gw});
   });
 }
 
-// (handle, device, x, w, bias, activation, residual, x_scale, w_scale, type of y or -1, keep pre) -> y, or y and pre
+// (handle, device, x, w, bias, activation, residual, x_scale, w_scale, type of y or -1, keep pre: 0, 1 or 2 in 8 bits)
+// -> y; y and pre; or y, pre and its scales
 PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded<11>(a, n, [&](Call c) -> PyObject * {
     const ss_dense mx = c.matrix(tensor(a[2], "x"), "x"), mw = c.matrix(tensor(a[3], "w"), "w");
@@ -187,40 +258,65 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (code < 0) code = mx.type == SS_VALUES_F8 ? SS_VALUES_BF16 : mx.type;
     const at::ScalarType out = type_of(code);
     const float *bias = c.floats(a[4], "bias", N), *sx = c.floats(a[7], "x_scale", M), *sw = c.floats(a[8], "w_scale", N);
-    const bool sum = a[6] != Py_None, keep = PyObject_IsTrue(a[10]) == 1;
+    const long keep = PyLong_AsLong(a[10]);
+    const bool sum = a[6] != Py_None;
     ss_dense mr = {}, mp = {};
     if (sum) mr = c.matrix(tensor(a[6], "residual"), "residual");
     const Tensor y = c.empty({M, N}, out);
+    const ss_dense my = dense(y, M, N, (int32_t)code);
+    const int32_t act = (int32_t)PyLong_AsLong(a[5]);
+    if (keep == 2) {
+      const Codes pre(c, M, N, false);
+      const Tensor room = c.scratch(ss_linear_keep_scratch(c.h, &mx, &mw));
+      const ss_status st = ss_linear_keep(c.h, &mx, sx, &mw, sw, bias, act, sum ? &mr : nullptr, &pre.m, &my, at_of(room),
+                                          size_of(room), c.stream());
+      return st ? status(st) : pack({y, pre.codes, pre.scale});
+    }
     Tensor pre;
     if (keep) {
       pre = c.empty({M, N}, out);
       mp = dense(pre, M, N, (int32_t)code);
     }
-    const ss_dense my = dense(y, M, N, (int32_t)code);
     const Tensor room = c.scratch(ss_linear_scratch(c.h, &mx, &mw));
-    const ss_status st = ss_linear(c.h, &mx, sx, &mw, sw, bias, (int32_t)PyLong_AsLong(a[5]), sum ? &mr : nullptr,
+    const ss_status st = ss_linear(c.h, &mx, sx, &mw, sw, bias, act, sum ? &mr : nullptr,
                                    keep ? &mp : nullptr, &my, at_of(room), size_of(room), c.stream());
     if (st) return status(st);
     return keep ? pack({y, pre}) : THPVariable_Wrap(y);
   });
 }
 
-// (handle, device, grad_y, x, w, pre or None, activation, type of the gradients or -1) -> grad_x, grad_w, grad_bias
+// (handle, device, grad_y, x, w, pre or None, activation, type of the gradients or -1, x's scales or None, pre's or None)
+// -> grad_x, grad_w, grad_bias
 PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return guarded<8>(a, n, [&](Call c) -> PyObject * {
+  return guarded<10>(a, n, [&](Call c) -> PyObject * {
     const Tensor &x = tensor(a[3], "x"), &w = tensor(a[4], "w");
-    const ss_dense mg = c.matrix(tensor(a[2], "grad_y"), "grad_y"), mx = c.matrix(x, "x"), mw = c.matrix(w, "w");
-    ss_dense mp = {};
-    if (a[5] != Py_None) mp = c.matrix(tensor(a[5], "pre"), "pre");
+    const bool x_kept = a[8] != Py_None, pre_kept = a[9] != Py_None, kept = x_kept || pre_kept;
+    const ss_dense mg = c.matrix(tensor(a[2], "grad_y"), "grad_y"), mw = c.matrix(w, "w");
+    ss_kept kx = {}, kp = {};
+    ss_dense mx = {}, mp = {};
+    if (x_kept) {
+      kx = c.kept(x, a[8], "x");
+      mx = {nullptr, kx.n_rows, kx.n_cols, kx.n_cols, mw.type};
+    } else {
+      mx = c.matrix(x, "x");
+    }
+    if (pre_kept)
+      kp = c.kept(tensor(a[5], "pre"), a[9], "pre");
+    else if (a[5] != Py_None)
+      mp = c.matrix(tensor(a[5], "pre"), "pre");
+    const ss_dense *pre = a[5] != Py_None && !pre_kept ? &mp : nullptr;
     const int32_t act = (int32_t)PyLong_AsLong(a[6]);
     int64_t code = PyLong_AsLongLong(a[7]);
     if (code < 0) code = mx.type;
     const at::ScalarType type = type_of(code);
     const Tensor gx = c.empty(x.sizes(), type), gw = c.empty(w.sizes(), type), gb = c.empty({mw.n_rows}, at::kFloat);
-    const Tensor room = c.scratch(ss_linear_backward_scratch(c.h, &mg, &mx, &mw, act));
+    const Tensor room = c.scratch(kept ? ss_linear_kept_backward_scratch(c.h, &mg, &mw, act)
+                                       : ss_linear_backward_scratch(c.h, &mg, &mx, &mw, act));
     const ss_dense mgx = dense(gx, mx.n_rows, mx.n_cols, (int32_t)code), mgw = dense(gw, mw.n_rows, mw.n_cols, (int32_t)code);
-    const ss_status st = ss_linear_backward(c.h, &mg, &mx, &mw, a[5] != Py_None ? &mp : nullptr, act, &mgx, &mgw,
-                                            gb.data_ptr<float>(), at_of(room), size_of(room), c.stream());
+    const ss_status st =
+        kept ? ss_linear_kept_backward(c.h, &mg, x_kept ? nullptr : &mx, x_kept ? &kx : nullptr, &mw, pre, pre_kept ? &kp : nullptr, act,
+                                       &mgx, &mgw, gb.data_ptr<float>(), at_of(room), size_of(room), c.stream())
+             : ss_linear_backward(c.h, &mg, &mx, &mw, pre, act, &mgx, &mgw, gb.data_ptr<float>(), at_of(room), size_of(room), c.stream());
     return st ? status(st) : pack({gx, gw, gb});
   });
 }
@@ -364,7 +460,7 @@ PyObject *cross_entropy_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define SS_CALL(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SS_CALL(norm),    SS_CALL(norm_backward),    SS_CALL(linear),       SS_CALL(linear_backward),
                          SS_CALL(distill), SS_CALL(distill_backward), SS_CALL(distill_step),
-                         SS_CALL(cross_entropy), SS_CALL(cross_entropy_backward), SS_CALL(cross_entropy_step), {nullptr, nullptr, 0, nullptr}};
+                         SS_CALL(compress), SS_CALL(expand), SS_CALL(cross_entropy), SS_CALL(cross_entropy_backward), SS_CALL(cross_entropy_step), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_dense_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -223,10 +223,16 @@ cudaError_t launch_rms_norm(ss_handle *h, const rms_args &a, cudaStream_t s, int
 struct rms_grad_args {
   ss_dense grad_y, total, weight, grad_total, grad_x, grad_weight;
   const float *rstd;
-  float *scratch;  // rms_grad_scratch bytes
+  float *scratch;      // rms_grad_scratch bytes
+  ss_kept total_kept;  // in total's place (which keeps its sizes and type, with null data), or null codes
 };
 int64_t rms_grad_scratch(const ss_handle *h, int64_t rows, int64_t cols);
+int64_t rms_kept_grad_scratch(const ss_handle *h, int64_t rows, int64_t cols, int32_t type);
 cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &a, cudaStream_t s, int *queued);
+
+// Values to codes and scales, and back (kept.cuh).
+cudaError_t launch_compress(const ss_dense &x, const ss_kept &out, cudaStream_t s, int *queued);
+cudaError_t launch_expand(const ss_kept &x, const ss_dense &y, cudaStream_t s, int *queued);
 
 // out[c] = the sum of column c over the n rows of part (one kernel; a fixed
 // order), rounded to `type`.
@@ -251,18 +257,20 @@ struct linear_args {
   const float *x_scale, *w_scale, *bias;
   int32_t activation;
   unsigned char *scratch;  // linear_scratch bytes
+  ss_kept keep;            // in pre's place, or null codes
 };
-int64_t linear_scratch(const ss_handle *h, const ss_dense &x, const ss_dense &w);
+int64_t linear_scratch(const ss_handle *h, const ss_dense &x, const ss_dense &w, bool keep);
 cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, int *queued);
 
 struct linear_grad_args {
   ss_dense grad_y, x, w, pre, grad_x, grad_w;  // grad_x, grad_w: or null
   float *grad_bias;                            // or null
   int32_t activation;
-  unsigned char *scratch;  // linear_grad_scratch bytes
+  unsigned char *scratch;    // linear_grad_scratch bytes
+  ss_kept x_kept, pre_kept;  // in x's and pre's place (x keeps its sizes and type, with null data), or null codes
 };
 int64_t linear_grad_scratch(const ss_handle *h, const ss_dense &grad_y, const ss_dense &x, const ss_dense &w,
-                            int32_t activation);
+                            int32_t activation, bool x_kept);
 cudaError_t launch_linear_grad(ss_handle *h, const linear_grad_args &a, cudaStream_t s, int *queued);
 
 // Each matrix itself, or its copy with padded rows at *scratch (advanced past

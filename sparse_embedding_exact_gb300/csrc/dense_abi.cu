@@ -47,6 +47,19 @@ ss_status same_type(ss_handle *h, const ss_dense *m, int32_t type, const char *c
   return report(h, SS_ERR_INVALID_ARG, "%s: %s has type %s, expected %s", call, name, type_name(m->type), type_name(type));
 }
 
+ss_status check_kept(ss_handle *h, const ss_kept *m, int64_t rows, int64_t cols, const char *call, const char *name) {
+  if (!m) return report(h, SS_ERR_INVALID_ARG, "%s: null %s", call, name);
+  if (m->n_rows != rows || m->n_cols != cols)
+    return report(h, SS_ERR_INVALID_ARG, "%s: %s is %lld x %lld, expected %lld x %lld", call, name, (long long)m->n_rows,
+                  (long long)m->n_cols, (long long)rows, (long long)cols);
+  const int64_t groups = (cols + SS_KEPT_GROUP - 1) / SS_KEPT_GROUP;
+  if (m->ld < cols || m->ld_scale < groups)
+    return report(h, SS_ERR_INVALID_ARG, "%s: %s: ld %lld < %lld columns or ld_scale %lld < %lld groups", call, name,
+                  (long long)m->ld, (long long)cols, (long long)m->ld_scale, (long long)groups);
+  if (rows > 0 && cols > 0 && (!m->codes || !m->scale)) return report(h, SS_ERR_INVALID_ARG, "%s: %s: null data", call, name);
+  return SS_OK;
+}
+
 ss_dense or_none(const ss_dense *m) { return m ? *m : ss_dense{nullptr, 0, 0, 0, 0}; }
 
 #define SS_TRY(expr)                        \
@@ -145,14 +158,10 @@ int64_t ss_rms_norm_backward_scratch(const ss_handle *h, int64_t n_rows, int64_t
              : 0;
 }
 
-ss_status ss_rms_norm_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *total, const ss_dense *weight,
-                               const float *rstd, const ss_dense *grad_total, const ss_dense *grad_x,
-                               const ss_dense *grad_weight, void *scratch, int64_t scratch_bytes, void *stream) {
-  if (!h) return SS_ERR_INVALID_ARG;
-  const char *call = "ss_rms_norm_backward";
-  if (!total) return report(h, SS_ERR_INVALID_ARG, "%s: null total", call);
+static ss_status rms_norm_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *total, const ss_kept *kept,
+                                   const ss_dense *weight, const float *rstd, const ss_dense *grad_total, const ss_dense *grad_x,
+                                   const ss_dense *grad_weight, void *scratch, int64_t scratch_bytes, void *stream, const char *call) {
   const int64_t R = total->n_rows, D = total->n_cols;
-  SS_TRY(check(h, total, R, D, F32 | HALVES, call, "total"));
   if (D < 1) return report(h, SS_ERR_INVALID_ARG, "%s: rows of no columns", call);
   SS_TRY(check(h, grad_y, R, D, F32 | HALVES, call, "grad_y"));
   SS_TRY(same_type(h, grad_y, total->type, call, "grad_y"));
@@ -167,14 +176,48 @@ ss_status ss_rms_norm_backward(ss_handle *h, const ss_dense *grad_y, const ss_de
   SS_TRY(check(h, grad_weight, 1, D, F32 | HALVES, call, "grad_weight"));
   SS_TRY(same_type(h, grad_weight, weight->type, call, "grad_weight"));
   if (R > 0 && !rstd) return report(h, SS_ERR_INVALID_ARG, "%s: null rstd", call);
-  SS_TRY(check_scratch(h, scratch, scratch_bytes, rms_grad_scratch(h, R, D), call));
+  SS_TRY(check_scratch(h, scratch, scratch_bytes, kept ? rms_kept_grad_scratch(h, R, D, total->type) : rms_grad_scratch(h, R, D), call));
   SS_RUN(h, cudaSetDevice(h->device));
   rms_grad_args a = {*grad_y, *total, *weight, or_none(grad_total), *grad_x, *grad_weight, rstd,
-                     static_cast<float *>(scratch)};
+                     static_cast<float *>(scratch), kept ? *kept : ss_kept{}};
   int queued = 0;
   SS_RUN(h, launch_rms_norm_grad(h, a, as_stream(stream), &queued));
   h->launches += queued;
   return SS_OK;
+}
+
+ss_status ss_rms_norm_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *total, const ss_dense *weight,
+                               const float *rstd, const ss_dense *grad_total, const ss_dense *grad_x,
+                               const ss_dense *grad_weight, void *scratch, int64_t scratch_bytes, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_rms_norm_backward";
+  if (!total) return report(h, SS_ERR_INVALID_ARG, "%s: null total", call);
+  SS_TRY(check(h, total, total->n_rows, total->n_cols, F32 | HALVES, call, "total"));
+  return rms_norm_backward(h, grad_y, total, nullptr, weight, rstd, grad_total, grad_x, grad_weight, scratch, scratch_bytes, stream, call);
+}
+
+int64_t ss_rms_norm_kept_backward_scratch(const ss_handle *h, int64_t n_rows, int64_t n_cols, int32_t type) {
+  return h && n_rows > 0 && n_cols > 0 && n_rows < SS_DENSE_MAX && n_cols < SS_DENSE_MAX
+             ? rms_kept_grad_scratch(h, n_rows, n_cols, type)
+             : 0;
+}
+
+ss_status ss_rms_norm_kept_backward(ss_handle *h, const ss_dense *grad_y, const ss_kept *total, const ss_dense *weight,
+                                    const float *rstd, const ss_dense *grad_total, const ss_dense *grad_x,
+                                    const ss_dense *grad_weight, void *scratch, int64_t scratch_bytes, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_rms_norm_kept_backward";
+  if (!grad_y) return report(h, SS_ERR_INVALID_ARG, "%s: null grad_y", call);
+  const int64_t R = grad_y->n_rows, D = grad_y->n_cols;
+  SS_TRY(check(h, grad_y, R, D, F32 | HALVES, call, "grad_y"));
+  SS_TRY(check_kept(h, total, R, D, call, "total"));
+  const ss_dense like = {nullptr, R, D, D, grad_y->type};
+  return rms_norm_backward(h, grad_y, &like, total, weight, rstd, grad_total, grad_x, grad_weight, scratch, scratch_bytes, stream, call);
+}
+
+static ss_status check_activation(ss_handle *h, int32_t activation, const char *call) {
+  if (activation >= SS_ACT_NONE && activation <= SS_ACT_LOG1P_RELU) return SS_OK;
+  return report(h, SS_ERR_INVALID_ARG, "%s: unknown activation %d", call, activation);
 }
 
 static ss_status check_linear(ss_handle *h, const ss_dense *x, const ss_dense *w, int types, int32_t activation,
@@ -183,20 +226,19 @@ static ss_status check_linear(ss_handle *h, const ss_dense *x, const ss_dense *w
   SS_TRY(check(h, x, x->n_rows, x->n_cols, types, call, "x"));
   SS_TRY(check(h, w, w->n_rows, x->n_cols, types, call, "w"));
   SS_TRY(same_type(h, w, x->type, call, "w"));
-  if (activation < SS_ACT_NONE || activation > SS_ACT_LOG1P_RELU)
-    return report(h, SS_ERR_INVALID_ARG, "%s: unknown activation %d", call, activation);
-  return SS_OK;
+  return check_activation(h, activation, call);
 }
 
 int64_t ss_linear_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w) {
-  return h && x && w ? linear_scratch(h, *x, *w) : 0;
+  return h && x && w ? linear_scratch(h, *x, *w, false) : 0;
+}
+int64_t ss_linear_keep_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w) {
+  return h && x && w ? linear_scratch(h, *x, *w, true) : 0;
 }
 
-ss_status ss_linear(ss_handle *h, const ss_dense *x, const float *x_scale, const ss_dense *w, const float *w_scale,
-                    const float *bias, int32_t activation, const ss_dense *residual, const ss_dense *pre,
-                    const ss_dense *y, void *scratch, int64_t scratch_bytes, void *stream) {
-  if (!h) return SS_ERR_INVALID_ARG;
-  const char *call = "ss_linear";
+static ss_status linear(ss_handle *h, const ss_dense *x, const float *x_scale, const ss_dense *w, const float *w_scale,
+                        const float *bias, int32_t activation, const ss_dense *residual, const ss_dense *pre, const ss_kept *keep,
+                        const ss_dense *y, void *scratch, int64_t scratch_bytes, void *stream, const char *call) {
   SS_TRY(check_linear(h, x, w, HALVES | F8, activation, call));
   const int64_t M = x->n_rows, N = w->n_rows;
   const bool f8 = x->type == SS_VALUES_F8;
@@ -214,31 +256,56 @@ ss_status ss_linear(ss_handle *h, const ss_dense *x, const float *x_scale, const
     SS_TRY(check(h, pre, M, N, F32 | HALVES, call, "pre"));
     SS_TRY(same_type(h, pre, y->type, call, "pre"));
   }
-  SS_TRY(check_scratch(h, scratch, scratch_bytes, linear_scratch(h, *x, *w), call));
+  if (keep) {
+    SS_TRY(check_kept(h, keep, M, N, call, "pre"));
+    if (x->n_cols < 1) return report(h, SS_ERR_INVALID_ARG, "%s: rows of no columns", call);
+  }
+  SS_TRY(check_scratch(h, scratch, scratch_bytes, linear_scratch(h, *x, *w, keep != nullptr), call));
   SS_RUN(h, cudaSetDevice(h->device));
   linear_args a = {*x, *w, or_none(residual), or_none(pre), *y, x_scale, w_scale, bias, activation,
-                   static_cast<unsigned char *>(scratch)};
+                   static_cast<unsigned char *>(scratch), keep ? *keep : ss_kept{}};
   int queued = 0;
   SS_RUN(h, launch_linear(h, a, as_stream(stream), &queued));
   h->launches += queued;
   return SS_OK;
 }
 
-int64_t ss_linear_backward_scratch(const ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_dense *w,
-                                   int32_t activation) {
-  return h && grad_y && x && w ? linear_grad_scratch(h, *grad_y, *x, *w, activation) : 0;
+ss_status ss_linear(ss_handle *h, const ss_dense *x, const float *x_scale, const ss_dense *w, const float *w_scale,
+                    const float *bias, int32_t activation, const ss_dense *residual, const ss_dense *pre,
+                    const ss_dense *y, void *scratch, int64_t scratch_bytes, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  return linear(h, x, x_scale, w, w_scale, bias, activation, residual, pre, nullptr, y, scratch, scratch_bytes, stream, "ss_linear");
 }
 
-ss_status ss_linear_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_dense *w,
-                             const ss_dense *pre, int32_t activation, const ss_dense *grad_x, const ss_dense *grad_w,
-                             float *grad_bias, void *scratch, int64_t scratch_bytes, void *stream) {
+ss_status ss_linear_keep(ss_handle *h, const ss_dense *x, const float *x_scale, const ss_dense *w, const float *w_scale,
+                         const float *bias, int32_t activation, const ss_dense *residual, const ss_kept *pre,
+                         const ss_dense *y, void *scratch, int64_t scratch_bytes, void *stream) {
   if (!h) return SS_ERR_INVALID_ARG;
-  const char *call = "ss_linear_backward";
-  SS_TRY(check_linear(h, x, w, HALVES, activation, call));
+  if (!pre) return report(h, SS_ERR_INVALID_ARG, "ss_linear_keep: null pre");
+  return linear(h, x, x_scale, w, w_scale, bias, activation, residual, nullptr, pre, y, scratch, scratch_bytes, stream, "ss_linear_keep");
+}
+
+int64_t ss_linear_backward_scratch(const ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_dense *w,
+                                   int32_t activation) {
+  return h && grad_y && x && w ? linear_grad_scratch(h, *grad_y, *x, *w, activation, false) : 0;
+}
+
+int64_t ss_linear_kept_backward_scratch(const ss_handle *h, const ss_dense *grad_y, const ss_dense *w, int32_t activation) {
+  if (!h || !grad_y || !w) return 0;
+  const ss_dense x = {nullptr, grad_y->n_rows, w->n_cols, w->n_cols, w->type};
+  return linear_grad_scratch(h, *grad_y, x, *w, activation, true);
+}
+
+static ss_status linear_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_kept *x_kept, const ss_dense *w,
+                                 const ss_dense *pre, const ss_kept *pre_kept, int32_t activation, const ss_dense *grad_x,
+                                 const ss_dense *grad_w, float *grad_bias, void *scratch, int64_t scratch_bytes, int64_t need,
+                                 void *stream, const char *call) {
   const int64_t M = x->n_rows, N = w->n_rows, K = x->n_cols;
   SS_TRY(check(h, grad_y, M, N, HALVES, call, "grad_y"));
   SS_TRY(same_type(h, grad_y, x->type, call, "grad_y"));
-  if (activation != SS_ACT_NONE) {
+  if (activation != SS_ACT_NONE && pre_kept) {
+    SS_TRY(check_kept(h, pre_kept, M, N, call, "pre"));
+  } else if (activation != SS_ACT_NONE) {
     SS_TRY(check(h, pre, M, N, HALVES, call, "pre"));
     SS_TRY(same_type(h, pre, x->type, call, "pre"));
   }
@@ -248,12 +315,70 @@ ss_status ss_linear_backward(ss_handle *h, const ss_dense *grad_y, const ss_dens
     SS_TRY(check(h, g, g == grad_x ? M : N, K, F32 | HALVES, call, name));
     if (g->type != SS_VALUES_F32) SS_TRY(same_type(h, g, x->type, call, name));
   }
-  SS_TRY(check_scratch(h, scratch, scratch_bytes, linear_grad_scratch(h, *grad_y, *x, *w, activation), call));
+  SS_TRY(check_scratch(h, scratch, scratch_bytes, need, call));
   SS_RUN(h, cudaSetDevice(h->device));
-  linear_grad_args a = {*grad_y, *x, *w, activation != SS_ACT_NONE ? *pre : or_none(nullptr), or_none(grad_x),
-                        or_none(grad_w), grad_bias, activation, static_cast<unsigned char *>(scratch)};
+  const bool act = activation != SS_ACT_NONE;
+  linear_grad_args a = {*grad_y,          *x, *w, act && !pre_kept ? *pre : or_none(nullptr), or_none(grad_x), or_none(grad_w), grad_bias, activation,
+                        static_cast<unsigned char *>(scratch), x_kept ? *x_kept : ss_kept{}, act && pre_kept ? *pre_kept : ss_kept{}};
   int queued = 0;
   SS_RUN(h, launch_linear_grad(h, a, as_stream(stream), &queued));
+  h->launches += queued;
+  return SS_OK;
+}
+
+ss_status ss_linear_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_dense *w,
+                             const ss_dense *pre, int32_t activation, const ss_dense *grad_x, const ss_dense *grad_w,
+                             float *grad_bias, void *scratch, int64_t scratch_bytes, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_linear_backward";
+  SS_TRY(check_linear(h, x, w, HALVES, activation, call));
+  const int64_t need = grad_y ? linear_grad_scratch(h, *grad_y, *x, *w, activation, false) : 0;
+  return linear_backward(h, grad_y, x, nullptr, w, pre, nullptr, activation, grad_x, grad_w, grad_bias, scratch, scratch_bytes, need, stream, call);
+}
+
+ss_status ss_linear_kept_backward(ss_handle *h, const ss_dense *grad_y, const ss_dense *x, const ss_kept *x_kept,
+                                  const ss_dense *w, const ss_dense *pre, const ss_kept *pre_kept, int32_t activation,
+                                  const ss_dense *grad_x, const ss_dense *grad_w, float *grad_bias, void *scratch,
+                                  int64_t scratch_bytes, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_linear_kept_backward";
+  if (!grad_y || !w) return report(h, SS_ERR_INVALID_ARG, "%s: null %s", call, grad_y ? "w" : "grad_y");
+  if ((x != nullptr) == (x_kept != nullptr) || (activation != SS_ACT_NONE && (pre != nullptr) == (pre_kept != nullptr)))
+    return report(h, SS_ERR_INVALID_ARG, "%s: x or x_kept, and pre or pre_kept", call);
+  const ss_dense like = {nullptr, grad_y->n_rows, w->n_cols, w->n_cols, w->type};
+  if (x) {
+    SS_TRY(check_linear(h, x, w, HALVES, activation, call));
+  } else {
+    SS_TRY(check_kept(h, x_kept, like.n_rows, like.n_cols, call, "x"));
+    SS_TRY(check(h, w, w->n_rows, w->n_cols, HALVES, call, "w"));
+    SS_TRY(check_activation(h, activation, call));
+  }
+  const int64_t need = linear_grad_scratch(h, *grad_y, like, *w, activation, true);
+  return linear_backward(h, grad_y, x ? x : &like, x_kept, w, pre, pre_kept, activation, grad_x, grad_w, grad_bias, scratch, scratch_bytes, need, stream, call);
+}
+
+ss_status ss_compress(ss_handle *h, const ss_dense *x, const ss_kept *out, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_compress";
+  if (!x) return report(h, SS_ERR_INVALID_ARG, "%s: null x", call);
+  SS_TRY(check(h, x, x->n_rows, x->n_cols, F32 | HALVES, call, "x"));
+  SS_TRY(check_kept(h, out, x->n_rows, x->n_cols, call, "out"));
+  SS_RUN(h, cudaSetDevice(h->device));
+  int queued = 0;
+  SS_RUN(h, launch_compress(*x, *out, as_stream(stream), &queued));
+  h->launches += queued;
+  return SS_OK;
+}
+
+ss_status ss_expand(ss_handle *h, const ss_kept *x, const ss_dense *y, void *stream) {
+  if (!h) return SS_ERR_INVALID_ARG;
+  const char *call = "ss_expand";
+  if (!y) return report(h, SS_ERR_INVALID_ARG, "%s: null y", call);
+  SS_TRY(check(h, y, y->n_rows, y->n_cols, F32 | HALVES, call, "y"));
+  SS_TRY(check_kept(h, x, y->n_rows, y->n_cols, call, "x"));
+  SS_RUN(h, cudaSetDevice(h->device));
+  int queued = 0;
+  SS_RUN(h, launch_expand(*x, *y, as_stream(stream), &queued));
   h->launches += queued;
   return SS_OK;
 }

@@ -47,6 +47,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "kept.cuh"
 #include "product.cuh"
 
 namespace {
@@ -140,6 +141,7 @@ struct Epilogue {
   int32_t act;
   int32_t vec;  // y, pre and residual rows start on 16-byte boundaries
   const float *factor;  // of the product, or null: 1 (a power of two)
+  ss_kept keep;         // in pre's place, or null codes
 };
 __device__ __forceinline__ float read_any(const ss_dense &m, int64_t i) {
   return m.type == SS_VALUES_F32    ? static_cast<const float *>(m.data)[i]
@@ -275,6 +277,34 @@ __device__ __forceinline__ void add_box(const Box &b, bool whole, uint32_t box, 
   }
   __syncwarp();
 }
+// A group of 32 values of each lane's row to codes and a scale.
+__device__ __forceinline__ void keep32(const Epilogue &ep, int64_t m, int64_t n0, const float (&v)[32]) {
+  const ss_kept &k = ep.keep;
+  if (m >= k.n_rows) return;
+  const bool whole = n0 + 32 <= k.n_cols;
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (whole || n0 + i < k.n_cols) most = max(most, finite_bits(v[i]));
+  const int e = exponent_of(most, least_exponent(ep.y.type));
+  const float down = power_of(-e);
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    w[j] = codes2(scaled_down(v[4 * j], down), scaled_down(v[4 * j + 1], down)) |
+           codes2(scaled_down(v[4 * j + 2], down), scaled_down(v[4 * j + 3], down)) << 16;
+  uint8_t *to = static_cast<uint8_t *>(k.codes) + m * k.ld + n0;
+  if (whole && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+    reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n0 + i < k.n_cols) to[i] = (uint8_t)(w[i / 4] >> i % 4 * 8);
+  }
+  k.scale[m * k.ld_scale + n0 / kGroup] = (uint8_t)(e + 127);
+}
+
 template <int kAct>
 __device__ __forceinline__ void act32(float (&v)[32]) {
 #pragma unroll
@@ -313,6 +343,7 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *
   }
   if (ep.bias) along32(ep.bias + n0, N - n0, [&](int i, float f) { v[i] += f; });
   if (ep.pre.data) put32(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);
+  if (ep.keep.codes) keep32(ep, m, n0, v);
   switch (ep.act) {
     case SS_ACT_RELU: act32<SS_ACT_RELU>(v); break;
     case SS_ACT_GELU: act32<SS_ACT_GELU>(v); break;
@@ -640,8 +671,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, kM == 1 ? 16 : 1) k_rows(const
 // columns over the block's rows into part[blockIdx.y][N] (or nowhere).  A warp
 // takes every eighth row of the block's share, two of them at a time.  Bound
 // by memory and, with a gelu, by instructions: 8192 x 4096 bf16 36 us (5.5 TB/s).
-template <typename T, int kN, int kAct>
-__global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, T *gz, int64_t ld, float *part) {
+template <typename T, int kN, int kAct, bool kKept>
+__global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, const ss_kept kept, T *gz, int64_t ld, float *part) {
   __shared__ float sm[8][32 * kN + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t M = grad_y.n_rows, N = grad_y.n_cols, c = ((int64_t)blockIdx.x * 32 + lane) * kN;
@@ -653,11 +684,15 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
   if (c < N)
     for (int64_t m = (int64_t)blockIdx.y * 8 + warp; m < M; m += 2 * step) {
       Pack<T, kN> gv[2], zv[2];
+      float zk[2][kN];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         if (m + u * step < M) {
           gv[u] = load_pack<T, kN>(gp + (m + u * step) * grad_y.ld);
-          if (kAct != SS_ACT_NONE) zv[u] = load_pack<T, kN>(zp + (m + u * step) * pre.ld);
+          if (kKept)
+            load_kept<kN>(kept, m + u * step, c, zk[u]);
+          else if (kAct != SS_ACT_NONE)
+            zv[u] = load_pack<T, kN>(zp + (m + u * step) * pre.ld);
         }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -665,9 +700,9 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
           float g[kN], z[kN];
           widen(gv[u], g);
           if (kAct != SS_ACT_NONE) {
-            widen(zv[u], z);
+            if (!kKept) widen(zv[u], z);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) g[i] *= act_slope<kAct>(z[i]);
+            for (int i = 0; i < kN; ++i) g[i] *= act_slope<kAct>(kKept ? zk[u][i] : z[i]);
           }
           if (gz) store_pack(gz + (m + u * step) * ld + c, narrow<T, kN>(g));
 #pragma unroll
@@ -811,7 +846,7 @@ struct Cut {
 // after the other with its set-up, its epilogue and, for a split sum, the
 // exchange.  It is an estimate: a tile of 5000 x 10000 x 2048 e4m3 takes 14,000
 // clocks where it counts 9,600.
-Cut cut_of(const ss_handle *h, int64_t rows_a, int64_t rows_b, int64_t blocks_k, int least, bool pairs) {
+Cut cut_of(const ss_handle *h, int64_t rows_a, int64_t rows_b, int64_t blocks_k, int least, bool pairs, int most_split = 8) {
   const int64_t sms = std::max(1, h->sm_count);
   auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   Cut best = {256, 1, false, 0.0};
@@ -819,7 +854,7 @@ Cut cut_of(const ss_handle *h, int64_t rows_a, int64_t rows_b, int64_t blocks_k,
   best.clocks = pairs ? 18e3 + (double)up(up(rows_a, 256) * up(rows_b, 256), std::max<int64_t>(1, sms / 2)) * std::max(600.0 * (double)blocks_k, 7e3) : 1e30;
   for (int bn = 256; bn >= least; bn /= 2) {
     if (bn < 256 && bn < 64 && rows_b > bn) break;  // narrow tiles: where they hold all of B's rows
-    for (int split = 1; split <= (bn <= 128 ? 8 : 1) && (split == 1 || blocks_k / split >= 2); split *= 2) {
+    for (int split = 1; split <= (bn <= 128 ? most_split : 1) && (split == 1 || blocks_k / split >= 2); split *= 2) {
       // Blocks at a time: clusters stay within a group of SMs, and of 152 SMs 36
       // of 4 blocks and 15 of 8 run at once (of 456 places 110 and 51).
       const int64_t an_sm = bn <= 32 ? 3 : bn == 64 ? 2 : 1, places = sms * an_sm;
@@ -962,16 +997,16 @@ cudaError_t launch_product(ss_handle *h, const ss_dense &A, int majA, const ss_d
   return product(h, A, majA, B, majB, false, cut_of(h, y.n_rows, y.n_cols, stages_of(A, K), 64, true), ep, s, queued);
 }
 
-int64_t linear_scratch(const ss_handle *, const ss_dense &x, const ss_dense &w) {
-  return few_rows(x) ? 0 : copy_bytes(x) + copy_bytes(w);
+int64_t linear_scratch(const ss_handle *, const ss_dense &x, const ss_dense &w, bool keep) {
+  return few_rows(x) && !keep ? 0 : copy_bytes(x) + copy_bytes(w);
 }
 
 int64_t linear_grad_scratch(const ss_handle *h, const ss_dense &grad_y, const ss_dense &x, const ss_dense &w,
-                            int32_t act) {
+                            int32_t act, bool x_kept) {
   const int64_t M = grad_y.n_rows, N = grad_y.n_cols;
   if (M == 0 || N == 0) return 0;  // the gradients are zeroed
   const bool own = act != SS_ACT_NONE || !rows_aligned(grad_y, 16);
-  return copy_bytes(x) + copy_bytes(w) + (own ? align_up(M * padded_ld(grad_y) * size_of(grad_y.type)) : 0) +
+  return (x_kept ? align_up(x.n_rows * padded_ld(x) * 2) : copy_bytes(x)) + copy_bytes(w) + (own ? align_up(M * padded_ld(grad_y) * size_of(grad_y.type)) : 0) +
          align_up(grad_parts(h, M, N) * N * (int64_t)sizeof(float));
 }
 
@@ -981,7 +1016,8 @@ cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, in
   Epilogue ep = {a.y, a.pre, a.residual, a.x_scale, a.w_scale, a.bias, a.activation, 0};
   auto aligned = [](const ss_dense &m) { return !m.data || rows_aligned(m, 16); };
   ep.vec = aligned(a.y) && aligned(a.pre) && aligned(a.residual);
-  if (few_rows(a.x)) {
+  if (a.keep.codes) ep.keep = a.keep;
+  if (few_rows(a.x) && !a.keep.codes) {
     *queued = 1;
     const int v = a.x.type == SS_VALUES_F8 ? 16 : 8;
     const bool vec = a.x.n_cols % v == 0 && rows_aligned(a.x, 16) && rows_aligned(a.w, 16);
@@ -999,6 +1035,8 @@ cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, in
   cudaError_t e;
   if ((e = aligned_rows(h, {&x, &w}, &scratch, s, queued)) != cudaSuccess) return e;
   const int64_t M = x.n_rows, N = w.n_rows, kb = stages_of(x, x.n_cols);
+  if (a.keep.codes)  // whole groups of a row in a thread: tiles of 64 columns at least, their sums not split
+    return product(h, x, kMajorK, w, kMajorK, false, cut_of(h, M, N, kb, 64, true, 1), ep, s, queued);
   const Cut cut = cut_of(h, M, N, kb, 16, true);
   if (M <= kSwapRows) {
     const Cut other = cut_of(h, N, M, kb, 16, false);
@@ -1026,13 +1064,21 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
   if (own || a.grad_bias) {
     T *to = own ? static_cast<T *>(gz.data) : nullptr;
     float *sums = a.grad_bias ? part : nullptr;
-    const bool vec = N % 8 == 0 && rows_aligned(a.grad_y, 16) && (!a.pre.data || rows_aligned(a.pre, 16));
-    auto run = [&](auto act) {
+    const bool kept = a.pre_kept.codes != nullptr;
+    const bool vec = N % 8 == 0 && rows_aligned(a.grad_y, 16) && (!a.pre.data || rows_aligned(a.pre, 16)) && (!kept || kept_aligned(a.pre_kept, 8));
+    auto run_of = [&](auto act, auto is_kept) {
       constexpr int kAct = decltype(act)::value;
+      constexpr bool kKept = decltype(is_kept)::value;
       if (vec)
-        k_act_grad<T, 8, kAct><<<dim3((unsigned)((N + 255) / 256), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, to, gz.ld, sums);
+        k_act_grad<T, 8, kAct, kKept><<<dim3((unsigned)((N + 255) / 256), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, a.pre_kept, to, gz.ld, sums);
       else
-        k_act_grad<T, 1, kAct><<<dim3((unsigned)((N + 31) / 32), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, to, gz.ld, sums);
+        k_act_grad<T, 1, kAct, kKept><<<dim3((unsigned)((N + 31) / 32), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, a.pre_kept, to, gz.ld, sums);
+    };
+    auto run = [&](auto act) {
+      if constexpr (decltype(act)::value != SS_ACT_NONE) {
+        if (kept) return run_of(act, std::true_type());
+      }
+      run_of(act, std::false_type());
     };
     switch (a.activation) {
       case SS_ACT_RELU: run(std::integral_constant<int, SS_ACT_RELU>()); break;
@@ -1060,7 +1106,15 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
     if ((e = product(h, gz, kMajorK, w, kMajorMN, false, cut_of(h, M, x.n_cols, stages_of(gz, N), 64, true), out(a.grad_x), s, queued)) != cudaSuccess) return e;
   }
   if (a.grad_w.data) {
-    if ((e = aligned_rows(h, {&x}, &scratch, s, queued)) != cudaSuccess) return e;
+    if (a.x_kept.codes) {
+      x.data = scratch;
+      x.ld = padded_ld(x);
+      int n = 0;
+      if ((e = launch_expand(a.x_kept, x, s, &n)) != cudaSuccess) return e;
+      *queued += n;
+    } else if ((e = aligned_rows(h, {&x}, &scratch, s, queued)) != cudaSuccess) {
+      return e;
+    }
     if ((e = product(h, gz, kMajorMN, x, kMajorMN, false, cut_of(h, N, x.n_cols, stages_of(gz, M), 64, true), out(a.grad_w), s, queued)) != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -829,8 +829,23 @@ int64_t rms_grad_scratch(const ss_handle *h, int64_t R, int64_t D) {
   return R > 0 ? most_parts(h, R) * D * (int64_t)sizeof(float) : 0;
 }
 
-cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &a, cudaStream_t s, int *queued) {
+static int64_t kept_total_at(const ss_handle *h, int64_t R, int64_t D) {
+  return (rms_grad_scratch(h, R, D) + SS_SCRATCH_ALIGN - 1) / SS_SCRATCH_ALIGN * SS_SCRATCH_ALIGN;
+}
+int64_t rms_kept_grad_scratch(const ss_handle *h, int64_t R, int64_t D, int32_t type) {
+  return kept_total_at(h, R, D) + R * ((D + 15) / 16 * 16) * size_of(type);
+}
+
+cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &given, cudaStream_t s, int *queued) {
   *queued = 0;
+  rms_grad_args a = given;
+  if (a.total_kept.codes) {
+    const int64_t R = a.total.n_rows, D = a.total.n_cols;
+    a.total.data = reinterpret_cast<unsigned char *>(a.scratch) + kept_total_at(h, R, D);
+    a.total.ld = (D + 15) / 16 * 16;
+    const cudaError_t e = launch_expand(a.total_kept, a.total, s, queued);
+    if (e != cudaSuccess) return e;
+  }
   switch (a.total.type) {
     case SS_VALUES_F32:
       return rms_grad_typed<float>(h, a, s, queued);

@@ -92,32 +92,52 @@ class DenseOperators:
         return y, scale, total
 
     def rms_norm_backward(self, grad_y: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
-                          grad_total: Optional[torch.Tensor] = None, stream=None):
+                          grad_total: Optional[torch.Tensor] = None, total_scale: Optional[torch.Tensor] = None,
+                          stream=None):
         """(grad_x, grad_weight); grad_x is the residual's gradient too.
-        grad_total: the gradient that reaches total past the norm."""
-        return self._run("norm_backward", stream, grad_y, total, weight, rstd, grad_total)
+        grad_total: the gradient that reaches total past the norm.
+        total_scale: with total as ``compress`` gave it."""
+        return self._run("norm_backward", stream, grad_y, total, weight, rstd, grad_total, total_scale)
 
     # -- linear layers
     def linear(self, x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, activation: str = "none",
                residual: Optional[torch.Tensor] = None, x_scale: Optional[torch.Tensor] = None,
                w_scale: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
-               save_pre: bool = False, stream=None):
+               save_pre: bool = False, compress_pre: bool = False, stream=None):
         """act(x w^T + bias) + residual, x (M, K) and w (N, K) in bfloat16,
         float16, or e4m3 with float32 scales of their rows; bias float32.
         out_dtype: x's type (bfloat16 for e4m3) or float32; residual has it
         too.  With save_pre the pair (y, pre), pre the activation's input as
-        ``linear_backward`` takes it."""
+        ``linear_backward`` takes it; with compress_pre the triple (y, pre,
+        pre_scale), pre kept in 8 bits as ``compress`` would."""
+        if save_pre and compress_pre:
+            raise ValueError("save_pre or compress_pre, not both")
         return self._run("linear", stream, x, w, bias, _activation(activation), residual, x_scale, w_scale,
-                         _type(out_dtype), save_pre)
+                         _type(out_dtype), 2 if compress_pre else 1 if save_pre else 0)
 
     def linear_backward(self, grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
                         pre: Optional[torch.Tensor] = None, activation: str = "none",
-                        grad_dtype: Optional[torch.dtype] = None, stream=None):
+                        grad_dtype: Optional[torch.dtype] = None, x_scale: Optional[torch.Tensor] = None,
+                        pre_scale: Optional[torch.Tensor] = None, stream=None):
         """(grad_x, grad_w, grad_bias) of ``linear`` for 16-bit x and w; pre as
         it kept it (not needed for activation "none").  grad_dtype: of grad_x
         and grad_w, x's type or float32; grad_bias is float32.  The residual's
-        gradient is grad_y."""
-        return self._run("linear_backward", stream, grad_y, x, w, pre, _activation(activation), _type(grad_dtype))
+        gradient is grad_y.  x_scale, pre_scale: with x or pre kept in 8 bits,
+        as ``compress`` or ``linear(compress_pre=True)`` gave them."""
+        return self._run("linear_backward", stream, grad_y, x, w, pre, _activation(activation), _type(grad_dtype),
+                         x_scale, pre_scale)
+
+    # -- activations kept in 8 bits
+    def compress(self, x: torch.Tensor, stream=None):
+        """(codes, scale): x in e4m3 with a power of two (float8_e8m0fnu) for
+        every 32 values of a row, for the gradients' calls.  Rows of codes
+        start on 16-byte boundaries."""
+        return self._run("compress", stream, x)
+
+    def expand(self, codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+        """The values that codes and scale stand for, in the given type (exact
+        in the one they came from)."""
+        return self._run("expand", stream, codes, scale, _type(dtype))
 
     # -- distillation
     def distill(self, logits: torch.Tensor, scores: torch.Tensor, items: torch.Tensor,
