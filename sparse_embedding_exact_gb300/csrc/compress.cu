@@ -14,126 +14,260 @@ using namespace dense;
 
 constexpr int kThreads = 256;
 
+// A unit of a row: 8 values as the words that the loads fill, or one value.
 template <typename T, int kN>
-__device__ __forceinline__ void load_values(const T *p, float (&f)[kN]) {
-  if constexpr (sizeof(T) == 4 && kN == 8) {
-    float a[4], b[4];
-    widen(load_pack<T, 4>(p), a);
-    widen(load_pack<T, 4>(p + 4), b);
+struct Unit {
+  static constexpr int kWords = kN * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = a[i];
-      f[4 + i] = b[i];
-    }
-  } else {
-    widen(load_pack<T, kN>(p), f);
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-}
-// Values to T, beyond its largest to that.
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
+      w[4 * i] = q.x;
+      w[4 * i + 1] = q.y;
+      w[4 * i + 2] = q.z;
+      w[4 * i + 3] = q.w;
+    }
+  }
+  __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  // Values 2 i and 2 i + 1.
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else if constexpr (std::is_same<T, __half>::value) {
+      __half2 h;
+      memcpy(&h, &w[i], 4);
+      return __half22float2(h);
+    } else {
+      return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+  }
+  __device__ __forceinline__ void set_pair(int i, float2 f) {
+    if constexpr (sizeof(T) == 4) {
+      w[2 * i] = __float_as_uint(f.x);
+      w[2 * i + 1] = __float_as_uint(f.y);
+    } else {
+      w[i] = narrow2(T(), f.x, f.y);
+    }
+  }
+  // The largest |value|, as float32 bits.  Absolute values order as the
+  // integers that hold them, infinities and NaN last.
+  __device__ __forceinline__ uint32_t most() const {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+      return m;
+    } else {
+      uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+      for (int i = 1; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      m = max(m >> 16, m & 0xFFFFu);
+      if constexpr (std::is_same<T, __half>::value)
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+      else
+        return m << 16;
+    }
+  }
+};
+template <typename T>
+struct Unit<T, 1> {
+  T v;
+  __device__ __forceinline__ void clear() { v = Type<T>::down(0.0f); }
+  __device__ __forceinline__ void load(const T *p) { v = *p; }
+  __device__ __forceinline__ uint32_t most() const { return abs_bits(Type<T>::up(v)); }
+};
+
+// A type's largest value: what stands for more becomes that.
 template <typename T>
 __device__ __forceinline__ constexpr float largest() {
   return sizeof(T) == 4 ? 3.40282347e38f : std::is_same<T, __half>::value ? 65504.0f : 3.38953139e38f;
 }
-template <typename T, int kN>
-__device__ __forceinline__ void store_values(T *p, float (&f)[kN]) {
-#pragma unroll
-  for (int i = 0; i < kN; ++i) f[i] = f[i] > largest<T>() ? largest<T>() : f[i] < -largest<T>() ? -largest<T>() : f[i];
-  if constexpr (sizeof(T) == 4 && kN == 8) {
-    float a[4], b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = f[i];
-      b[i] = f[4 + i];
-    }
-    store_pack(p, narrow<T, 4>(a));
-    store_pack(p + 4, narrow<T, 4>(b));
-  } else {
-    store_pack(p, narrow<T, kN>(f));
-  }
+template <typename T>
+__device__ __forceinline__ float within(float v) {
+  return v > largest<T>() ? largest<T>() : v < -largest<T>() ? -largest<T>() : v;
+}
+// Bytes of scales up to which no code reaches beyond the type: 448 2^e = 1.75 2^(e + 8).
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t safe_byte() {
+  return std::is_same<T, __half>::value ? 127 + 6 : 127 + 118;
 }
 
-// Blocks of blockDim.x threads along a row and blockDim.y rows.
-template <typename T, int kN>
+// Where a thread's four units of kN values lie: kAlong of them along a row, a
+// block's width apart, in each of kDown rows, a block's rows apart.  All four
+// are asked for before the first is used: with one at a time too few bytes were
+// under way (16,384 x 4096 bf16: 44 us to codes and 48 back).
+template <int kAlong>
+struct Place {
+  static constexpr int kDown = 4 / kAlong;
+  int64_t row;
+  int32_t unit;  // of a row: fewer than 2^28
+  __device__ Place()
+      : row((int64_t)blockIdx.x * (blockDim.y * kDown) + threadIdx.y), unit((int32_t)(blockIdx.y * (blockDim.x * kAlong) + threadIdx.x)) {}
+  __device__ __forceinline__ int64_t row_of(int down) const { return row + (int64_t)(down * (int)blockDim.y); }
+  __device__ __forceinline__ int32_t unit_of(int along) const { return unit + along * (int32_t)blockDim.x; }
+};
+
+template <typename T, int kN, int kAlong>
 __global__ void __launch_bounds__(kThreads) k_compress(const ss_dense x, const ss_kept out, int least) {
-  constexpr int kShare = kGroup / kN;  // threads of a group
-  const int64_t units = (x.n_cols + kN - 1) / kN;
-  const int64_t padded = (units + kShare - 1) / kShare * kShare;  // every thread of a warp takes part in its shuffles
-  for (int64_t row0 = (int64_t)blockIdx.x * blockDim.y; row0 < x.n_rows; row0 += (int64_t)gridDim.x * blockDim.y) {
-    const int64_t row = row0 + threadIdx.y;
-    for (int64_t u0 = 0; u0 < padded; u0 += blockDim.x) {
-      const int64_t u = u0 + threadIdx.x;
-      const bool in = row < x.n_rows && u < units;
-      float f[kN];
+  constexpr int kShare = kGroup / kN;  // threads of a group: neighbours in a warp
+  const int32_t units = (int32_t)((x.n_cols + kN - 1) / kN);
+  const Place<kAlong> at;
+  Unit<T, kN> v[4];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) f[i] = 0.0f;
-      if (in) load_values<T, kN>(static_cast<const T *>(x.data) + row * x.ld + u * kN, f);
-      uint32_t most = 0;
+  for (int d = 0; d < at.kDown; ++d) {
+    const bool there = at.row_of(d) < x.n_rows;
+    const T *p = static_cast<const T *>(x.data) + at.row_of(d) * x.ld;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) most = max(most, finite_bits(f[i]));
+    for (int k = 0; k < kAlong; ++k) {
+      v[d * kAlong + k].clear();
+      if (there && at.unit_of(k) < units) v[d * kAlong + k].load(p + (int64_t)at.unit_of(k) * kN);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < at.kDown; ++d) {
+    const bool there = at.row_of(d) < x.n_rows;
+    uint8_t *codes = static_cast<uint8_t *>(out.codes) + at.row_of(d) * out.ld, *scale = out.scale + at.row_of(d) * out.ld_scale;
+#pragma unroll
+    for (int k = 0; k < kAlong; ++k) {
+      const Unit<T, kN> &f = v[d * kAlong + k];
+      const int32_t u = at.unit_of(k);
+      uint32_t most = f.most();
+      const bool odd = most >= kInfBits;  // an infinity or a NaN here: rare
+      if (odd) {
+        most = 0;
+        if constexpr (kN == 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) most = max(most, max(finite_bits(f.pair(i).x), finite_bits(f.pair(i).y)));
+      }
 #pragma unroll
       for (int o = kShare / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
       const int e = exponent_of(most, least);
       const float down = power_of(-e);
-      if (!in) continue;
-      uint8_t *to = static_cast<uint8_t *>(out.codes) + row * out.ld + u * kN;
-#pragma unroll
-      for (int i = 0; i < kN; ++i) f[i] = scaled_down(f[i], down);
+      if (!there || u >= units) continue;
       if constexpr (kN == 8) {
-        uint2 q;
-        q.x = codes2(f[0], f[1]) | codes2(f[2], f[3]) << 16;
-        q.y = codes2(f[4], f[5]) | codes2(f[6], f[7]) << 16;
-        *reinterpret_cast<uint2 *>(to) = q;
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 g = f.pair(i);
+          q[i] = codes2(g.x * down, g.y * down);
+        }
+        if (odd) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[i] = codes2(scaled_down(f.pair(i).x, down), scaled_down(f.pair(i).y, down));
+        }
+        *reinterpret_cast<uint2 *>(codes + (int64_t)u * kN) = make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
       } else {
-        *to = (uint8_t)codes2(f[0], 0.0f);
+        codes[u] = (uint8_t)codes2(scaled_down(Type<T>::up(f.v), down), 0.0f);
       }
-      if (u % kShare == 0) out.scale[row * out.ld_scale + u / kShare] = (uint8_t)(e + 127);
+      if (u % kShare == 0) scale[u / kShare] = (uint8_t)(e + 127);
     }
   }
 }
 
-template <typename T, int kN>
+template <typename T, int kN, int kAlong>
 __global__ void __launch_bounds__(kThreads) k_expand(const ss_kept x, const ss_dense y) {
-  const int64_t units = (y.n_cols + kN - 1) / kN;
-  for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < y.n_rows; row += (int64_t)gridDim.x * blockDim.y)
-    for (int64_t u = threadIdx.x; u < units; u += blockDim.x) {
-      float f[kN];
-      load_kept<kN>(x, row, u * kN, f);
-      store_values<T, kN>(static_cast<T *>(y.data) + row * y.ld + u * kN, f);
+  const int32_t units = (int32_t)((y.n_cols + kN - 1) / kN);
+  const Place<kAlong> at;
+  uint2 q[4];
+  uint32_t byte[4];
+#pragma unroll
+  for (int d = 0; d < at.kDown; ++d) {
+    const uint8_t *codes = static_cast<const uint8_t *>(x.codes) + at.row_of(d) * x.ld, *scale = x.scale + at.row_of(d) * x.ld_scale;
+#pragma unroll
+    for (int k = 0; k < kAlong; ++k)
+      if (at.row_of(d) < y.n_rows && at.unit_of(k) < units) {
+        const int32_t u = at.unit_of(k);
+        if constexpr (kN == 8)
+          q[d * kAlong + k] = *reinterpret_cast<const uint2 *>(codes + (int64_t)u * kN);
+        else
+          q[d * kAlong + k].x = codes[u];
+        byte[d * kAlong + k] = scale[u / (kGroup / kN)];
+      }
+  }
+#pragma unroll
+  for (int d = 0; d < at.kDown; ++d) {
+    T *to = static_cast<T *>(y.data) + at.row_of(d) * y.ld;
+#pragma unroll
+    for (int k = 0; k < kAlong; ++k) {
+      const int i = d * kAlong + k;
+      const int32_t u = at.unit_of(k);
+      if (at.row_of(d) >= y.n_rows || u >= units) continue;
+      const float s = scale_of_byte(byte[i]);
+      if constexpr (kN == 8) {
+        Unit<T, 8> out;
+        float2 f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 c = widen_codes2((j < 2 ? q[i].x : q[i].y) >> j % 2 * 16 & 0xFFFFu);
+          f[j] = both(two(c.x, c.y) * two(s, s));
+        }
+        if (byte[i] > safe_byte<T>()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = make_float2(within<T>(f[j].x), within<T>(f[j].y));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out.set_pair(j, f[j]);
+        out.store(to + (int64_t)u * kN);
+      } else {
+        to[u] = Type<T>::down(within<T>(widen_code((uint8_t)q[i].x) * s));
+      }
     }
+  }
 }
 
-// The threads along a row (a power of two, whole groups and, one value a
-// thread, whole warps) and the rows of a block.
-dim3 block_for(int64_t units, int least) {
+// Calls run(kAlong, grid, block) for `rows` rows of `units` units; a block's
+// width is a power of two of at least `least` threads, so that a group's (one
+// value a thread: a warp's) threads are neighbours of one row.
+template <typename F>
+void laid_out(int64_t rows, int64_t units, int least, F run) {
   int64_t x = least;
   while (x < units && x < kThreads) x *= 2;
-  return dim3((unsigned)x, (unsigned)(kThreads / x));
+  const int64_t y = kThreads / x;
+  const dim3 block((unsigned)x, (unsigned)y);
+  auto grid = [&](int64_t along) {
+    return dim3((unsigned)((rows + y * (4 / along) - 1) / (y * (4 / along))), (unsigned)((units + x * along - 1) / (x * along)));
+  };
+  if (units <= x)
+    run(std::integral_constant<int, 1>(), grid(1), block);
+  else if (units <= 2 * x)
+    run(std::integral_constant<int, 2>(), grid(2), block);
+  else
+    run(std::integral_constant<int, 4>(), grid(4), block);
 }
-unsigned blocks_for(int64_t rows, const dim3 &block) {
-  return (unsigned)std::min<int64_t>((rows + block.y - 1) / block.y, (int64_t)1 << 30);
-}
+// Columns of a call, as a grid has at most 65,535 blocks that way: whole groups.
+constexpr int64_t kMostCols = (int64_t)65535 * kThreads * 4;
 
 template <typename T>
 cudaError_t compress_typed(const ss_dense &x, const ss_kept &out, cudaStream_t s) {
   const int least = least_exponent(x.type);
-  if (x.n_cols % 8 == 0 && rows_aligned(x, 16) && kept_aligned(out, 8)) {
-    const dim3 block = block_for(x.n_cols / 8, 4);
-    k_compress<T, 8><<<blocks_for(x.n_rows, block), block, 0, s>>>(x, out, least);
-  } else {
-    const dim3 block = block_for(x.n_cols, 32);
-    k_compress<T, 1><<<blocks_for(x.n_rows, block), block, 0, s>>>(x, out, least);
-  }
+  if (x.n_cols % 8 == 0 && rows_aligned(x, 16) && kept_aligned(out, 8))
+    laid_out(x.n_rows, x.n_cols / 8, 4, [&](auto along, dim3 grid, dim3 block) {
+      k_compress<T, 8, decltype(along)::value><<<grid, block, 0, s>>>(x, out, least);
+    });
+  else
+    laid_out(x.n_rows, x.n_cols, 32, [&](auto along, dim3 grid, dim3 block) {
+      k_compress<T, 1, decltype(along)::value><<<grid, block, 0, s>>>(x, out, least);
+    });
   return cudaGetLastError();
 }
 template <typename T>
 cudaError_t expand_typed(const ss_kept &x, const ss_dense &y, cudaStream_t s) {
-  if (y.n_cols % 8 == 0 && rows_aligned(y, 16) && kept_aligned(x, 8)) {
-    const dim3 block = block_for(y.n_cols / 8, 4);
-    k_expand<T, 8><<<blocks_for(y.n_rows, block), block, 0, s>>>(x, y);
-  } else {
-    const dim3 block = block_for(y.n_cols, 32);
-    k_expand<T, 1><<<blocks_for(y.n_rows, block), block, 0, s>>>(x, y);
-  }
+  if (y.n_cols % 8 == 0 && rows_aligned(y, 16) && kept_aligned(x, 8))
+    laid_out(y.n_rows, y.n_cols / 8, 4, [&](auto along, dim3 grid, dim3 block) {
+      k_expand<T, 8, decltype(along)::value><<<grid, block, 0, s>>>(x, y);
+    });
+  else
+    laid_out(y.n_rows, y.n_cols, 32, [&](auto along, dim3 grid, dim3 block) {
+      k_expand<T, 1, decltype(along)::value><<<grid, block, 0, s>>>(x, y);
+    });
   return cudaGetLastError();
 }
 
@@ -142,6 +276,21 @@ cudaError_t expand_typed(const ss_kept &x, const ss_dense &y, cudaStream_t s) {
 cudaError_t launch_compress(const ss_dense &x, const ss_kept &out, cudaStream_t s, int *queued) {
   *queued = x.n_rows > 0 && x.n_cols > 0;
   if (!*queued) return cudaSuccess;
+  if (x.n_cols > kMostCols) {  // in slices: 64 million columns a row
+    for (int64_t c = 0; c < x.n_cols; c += kMostCols) {
+      ss_dense part = x;
+      ss_kept to = out;
+      part.n_cols = to.n_cols = std::min(kMostCols, x.n_cols - c);
+      part.data = static_cast<unsigned char *>(x.data) + c * size_of(x.type);
+      to.codes = static_cast<uint8_t *>(out.codes) + c;
+      to.scale += c / kGroup;
+      int one;
+      const cudaError_t e = launch_compress(part, to, s, &one);
+      if (e != cudaSuccess) return e;
+      *queued += c > 0;
+    }
+    return cudaSuccess;
+  }
   switch (x.type) {
     case SS_VALUES_F32: return compress_typed<float>(x, out, s);
     case SS_VALUES_BF16: return compress_typed<__nv_bfloat16>(x, out, s);
@@ -152,6 +301,21 @@ cudaError_t launch_compress(const ss_dense &x, const ss_kept &out, cudaStream_t 
 cudaError_t launch_expand(const ss_kept &x, const ss_dense &y, cudaStream_t s, int *queued) {
   *queued = y.n_rows > 0 && y.n_cols > 0;
   if (!*queued) return cudaSuccess;
+  if (y.n_cols > kMostCols) {
+    for (int64_t c = 0; c < y.n_cols; c += kMostCols) {
+      ss_dense part = y;
+      ss_kept from = x;
+      part.n_cols = from.n_cols = std::min(kMostCols, y.n_cols - c);
+      part.data = static_cast<unsigned char *>(y.data) + c * size_of(y.type);
+      from.codes = static_cast<uint8_t *>(x.codes) + c;
+      from.scale += c / kGroup;
+      int one;
+      const cudaError_t e = launch_expand(from, part, s, &one);
+      if (e != cudaSuccess) return e;
+      *queued += c > 0;
+    }
+    return cudaSuccess;
+  }
   switch (y.type) {
     case SS_VALUES_F32: return expand_typed<float>(x, y, s);
     case SS_VALUES_BF16: return expand_typed<__nv_bfloat16>(x, y, s);

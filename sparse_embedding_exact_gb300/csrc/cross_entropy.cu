@@ -53,10 +53,11 @@ __device__ __forceinline__ float base_of(float most, float c) { return most == -
 // follow one another, so that the tiles in flight share w's rows in L2.
 struct UnitWalk {
   int64_t unit, step, tiles_a, tiles_b, units;  // units of a row of tiles
+  int32_t kb;
   int64_t tb = 0, end = 0, ta = 0;
   int64_t number = 0;
   bool first = false;
-  __device__ __forceinline__ bool next(int64_t &ta_out, int64_t &tb_out) {
+  __device__ __forceinline__ bool next(Tile &t) {
     first = tb == end;
     if (first) {
       if (unit >= tiles_a * units) return false;
@@ -66,8 +67,7 @@ struct UnitWalk {
       end = tiles_b * (number + 1) / units;
       unit += step;
     }
-    ta_out = ta;
-    tb_out = tb++;
+    t = {ta, tb++, 0, kb, 0};
     return true;
   }
   __device__ __forceinline__ bool last() const { return tb == end; }
@@ -119,10 +119,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
   walk.tiles_a = a.tiles_a;
   walk.tiles_b = a.tiles_b;
   walk.units = a.units;
-  pair_products<kBN, kMajorK, kMajorK, false>(
-      a.a, a.b, a.blocks_k, a.idesc, a.status, walk,
-      [&](const UnitWalk &w, int q, int quarter, int64_t ta, int64_t tb, uint32_t acc, uint32_t boxes, auto release) {
-        const int64_t m0 = ta * 2 * kTileM + rank_rows + q * 32, m = m0 + lane;
+  walk.kb = a.blocks_k;
+  pair_products<kBN, kMajorK, kMajorK, false, kGrad ? 1 : 0>(
+      &a.a, &a.b, &a.idesc, a.status, walk,
+      [&](const UnitWalk &w, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
+        const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32, m = m0 + lane;
         const bool rows = m0 < a.M;
         float base = 0.0f, scale = 0.0f, share = 0.0f;
         bool absent = true;
@@ -146,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int col = quarter * (kBN / 4) + half * 32;
-          const int64_t n0 = tb * kBN + col;
+          const int64_t n0 = t.tb * kBN + col;
           float v[32];
           {
             uint32_t r[32];
@@ -322,7 +323,7 @@ int64_t units_of(const ss_handle *h, int64_t tiles_a, int64_t tiles_b) {
 // The scratch of a call, in this order.
 struct Room {
   int64_t V, K, piece, x, w, factor, part, here, stats, gz, acc, sums;
-  int64_t units;
+  int64_t units, parts;
   Room(const ss_handle *h, const ss_dense &x_, const ss_dense &w_, int32_t mode) {
     const int64_t M = x_.n_rows, tiles_a = up(M, 2 * kTileM);
     V = w_.n_rows;
@@ -339,7 +340,8 @@ struct Room {
     here = loss ? align_up(M * 4) : 0;
     stats = mode == XENT_STEP ? align_up(M * 8) : 0;
     gz = grad ? align_up(M * piece * 2) : 0;
-    acc = grad && piece < V ? align_up(M * up(K, 4) * 16) : 0;
+    parts = grad ? grad_product_parts(h, M, piece, K) : 1;
+    acc = grad && (piece < V || parts > 1) ? parts * grad_part_bytes(M, K) : 0;
     sums = grad ? align_up(tiles_a * 8 * piece * 4) : 0;
   }
   int64_t bytes() const { return x + w + factor + part + here + stats + gz + acc + sums; }
@@ -364,10 +366,10 @@ cudaError_t run_logits(ss_handle *h, Logits &p, const ss_dense &x, const ss_dens
   cudaError_t e = encode(&p.a, x, kRowBytes / 2, kTileM);
   if (e == cudaSuccess) e = encode(&p.b, w, kRowBytes / 2, kBN / 2);
   if (e == cudaSuccess && kGrad) e = encode_out(&p.gz, p.out);
-  if (e == cudaSuccess) e = ensure_dyn_smem(k_logits<kGrad>, PairRing<kBN>::kSmem);
+  if (e == cudaSuccess) e = ensure_dyn_smem(k_logits<kGrad>, PairRing<kBN, kGrad ? 1 : 0>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t pairs = std::min<int64_t>((int64_t)p.tiles_a * p.units, std::max(1, h->sm_count / 2));
-  k_logits<kGrad><<<(unsigned)(2 * pairs), kPairThreads, PairRing<kBN>::kSmem, s>>>(p);
+  k_logits<kGrad><<<(unsigned)(2 * pairs), kPairThreads, PairRing<kBN, kGrad ? 1 : 0>::kSmem, s>>>(p);
   *queued += 1;
   return cudaGetLastError();
 }
@@ -439,13 +441,16 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   p.factor = factor;
   p.inv_t = 1.0f / a.temperature;
   void *gz = take(room.gz);
-  const ss_dense acc = {take(room.acc), M, K, up(K, 4) * 4, SS_VALUES_F32};
+  grad_products g = {};
+  g.x = x;
+  g.grad_x = a.grad_x;
+  g.acc = reinterpret_cast<float *>(take(room.acc));
+  g.parts = (int32_t)room.parts;
+  g.factor = factor ? factor + 1 : nullptr;
   float *sums = reinterpret_cast<float *>(take(room.sums));
   const int64_t tiles_a = up(M, 2 * kTileM);
-  const float *back = factor ? factor + 1 : nullptr;
   for (int64_t first = 0; first < V; first += room.piece) {
     const int64_t n = std::min(room.piece, V - first);
-    const bool begun = first > 0, ends = first + n == V;
     const ss_dense wp = rows_from(w, first, n);
     p.out = {gz, M, n, room.piece, a.x.type};
     p.first = first;
@@ -457,15 +462,12 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
       if ((e = launch_sum_rows(h, sums, up(M, 32), n, a.grad_bias + first, SS_VALUES_F32, s)) != cudaSuccess) return e;
       *queued += 1;
     }
-    if (a.grad_x.data) {
-      const ss_dense none = {};
-      if ((e = launch_product(h, p.out, kMajorK, wp, kMajorMN, ends ? a.grad_x : acc, begun ? acc : none, back, s, queued)) != cudaSuccess)
-        return e;
-    }
-    if (a.grad_w.data) {
-      const ss_dense none = {};
-      if ((e = launch_product(h, p.out, kMajorMN, x, kMajorMN, rows_from(a.grad_w, first, n), none, back, s, queued)) != cudaSuccess) return e;
-    }
+    g.wide = wp;
+    g.gz = p.out;
+    g.grad_w = a.grad_w.data ? rows_from(a.grad_w, first, n) : a.grad_w;
+    g.begun = first > 0;
+    g.ends = first + n == V;
+    if ((e = launch_grad_products(h, g, s, queued)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

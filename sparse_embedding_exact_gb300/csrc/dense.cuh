@@ -277,11 +277,25 @@ cudaError_t launch_linear_grad(ss_handle *h, const linear_grad_args &a, cudaStre
 // it, copy_bytes of each); `other` may be null.
 cudaError_t launch_aligned_rows(ss_handle *h, ss_dense *m, ss_dense *other, unsigned char **scratch, cudaStream_t s, int *queued);
 
-// y = factor A B + plus over the summed dimension; A and B are [rows][summed]
-// (kMajorK) or [summed][rows] (kMajorMN), 16-bit, their rows aligned.  plus: or
-// null data; float32 or y's type, and may be y.  factor: device float or null.
-cudaError_t launch_product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B, int majB, const ss_dense &y,
-                           const ss_dense &plus, const float *factor, cudaStream_t s, int *queued);
+// A layer's two gradient products in one launch, all matrices of 16 bits with
+// 16-byte aligned rows:
+//   grad_x (+)= factor gz wide  and  grad_w = factor gz^T x
+// grad_x may come in several calls (`begun`: an earlier one added to acc;
+// `ends`: grad_x is written), each of another gz and wide of the same sizes or
+// less.  Its sum is split over `parts` (grad_product_parts of the largest gz)
+// shares of the summed dimension, each in its own float32 matrix of acc
+// (grad_part_bytes each; none is needed for one part in one call).
+struct grad_products {
+  ss_dense gz, wide, x;     // [M][N], [N][K], [M][K]
+  ss_dense grad_x, grad_w;  // [M][K], [N][K], of x's type or float32, or null data
+  float *acc;
+  const float *factor;  // device float or null: 1
+  int32_t parts;
+  bool begun, ends;
+};
+int64_t grad_product_parts(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *clocks = nullptr);
+int64_t grad_part_bytes(int64_t M, int64_t K);
+cudaError_t launch_grad_products(ss_handle *h, const grad_products &g, cudaStream_t s, int *queued);
 
 struct xent_args {
   ss_dense x, w, grad_x, grad_w;  // grad_x, grad_w: or null

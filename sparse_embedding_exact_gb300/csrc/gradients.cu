@@ -1,0 +1,242 @@
+// The two products of a layer's gradient in one launch.
+//
+//   grad_x = gz w  (summed over the N features),  grad_w = gz^T x  (over the M rows)
+//
+// Both cost M N K multiply-adds, but their tiles do not: grad_x has few (M K /
+// 256^2) with long sums where a layer is wide, grad_w many with short ones.  On
+// their own grad_x leaves SMs idle (2500 x 1024 over 50,176 features: 40 tiles
+// of 256 x 256 for 76 pairs of blocks; by blocks of 128 x 256 265 us, where 133
+// are the tensor cores' time) and every launch its last turn.  Together they are
+// dealt out in advance: grad_x's tiles first, one each or a few, then grad_w's
+// to whoever has less, so that all pairs end within a tile of each other.  Where
+// grad_x's tiles are too few or too long for that, its sum is split into shares
+// (`parts`), each added up in a float32 matrix of its own, which k_join_parts
+// adds up in their order: no atomics, the same bits every time.
+//
+// Bound by the tensor cores.
+#include <algorithm>
+
+#include "product.cuh"
+
+namespace {
+
+using namespace dense;
+
+constexpr int kBN = 256;
+
+// Which units a pair of blocks takes: first units of grad_x (number `pair`,
+// `pair` + pairs, ...), then tiles of grad_w.  Pairs below `more` have one unit
+// more than the others, and many_w tiles, the others few_w first.
+struct Deal {
+  int32_t pairs, units, more;     // units of grad_x: parts of its tiles, a part's tiles side by side
+  int32_t tiles_m, tiles_n, tiles_k, parts, stages_n, stages_m;
+  int32_t tiles_w, each_more, each_less;  // tiles of grad_w: of a pair below `more`, and of another
+};
+
+struct DealWalk {
+  Deal d;
+  int32_t pair, unit, turn;
+  __device__ __forceinline__ bool next(Tile &t) {
+    if (unit < d.units) {
+      const int32_t tiles = d.tiles_m * d.tiles_k, part = unit / tiles, tile = unit % tiles;
+      t.ta = tile % d.tiles_m;
+      t.tb = tile / d.tiles_m;
+      t.k0 = (int32_t)((int64_t)d.stages_n * part / d.parts);
+      t.kb = (int32_t)((int64_t)d.stages_n * (part + 1) / d.parts) - t.k0;
+      t.kind = 0;
+      unit += d.pairs;
+      return true;
+    }
+    const int32_t others = d.pairs - d.more;
+    const bool less = pair >= d.more;
+    if (turn >= (less ? d.each_less : d.each_more)) return false;
+    const int64_t tile = less ? (int64_t)turn * others + (pair - d.more) : (int64_t)d.each_less * others + (int64_t)turn * d.more + pair;
+    ++turn;
+    if (tile >= d.tiles_w) return false;
+    t = {tile / d.tiles_k, tile % d.tiles_k, 0, d.stages_m, 1};
+    return true;
+  }
+  __device__ __forceinline__ int32_t part_of(const Tile &t) const { return d.parts == 1 ? 0 : (unit - d.pairs) / (d.tiles_m * d.tiles_k); }
+};
+
+struct Products {
+  CUtensorMap a[2], b[2], out[2];
+  uint32_t idesc[2];
+  Deal deal;
+  ss_dense y[2];        // grad_x or the parts (one under the other), and grad_w
+  int32_t vec[2];       // their rows start on 16-byte boundaries
+  const float *before;  // what earlier calls added up, or null
+  int64_t ld_before, part_rows;
+  const float *factor;
+  int32_t *status;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_grad_products(const __grid_constant__ Products a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rank_rows = (int64_t)tc::cluster_rank() * kTileM;
+  const int32_t pair = (int32_t)(blockIdx.x / 2);
+  pair_products<kBN, kMajorByKind, kMajorMN, false, 1>(
+      a.a, a.b, a.idesc, a.status, DealWalk{a.deal, pair, pair, 0},
+      [&](const DealWalk &w, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
+        const float factor = a.factor ? *a.factor : 1.0f;
+        ss_dense y = a.y[t.kind];
+        int64_t under = 0;  // rows of the parts before this one
+        if (t.kind == 0 && a.part_rows) {
+          under = a.part_rows * w.part_of(t);
+          y.n_rows = under + a.part_rows;
+        }
+        const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32, row = under + m0;
+        const bool there = row < y.n_rows;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int col = quarter * (kBN / 4) + half * 32;
+          const int64_t n0 = t.tb * kBN + col;
+          float v[32];
+          {
+            uint32_t r[32];
+            tc::load_acc32(acc + (uint32_t)col, r);
+            tc::load_acc_wait();
+            if (half == 1) release();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * factor;
+          }
+          if (!there || n0 >= y.n_cols) continue;
+          if (t.kind == 0 && a.before && row + lane < y.n_rows) {
+            const float *p = a.before + (row + lane) * a.ld_before + n0;  // rows of whole 32 values
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 f = reinterpret_cast<const float4 *>(p)[j];
+              v[4 * j] += f.x;
+              v[4 * j + 1] += f.y;
+              v[4 * j + 2] += f.z;
+              v[4 * j + 3] += f.w;
+            }
+          }
+          if (t.kind == 0 && a.part_rows) {  // whole rows of the parts: the padding's values stay there
+            float *p = static_cast<float *>(y.data) + (row + lane) * y.ld + n0;
+            if (row + lane < y.n_rows) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) reinterpret_cast<float4 *>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+          } else {
+            put32(y, &a.out[t.kind], a.vec[t.kind], boxes, lane, m0, n0, v);
+          }
+        }
+      });
+}
+
+// out = the sum of the parts.
+template <typename T>
+__global__ void __launch_bounds__(256) k_join_parts(const float *parts, int64_t ld, int32_t n, const ss_dense out) {
+  for (int64_t row = blockIdx.x; row < out.n_rows; row += gridDim.x)
+    for (int64_t c = threadIdx.x; c < out.n_cols; c += 256) {
+      float v = 0.0f;
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) v += parts[((int64_t)p * out.n_rows + row) * ld + c];
+      static_cast<T *>(out.data)[row * out.ld + c] = Type<T>::down(v);
+    }
+}
+
+int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
+int64_t part_ld(int64_t K) { return up(K, 32) * 32; }
+
+// The deal for grad_x in `parts` shares, and the clocks until its last pair is
+// done: 600 a stage (512 are the tensor cores' own), a tile's epilogue at least.
+int64_t clocks_of(int64_t stages) { return std::max<int64_t>(600 * stages, 5000); }
+Deal deal_of(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t parts, bool with_x, bool with_w, int64_t *clocks) {
+  Deal d = {};
+  d.tiles_m = (int32_t)up(M, 256);
+  d.tiles_n = (int32_t)up(N, 256);
+  d.tiles_k = (int32_t)up(K, 256);
+  d.stages_n = (int32_t)up(N, 64);
+  d.stages_m = (int32_t)up(M, 64);
+  d.parts = (int32_t)parts;
+  d.units = with_x ? d.tiles_m * d.tiles_k * d.parts : 0;
+  d.tiles_w = with_w ? d.tiles_n * d.tiles_k : 0;
+  const int64_t pairs = std::min<int64_t>(std::max(1, h->sm_count / 2), std::max<int64_t>(1, (int64_t)d.units + d.tiles_w));
+  d.pairs = (int32_t)pairs;
+  d.more = (int32_t)(d.units % pairs);
+  const int64_t cost_x = clocks_of(up(d.stages_n, parts)), cost_w = clocks_of(d.stages_m);
+  const int64_t less = d.units / pairs * cost_x, more = d.more ? less + cost_x : less;
+  // the least end by which the pairs can take all of grad_w's tiles
+  int64_t lo = more, hi = more + (up(d.tiles_w, pairs) + 1) * cost_w;
+  auto room = [&](int64_t end) { return (pairs - d.more) * ((end - less) / cost_w) + d.more * ((end - more) / cost_w); };
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (room(mid) >= d.tiles_w)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  d.each_less = (int32_t)((lo - less) / cost_w);
+  d.each_more = (int32_t)((lo - more) / cost_w);
+  if (clocks) *clocks = lo;
+  return d;
+}
+
+}  // namespace
+
+int64_t grad_product_parts(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *estimate) {
+  int64_t best = 1, least = INT64_MAX;
+  for (int64_t parts = 1; parts <= 16 && (parts == 1 || up(N, 64) / parts >= 4); ++parts) {
+    int64_t clocks;
+    deal_of(h, M, N, K, parts, true, true, &clocks);
+    // the parts written and read again, at 3,000 bytes a clock, and a launch
+    if (parts > 1) clocks += 2 * parts * M * K * 4 / 3000 + 4000;
+    if (clocks < least) {
+      least = clocks;
+      best = parts;
+    }
+  }
+  if (estimate) *estimate = least;
+  return best;
+}
+int64_t grad_part_bytes(int64_t M, int64_t K) { return align_up(M * part_ld(K) * 4); }
+
+cudaError_t launch_grad_products(ss_handle *h, const grad_products &g, cudaStream_t s, int *queued) {
+  const int64_t M = g.gz.n_rows, N = g.gz.n_cols, K = g.x.n_cols;
+  const bool with_x = g.grad_x.data != nullptr, with_w = g.grad_w.data != nullptr;
+  if (!with_x && !with_w) return cudaSuccess;
+  Products p = {};
+  const int64_t parts = std::min<int64_t>(g.parts, up(N, 64));
+  p.deal = deal_of(h, M, N, K, parts, with_x, with_w, nullptr);
+  p.factor = g.factor;
+  p.status = h->d_status;
+  cudaError_t e = cudaSuccess;
+  if (with_x) {
+    const bool direct = g.parts == 1 && g.ends;
+    const ss_dense acc = {g.acc, M * g.parts, K, part_ld(K), SS_VALUES_F32};
+    p.y[0] = direct ? g.grad_x : acc;
+    p.part_rows = direct ? 0 : M;
+    p.before = g.begun ? g.acc : nullptr;
+    p.ld_before = part_ld(K);
+    p.vec[0] = rows_aligned(p.y[0], 16);
+    e = encode(&p.a[0], g.gz, 64, kTileM);
+    if (e == cudaSuccess) e = encode(&p.b[0], g.wide, 64, 64);
+    if (e == cudaSuccess && direct && p.vec[0]) e = encode_out(&p.out[0], p.y[0]);
+    p.idesc[0] = idesc_of(g.gz, kMajorK, kMajorMN, 2 * kTileM, kBN);
+  }
+  if (e == cudaSuccess && with_w) {
+    p.y[1] = g.grad_w;
+    p.vec[1] = rows_aligned(g.grad_w, 16);
+    e = encode(&p.a[1], g.gz, 64, 64);
+    if (e == cudaSuccess) e = encode(&p.b[1], g.x, 64, 64);
+    if (e == cudaSuccess && p.vec[1]) e = encode_out(&p.out[1], p.y[1]);
+    p.idesc[1] = idesc_of(g.gz, kMajorMN, kMajorMN, 2 * kTileM, kBN);
+  }
+  constexpr int kSmem = PairRing<kBN, 1>::kSmem;
+  if (e == cudaSuccess) e = ensure_dyn_smem(k_grad_products, kSmem);
+  if (e != cudaSuccess) return e;
+  k_grad_products<<<(unsigned)(2 * p.deal.pairs), kPairThreads, kSmem, s>>>(p);
+  *queued += 1;
+  if ((e = cudaGetLastError()) != cudaSuccess || !with_x || !g.ends || g.parts == 1) return e;
+  const unsigned blocks = (unsigned)std::min<int64_t>(M, 8 * (int64_t)std::max(1, h->sm_count));
+  if (g.grad_x.type == SS_VALUES_F32)
+    k_join_parts<float><<<blocks, 256, 0, s>>>(g.acc, part_ld(K), g.parts, g.grad_x);
+  else if (g.grad_x.type == SS_VALUES_BF16)
+    k_join_parts<__nv_bfloat16><<<blocks, 256, 0, s>>>(g.acc, part_ld(K), g.parts, g.grad_x);
+  else
+    k_join_parts<__half><<<blocks, 256, 0, s>>>(g.acc, part_ld(K), g.parts, g.grad_x);
+  *queued += 1;
+  return cudaGetLastError();
+}

@@ -140,8 +140,7 @@ struct Epilogue {
   const float *row_scale, *col_scale, *bias;
   int32_t act;
   int32_t vec;  // y, pre and residual rows start on 16-byte boundaries
-  const float *factor;  // of the product, or null: 1 (a power of two)
-  ss_kept keep;         // in pre's place, or null codes
+  ss_kept keep;   // in pre's place, or null codes; by kernels of their own (their code cost the others registers)
 };
 __device__ __forceinline__ float read_any(const ss_dense &m, int64_t i) {
   return m.type == SS_VALUES_F32    ? static_cast<const float *>(m.data)[i]
@@ -157,7 +156,6 @@ __device__ __forceinline__ void write_any(const ss_dense &m, int64_t i, float v)
     static_cast<__half *>(m.data)[i] = __float2half_rn(v);
 }
 __device__ __forceinline__ void finish_one(const Epilogue &ep, int64_t m, int64_t n, float v) {
-  if (ep.factor) v *= *ep.factor;
   if (ep.row_scale) v = v * ep.row_scale[m] * ep.col_scale[n];  // one after the other: their product may leave float32's range
   if (ep.bias) v += ep.bias[n];
   if (ep.pre.data) write_any(ep.pre, m * ep.pre.ld + n, v);
@@ -192,11 +190,6 @@ __device__ __forceinline__ void finish16(const Epilogue &ep, int64_t m, int64_t 
     for (int i = 0; i < 16; ++i)
       if (n + i < ep.y.n_cols) finish_one(ep, m, n + i, v[i]);
     return;
-  }
-  if (ep.factor) {
-    const float f = *ep.factor;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= f;
   }
   if (ep.row_scale) {
     const float s = ep.row_scale[m];
@@ -288,19 +281,23 @@ __device__ __forceinline__ void keep32(const Epilogue &ep, int64_t m, int64_t n0
     if (whole || n0 + i < k.n_cols) most = max(most, finite_bits(v[i]));
   const int e = exponent_of(most, least_exponent(ep.y.type));
   const float down = power_of(-e);
-  uint32_t w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j] = codes2(scaled_down(v[4 * j], down), scaled_down(v[4 * j + 1], down)) |
-           codes2(scaled_down(v[4 * j + 2], down), scaled_down(v[4 * j + 3], down)) << 16;
   uint8_t *to = static_cast<uint8_t *>(k.codes) + m * k.ld + n0;
-  if (whole && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
-    reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  } else {
+  const bool wide = whole && (reinterpret_cast<uintptr_t>(to) & 15) == 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (n0 + i < k.n_cols) to[i] = (uint8_t)(w[i / 4] >> i % 4 * 8);
+  for (int part = 0; part < 2; ++part) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float *f = v + 16 * part + 4 * j;
+      w[j] = codes2(scaled_down(f[0], down), scaled_down(f[1], down)) | codes2(scaled_down(f[2], down), scaled_down(f[3], down)) << 16;
+    }
+    if (wide) {
+      reinterpret_cast<uint4 *>(to)[part] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (n0 + 16 * part + i < k.n_cols) to[16 * part + i] = (uint8_t)(w[i / 4] >> i % 4 * 8);
+    }
   }
   k.scale[m * k.ld_scale + n0 / kGroup] = (uint8_t)(e + 127);
 }
@@ -314,7 +311,7 @@ __device__ __forceinline__ void act32(float (&v)[32]) {
 // 32 columns n0 .. of rows m0 + lane: everything that follows the product,
 // from the accumulators at `acc`; `done` is called once they are read.  The
 // warp's boxes: one for what goes out, one for the residual.
-template <typename F>
+template <bool kKeep, typename F>
 __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *map_y, const CUtensorMap *map_pre, uint32_t boxes,
                                          int lane, int64_t m0, int64_t n0, uint32_t acc, F done) {
   const int64_t m = m0 + lane, M = ep.y.n_rows, N = ep.y.n_cols;
@@ -332,18 +329,15 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
   }
   if (!there) return;
-  if (ep.factor) {
-    const float f = *ep.factor;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= f;
-  }
   if (ep.row_scale) {
     const float s = m < M ? ep.row_scale[m] : 0.0f;
     along32(ep.col_scale + n0, N - n0, [&](int i, float f) { v[i] = v[i] * s * f; });
   }
   if (ep.bias) along32(ep.bias + n0, N - n0, [&](int i, float f) { v[i] += f; });
-  if (ep.pre.data) put32(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);
-  if (ep.keep.codes) keep32(ep, m, n0, v);
+  if (kKeep)
+    keep32(ep, m, n0, v);
+  else if (ep.pre.data)
+    put32(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);
   switch (ep.act) {
     case SS_ACT_RELU: act32<SS_ACT_RELU>(v); break;
     case SS_ACT_GELU: act32<SS_ACT_GELU>(v); break;
@@ -390,7 +384,7 @@ struct Ring {
 };
 
 // One tile a cluster; its blocks take equal shares of the summed dimension.
-template <int kBN, int kMajA, int kMajB, bool kF8>
+template <int kBN, int kMajA, int kMajB, bool kF8, bool kKeep>
 __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Product a) {
   using R = Ring<kBN>;
   extern __shared__ unsigned char raw[];
@@ -514,7 +508,7 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
         const uint32_t boxes = ring + (uint32_t)((warp - 2) * 2 * kStaging);
 #pragma unroll 1
         for (int c = slice0; c < slice1; c += 32)
-          finish32(a.ep, &a.y, &a.pre, boxes, lane, (int64_t)row_a + q * 32, (int64_t)row_b + c, lanes + (uint32_t)c, [] {});
+          finish32<kKeep>(a.ep, &a.y, &a.pre, boxes, lane, (int64_t)row_a + q * 32, (int64_t)row_b + c, lanes + (uint32_t)c, [] {});
         if (lane == 0) tc::store_wait_all();
       }
     }
@@ -578,19 +572,19 @@ struct PairProduct {
 };
 
 // Persistent: each pair of blocks takes every n-th tile of 256 x kBN.
-template <int kBN, int kMajA, int kMajB, bool kF8>
+template <int kBN, int kMajA, int kMajB, bool kF8, bool kKeep>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_product_pair(const __grid_constant__ PairProduct a) {
   const int lane = threadIdx.x & 31;
   const int64_t rank_rows = (int64_t)tc::cluster_rank() * kTileM;
-  pair_products<kBN, kMajA, kMajB, kF8>(
-      a.a, a.b, a.blocks_k, a.idesc, a.status, TileWalk{blockIdx.x / 2, gridDim.x / 2, a.tiles_a, a.tiles_b},
-      [&](const TileWalk &, int q, int quarter, int64_t ta, int64_t tb, uint32_t acc, uint32_t boxes, auto release) {
-        const int64_t m0 = ta * 2 * kTileM + rank_rows + q * 32;
+  pair_products<kBN, kMajA, kMajB, kF8, 2>(
+      &a.a, &a.b, &a.idesc, a.status, TileWalk{blockIdx.x / 2, gridDim.x / 2, a.tiles_a, a.tiles_b, a.blocks_k},
+      [&](const TileWalk &, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
+        const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32;
 #pragma unroll 1
         for (int c = quarter * (kBN / 4); c < (quarter + 1) * (kBN / 4); c += 32) {
           const bool last = c + 32 == (quarter + 1) * (kBN / 4);
-          finish32(a.ep, &a.y, &a.pre, boxes, lane, m0, tb * kBN + c, acc + (uint32_t)c, [&] {
+          finish32<kKeep>(a.ep, &a.y, &a.pre, boxes, lane, m0, t.tb * kBN + c, acc + (uint32_t)c, [&] {
             if (last) release();
           });
         }
@@ -780,7 +774,9 @@ cudaError_t aligned_rows(ss_handle *h, std::initializer_list<ss_dense *> ms, uns
 
 template <int kBN, int kMajA, int kMajB, bool kF8>
 cudaError_t run_product(Product &p, int split, cudaStream_t s) {
-  auto kernel = k_product<kBN, kMajA, kMajB, kF8>;
+  auto kernel = k_product<kBN, kMajA, kMajB, kF8, false>;
+  if constexpr (kBN >= 64 && kMajA == kMajorK && kMajB == kMajorK)
+    if (p.ep.keep.codes) kernel = k_product<kBN, kMajA, kMajB, kF8, true>;
   cudaError_t e = ensure_dyn_smem(kernel, Ring<kBN>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -799,12 +795,14 @@ cudaError_t run_product(Product &p, int split, cudaStream_t s) {
 
 template <int kBN, int kMajA, int kMajB, bool kF8>
 cudaError_t run_pair(ss_handle *h, PairProduct &p, cudaStream_t s) {
-  auto kernel = k_product_pair<kBN, kMajA, kMajB, kF8>;
-  cudaError_t e = ensure_dyn_smem(kernel, PairRing<kBN>::kSmem);
+  auto kernel = k_product_pair<kBN, kMajA, kMajB, kF8, false>;
+  if constexpr (kMajA == kMajorK && kMajB == kMajorK)
+    if (p.ep.keep.codes) kernel = k_product_pair<kBN, kMajA, kMajB, kF8, true>;
+  cudaError_t e = ensure_dyn_smem(kernel, PairRing<kBN, 2>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.tiles_a * p.tiles_b;
   const int64_t pairs = std::min<int64_t>(tiles, std::max(1, h->sm_count / 2));
-  kernel<<<(unsigned)(2 * pairs), kPairThreads, PairRing<kBN>::kSmem, s>>>(p);
+  kernel<<<(unsigned)(2 * pairs), kPairThreads, PairRing<kBN, 2>::kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -973,6 +971,19 @@ int64_t grad_parts(const ss_handle *h, int64_t M, int64_t N) {
   return std::max<int64_t>(1, std::min<int64_t>((M + 63) / 64, 8 * (int64_t)std::max(1, h->sm_count) / slabs));
 }
 
+// Whether a gradient's products take less time as one launch (gradients.cu) than
+// as two, by their estimates, and that launch's scratch.
+bool together(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *parts) {
+  int64_t clocks;
+  *parts = grad_product_parts(h, M, N, K, &clocks);
+  const double apart = cut_of(h, M, K, (N + 63) / 64, 64, true).clocks + cut_of(h, N, K, (M + 63) / 64, 64, true).clocks;
+  return K > 0 && (double)clocks + 18e3 < apart;
+}
+int64_t together_bytes(const ss_handle *h, int64_t M, int64_t N, int64_t K) {
+  int64_t parts;
+  return together(h, M, N, K, &parts) && parts > 1 ? parts * grad_part_bytes(M, K) : 0;
+}
+
 }  // namespace
 
 cudaError_t launch_aligned_rows(ss_handle *h, ss_dense *m, ss_dense *other, unsigned char **scratch, cudaStream_t s, int *queued) {
@@ -986,17 +997,6 @@ cudaError_t launch_aligned_rows(ss_handle *h, ss_dense *m, ss_dense *other, unsi
   return e;
 }
 
-cudaError_t launch_product(ss_handle *h, const ss_dense &A, int majA, const ss_dense &B, int majB, const ss_dense &y,
-                           const ss_dense &plus, const float *factor, cudaStream_t s, int *queued) {
-  Epilogue ep = {};
-  ep.y = y;
-  ep.residual = plus;
-  ep.factor = factor;
-  ep.vec = rows_aligned(y, 16) && (!plus.data || rows_aligned(plus, 16));
-  const int64_t K = majA == kMajorK ? A.n_cols : A.n_rows;
-  return product(h, A, majA, B, majB, false, cut_of(h, y.n_rows, y.n_cols, stages_of(A, K), 64, true), ep, s, queued);
-}
-
 int64_t linear_scratch(const ss_handle *, const ss_dense &x, const ss_dense &w, bool keep) {
   return few_rows(x) && !keep ? 0 : copy_bytes(x) + copy_bytes(w);
 }
@@ -1006,7 +1006,7 @@ int64_t linear_grad_scratch(const ss_handle *h, const ss_dense &grad_y, const ss
   const int64_t M = grad_y.n_rows, N = grad_y.n_cols;
   if (M == 0 || N == 0) return 0;  // the gradients are zeroed
   const bool own = act != SS_ACT_NONE || !rows_aligned(grad_y, 16);
-  return (x_kept ? align_up(x.n_rows * padded_ld(x) * 2) : copy_bytes(x)) + copy_bytes(w) + (own ? align_up(M * padded_ld(grad_y) * size_of(grad_y.type)) : 0) +
+  return (x_kept ? align_up(x.n_rows * padded_ld(x) * 2) : copy_bytes(x)) + copy_bytes(w) + together_bytes(h, M, N, x.n_cols) + (own ? align_up(M * padded_ld(grad_y) * size_of(grad_y.type)) : 0) +
          align_up(grad_parts(h, M, N) * N * (int64_t)sizeof(float));
 }
 
@@ -1101,22 +1101,30 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
     ep.vec = rows_aligned(m, 16);
     return ep;
   };
-  if (a.grad_x.data) {
-    if ((e = aligned_rows(h, {&w}, &scratch, s, queued)) != cudaSuccess) return e;
-    if ((e = product(h, gz, kMajorK, w, kMajorMN, false, cut_of(h, M, x.n_cols, stages_of(gz, N), 64, true), out(a.grad_x), s, queued)) != cudaSuccess) return e;
-  }
+  if (a.grad_x.data && (e = aligned_rows(h, {&w}, &scratch, s, queued)) != cudaSuccess) return e;
   if (a.grad_w.data) {
     if (a.x_kept.codes) {
-      x.data = scratch;
       x.ld = padded_ld(x);
+      x.data = scratch;
+      scratch += align_up(x.n_rows * x.ld * (int64_t)sizeof(T));
       int n = 0;
       if ((e = launch_expand(a.x_kept, x, s, &n)) != cudaSuccess) return e;
       *queued += n;
     } else if ((e = aligned_rows(h, {&x}, &scratch, s, queued)) != cudaSuccess) {
       return e;
     }
-    if ((e = product(h, gz, kMajorMN, x, kMajorMN, false, cut_of(h, N, x.n_cols, stages_of(gz, M), 64, true), out(a.grad_w), s, queued)) != cudaSuccess) return e;
   }
+  int64_t parts_x;
+  if (a.grad_x.data && a.grad_w.data && together(h, M, N, x.n_cols, &parts_x)) {
+    grad_products g = {gz, w, x, a.grad_x, a.grad_w, reinterpret_cast<float *>(scratch), nullptr, (int32_t)parts_x, false, true};
+    return launch_grad_products(h, g, s, queued);
+  }
+  if (a.grad_x.data &&
+      (e = product(h, gz, kMajorK, w, kMajorMN, false, cut_of(h, M, x.n_cols, stages_of(gz, N), 64, true), out(a.grad_x), s, queued)) != cudaSuccess)
+    return e;
+  if (a.grad_w.data &&
+      (e = product(h, gz, kMajorMN, x, kMajorMN, false, cut_of(h, N, x.n_cols, stages_of(gz, M), 64, true), out(a.grad_w), s, queued)) != cudaSuccess)
+    return e;
   return cudaSuccess;
 }
 

@@ -14,7 +14,7 @@ constexpr int kRowBytes = 128;  // of the summed dimension a stage, both operand
 constexpr int kSmemMost = 227 * 1024;
 constexpr int kStaging = 32 * 64;  // an epilogue warp's box: 32 rows of 64 bytes
 
-enum : int { kMajorK = 0, kMajorMN = 1 };
+enum : int { kMajorK = 0, kMajorMN = 1, kMajorByKind = 2 };  // by a tile's kind: 0 along the sum, 1 across it
 
 // ---------------------------------------------------------------- boxes
 // An epilogue warp takes 32 rows x 32 columns at a time.  Its boxes in shared
@@ -111,40 +111,49 @@ __device__ __forceinline__ void along32(const float *p, int64_t n, F f) {
 constexpr int kEpiWarps = 16;                   // four for each 32 tensor-memory lanes, a quarter of the columns each
 constexpr int kPairThreads = 64 + 32 * kEpiWarps;
 
-template <int kBN>
+// kBoxesEach: staging boxes of an epilogue warp.
+template <int kBN, int kBoxesEach>
 struct PairRing {
   static constexpr int kBytesA = kTileM * kRowBytes, kBytesB = kBN / 2 * kRowBytes;
   static constexpr int kStage = kBytesA + kBytesB;  // a block's part
-  static constexpr int kBoxes = kEpiWarps * 2 * kStaging;
+  static constexpr int kBoxes = kEpiWarps * kBoxesEach * kStaging;
   static constexpr int kStages = (kSmemMost - 2048 - kBoxes) / kStage;
   static constexpr int kSmem = kStages * kStage + kBoxes + 1024;
+};
+
+// A tile's place, its share of the summed dimension (stages k0 to k0 + kb) and,
+// where a kernel has two products, whose it is.
+struct Tile {
+  int64_t ta, tb;
+  int32_t k0, kb, kind;
 };
 
 // Every n-th tile of tiles_a x tiles_b, from `tile` on; down groups of 8 tile
 // rows, so that the tiles in flight share both operands in L2.
 struct TileWalk {
   int64_t tile, step, tiles_a, tiles_b;
-  __device__ __forceinline__ bool next(int64_t &ta, int64_t &tb) {
+  int32_t kb;
+  __device__ __forceinline__ bool next(Tile &t) {
     if (tile >= tiles_a * tiles_b) return false;
     const int64_t group = 8 * tiles_b, g0 = tile / group * 8, gh = min((int64_t)8, tiles_a - g0);
-    ta = g0 + (tile % group) % gh;
-    tb = (tile % group) / gh;
+    t = {g0 + (tile % group) % gh, (tile % group) / gh, 0, kb, 0};
     tile += step;
     return true;
   }
 };
 
 // The body of a persistent kernel of pairs of blocks (clusters of two, of
-// kPairThreads): tiles of 256 x kBN of the product of `map_a` and `map_b`, the
-// ones that `walk` gives this pair.  Each tile goes to epi(w, q, quarter, ta, tb,
-// acc, boxes, release) in every epilogue warp, w the walk past this tile: rows q * 32 + lane of this
+// kPairThreads): tiles of 256 x kBN of the products of `map_a` and `map_b` (one a
+// kind, and an `idesc`), the ones that `walk` gives this pair.  Each tile goes to
+// epi(w, tile, q, quarter, acc, boxes, release) in every epilogue warp, w the
+// walk past this tile: rows q * 32 + lane of this
 // block's 128, columns quarter * kBN / 4 on, accumulators from column 0 of the
-// tile at tensor-memory address `acc`, the warp's two boxes; it calls release()
+// tile at tensor-memory address `acc`, the warp's boxes; it calls release()
 // once, after its last load of them.  Copies out are waited for here.
-template <int kBN, int kMajA, int kMajB, bool kF8, typename Walk, typename Epi>
-__device__ __forceinline__ void pair_products(const CUtensorMap &map_a, const CUtensorMap &map_b, const int kb, const uint32_t idesc,
+template <int kBN, int kMajA, int kMajB, bool kF8, int kBoxesEach, typename Walk, typename Epi>
+__device__ __forceinline__ void pair_products(const CUtensorMap *map_a, const CUtensorMap *map_b, const uint32_t *idesc,
                                               int32_t *status, const Walk walk, Epi epi) {
-  using R = PairRing<kBN>;
+  using R = PairRing<kBN, kBoxesEach>;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t bars[2 * R::kStages + 4];
   __shared__ uint32_t tmem_slot;
@@ -160,8 +169,10 @@ __device__ __forceinline__ void pair_products(const CUtensorMap &map_a, const CU
     for (int i = 0; i < 2 * R::kStages + 2; ++i) tc::bar_init(tc::smem_u32(&bars[i]), 1);
     for (int b = 0; b < 2; ++b) tc::bar_init(acc_free(b), 2 * kEpiWarps);
     tc::bar_init_fence();
-    tc::prefetch_map(&map_a);
-    tc::prefetch_map(&map_b);
+    for (int i = 0; i < (kMajA == kMajorByKind ? 2 : 1); ++i) {
+      tc::prefetch_map(map_a + i);
+      tc::prefetch_map(map_b + i);
+    }
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_slot)),
@@ -177,79 +188,101 @@ __device__ __forceinline__ void pair_products(const CUtensorMap &map_a, const CU
 
   constexpr int kUnit = kF8 ? kRowBytes : kRowBytes / 2;
 
+  // Stages and their phases are counted up by hand: a 64-bit remainder a stage
+  // kept the copies' and the products' threads behind the tensor cores.
   if (warp == 0) {
     if (lane == 0) {
+      int s = 0;
+      uint32_t phase = 1;  // of the slot's last reading; a slot's first wait passes
       int64_t issued = 0;
       bool ok = true;
+      const uint32_t bars_there = tc::map_rank(full(0), 0);
       Walk w = walk;
-      for (int64_t ta, tb; ok && w.next(ta, tb);) {
-        const int32_t row_a = (int32_t)(ta * 2 * kTileM + rank * kTileM), row_b = (int32_t)(tb * kBN + rank * (kBN / 2));
-        for (int k = 0; k < kb; ++k, ++issued) {
-          const int s = (int)(issued % R::kStages);
-          const int64_t turn = issued / R::kStages;
-          if (turn > 0 && !(ok = tc::bar_wait(empty(s), (uint32_t)((turn - 1) & 1), status))) break;
+      for (Tile t; ok && w.next(t);) {
+        const int32_t row_a = (int32_t)(t.ta * 2 * kTileM + rank * kTileM), row_b = (int32_t)(t.tb * kBN + rank * (kBN / 2));
+        const CUtensorMap *ma = map_a, *mb = map_b;
+        bool across_a = kMajA == kMajorMN;
+        if (kMajA == kMajorByKind) {
+          ma += t.kind;
+          mb += t.kind;
+          across_a = t.kind != 0;
+        }
+        for (int k = t.k0; k < t.k0 + t.kb; ++k, ++issued) {
+          if (!(ok = tc::bar_wait(empty(s), phase, status))) break;
           if (rank == 0) tc::bar_expect(full(s), 2 * R::kStage);
-          const uint32_t bar = tc::map_rank(full(s), 0);
+          const uint32_t bar = bars_there + 8u * (uint32_t)s;
           const uint32_t sa = ring + (uint32_t)(s * R::kStage), sb = sa + R::kBytesA;
-          if (kMajA == kMajorK) {
-            tc::load_2d_pair(sa, &map_a, k * kUnit, row_a, bar);
+          if (!across_a) {
+            tc::load_2d_pair(sa, ma, k * kUnit, row_a, bar);
           } else {
 #pragma unroll
-            for (int i = 0; i < kTileM / 64; ++i) tc::load_2d_pair(sa + i * 8192, &map_a, row_a + 64 * i, k * kUnit, bar);
+            for (int i = 0; i < kTileM / 64; ++i) tc::load_2d_pair(sa + i * 8192, ma, row_a + 64 * i, k * kUnit, bar);
           }
           if (kMajB == kMajorK) {
-            tc::load_2d_pair(sb, &map_b, k * kUnit, row_b, bar);
+            tc::load_2d_pair(sb, mb, k * kUnit, row_b, bar);
           } else {
 #pragma unroll
-            for (int i = 0; i < kBN / 128; ++i) tc::load_2d_pair(sb + i * 8192, &map_b, row_b + 64 * i, k * kUnit, bar);
+            for (int i = 0; i < kBN / 128; ++i) tc::load_2d_pair(sb + i * 8192, mb, row_b + 64 * i, k * kUnit, bar);
+          }
+          if (++s == R::kStages) {
+            s = 0;
+            phase ^= 1;
           }
         }
       }
       // The first block, whose barriers count both blocks' copies, waits for
       // the last one into each stage; neither block leaves before that.
       if (rank == 0)
-        for (int s = 0; s < R::kStages; ++s) {
-          const int64_t m = (issued + R::kStages - 1 - s) / R::kStages;
-          if (m > 0) tc::bar_wait(full(s), (uint32_t)((m - 1) & 1), status);
+        for (int i = 0; i < R::kStages; ++i) {
+          const int64_t m = (issued + R::kStages - 1 - i) / R::kStages;
+          if (m > 0) tc::bar_wait(full(i), (uint32_t)((m - 1) & 1), status);
         }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      int64_t i = 0;
-      int t = 0;
+      int s = 0, n = 0;
+      uint32_t phase = 0;
       bool ok = true;
       Walk w = walk;
-      for (int64_t ta, tb; ok && w.next(ta, tb); ++t) {
-        const int b = t & 1;
-        if (t >= 2 && !(ok = tc::bar_wait(acc_free(b), (uint32_t)(((t - 2) >> 1) & 1), status))) break;
+      // The operands' descriptors in stage 0; a stage, a block of 16 rows or a
+      // slab further on their addresses (in units of 16 bytes) grow.
+      const uint64_t da_along = tc::desc_128b(ring, 16, 1024), da_across = tc::desc_128b(ring, 8192, 1024);
+      const uint64_t db0 = kMajB == kMajorK ? tc::desc_128b(ring + R::kBytesA, 16, 1024) : tc::desc_128b(ring + R::kBytesA, 8192, 1024);
+      for (Tile t; ok && w.next(t); ++n) {
+        const int b = n & 1;
+        if (n >= 2 && !(ok = tc::bar_wait(acc_free(b), (uint32_t)(((n - 2) >> 1) & 1), status))) break;
         tc::fence_after();
         const uint32_t d = tmem + (uint32_t)(b * kBN);
-        for (int k = 0; k < kb; ++k, ++i) {
-          const int s = (int)(i % R::kStages);
-          if (!(ok = tc::bar_wait(full(s), (uint32_t)((i / R::kStages) & 1), status))) break;
+        const bool across_a = kMajA == kMajorByKind ? t.kind != 0 : kMajA == kMajorMN;
+        const uint64_t da0 = across_a ? da_across : da_along, step_a = across_a ? 128 : 2;
+        const uint32_t id = idesc[kMajA == kMajorByKind ? t.kind : 0];
+        for (int k = 0; k < t.kb; ++k) {
+          if (!(ok = tc::bar_wait(full(s), phase, status))) break;
           tc::fence_after();
-          const uint32_t sa = ring + (uint32_t)(s * R::kStage), sb = sa + R::kBytesA;
+          const uint64_t at = (uint64_t)(uint32_t)(s * (R::kStage / 16));
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint64_t da = kMajA == kMajorK ? tc::desc_128b(sa + 32 * j, 16, 1024) : tc::desc_128b(sa + 2048 * j, 8192, 1024);
-            const uint64_t db = kMajB == kMajorK ? tc::desc_128b(sb + 32 * j, 16, 1024) : tc::desc_128b(sb + 2048 * j, 8192, 1024);
-            tc::mma_pair<kF8>(d, da, db, idesc, (k > 0 || j > 0) ? 1u : 0u);
-          }
+          for (int j = 0; j < 4; ++j)
+            tc::mma_pair<kF8>(d, da0 + at + (uint64_t)j * step_a, db0 + at + (uint64_t)(j * (kMajB == kMajorK ? 2 : 128)), id,
+                              (k > 0 || j > 0) ? 1u : 0u);
           tc::commit_pair(empty(s));
+          if (++s == R::kStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
         tc::commit_pair(acc_full(b));
       }
     }
   } else {
     const int q = warp & 3, quarter = (warp - 2) >> 2;
-    const uint32_t boxes = ring + (uint32_t)(R::kStages * R::kStage + (warp - 2) * 2 * kStaging);
-    int t = 0;
+    const uint32_t boxes = ring + (uint32_t)(R::kStages * R::kStage + (warp - 2) * kBoxesEach * kStaging);
+    int n = 0;
     Walk w = walk;
-    for (int64_t ta, tb; w.next(ta, tb); ++t) {
-      const int b = t & 1;
-      if (!tc::bar_wait(acc_full(b), (uint32_t)((t >> 1) & 1), status)) break;
+    for (Tile t; w.next(t); ++n) {
+      const int b = n & 1;
+      if (!tc::bar_wait(acc_full(b), (uint32_t)((n >> 1) & 1), status)) break;
       tc::fence_after();
-      epi(w, q, quarter, ta, tb, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kBN), boxes, [&] {
+      epi(w, t, q, quarter, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kBN), boxes, [&] {
         tc::fence_before();  // read out: the products may write it again
         __syncwarp();
         if (lane == 0) tc::arrive_remote(tc::map_rank(acc_free(b), 0));
