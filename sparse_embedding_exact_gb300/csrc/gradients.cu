@@ -7,8 +7,8 @@
 // their own grad_x leaves SMs idle (2500 x 1024 over 50,176 features: 40 tiles
 // of 256 x 256 for 76 pairs of blocks; by blocks of 128 x 256 265 us, where 133
 // are the tensor cores' time) and every launch its last turn.  Together they are
-// dealt out in advance: grad_x's tiles first, one each or a few, then grad_w's
-// to whoever has less, so that all pairs end within a tile of each other.  Where
+// dealt out in advance: one product's tiles evenly, the other's to whoever has
+// less, so that all pairs end within a tile of each other.  Where
 // grad_x's tiles are too few or too long for that, its sum is split into shares
 // (`parts`), each added up in a float32 matrix of its own, which k_join_parts
 // adds up in their order: no atomics, the same bits every time.
@@ -24,39 +24,51 @@ using namespace dense;
 
 constexpr int kBN = 256;
 
-// Which units a pair of blocks takes: first units of grad_x (number `pair`,
-// `pair` + pairs, ...), then tiles of grad_w.  Pairs below `more` have one unit
-// more than the others, and many_w tiles, the others few_w first.
+// Which tiles a pair of blocks takes: first units of grad_x (a part's tiles side
+// by side), then tiles of grad_w.  Pairs below `more` may have other numbers of
+// each than the others.
 struct Deal {
-  int32_t pairs, units, more;     // units of grad_x: parts of its tiles, a part's tiles side by side
-  int32_t tiles_m, tiles_n, tiles_k, parts, stages_n, stages_m;
-  int32_t tiles_w, each_more, each_less;  // tiles of grad_w: of a pair below `more`, and of another
+  int32_t pairs, more;
+  int32_t x_more, x_less, w_more, w_less;
+  int32_t tiles_m, tiles_k, parts, stages_n, stages_m;
+  int32_t units, tiles_w;
 };
 
 struct DealWalk {
   Deal d;
-  int32_t pair, unit, turn;
+  int32_t pair, turn_x, turn_w;
+  // The turn-th of a pair that has `mine` of them: turn by turn over all pairs,
+  // then over those that have more turns.
+  __device__ __forceinline__ int64_t number(int32_t turn, int32_t of_more, int32_t of_less) const {
+    const int32_t all = min(of_more, of_less);
+    if (turn < all) return (int64_t)turn * d.pairs + pair;
+    const bool high = pair < d.more;
+    return (int64_t)all * d.pairs + (int64_t)(turn - all) * (high ? d.more : d.pairs - d.more) + (high ? pair : pair - d.more);
+  }
   __device__ __forceinline__ bool next(Tile &t) {
-    if (unit < d.units) {
-      const int32_t tiles = d.tiles_m * d.tiles_k, part = unit / tiles, tile = unit % tiles;
+    while (turn_x < (pair < d.more ? d.x_more : d.x_less)) {
+      const int64_t unit = number(turn_x++, d.x_more, d.x_less);
+      if (unit >= d.units) continue;
+      const int32_t tiles = d.tiles_m * d.tiles_k, part = (int32_t)unit / tiles, tile = (int32_t)unit % tiles;
       t.ta = tile % d.tiles_m;
       t.tb = tile / d.tiles_m;
       t.k0 = (int32_t)((int64_t)d.stages_n * part / d.parts);
       t.kb = (int32_t)((int64_t)d.stages_n * (part + 1) / d.parts) - t.k0;
       t.kind = 0;
-      unit += d.pairs;
       return true;
     }
-    const int32_t others = d.pairs - d.more;
-    const bool less = pair >= d.more;
-    if (turn >= (less ? d.each_less : d.each_more)) return false;
-    const int64_t tile = less ? (int64_t)turn * others + (pair - d.more) : (int64_t)d.each_less * others + (int64_t)turn * d.more + pair;
-    ++turn;
-    if (tile >= d.tiles_w) return false;
-    t = {tile / d.tiles_k, tile % d.tiles_k, 0, d.stages_m, 1};
-    return true;
+    while (turn_w < (pair < d.more ? d.w_more : d.w_less)) {
+      const int64_t tile = number(turn_w++, d.w_more, d.w_less);
+      if (tile >= d.tiles_w) continue;
+      t = {tile / d.tiles_k, tile % d.tiles_k, 0, d.stages_m, 1};
+      return true;
+    }
+    return false;
   }
-  __device__ __forceinline__ int32_t part_of(const Tile &t) const { return d.parts == 1 ? 0 : (unit - d.pairs) / (d.tiles_m * d.tiles_k); }
+  // The part of a tile of grad_x, the last that next() gave.
+  __device__ __forceinline__ int32_t part() const {
+    return d.parts == 1 ? 0 : (int32_t)(number(turn_x - 1, d.x_more, d.x_less) / (d.tiles_m * d.tiles_k));
+  }
 };
 
 struct Products {
@@ -76,13 +88,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_g
   const int64_t rank_rows = (int64_t)tc::cluster_rank() * kTileM;
   const int32_t pair = (int32_t)(blockIdx.x / 2);
   pair_products<kBN, kMajorByKind, kMajorMN, false, 1>(
-      a.a, a.b, a.idesc, a.status, DealWalk{a.deal, pair, pair, 0},
+      a.a, a.b, a.idesc, a.status, DealWalk{a.deal, pair, 0, 0},
       [&](const DealWalk &w, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
         const float factor = a.factor ? *a.factor : 1.0f;
         ss_dense y = a.y[t.kind];
         int64_t under = 0;  // rows of the parts before this one
         if (t.kind == 0 && a.part_rows) {
-          under = a.part_rows * w.part_of(t);
+          under = a.part_rows * w.part();
           y.n_rows = under + a.part_rows;
         }
         const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32, row = under + m0;
@@ -140,37 +152,48 @@ __global__ void __launch_bounds__(256) k_join_parts(const float *parts, int64_t 
 int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t part_ld(int64_t K) { return up(K, 32) * 32; }
 
+// Clocks of a tile: 590 a stage (512 are the tensor cores' own) and 3,500, or its
+// epilogue, as measured over 16 and 64 stages.
+int64_t clocks_of(int64_t stages) { return std::max<int64_t>(590 * stages + 3500, 6500); }
 // The deal for grad_x in `parts` shares, and the clocks until its last pair is
-// done: 600 a stage (512 are the tensor cores' own), a tile's epilogue at least.
-int64_t clocks_of(int64_t stages) { return std::max<int64_t>(600 * stages, 5000); }
+// done.  One product's tiles are spread evenly, the other's go where there is
+// room until the least possible end: whichever way round ends sooner.
 Deal deal_of(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t parts, bool with_x, bool with_w, int64_t *clocks) {
   Deal d = {};
   d.tiles_m = (int32_t)up(M, 256);
-  d.tiles_n = (int32_t)up(N, 256);
   d.tiles_k = (int32_t)up(K, 256);
   d.stages_n = (int32_t)up(N, 64);
   d.stages_m = (int32_t)up(M, 64);
   d.parts = (int32_t)parts;
   d.units = with_x ? d.tiles_m * d.tiles_k * d.parts : 0;
-  d.tiles_w = with_w ? d.tiles_n * d.tiles_k : 0;
+  d.tiles_w = with_w ? (int32_t)up(N, 256) * d.tiles_k : 0;
   const int64_t pairs = std::min<int64_t>(std::max(1, h->sm_count / 2), std::max<int64_t>(1, (int64_t)d.units + d.tiles_w));
   d.pairs = (int32_t)pairs;
-  d.more = (int32_t)(d.units % pairs);
   const int64_t cost_x = clocks_of(up(d.stages_n, parts)), cost_w = clocks_of(d.stages_m);
-  const int64_t less = d.units / pairs * cost_x, more = d.more ? less + cost_x : less;
-  // the least end by which the pairs can take all of grad_w's tiles
-  int64_t lo = more, hi = more + (up(d.tiles_w, pairs) + 1) * cost_w;
-  auto room = [&](int64_t end) { return (pairs - d.more) * ((end - less) / cost_w) + d.more * ((end - more) / cost_w); };
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (room(mid) >= d.tiles_w)
-      hi = mid;
-    else
-      lo = mid + 1;
+  int64_t best = INT64_MAX;
+  for (int even = 0; even < 2; ++even) {
+    const int64_t spread = even ? d.tiles_w : d.units, filled = even ? d.units : d.tiles_w;
+    const int64_t cost_s = even ? cost_w : cost_x, cost_f = even ? cost_x : cost_w;
+    const int64_t more = spread % pairs, n_less = spread / pairs, n_more = n_less + (more > 0);
+    const int64_t less_end = n_less * cost_s, more_end = n_more * cost_s;
+    auto room = [&](int64_t end) { return (pairs - more) * ((end - less_end) / cost_f) + more * ((end - more_end) / cost_f); };
+    int64_t lo = more_end, hi = more_end + (up(filled, pairs) + 1) * cost_f;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (room(mid) >= filled)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    if (lo >= best) continue;
+    best = lo;
+    d.more = (int32_t)more;
+    (even ? d.w_less : d.x_less) = (int32_t)n_less;
+    (even ? d.w_more : d.x_more) = (int32_t)n_more;
+    (even ? d.x_less : d.w_less) = (int32_t)((lo - less_end) / cost_f);
+    (even ? d.x_more : d.w_more) = (int32_t)((lo - more_end) / cost_f);
   }
-  d.each_less = (int32_t)((lo - less) / cost_w);
-  d.each_more = (int32_t)((lo - more) / cost_w);
-  if (clocks) *clocks = lo;
+  if (clocks) *clocks = best;
   return d;
 }
 

@@ -50,23 +50,41 @@ __device__ __forceinline__ float scaled_down(float x, float down) {
   return abs_bits(x) == kInfBits ? __uint_as_float(0x7FC00000u) : x * down;
 }
 
-// kN (8 or 1) values of a row from column c on, in float32, before their type's
-// largest.
+// kN codes of a row (8, 4 or 1) as a load leaves them.
+template <int kN>
+struct Codes {
+  static_assert(kN == 8 || kN == 4 || kN == 1, "codes of one load");
+  uint32_t w[(kN + 3) / 4];
+  __device__ __forceinline__ void load(const uint8_t *p) {
+    if constexpr (kN == 8) {
+      const uint2 q = *reinterpret_cast<const uint2 *>(p);
+      w[0] = q.x;
+      w[1] = q.y;
+    } else if constexpr (kN == 4) {
+      w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+      w[0] = *p;
+    }
+  }
+  // Codes 2 i and 2 i + 1.
+  __device__ __forceinline__ float2 pair(int i) const { return widen_codes2(w[i / 2] >> i % 2 * 16 & 0xFFFFu); }
+  __device__ __forceinline__ float one() const { return widen_code((uint8_t)w[0]); }
+};
+// kN values of a row from column c on, in float32, before their type's largest.
 template <int kN>
 __device__ __forceinline__ void load_kept(const ss_kept &m, int64_t row, int64_t c, float (&f)[kN]) {
-  const uint8_t *p = static_cast<const uint8_t *>(m.codes) + row * m.ld + c;
+  Codes<kN> q;
+  q.load(static_cast<const uint8_t *>(m.codes) + row * m.ld + c);
   const float s = scale_of_byte(m.scale[row * m.ld_scale + c / kGroup]);
-  if constexpr (kN == 8) {
-    const uint2 q = *reinterpret_cast<const uint2 *>(p);
+  if constexpr (kN == 1) {
+    f[0] = q.one() * s;
+  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = widen_codes2((i < 2 ? q.x : q.y) >> i % 2 * 16 & 0xFFFFu);
+    for (int i = 0; i < kN / 2; ++i) {
+      const float2 v = q.pair(i);
       f[2 * i] = v.x * s;
       f[2 * i + 1] = v.y * s;
     }
-  } else {
-    static_assert(kN == 1, "8 values or one");
-    f[0] = widen_code(*p) * s;
   }
 }
 inline bool kept_aligned(const ss_kept &m, int64_t unit) {

@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <initializer_list>
 
+#include "kept.cuh"
 #include "tc.cuh"
 
 namespace {
@@ -546,6 +547,190 @@ __global__ void __launch_bounds__(grad_threads(kN, kPer), kN * kPer == 16 ? 3 : 
   }
 }
 
+// The same from a total kept in 8 bits: 5 bytes a value of 16 bits in place of 6,
+// and no copy of it widened.  A thread has kPer units of kN columns of every row.
+// Where rows start on 16-byte boundaries it copies its units of the next rows
+// into shared memory, which it alone reads, a slot a row: no barrier, and no
+// registers for what is under way.  (Loads one row ahead into registers left
+// room for half the warps.)  Other rows are loaded value by value.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kBytes) : "memory");
+}
+template <typename T, int kN, int kPer>
+struct KeptRow {
+  Pack<T, kN> g[kPer], t[kPer];
+  Codes<kN> c[kPer];
+};
+// A thread's small change of a row, asked for two rows ahead.
+template <int kPer>
+struct KeptScales {
+  float rstd;
+  uint8_t byte[kPer];
+};
+
+constexpr int kKeptThreads = 256;  // of a block, or a row's own where it has more
+constexpr int kKeptSlots = 4;
+template <typename T, int kN, int kPer, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_rms_grad_kept(const rms_grad_args a, int threads) {
+  using W = Work<T, kN>;
+  constexpr bool kAsync = kN > 1;
+  extern __shared__ __align__(16) unsigned char raw[];
+  __shared__ float2 sm[2][32];
+  const Group gr(threads);
+  const int D = (int)a.total.n_cols;
+  const int64_t R = a.total.n_rows, step = (int64_t)gridDim.x * (blockDim.x / threads);
+  const float inv_d = 1.0f / (float)D;
+  const bool past = a.grad_total.data != nullptr;
+  int at[kPer];
+  typename W::V w[kPer][W::kM], gw[kPer][W::kM];
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    at[p] = (p * threads + gr.lane) * kN;
+    float f[kN];
+    load_weights<kN>(a.weight, min(at[p], D), f);
+#pragma unroll
+    for (int i = 0; i < W::kM; ++i) {
+      w[p][i] = W::of(f, i);
+      gw[p][i] = W::all(0.0f);
+    }
+  }
+  const int64_t first = (int64_t)gr.index * gridDim.x + blockIdx.x;
+  const int apart = threads * kN;  // from one unit of this thread to the next
+  // What is read next, and written: at this thread's first unit, a step of rows
+  // further every turn
+  const T *gy = static_cast<const T *>(a.grad_y.data) + first * a.grad_y.ld + at[0];
+  const T *gt = static_cast<const T *>(a.grad_total.data) + (past ? first * a.grad_total.ld + at[0] : 0);
+  const uint8_t *codes = static_cast<const uint8_t *>(a.total_kept.codes) + first * a.total_kept.ld + at[0];
+  const uint8_t *scale = a.total_kept.scale + first * a.total_kept.ld_scale;
+  T *gx = static_cast<T *>(a.grad_x.data) + first * a.grad_x.ld + at[0];
+  const int64_t step_g = step * a.grad_y.ld, step_t = step * a.grad_total.ld, step_c = step * a.total_kept.ld;
+  const int64_t step_s = step * a.total_kept.ld_scale, step_x = step * a.grad_x.ld;
+  // This thread's units of a slot: 16 bytes of g and of t, kN of codes
+  auto unit = [&](int slot, int p) { return (uint32_t)((slot * kPer + p) * (int)blockDim.x + (int)threadIdx.x); };
+  const uint32_t base = tc::smem_u32(raw), units = (uint32_t)(kKeptSlots * kPer) * blockDim.x;
+  auto fetch = [&](int slot, int64_t row) {
+    if (row < R) {
+#pragma unroll
+      for (int p = 0; p < kPer; ++p)
+        if (at[p] < D) {
+          const uint32_t u = unit(slot, p);
+          copy_async<16>(base + 16 * u, gy + p * apart);
+          if (past) copy_async<16>(base + 16 * (units + u), gt + p * apart);
+          copy_async<kN == 1 ? 4 : kN>(base + 32 * units + kN * u, codes + p * apart);
+        }
+      gy += step_g;
+      gt += step_t;
+      codes += step_c;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto scales = [&](int64_t row) {
+    KeptScales<kPer> s = {};
+    if (row < R) {
+      s.rstd = a.rstd[row];
+#pragma unroll
+      for (int p = 0; p < kPer; ++p)
+        if (at[p] < D) s.byte[p] = scale[at[p] / kGroup];
+      scale += step_s;
+    }
+    return s;
+  };
+  int set = 0, slot = 0;
+  KeptScales<kPer> s0 = scales(first), s1 = scales(first + step), s2;
+  if (kAsync)
+    for (int i = 0; i < kKeptSlots - 1; ++i) fetch(i, first + i * step);
+  for (int64_t row = first; row < R; row += step, set ^= 1) {
+    KeptRow<T, kN, kPer> v;
+    if constexpr (kAsync) {
+      fetch(slot == 0 ? kKeptSlots - 1 : slot - 1, row + (kKeptSlots - 1) * step);  // the slot of the row before
+      asm volatile("cp.async.wait_group %0;" ::"n"(kKeptSlots - 1) : "memory");
+#pragma unroll
+      for (int p = 0; p < kPer; ++p)
+        if (at[p] < D) {
+          const uint32_t u = unit(slot, p);
+          v.g[p] = *reinterpret_cast<const Pack<T, kN> *>(raw + 16 * u);
+          if (past) v.t[p] = *reinterpret_cast<const Pack<T, kN> *>(raw + 16 * (units + u));
+          v.c[p].load(raw + 32 * units + kN * u);
+        }
+      if (++slot == kKeptSlots) slot = 0;
+    } else {
+#pragma unroll
+      for (int p = 0; p < kPer; ++p)
+        if (at[p] < D) {
+          v.g[p] = load_pack<T, kN>(gy + p * apart);
+          if (past) v.t[p] = load_pack<T, kN>(gt + p * apart);
+          v.c[p].load(codes + p * apart);
+        }
+      gy += step_g;
+      gt += step_t;
+      codes += step_c;
+    }
+    s2 = scales(row + 2 * step);
+    auto code = [&](int p, int i) {
+      if constexpr (kN == 1) {
+        return v.c[p].one();
+      } else {
+        const float2 f = v.c[p].pair(i);
+        return two(f.x, f.y);
+      }
+    };
+    typename W::V dot = W::all(0.0f);
+#pragma unroll
+    for (int p = 0; p < kPer; ++p)
+      if (at[p] < D) {
+        const typename W::V s = W::all(scale_of_byte(s0.byte[p]) * s0.rstd);
+#pragma unroll
+        for (int i = 0; i < W::kM; ++i) {
+          const typename W::V g = W::get(v.g[p], i), xh = code(p, i) * s;
+          gw[p][i] = fma_of(g, xh, gw[p][i]);
+          dot = fma_of(g * w[p][i], xh, dot);
+        }
+      }
+    const float mean = group_reduce<false>(gr, W::sum(dot), 0.0f, sm, set).x * inv_d;
+#pragma unroll
+    for (int p = 0; p < kPer; ++p)
+      if (at[p] < D) {
+        const typename W::V fx = W::all(-s0.rstd * s0.rstd * mean), fg = W::all(s0.rstd), s = W::all(scale_of_byte(s0.byte[p]));
+        float y[kN];
+#pragma unroll
+        for (int i = 0; i < W::kM; ++i) {
+          const typename W::V t = past ? W::get(v.t[p], i) : W::all(0.0f);
+          W::put(y, i, fma_of(W::get(v.g[p], i) * w[p][i], fg, fma_of(code(p, i) * s, fx, t)));
+        }
+        store_pack(gx + p * apart, narrow<T, kN>(y));
+      }
+    gx += step_x;
+    s0 = s1;
+    s1 = s2;
+  }
+  if (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
+  // The groups' sums in their order, through shared memory where there are several.
+  const int groups = blockDim.x / threads;
+  float *place = reinterpret_cast<float *>(raw), *mine = groups > 1 ? place + gr.index * D : a.scratch + (int64_t)blockIdx.x * D;
+  if (groups > 1) __syncthreads();  // the slots have all been read
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    float f[kN];
+#pragma unroll
+    for (int i = 0; i < W::kM; ++i) W::put(f, i, gw[p][i]);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (at[p] + i < D) mine[at[p] + i] = f[i];
+  }
+  if (groups > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += blockDim.x) {
+      float v = place[c];
+      for (int g = 1; g < groups; ++g) v += place[g * D + c];
+      a.scratch[(int64_t)blockIdx.x * D + c] = v;
+    }
+  }
+}
+
 // The same for rows too wide for registers: grad_x alone, the row read twice.
 template <typename T, int kN>
 __global__ void __launch_bounds__(kWideThreads) k_rms_grad_wide(const rms_grad_args a) {
@@ -752,6 +937,43 @@ int64_t most_parts(const ss_handle *h, int64_t R) {
   return std::min<int64_t>(R, (int64_t)kGradBlocks * std::max(1, h->sm_count));
 }
 
+// Rows of more values than this are widened into scratch and take the other
+// kernels: a thread's sums over the rows would not stay in registers.
+constexpr int64_t kKeptMost = 16 * kMostThreads;
+
+template <typename T>
+cudaError_t rms_grad_kept_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s, int *queued) {
+  constexpr int kV = Type<T>::kVec;
+  const int64_t R = a.total.n_rows, D = a.total.n_cols;
+  if (R == 0) return cudaMemsetAsync(a.grad_weight.data, 0, (size_t)(D * size_of(a.grad_weight.type)), s);
+  bool vec = D % kV == 0 && kept_aligned(a.total_kept, kV);
+  for (const ss_dense *m : {&a.grad_y, &a.grad_total, &a.grad_x}) vec = vec && (!m->data || rows_aligned(*m, 16));
+  // units a thread: as few as a block's threads cover (values one by one: four)
+  const int64_t units = vec ? D / kV : D;
+  int64_t per = vec ? 1 : 4;
+  while ((units + per - 1) / per > (per == 1 ? kKeptThreads : kMostThreads)) per *= 2;
+  const int threads = (int)(((units + per - 1) / per + 31) / 32 * 32), groups = std::max(1, kKeptThreads / threads);
+  const size_t slots = vec ? (size_t)kKeptSlots * per * (threads * groups) * (32 + kV) : 0;
+  const size_t smem = std::max(slots, groups > 1 ? (size_t)groups * D * sizeof(float) : 0);
+  auto run = [&](auto kernel, int an_sm) -> cudaError_t {
+    cudaError_t e = ensure_dyn_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t n = std::min<int64_t>((R + groups - 1) / groups, (int64_t)std::max(1, h->sm_count) * an_sm);
+    kernel<<<(unsigned)n, groups * threads, smem, s>>>(a, threads);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    *queued += 2;
+    return launch_sum_rows(h, a.scratch, n, D, a.grad_weight.data, a.grad_weight.type, s);
+  };
+  const bool small = threads * groups <= kKeptThreads;
+  if (vec) {
+    if (per == 1) return run(k_rms_grad_kept<T, kV, 1, kKeptThreads>, 3);
+    if (per == 2) return small ? run(k_rms_grad_kept<T, kV, 2, kKeptThreads>, 3) : run(k_rms_grad_kept<T, kV, 2, kMostThreads>, 1);
+    if constexpr (kV == 4) return run(k_rms_grad_kept<T, kV, 4, kMostThreads>, 1);
+  }
+  if (per == 4) return small ? run(k_rms_grad_kept<T, 1, 4, kKeptThreads>, 3) : run(k_rms_grad_kept<T, 1, 4, kMostThreads>, 1);
+  return per == 8 ? run(k_rms_grad_kept<T, 1, 8, kMostThreads>, 1) : run(k_rms_grad_kept<T, 1, 16, kMostThreads>, 1);
+}
+
 template <typename T>
 cudaError_t rms_grad_typed(ss_handle *h, const rms_grad_args &a, cudaStream_t s, int *queued) {
   constexpr int kV = Type<T>::kVec;
@@ -833,12 +1055,22 @@ static int64_t kept_total_at(const ss_handle *h, int64_t R, int64_t D) {
   return (rms_grad_scratch(h, R, D) + SS_SCRATCH_ALIGN - 1) / SS_SCRATCH_ALIGN * SS_SCRATCH_ALIGN;
 }
 int64_t rms_kept_grad_scratch(const ss_handle *h, int64_t R, int64_t D, int32_t type) {
-  return kept_total_at(h, R, D) + R * ((D + 15) / 16 * 16) * size_of(type);
+  return D <= kKeptMost ? rms_grad_scratch(h, R, D) : kept_total_at(h, R, D) + R * ((D + 15) / 16 * 16) * size_of(type);
 }
 
 cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &given, cudaStream_t s, int *queued) {
   *queued = 0;
   rms_grad_args a = given;
+  if (a.total_kept.codes && a.total.n_cols <= kKeptMost) {
+    switch (a.total.type) {
+      case SS_VALUES_F32:
+        return rms_grad_kept_typed<float>(h, a, s, queued);
+      case SS_VALUES_BF16:
+        return rms_grad_kept_typed<__nv_bfloat16>(h, a, s, queued);
+      default:
+        return rms_grad_kept_typed<__half>(h, a, s, queued);
+    }
+  }
   if (a.total_kept.codes) {
     const int64_t R = a.total.n_rows, D = a.total.n_cols;
     a.total.data = reinterpret_cast<unsigned char *>(a.scratch) + kept_total_at(h, R, D);
