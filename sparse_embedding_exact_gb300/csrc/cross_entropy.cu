@@ -9,15 +9,15 @@
 // float32.  A row without a target, with one that the bias masks (its logit is
 // -inf) or of weight 0 is absent: loss 0 and gradient 0, whatever x holds.
 //
-// The loss (k_logits<false>): tiles of 256 x 256 logits by pairs of blocks
+// The loss (k_statistics): tiles of 256 x 256 logits by pairs of blocks
 // (product.cuh) that stay in tensor memory.  A thread of the epilogue owns a row
 // of the block's and 64 of the tile's columns; it keeps their running maximum
 // and sum of exponentials in registers over a unit of consecutive tiles of one
-// row of tiles, and writes one pair a unit.  k_join adds the pairs up in a fixed
-// order.  Bound by the tensor cores where rows are many and by reading w where
+// row of tiles, and writes one pair a unit.  k_between adds the pairs up in
+// a fixed order.  Bound by the tensor cores where rows are many and by reading w where
 // they are few.
 //
-// The gradients, in pieces of the items: k_logits<true> computes a piece's
+// The gradients, in pieces of the items: k_logit_gradient computes a piece's
 // logits again and writes gz, rounded to x's type, as the two products that
 // follow take it: grad_w's rows of the piece at once, grad_x added up over the
 // pieces in float32.  Nothing of the size of the logits is ever held; the
@@ -73,6 +73,14 @@ struct UnitWalk {
   __device__ __forceinline__ bool last() const { return tb == end; }
 };
 
+// What the gradient of a row's logits takes: gz_v = exp2(c z_v - base) share,
+// less `scale` at the target.
+struct alignas(16) Row {
+  float base, share, scale;
+  int32_t target;
+};
+__device__ __forceinline__ Row absent_row() { return {INFINITY, 0.0f, 0.0f, -1}; }  // exp2(-inf) 0
+
 struct Logits {
   CUtensorMap a, b, gz;
   int32_t blocks_k, tiles_a, tiles_b, units;
@@ -81,38 +89,47 @@ struct Logits {
   int64_t M, V;          // rows, and items of the piece
   int64_t first;         // the piece's first item
   const float *bias;     // of the piece, or null
-  const int64_t *targets;
+  int32_t bias_pairs;    // it starts on an 8-byte boundary
   float c;               // log2(e) / T
   // statistics
+  const int64_t *targets;
   float2 *part;          // [units * 4][M]
   float *here;           // [M]: the target's logit
   // gradient
-  const float2 *stats;
-  const float *weight, *grad_loss, *factor;
-  float inv_t;
+  const Row *rows;
+  const float *factor;   // gz's power of two, or null: 1
   ss_dense out;
-  float *sums;           // [tiles_a * 8][V] or null: columns' sums over 32 rows
+  float *sums;           // [tiles_a * 2][ld_sums] or null: columns' sums over 128 rows
+  int64_t ld_sums;
 };
 
-// The sum over the lanes of v[j], in lane j.
-__device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
+// A thread of the loss's epilogue: its row's largest logit so far and the sum of
+// exponentials, over its columns of a unit.
+struct Running {
+  float most, sum;
+  __device__ __forceinline__ void add32(float (&v)[32], float c) {
+    float top = most;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const bool up = lane & o;
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+    const float b = base_of(top, c);
+    sum = most == -INFINITY ? 0.0f : sum * exp2_fast(base_of(most, c) - b);
+    most = top;
+    const Two c2 = two(c, c), b2 = two(-b, -b);
+    Two s = two(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+    for (int i = 0; i < 32; i += 2) {
+      const float2 e = both(fma_of(two(v[i], v[i + 1]), c2, b2));
+      s = s + two(exp2_fast(e.x), exp2_fast(e.y));
     }
+    const float2 r = both(s);
+    sum += r.x + r.y;
   }
-  return v[0];
-}
+};
 
-template <bool kGrad>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_logits(const __grid_constant__ Logits a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_statistics(const __grid_constant__ Logits a) {
   const int lane = threadIdx.x & 31;
   const int64_t rank_rows = (int64_t)tc::cluster_rank() * kTileM;
-  float most = -INFINITY, sum = 0.0f;
+  Running run = {-INFINITY, 0.0f};
   UnitWalk walk = {};
   walk.unit = blockIdx.x / 2;
   walk.step = gridDim.x / 2;
@@ -120,30 +137,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
   walk.tiles_b = a.tiles_b;
   walk.units = a.units;
   walk.kb = a.blocks_k;
-  pair_products<kBN, kMajorK, kMajorK, false, kGrad ? 1 : 0>(
+  pair_products<kBN, kMajorK, kMajorK, false, 0>(
       &a.a, &a.b, &a.idesc, a.status, walk,
-      [&](const UnitWalk &w, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
+      [&](const UnitWalk &w, const Tile &t, int q, int quarter, uint32_t acc, uint32_t, auto release) {
         const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32, m = m0 + lane;
-        const bool rows = m0 < a.M;
-        float base = 0.0f, scale = 0.0f, share = 0.0f;
-        bool absent = true;
-        int64_t target = -1;
-        if (m < a.M) {
-          target = a.targets[m] - a.first;
-          if (kGrad) {
-            const float2 st = a.stats[m];
-            const float weight = a.weight ? a.weight[m] : 1.0f;
-            absent = st.y == INFINITY || weight == 0.0f;
-            scale = weight * (a.grad_loss ? a.grad_loss[m] : 1.0f) * a.inv_t;
-            if (a.factor) scale *= a.factor[0];
-            share = scale / st.y;
-            base = base_of(st.x, a.c);
-          }
-        }
-        if (!kGrad && w.first) {
-          most = -INFINITY;
-          sum = 0.0f;
-        }
+        const int64_t target = m < a.M ? a.targets[m] : -1;
+        if (w.first) run = {-INFINITY, 0.0f};
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int col = quarter * (kBN / 4) + half * 32;
@@ -157,74 +156,196 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
           }
-          if (!rows || n0 >= a.V) continue;
+          if (m0 >= a.M || n0 >= a.V) continue;
           if (a.bias) along32(a.bias + n0, a.V - n0, [&](int i, float f) { v[i] += f; });
-          const uint64_t at = (uint64_t)(target - n0);
-          if (!kGrad) {
-            if (n0 + 32 > a.V) {
+          if (n0 + 32 > a.V) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (n0 + i >= a.V) v[i] = -INFINITY;
-            }
-            if (at < 32) {
-              // by bits: where i == at picks it, the compiler puts v into memory
-              const uint32_t bit = 1u << (uint32_t)at;
-              float z = 0.0f;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (bit & (1u << i)) z = v[i];
-              if (n0 + (int64_t)at < a.V) a.here[m] = z;
-            }
-            float top = most;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
-            const float b = base_of(top, a.c);
-            float s = most == -INFINITY ? 0.0f : sum * exp2_fast(base_of(most, a.c) - b), s2 = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              s += exp2_fast(fmaf(v[i], a.c, -b));
-              s2 += exp2_fast(fmaf(v[i + 1], a.c, -b));
-            }
-            sum = s + s2;
-            most = top;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = exp2_fast(fmaf(v[i], a.c, -base)) * share;
-            if (at < 32) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] -= i == (int)at ? scale : 0.0f;
-            }
-            if (absent) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-            }
-            put32(a.out, &a.gz, true, boxes, lane, m0, n0, v);
-            if (a.sums) {
-              float total = column_sums(v, lane);
-              if (a.factor) total *= a.factor[1];
-              if (n0 + lane < a.V) a.sums[(m0 / 32) * a.V + n0 + lane] = total;
-            }
+            for (int i = 0; i < 32; ++i)
+              if (n0 + i >= a.V) v[i] = -INFINITY;
           }
+          const uint64_t at = (uint64_t)(target - n0);
+          if (at < 32) {
+            // by bits: where i == at picks it, the compiler puts v into memory
+            const uint32_t bit = 1u << (uint32_t)at;
+            float z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (bit & (1u << i)) z = v[i];
+            if (target < a.V) a.here[m] = z;
+          }
+          run.add32(v, a.c);
         }
-        if (!kGrad && w.last() && m < a.M) a.part[(w.number * 4 + quarter) * a.M + m] = make_float2(most, sum);
+        if (w.last() && m < a.M) a.part[(w.number * 4 + quarter) * a.M + m] = make_float2(run.most, run.sum);
       });
 }
 
-// The rows' losses and statistics from the units' pairs, in their order: a block
-// takes 32 rows, eight threads a row.
-struct Join {
-  const float2 *part;
-  const float *here, *weight;
+// The sums over the lanes t with one t % 4 of v[j]: that of j = 4 (t & 16 ? 1 : 0) +
+// 2 (t & 8 ? 1 : 0) + (t & 4 ? 1 : 0) in thread t.
+__device__ __forceinline__ float sum_eighth(float (&v)[8], int lane) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    const bool up = lane & (o * 4);
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o * 4);
+    }
+  }
+  return v[0];
+}
+
+// gz of a piece.  The accumulators are read as the matrix fragments that stmatrix
+// takes: a thread has 8 columns of 4 rows, so that a column's sum over 32 rows
+// is 3 additions and 3 shuffles' worth in place of 5 of 32 (a row a thread,
+// 31 shuffles a block of 32 x 32: 192 us for 2500 x 50,176 x 1024, where this
+// takes XXX).
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_logit_gradient(const __grid_constant__ Logits a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t rank_rows = (int64_t)tc::cluster_rank() * kTileM;
+  UnitWalk walk = {};
+  walk.unit = blockIdx.x / 2;
+  walk.step = gridDim.x / 2;
+  walk.tiles_a = a.tiles_a;
+  walk.tiles_b = a.tiles_b;
+  walk.units = a.units;
+  walk.kb = a.blocks_k;
+  pair_products<kBN, kMajorK, kMajorK, false, 2>(
+      &a.a, &a.b, &a.idesc, a.status, walk,
+      [&](const UnitWalk &, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
+        const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32;
+        const float factor = a.factor ? a.factor[0] : 1.0f;
+        Row row[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t m = m0 + lane / 4 + 8 * k;
+          row[k] = m < a.M ? a.rows[m] : absent_row();
+          row[k].share *= factor;
+          row[k].scale *= factor;
+        }
+        const Two c2 = two(a.c, a.c);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int col = quarter * (kBN / 4) + half * 32;
+          const int64_t n0 = t.tb * kBN + col;
+          uint32_t r[32];
+          tc::load_acc16x32(acc + (uint32_t)col, r);
+          tc::load_acc16x32(acc + (uint32_t)col + (16u << 16), r + 16);
+          tc::load_acc_wait();
+          if (half == 1) release();
+          if (n0 >= a.V) continue;
+          const int64_t left = a.V - n0;
+          float sums[8];
+          if (m0 < a.M) {
+            Two bias[4];
+            if (a.bias) {
+              const float *p = a.bias + n0 + 2 * (lane % 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (left >= 32 && a.bias_pairs) {
+                  const float2 f = __ldg(reinterpret_cast<const float2 *>(p + 8 * i));
+                  bias[i] = two(f.x, f.y);
+                } else {
+                  const int64_t n = 8 * i + 2 * (lane % 4);
+                  bias[i] = two(n < left ? __ldg(p + 8 * i) : 0.0f, n + 1 < left ? __ldg(p + 8 * i + 1) : 0.0f);
+                }
+              }
+            }
+            bool hot = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) hot = hot || (uint64_t)(row[k].target - (a.first + n0)) < 32;
+            const bool any_hot = __any_sync(0xFFFFFFFFu, hot);
+            if (lane == 0) tc::store_wait_read();  // the box's last copy out
+            __syncwarp();
+            uint32_t packed[4][4];  // of rows 8 k on, columns 8 i on
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              Two sum = two(0.0f, 0.0f);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t *f = r + 16 * (k / 2) + 4 * i + 2 * (k % 2);
+                Two z = two(__uint_as_float(f[0]), __uint_as_float(f[1]));
+                if (a.bias) z = z + bias[i];
+                const float2 e = both(fma_of(z, c2, two(-row[k].base, -row[k].base)));
+                Two g = two(exp2_fast(e.x), exp2_fast(e.y)) * two(row[k].share, row[k].share);
+                if (any_hot) {
+                  const int64_t at = row[k].target - (a.first + n0) - (8 * i + 2 * (lane % 4));
+                  g = g + two(at == 0 ? -row[k].scale : 0.0f, at == 1 ? -row[k].scale : 0.0f);
+                }
+                sum = sum + g;
+                const float2 h = both(g);
+                packed[k][i] = narrow2(T(), h.x, h.y);
+              }
+              const float2 h = both(sum);
+              sums[2 * i] = h.x;
+              sums[2 * i + 1] = h.y;
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; i += 2)
+                tc::store_matrices(unit_at(boxes, 16 * b + (lane / 8 & 1) * 8 + lane % 8, i + lane / 16), packed[2 * b][i], packed[2 * b + 1][i],
+                                   packed[2 * b][i + 1], packed[2 * b + 1][i + 1]);
+            tc::fence_async();
+            __syncwarp();
+            if (lane == 0) {
+              tc::store_2d(&a.gz, boxes, (int)n0, (int)m0);
+              tc::store_commit();
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sums[i] = 0.0f;
+          }
+          if (a.sums) {
+            // columns 8 i + 2 (t % 4) + j: thread t ends with i = t / 8 and j = t / 4 % 2
+            float total = sum_eighth(sums, lane);
+            const uint32_t mine = boxes + kStaging + (uint32_t)(half * 128);
+            tc::write_shared(mine + 4 * (uint32_t)(lane / 8 * 8 + lane % 4 * 2 + (lane / 4 & 1)), total);
+            // the four warps of these columns; a half's place is written again
+            // only after the other half's barrier, when all have read it
+            tc::named_sync(1 + quarter, 128);
+            if (q == half) {
+              const int warp = (int)(threadIdx.x >> 5) - 2;
+              const uint32_t firsts = mine - (uint32_t)((warp & 3) * 2 * kStaging);
+              total = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) total += tc::read_shared<float>(firsts + (uint32_t)(k * 2 * kStaging) + 4 * (uint32_t)lane);
+              if (a.factor) total *= a.factor[1];
+              if (lane < left) a.sums[(m0 / kTileM) * a.ld_sums + n0 + lane] = total;
+            }
+          }
+        }
+      });
+}
+
+// Between the two: the rows' losses and statistics from the units' pairs, in
+// their order (unless the statistics are given), what gz takes of each row, x
+// with the absent rows' values 0, as 0 times an infinity or NaN there would
+// reach grad_w, and binary16's power of two and its reciprocal.  A block takes
+// 32 rows, 16 threads a row.
+struct Between {
+  const float2 *part;  // or null: stats are given
+  const float *here, *weight, *grad_loss;
   const int64_t *targets;
   int64_t M, V;
-  int32_t parts;
-  float c;
+  int32_t parts, vec;
+  float c, inv_t;
   float *loss;
   float2 *stats;
   int32_t *status;
+  // for the gradient, or null
+  Row *rows;
+  ss_dense x;
+  void *to;            // x's copy, or x's own data: absent rows alone are written then
+  int64_t ld;
+  float *factor;       // or null
 };
-__global__ void __launch_bounds__(256) k_join(const Join a) {
-  __shared__ float2 sm[8][32];
+constexpr int kBetweenWarps = 16;
+__global__ void __launch_bounds__(32 * kBetweenWarps) k_between(const Between a) {
+  __shared__ float2 sm[kBetweenWarps][32];
+  __shared__ bool there[32];
+  tc::wait_before();
+  tc::let_next();
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int64_t m = (int64_t)blockIdx.x * 32 + lane;
   float most = -INFINITY, sum = 0.0f;
@@ -234,68 +355,75 @@ __global__ void __launch_bounds__(256) k_join(const Join a) {
           (p.x == -INFINITY && p.y == 0.0f ? 0.0f : p.y * exp2_fast(base_of(p.x, a.c) - b));
     most = top;
   };
-  if (m < a.M)
-#pragma unroll 4
-    for (int p = g; p < a.parts; p += 8) add(a.part[(int64_t)p * a.M + m]);
-  sm[g][lane] = make_float2(most, sum);
-  __syncthreads();
-  if (g != 0 || m >= a.M) return;
-  for (int k = 1; k < 8; ++k) add(sm[k][lane]);
-  const int64_t target = a.targets[m];
-  const float weight = a.weight ? a.weight[m] : 1.0f;
-  const bool past = target >= a.V;
-  if (past) flag(a.status, DEV_OUT_OF_RANGE);
-  bool live = target >= 0 && !past && weight != 0.0f;
-  float loss = 0.0f;
-  if (live) {
-    const float z = a.here[m];
-    live = z != -INFINITY;
-    if (live) loss = weight * (kLn2 * (log2f(sum) - fmaf(z, a.c, -base_of(most, a.c))));
+  if (a.part) {
+    if (m < a.M)
+      for (int p0 = g; p0 < a.parts; p0 += 8 * kBetweenWarps) {
+        float2 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = p0 + k * kBetweenWarps < a.parts ? a.part[(int64_t)(p0 + k * kBetweenWarps) * a.M + m] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) add(v[k]);
+      }
+    sm[g][lane] = make_float2(most, sum);
+    __syncthreads();
   }
-  a.loss[m] = loss;
-  a.stats[m] = make_float2(most, live ? sum : INFINITY);
-}
-
-// x with the absent rows' values 0, as 0 times an infinity or NaN there would
-// reach grad_w; and for binary16 gz's power of two and its reciprocal.
-struct Prepare {
-  ss_dense x;
-  void *to;
-  int64_t ld;
-  const int64_t *targets;
-  const float *weight, *grad_loss;
-  float inv_t;
-  int64_t V;
-  float *factor;  // or null
-};
-template <int kN>
-__global__ void __launch_bounds__(256) k_prepare(const Prepare a) {
-  using P = Pack<uint16_t, kN>;
-  const int64_t M = a.x.n_rows, K = a.x.n_cols;
-  for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
-    const int64_t t = a.targets[m];
-    const bool there = t >= 0 && t < a.V && (!a.weight || a.weight[m] != 0.0f);
-    const uint16_t *from = static_cast<const uint16_t *>(a.x.data) + m * a.x.ld;
-    uint16_t *to = static_cast<uint16_t *>(a.to) + m * a.ld;
-    for (int64_t c = (int64_t)threadIdx.x * kN; c < K; c += 256 * kN) {
-      P v = {};
-      if (there) v = *reinterpret_cast<const P *>(from + c);
-      *reinterpret_cast<P *>(to + c) = v;
+  if (g == 0 && m < a.M) {
+    const int64_t target = a.targets[m];
+    const float weight = a.weight ? a.weight[m] : 1.0f;
+    const bool past = target >= a.V;
+    if (past) flag(a.status, DEV_OUT_OF_RANGE);
+    bool live = target >= 0 && !past && weight != 0.0f;
+    there[lane] = live;
+    if (a.part) {
+      for (int k = 1; k < kBetweenWarps; ++k) add(sm[k][lane]);
+      float loss = 0.0f;
+      if (live) {
+        const float z = a.here[m];
+        live = z != -INFINITY;
+        if (live) loss = weight * (kLn2 * (log2f(sum) - fmaf(z, a.c, -base_of(most, a.c))));
+      }
+      a.loss[m] = loss;
+      if (a.stats) a.stats[m] = make_float2(most, live ? sum : INFINITY);
+    } else {
+      most = a.stats[m].x;
+      sum = a.stats[m].y;
+      live = live && sum != INFINITY;
+    }
+    if (a.rows) {
+      const float scale = weight * (a.grad_loss ? a.grad_loss[m] : 1.0f) * a.inv_t;
+      a.rows[m] = live ? Row{base_of(most, a.c), scale / sum, scale, (int32_t)target} : absent_row();
+    }
+  }
+  if (!a.rows) return;
+  __syncthreads();
+  for (int r = g; r < 32; r += kBetweenWarps) {
+    const int64_t row = (int64_t)blockIdx.x * 32 + r;
+    if (row >= a.M) break;
+    uint16_t *to = static_cast<uint16_t *>(a.to) + row * a.ld;
+    const uint16_t *from = static_cast<const uint16_t *>(a.x.data) + row * a.x.ld;
+    const bool same = from == to;
+    if (same && there[r]) continue;
+    if (a.vec) {
+      for (int64_t c = (int64_t)lane * 8; c < a.x.n_cols; c += 256)
+        *reinterpret_cast<uint4 *>(to + c) = there[r] ? *reinterpret_cast<const uint4 *>(from + c) : make_uint4(0, 0, 0, 0);
+    } else {
+      for (int64_t c = lane; c < a.x.n_cols; c += 32) to[c] = there[r] ? from[c] : (uint16_t)0;
     }
   }
   if (!a.factor || blockIdx.x != 0) return;
-  __shared__ float sm[8];
-  float most = 0.0f;
-  for (int64_t m = threadIdx.x; m < M; m += 256) {
-    const float g = fabsf((a.weight ? a.weight[m] : 1.0f) * (a.grad_loss ? a.grad_loss[m] : 1.0f) * a.inv_t);
-    if (g < INFINITY) most = fmaxf(most, g);
+  most = 0.0f;
+#pragma unroll 4
+  for (int64_t r = threadIdx.x; r < a.M; r += 32 * kBetweenWarps) {
+    const float v = fabsf((a.weight ? a.weight[r] : 1.0f) * (a.grad_loss ? a.grad_loss[r] : 1.0f) * a.inv_t);
+    if (v < INFINITY) most = fmaxf(most, v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = most;
+  if (lane == 0) sm[g][0].x = most;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int k = 1; k < 8; ++k) most = fmaxf(most, sm[k]);
+    for (int k = 1; k < kBetweenWarps; ++k) most = fmaxf(most, sm[k][0].x);
     const int e = most > 0.0f ? max(-100, min(100, 14 - ilogbf(most))) : 0;
     a.factor[0] = ldexpf(1.0f, e);
     a.factor[1] = ldexpf(1.0f, -e);
@@ -322,8 +450,9 @@ int64_t units_of(const ss_handle *h, int64_t tiles_a, int64_t tiles_b) {
 
 // The scratch of a call, in this order.
 struct Room {
-  int64_t V, K, piece, x, w, factor, part, here, stats, gz, acc, sums;
+  int64_t V, K, piece, x, w, factor, part, here, rows, gz, acc, sums;
   int64_t units, parts;
+  bool whole_sums;  // the columns' sums of all pieces at once
   Room(const ss_handle *h, const ss_dense &x_, const ss_dense &w_, int32_t mode) {
     const int64_t M = x_.n_rows, tiles_a = up(M, 2 * kTileM);
     V = w_.n_rows;
@@ -338,13 +467,14 @@ struct Room {
     factor = grad ? SS_SCRATCH_ALIGN : 0;
     part = loss ? align_up(units * 4 * M * (int64_t)sizeof(float2)) : 0;
     here = loss ? align_up(M * 4) : 0;
-    stats = mode == XENT_STEP ? align_up(M * 8) : 0;
+    rows = grad ? align_up(M * (int64_t)sizeof(Row)) : 0;
     gz = grad ? align_up(M * piece * 2) : 0;
     parts = grad ? grad_product_parts(h, M, piece, K) : 1;
     acc = grad && (piece < V || parts > 1) ? parts * grad_part_bytes(M, K) : 0;
-    sums = grad ? align_up(tiles_a * 8 * piece * 4) : 0;
+    whole_sums = tiles_a * 2 * V <= (int64_t)1 << 26;
+    sums = grad ? align_up(tiles_a * 2 * (whole_sums ? V : piece) * 4) : 0;
   }
-  int64_t bytes() const { return x + w + factor + part + here + stats + gz + acc + sums; }
+  int64_t bytes() const { return x + w + factor + part + here + rows + gz + acc + sums; }
 };
 
 ss_dense rows_from(const ss_dense &m, int64_t first, int64_t n) {
@@ -354,8 +484,7 @@ ss_dense rows_from(const ss_dense &m, int64_t first, int64_t n) {
   return r;
 }
 
-template <bool kGrad>
-cudaError_t run_logits(ss_handle *h, Logits &p, const ss_dense &x, const ss_dense &w, cudaStream_t s, int *queued) {
+cudaError_t run_logits(ss_handle *h, Logits &p, const ss_dense &x, const ss_dense &w, bool gradient, bool beside, cudaStream_t s, int *queued) {
   p.blocks_k = (int32_t)up(x.n_cols, kRowBytes / 2);
   p.tiles_a = (int32_t)up(x.n_rows, 2 * kTileM);
   p.tiles_b = (int32_t)up(w.n_rows, kBN);
@@ -363,15 +492,17 @@ cudaError_t run_logits(ss_handle *h, Logits &p, const ss_dense &x, const ss_dens
   p.status = h->d_status;
   p.M = x.n_rows;
   p.V = w.n_rows;
+  p.bias_pairs = reinterpret_cast<uintptr_t>(p.bias) % 8 == 0;
+  auto kernel = !gradient ? k_statistics : x.type == SS_VALUES_BF16 ? k_logit_gradient<__nv_bfloat16> : k_logit_gradient<__half>;
+  const size_t smem = gradient ? PairRing<kBN, 2>::kSmem : PairRing<kBN, 0>::kSmem;
   cudaError_t e = encode(&p.a, x, kRowBytes / 2, kTileM);
   if (e == cudaSuccess) e = encode(&p.b, w, kRowBytes / 2, kBN / 2);
-  if (e == cudaSuccess && kGrad) e = encode_out(&p.gz, p.out);
-  if (e == cudaSuccess) e = ensure_dyn_smem(k_logits<kGrad>, PairRing<kBN, kGrad ? 1 : 0>::kSmem);
+  if (e == cudaSuccess && gradient) e = encode_out(&p.gz, p.out);
+  if (e == cudaSuccess) e = ensure_dyn_smem(kernel, smem);
   if (e != cudaSuccess) return e;
   const int64_t pairs = std::min<int64_t>((int64_t)p.tiles_a * p.units, std::max(1, h->sm_count / 2));
-  k_logits<kGrad><<<(unsigned)(2 * pairs), kPairThreads, PairRing<kBN, kGrad ? 1 : 0>::kSmem, s>>>(p);
   *queued += 1;
-  return cudaGetLastError();
+  return launch_beside(kernel, (unsigned)(2 * pairs), kPairThreads, smem, s, beside, p);
 }
 
 }  // namespace
@@ -400,53 +531,64 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
     return p;
   };
   ss_dense x = a.x, w = a.w;
-  float *factor = nullptr;
+  void *copy = grad ? take(room.x) : nullptr;
   if (grad) {
-    Prepare p = {a.x, take(room.x), padded_ld(a.x), a.targets, a.weight, a.grad_loss, 1.0f / a.temperature, V, nullptr};
-    x.data = p.to;
-    x.ld = p.ld;
-    if ((e = launch_aligned_rows(h, &w, nullptr, &at, s, queued)) != cudaSuccess) return e;
-    float *f = reinterpret_cast<float *>(take(room.factor));
-    if (a.x.type == SS_VALUES_F16) p.factor = factor = f;
-    const unsigned blocks = (unsigned)std::min<int64_t>(M, 8 * (int64_t)std::max(1, h->sm_count));
-    if (rows_aligned(a.x, 16) && K % 8 == 0)
-      k_prepare<8><<<blocks, 256, 0, s>>>(p);
-    else
-      k_prepare<1><<<blocks, 256, 0, s>>>(p);
-    *queued += 1;
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    unsigned char *to = static_cast<unsigned char *>(copy);
+    // rows that start anywhere are copied here, the absent ones cleared later
+    if ((e = launch_aligned_rows(h, &x, &w, &to, s, queued)) != cudaSuccess) return e;
+    at += room.w;
   } else if ((e = launch_aligned_rows(h, &x, &w, &at, s, queued)) != cudaSuccess) {
     return e;
   }
-  float2 *stats = reinterpret_cast<float2 *>(a.stats);
   Logits p = {};
-  p.targets = a.targets;
   p.c = kLog2e / a.temperature;
+  p.factor = nullptr;
+  Between b = {};
+  b.weight = a.weight;
+  b.grad_loss = a.grad_loss;
+  b.targets = a.targets;
+  b.M = M;
+  b.V = V;
+  b.c = p.c;
+  b.inv_t = 1.0f / a.temperature;
+  b.loss = a.loss;
+  b.stats = reinterpret_cast<float2 *>(a.stats);
+  b.status = h->d_status;
+  float *factor = reinterpret_cast<float *>(take(room.factor));
   if (loss) {
+    p.targets = a.targets;
     p.part = reinterpret_cast<float2 *>(take(room.part));
     p.here = reinterpret_cast<float *>(take(room.here));
-    if (mode == XENT_STEP) stats = reinterpret_cast<float2 *>(take(room.stats));
     p.bias = a.bias;
     p.units = (int32_t)room.units;
-    if ((e = run_logits<false>(h, p, x, w, s, queued)) != cudaSuccess) return e;
-    const Join j = {p.part, p.here, a.weight, a.targets, M, V, (int32_t)room.units * 4, p.c, a.loss, stats, h->d_status};
-    k_join<<<(unsigned)up(M, 32), 256, 0, s>>>(j);
-    *queued += 1;
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = run_logits(h, p, x, w, false, *queued > 0, s, queued)) != cudaSuccess) return e;
+    b.part = p.part;
+    b.here = p.here;
+    b.parts = (int32_t)room.units * 4;
   }
-  if (!grad) return cudaSuccess;
-  p.stats = stats;
-  p.weight = a.weight;
-  p.grad_loss = a.grad_loss;
-  p.factor = factor;
-  p.inv_t = 1.0f / a.temperature;
+  if (grad) {
+    b.rows = reinterpret_cast<Row *>(take(room.rows));
+    b.x = x;
+    b.to = copy;
+    b.ld = padded_ld(a.x);
+    b.vec = K % 8 == 0 && rows_aligned(x, 16);
+    b.factor = a.x.type == SS_VALUES_F16 ? factor : nullptr;
+  }
+  const bool first = *queued == 0;
+  *queued += 1;
+  if ((e = launch_beside(k_between, (unsigned)up(M, 32), 32 * kBetweenWarps, 0, s, !first, b)) != cudaSuccess || !grad) return e;
+  x.data = copy;
+  x.ld = b.ld;
+  p.rows = b.rows;
+  p.factor = b.factor;
   void *gz = take(room.gz);
   grad_products g = {};
   g.x = x;
   g.grad_x = a.grad_x;
   g.acc = reinterpret_cast<float *>(take(room.acc));
   g.parts = (int32_t)room.parts;
-  g.factor = factor ? factor + 1 : nullptr;
+  g.beside = true;
+  g.factor = b.factor ? b.factor + 1 : nullptr;
   float *sums = reinterpret_cast<float *>(take(room.sums));
   const int64_t tiles_a = up(M, 2 * kTileM);
   for (int64_t first = 0; first < V; first += room.piece) {
@@ -455,18 +597,22 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
     p.out = {gz, M, n, room.piece, a.x.type};
     p.first = first;
     p.bias = a.bias ? a.bias + first : nullptr;
-    p.sums = a.grad_bias ? sums : nullptr;
+    p.ld_sums = room.whole_sums ? V : n;
+    p.sums = a.grad_bias ? sums + (room.whole_sums ? first : 0) : nullptr;
     p.units = (int32_t)units_of(h, tiles_a, up(n, kBN));
-    if ((e = run_logits<true>(h, p, x, wp, s, queued)) != cudaSuccess) return e;
-    if (a.grad_bias) {
-      if ((e = launch_sum_rows(h, sums, up(M, 32), n, a.grad_bias + first, SS_VALUES_F32, s)) != cudaSuccess) return e;
-      *queued += 1;
-    }
+    if ((e = run_logits(h, p, x, wp, true, true, s, queued)) != cudaSuccess) return e;
     g.wide = wp;
     g.gz = p.out;
     g.grad_w = a.grad_w.data ? rows_from(a.grad_w, first, n) : a.grad_w;
     g.begun = first > 0;
     g.ends = first + n == V;
+    g.sums = nullptr;
+    if (a.grad_bias && (g.ends || !room.whole_sums)) {
+      g.sums = sums;
+      g.sum_rows = up(M, kTileM);
+      g.sum_cols = room.whole_sums ? V : n;
+      g.sum_to = a.grad_bias + (room.whole_sums ? 0 : first);
+    }
     if ((e = launch_grad_products(h, g, s, queued)) != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -292,6 +292,11 @@ struct grad_products {
   const float *factor;  // device float or null: 1
   int32_t parts;
   bool begun, ends;
+  bool beside;  // the kernel before is of the same call
+  // with it, sum_to[c] = the sum of column c of sums[sum_rows][sum_cols], or null
+  const float *sums;
+  int64_t sum_rows, sum_cols;
+  float *sum_to;
 };
 int64_t grad_product_parts(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *clocks = nullptr);
 int64_t grad_part_bytes(int64_t M, int64_t K);

@@ -10,8 +10,8 @@
 // dealt out in advance: one product's tiles evenly, the other's to whoever has
 // less, so that all pairs end within a tile of each other.  Where
 // grad_x's tiles are too few or too long for that, its sum is split into shares
-// (`parts`), each added up in a float32 matrix of its own, which k_join_parts
-// adds up in their order: no atomics, the same bits every time.
+// (`parts`), each added up in a float32 matrix of its own, which k_finish adds
+// up in their order: no atomics, the same bits every time.
 //
 // Bound by the tensor cores.
 #include <algorithm>
@@ -137,16 +137,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_g
       });
 }
 
-// out = the sum of the parts.
+// What is left to add up: grad_x of its parts, and the sums of columns (a
+// bias's gradient), each in a fixed order.  Blocks of the first kind take rows of
+// grad_x, then come those of 1024 columns.
+struct Finish {
+  const float *parts;
+  int64_t ld;
+  int32_t n;
+  ss_dense out;
+  int32_t blocks_x;
+  const float *sums;
+  int64_t sum_rows, sum_cols;
+  float *sum_to;
+};
 template <typename T>
-__global__ void __launch_bounds__(256) k_join_parts(const float *parts, int64_t ld, int32_t n, const ss_dense out) {
-  for (int64_t row = blockIdx.x; row < out.n_rows; row += gridDim.x)
-    for (int64_t c = threadIdx.x; c < out.n_cols; c += 256) {
-      float v = 0.0f;
+__global__ void __launch_bounds__(256) k_finish(const Finish a) {
+  tc::wait_before();
+  tc::let_next();
+  if ((int)blockIdx.x < a.blocks_x) {
+    for (int64_t row = blockIdx.x; row < a.out.n_rows; row += a.blocks_x)
+      for (int64_t c = threadIdx.x; c < a.out.n_cols; c += 256) {
+        float v = 0.0f;
 #pragma unroll 4
-      for (int p = 0; p < n; ++p) v += parts[((int64_t)p * out.n_rows + row) * ld + c];
-      static_cast<T *>(out.data)[row * out.ld + c] = Type<T>::down(v);
-    }
+        for (int p = 0; p < a.n; ++p) v += a.parts[((int64_t)p * a.out.n_rows + row) * a.ld + c];
+        static_cast<T *>(a.out.data)[row * a.out.ld + c] = Type<T>::down(v);
+      }
+    return;
+  }
+  const int64_t c0 = (int64_t)((int)blockIdx.x - a.blocks_x) * 1024 + threadIdx.x;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int64_t r = 0; r < a.sum_rows; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c0 + 256 * i < a.sum_cols) v[i] += a.sums[r * a.sum_cols + c0 + 256 * i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c0 + 256 * i < a.sum_cols) a.sum_to[c0 + 256 * i] = v[i];
 }
 
 int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
@@ -219,7 +246,7 @@ int64_t grad_part_bytes(int64_t M, int64_t K) { return align_up(M * part_ld(K) *
 cudaError_t launch_grad_products(ss_handle *h, const grad_products &g, cudaStream_t s, int *queued) {
   const int64_t M = g.gz.n_rows, N = g.gz.n_cols, K = g.x.n_cols;
   const bool with_x = g.grad_x.data != nullptr, with_w = g.grad_w.data != nullptr;
-  if (!with_x && !with_w) return cudaSuccess;
+  if (!with_x && !with_w && !g.sums) return cudaSuccess;
   Products p = {};
   const int64_t parts = std::min<int64_t>(g.parts, up(N, 64));
   p.deal = deal_of(h, M, N, K, parts, with_x, with_w, nullptr);
@@ -250,16 +277,26 @@ cudaError_t launch_grad_products(ss_handle *h, const grad_products &g, cudaStrea
   constexpr int kSmem = PairRing<kBN, 1>::kSmem;
   if (e == cudaSuccess) e = ensure_dyn_smem(k_grad_products, kSmem);
   if (e != cudaSuccess) return e;
-  k_grad_products<<<(unsigned)(2 * p.deal.pairs), kPairThreads, kSmem, s>>>(p);
+  if (with_x || with_w) {
+    e = launch_beside(k_grad_products, (unsigned)(2 * p.deal.pairs), kPairThreads, kSmem, s, g.beside, p);
+    *queued += 1;
+  }
+  const bool join = with_x && g.ends && g.parts > 1;
+  if (e != cudaSuccess || (!join && !g.sums)) return e;
+  Finish f = {};
+  if (join) {
+    f.parts = g.acc;
+    f.ld = part_ld(K);
+    f.n = g.parts;
+    f.out = g.grad_x;
+    f.blocks_x = (int32_t)std::min<int64_t>(M, 8 * (int64_t)std::max(1, h->sm_count));
+  }
+  f.sums = g.sums;
+  f.sum_rows = g.sum_rows;
+  f.sum_cols = g.sum_cols;
+  f.sum_to = g.sum_to;
+  const unsigned blocks = (unsigned)(f.blocks_x + (g.sums ? up(g.sum_cols, 1024) : 0));
   *queued += 1;
-  if ((e = cudaGetLastError()) != cudaSuccess || !with_x || !g.ends || g.parts == 1) return e;
-  const unsigned blocks = (unsigned)std::min<int64_t>(M, 8 * (int64_t)std::max(1, h->sm_count));
-  if (g.grad_x.type == SS_VALUES_F32)
-    k_join_parts<float><<<blocks, 256, 0, s>>>(g.acc, part_ld(K), g.parts, g.grad_x);
-  else if (g.grad_x.type == SS_VALUES_BF16)
-    k_join_parts<__nv_bfloat16><<<blocks, 256, 0, s>>>(g.acc, part_ld(K), g.parts, g.grad_x);
-  else
-    k_join_parts<__half><<<blocks, 256, 0, s>>>(g.acc, part_ld(K), g.parts, g.grad_x);
-  *queued += 1;
-  return cudaGetLastError();
+  auto kernel = g.grad_x.type == SS_VALUES_F32 ? k_finish<float> : g.grad_x.type == SS_VALUES_BF16 ? k_finish<__nv_bfloat16> : k_finish<__half>;
+  return launch_beside(kernel, blocks, 256, 0, s, true, f);
 }

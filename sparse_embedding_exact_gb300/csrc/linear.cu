@@ -1116,7 +1116,7 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
   }
   int64_t parts_x;
   if (a.grad_x.data && a.grad_w.data && together(h, M, N, x.n_cols, &parts_x)) {
-    grad_products g = {gz, w, x, a.grad_x, a.grad_w, reinterpret_cast<float *>(scratch), nullptr, (int32_t)parts_x, false, true};
+    grad_products g = {gz, w, x, a.grad_x, a.grad_w, reinterpret_cast<float *>(scratch), nullptr, (int32_t)parts_x, false, true, *queued > 0};
     return launch_grad_products(h, g, s, queued);
   }
   if (a.grad_x.data &&

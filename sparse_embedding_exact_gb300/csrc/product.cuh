@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <utility>
 
 #include "tc.cuh"
 
@@ -157,6 +158,7 @@ __device__ __forceinline__ void pair_products(const CUtensorMap *map_a, const CU
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t bars[2 * R::kStages + 4];
   __shared__ uint32_t tmem_slot;
+  __shared__ int stalled;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = (tc::smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t rank = tc::cluster_rank();
@@ -166,6 +168,7 @@ __device__ __forceinline__ void pair_products(const CUtensorMap *map_a, const CU
   auto acc_free = [&](int b) { return tc::smem_u32(&bars[2 * R::kStages + 2 + b]); };
   constexpr uint32_t kCols = 2 * kBN;
   if (tid == 0) {
+    stalled = 0;
     for (int i = 0; i < 2 * R::kStages + 2; ++i) tc::bar_init(tc::smem_u32(&bars[i]), 1);
     for (int b = 0; b < 2; ++b) tc::bar_init(acc_free(b), 2 * kEpiWarps);
     tc::bar_init_fence();
@@ -185,6 +188,8 @@ __device__ __forceinline__ void pair_products(const CUtensorMap *map_a, const CU
   tc::cluster_sync();  // both blocks' barriers exist before either is signalled
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
+  tc::wait_before();
+  tc::let_next();
 
   constexpr int kUnit = kF8 ? kRowBytes : kRowBytes / 2;
 
@@ -280,7 +285,9 @@ __device__ __forceinline__ void pair_products(const CUtensorMap *map_a, const CU
     Walk w = walk;
     for (Tile t; w.next(t); ++n) {
       const int b = n & 1;
-      if (!tc::bar_wait(acc_full(b), (uint32_t)((n >> 1) & 1), status)) break;
+      // a wait that runs out is flagged and gone on from, as the warps may meet
+      // at barriers of their own
+      tc::bar_wait_on(acc_full(b), (uint32_t)((n >> 1) & 1), status, &stalled);
       tc::fence_after();
       epi(w, t, q, quarter, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kBN), boxes, [&] {
         tc::fence_before();  // read out: the products may write it again
@@ -301,6 +308,24 @@ __device__ __forceinline__ void pair_products(const CUtensorMap *map_a, const CU
 }
 
 // ---------------------------------------------------------------- host side
+// Launches a kernel that may start while the one before it in the stream ends:
+// it sets itself up and waits for that one's end (tc::wait_before) before it
+// touches its data.  The kernel before must be one of the same call.
+template <typename... P, typename... A>
+cudaError_t launch_beside(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, bool beside, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

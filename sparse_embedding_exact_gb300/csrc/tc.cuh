@@ -256,6 +256,28 @@ __device__ __forceinline__ void load_acc16(uint32_t addr, float (&f)[16]) {
   for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(r[i]);
 }
 
+// 32 columns of 16 tensor-memory lanes, without the wait: of columns 8 i + 2 (t % 4)
+// and the next, thread t has those of lane t / 4 in r[4 i], r[4 i + 1] and those of
+// lane t / 4 + 8 in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void load_acc16x32(uint32_t addr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+// Four matrices of 8 x 8 16-bit values: thread t holds values (t / 4, 2 (t % 4))
+// and the next of each, and the shared address of row t % 8 of matrix t / 8.
+__device__ __forceinline__ void store_matrices(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// For kernels launched beside the end of the one before (launch_beside): until
+// that one is done, and leave for the next one to be launched.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
