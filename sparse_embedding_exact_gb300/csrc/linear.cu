@@ -81,6 +81,31 @@ __device__ __forceinline__ float normal_cdf(float z, float &e) {
   return z > 0.0f ? 1.0f - tail : tail;
 }
 
+// The same for two values, one instruction for both where there is one: the same
+// operations in the same order, so the same bits.
+__device__ __forceinline__ Two normal_cdf2(Two z, Two &e) {
+  const float2 f = both(z);
+  float2 t, x;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(fmaf(0.304055929f, fabsf(f.x), 1.0f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(fmaf(0.304055929f, fabsf(f.y), 1.0f)));
+  const float2 q = both(z * z * two(-0.72134752044448170f, -0.72134752044448170f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.x) : "f"(q.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.y) : "f"(q.y));
+  e = two(x.x, x.y);
+  const Two u = two(t.x, t.y);
+  auto same = [](float c) { return two(c, c); };
+  Two poly = fma_of(u, same(0.0368539476f), same(-0.155186636f));
+  poly = fma_of(u, poly, same(0.191852769f));
+  poly = fma_of(u, poly, same(-0.0428628107f));
+  poly = fma_of(u, poly, same(0.12342219f));
+  poly = fma_of(u, poly, same(0.102475558f));
+  poly = fma_of(u, poly, same(0.12218772f));
+  poly = fma_of(u, poly, same(0.121257304f));
+  const Two tail = u * poly * e;
+  const float2 low = both(tail), high = both(fma_of(tail, same(-1.0f), same(1.0f)));
+  return two(f.x > 0.0f ? high.x : low.x, f.y > 0.0f ? high.y : low.y);
+}
+
 // (1 + tanh u) / 2 with u = sqrt(2 / pi) (z + 0.044715 z^3), as 1 / (1 + exp(-2 u)):
 // 1 + tanh u itself is the difference of two values near 1 where z is negative.
 __device__ __forceinline__ float tanh_share(float z) {
@@ -275,10 +300,23 @@ __device__ __forceinline__ void keep32(const Epilogue &ep, int64_t m, int64_t n0
   const ss_kept &k = ep.keep;
   if (m >= k.n_rows) return;
   const bool whole = n0 + 32 <= k.n_cols;
-  uint32_t most = 0;
+  float top = 0.0f;  // NaN is left out by fmaxf, an infinity after it
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (whole || n0 + i < k.n_cols) most = max(most, finite_bits(v[i]));
+    for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(v[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n0 + i < k.n_cols) top = fmaxf(top, fabsf(v[i]));
+  }
+  const bool odd = top == INFINITY;
+  uint32_t most = __float_as_uint(top);
+  if (odd) {
+    most = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n0 + i < k.n_cols) most = max(most, finite_bits(v[i]));
+  }
   const int e = exponent_of(most, least_exponent(ep.y.type));
   const float down = power_of(-e);
   uint8_t *to = static_cast<uint8_t *>(k.codes) + m * k.ld + n0;
@@ -289,7 +327,14 @@ __device__ __forceinline__ void keep32(const Epilogue &ep, int64_t m, int64_t n0
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float *f = v + 16 * part + 4 * j;
-      w[j] = codes2(scaled_down(f[0], down), scaled_down(f[1], down)) | codes2(scaled_down(f[2], down), scaled_down(f[3], down)) << 16;
+      w[j] = codes2(f[0] * down, f[1] * down) | codes2(f[2] * down, f[3] * down) << 16;
+    }
+    if (odd) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float *f = v + 16 * part + 4 * j;
+        w[j] = codes2(scaled_down(f[0], down), scaled_down(f[1], down)) | codes2(scaled_down(f[2], down), scaled_down(f[3], down)) << 16;
+      }
     }
     if (wide) {
       reinterpret_cast<uint4 *>(to)[part] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -304,8 +349,19 @@ __device__ __forceinline__ void keep32(const Epilogue &ep, int64_t m, int64_t n0
 
 template <int kAct>
 __device__ __forceinline__ void act32(float (&v)[32]) {
+  if constexpr (kAct == SS_ACT_GELU) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_of<kAct>(v[i]);
+    for (int i = 0; i < 32; i += 2) {
+      const Two z = two(v[i], v[i + 1]);
+      Two e;
+      const float2 y = both(z * normal_cdf2(z, e));
+      v[i] = y.x;
+      v[i + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = act_of<kAct>(v[i]);
+  }
 }
 
 // 32 columns n0 .. of rows m0 + lane: everything that follows the product,
@@ -318,7 +374,9 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *
   const bool there = m0 < M && n0 < N, whole = ep.vec && n0 + 32 <= N;
   const bool by_box = there && ep.residual.data && ep.residual.type != SS_VALUES_F32;
   Box res;
-  if (by_box) res = load_box(ep.residual, whole, m0, n0, lane);  // asked for early: the rest hides the wait
+  // asked for early, the rest hides the wait; where z is kept in 8 bits late, as
+  // its 16 registers would be spilled
+  if (!kKeep && by_box) res = load_box(ep.residual, whole, m0, n0, lane);
   float v[32];
   {
     uint32_t r[32];
@@ -347,6 +405,7 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *
     default: break;
   }
   if (by_box) {
+    if (kKeep) res = load_box(ep.residual, whole, m0, n0, lane);
     if (ep.residual.type == SS_VALUES_BF16)
       add_box<__nv_bfloat16>(res, whole, boxes + kStaging, lane, v);
     else
@@ -695,8 +754,21 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
           widen(gv[u], g);
           if (kAct != SS_ACT_NONE) {
             if (!kKept) widen(zv[u], z);
+            const float *of = kKept ? zk[u] : z;
+            if constexpr (kAct == SS_ACT_GELU && kN > 1) {
 #pragma unroll
-            for (int i = 0; i < kN; ++i) g[i] *= act_slope<kAct>(kKept ? zk[u][i] : z[i]);
+              for (int i = 0; i < kN; i += 2) {
+                const Two zz = two(of[i], of[i + 1]);
+                Two ex;
+                const Two cdf = normal_cdf2(zz, ex);
+                const float2 slope = both(fma_of(zz * two(0.39894228040143268f, 0.39894228040143268f), ex, cdf));
+                g[i] *= slope.x;
+                g[i + 1] *= slope.y;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kN; ++i) g[i] *= act_slope<kAct>(of[i]);
+            }
           }
           if (gz) store_pack(gz + (m + u * step) * ld + c, narrow<T, kN>(g));
 #pragma unroll
