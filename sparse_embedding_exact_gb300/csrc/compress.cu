@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "kept.cuh"
+#include "tc.cuh"
 
 namespace {
 
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) k_compress(const ss_dense x, const s
 
 template <typename T, int kN, int kAlong>
 __global__ void __launch_bounds__(kThreads) k_expand(const ss_kept x, const ss_dense y) {
+  tc::let_next();
   const int32_t units = (int32_t)((y.n_cols + kN - 1) / kN);
   const Place<kAlong> at;
   uint2 q[4];
@@ -221,6 +223,7 @@ __global__ void __launch_bounds__(kThreads) k_expand(const ss_kept x, const ss_d
       }
     }
   }
+  tc::wait_before();  // what follows waits for this kernel, and so for the one before it
 }
 
 // Calls run(kAlong, grid, block) for `rows` rows of `units` units; a block's
@@ -259,16 +262,28 @@ cudaError_t compress_typed(const ss_dense &x, const ss_kept &out, cudaStream_t s
   return cudaGetLastError();
 }
 template <typename T>
-cudaError_t expand_typed(const ss_kept &x, const ss_dense &y, cudaStream_t s) {
+cudaError_t expand_typed(const ss_kept &x, const ss_dense &y, cudaStream_t s, bool beside) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  cudaError_t e = cudaSuccess;
   if (y.n_cols % 8 == 0 && rows_aligned(y, 16) && kept_aligned(x, 8))
     laid_out(y.n_rows, y.n_cols / 8, 4, [&](auto along, dim3 grid, dim3 block) {
-      k_expand<T, 8, decltype(along)::value><<<grid, block, 0, s>>>(x, y);
+      cfg.gridDim = grid;
+      cfg.blockDim = block;
+      e = cudaLaunchKernelEx(&cfg, k_expand<T, 8, decltype(along)::value>, x, y);
     });
   else
     laid_out(y.n_rows, y.n_cols, 32, [&](auto along, dim3 grid, dim3 block) {
-      k_expand<T, 1, decltype(along)::value><<<grid, block, 0, s>>>(x, y);
+      cfg.gridDim = grid;
+      cfg.blockDim = block;
+      e = cudaLaunchKernelEx(&cfg, k_expand<T, 1, decltype(along)::value>, x, y);
     });
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
@@ -298,7 +313,7 @@ cudaError_t launch_compress(const ss_dense &x, const ss_kept &out, cudaStream_t 
   }
 }
 
-cudaError_t launch_expand(const ss_kept &x, const ss_dense &y, cudaStream_t s, int *queued) {
+cudaError_t launch_expand(const ss_kept &x, const ss_dense &y, cudaStream_t s, int *queued, bool beside) {
   *queued = y.n_rows > 0 && y.n_cols > 0;
   if (!*queued) return cudaSuccess;
   if (y.n_cols > kMostCols) {
@@ -310,15 +325,15 @@ cudaError_t launch_expand(const ss_kept &x, const ss_dense &y, cudaStream_t s, i
       from.codes = static_cast<uint8_t *>(x.codes) + c;
       from.scale += c / kGroup;
       int one;
-      const cudaError_t e = launch_expand(from, part, s, &one);
+      const cudaError_t e = launch_expand(from, part, s, &one, beside || c > 0);
       if (e != cudaSuccess) return e;
       *queued += c > 0;
     }
     return cudaSuccess;
   }
   switch (y.type) {
-    case SS_VALUES_F32: return expand_typed<float>(x, y, s);
-    case SS_VALUES_BF16: return expand_typed<__nv_bfloat16>(x, y, s);
-    default: return expand_typed<__half>(x, y, s);
+    case SS_VALUES_F32: return expand_typed<float>(x, y, s, beside);
+    case SS_VALUES_BF16: return expand_typed<__nv_bfloat16>(x, y, s, beside);
+    default: return expand_typed<__half>(x, y, s, beside);
   }
 }

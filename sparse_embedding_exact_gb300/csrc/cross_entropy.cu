@@ -436,16 +436,17 @@ int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 // Units of a row of tiles: the fewest for which the pairs, each taking whole
 // units in turn, end soonest.
 int64_t units_of(const ss_handle *h, int64_t tiles_a, int64_t tiles_b) {
-  const int64_t pairs = std::max(1, h->sm_count / 2), most = std::min<int64_t>(tiles_b, 256);
+  const int64_t pairs = std::max(1, h->sm_count / 2);
+  const int64_t most = std::min<int64_t>({tiles_b, 256, 16 * pairs / tiles_a + 4});
   int64_t best = 1, least = INT64_MAX;
-  for (int64_t n = 1; n <= most; ++n) {
-    const int64_t tiles = up(tiles_a * n, pairs) * up(tiles_b, n);
-    if (tiles < least) {
-      least = tiles;
-      best = n;
+  for (int64_t turns = up(tiles_a, pairs);; ++turns) {  // the units that `turns` turns of all pairs take
+    const int64_t n = std::min(most, turns * pairs / tiles_a), tiles = up(tiles_b, n);
+    if (turns * tiles < least) {
+      least = turns * tiles;
+      best = up(tiles_b, tiles);
     }
+    if (n == most) return best;
   }
-  return best;
 }
 
 // The scratch of a call, in this order.

@@ -232,7 +232,8 @@ cudaError_t launch_rms_norm_grad(ss_handle *h, const rms_grad_args &a, cudaStrea
 
 // Values to codes and scales, and back (kept.cuh).
 cudaError_t launch_compress(const ss_dense &x, const ss_kept &out, cudaStream_t s, int *queued);
-cudaError_t launch_expand(const ss_kept &x, const ss_dense &y, cudaStream_t s, int *queued);
+// beside: at the end of the kernel before, which is of the same call.
+cudaError_t launch_expand(const ss_kept &x, const ss_dense &y, cudaStream_t s, int *queued, bool beside = false);
 
 // out[c] = the sum of column c over the n rows of part (one kernel; a fixed
 // order), rounded to `type`.

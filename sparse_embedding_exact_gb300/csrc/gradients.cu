@@ -139,7 +139,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_g
 
 // What is left to add up: grad_x of its parts, and the sums of columns (a
 // bias's gradient), each in a fixed order.  Blocks of the first kind take rows of
-// grad_x, then come those of 1024 columns.
+// grad_x, then come those of 32
+// columns, eight threads a column.
 struct Finish {
   const float *parts;
   int64_t ld;
@@ -164,16 +165,19 @@ __global__ void __launch_bounds__(256) k_finish(const Finish a) {
       }
     return;
   }
-  const int64_t c0 = (int64_t)((int)blockIdx.x - a.blocks_x) * 1024 + threadIdx.x;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int64_t r = 0; r < a.sum_rows; ++r)
+  __shared__ float sm[8][33];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int64_t c = (int64_t)((int)blockIdx.x - a.blocks_x) * 32 + lane;
+  float v = 0.0f;
+  if (c < a.sum_cols)
+#pragma unroll 8
+    for (int64_t r = g; r < a.sum_rows; r += 8) v += a.sums[r * a.sum_cols + c];
+  sm[g][lane] = v;
+  __syncthreads();
+  if (g != 0 || c >= a.sum_cols) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c0 + 256 * i < a.sum_cols) v[i] += a.sums[r * a.sum_cols + c0 + 256 * i];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (c0 + 256 * i < a.sum_cols) a.sum_to[c0 + 256 * i] = v[i];
+  for (int k = 1; k < 8; ++k) v += sm[k][lane];
+  a.sum_to[c] = v;
 }
 
 int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
@@ -204,14 +208,10 @@ Deal deal_of(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t parts,
     const int64_t more = spread % pairs, n_less = spread / pairs, n_more = n_less + (more > 0);
     const int64_t less_end = n_less * cost_s, more_end = n_more * cost_s;
     auto room = [&](int64_t end) { return (pairs - more) * ((end - less_end) / cost_f) + more * ((end - more_end) / cost_f); };
-    int64_t lo = more_end, hi = more_end + (up(filled, pairs) + 1) * cost_f;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (room(mid) >= filled)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
+    // from the mean on, over the ends at which a pair has room for one more
+    int64_t lo = std::max(more_end, (filled * cost_f + less_end * (pairs - more) + more_end * more) / pairs);
+    while (room(lo) < filled)
+      lo = std::min(less_end + ((lo - less_end) / cost_f + 1) * cost_f, more_end + ((lo - more_end) / cost_f + 1) * cost_f);
     if (lo >= best) continue;
     best = lo;
     d.more = (int32_t)more;
@@ -228,7 +228,8 @@ Deal deal_of(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t parts,
 
 int64_t grad_product_parts(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *estimate) {
   int64_t best = 1, least = INT64_MAX;
-  for (int64_t parts = 1; parts <= 16 && (parts == 1 || up(N, 64) / parts >= 4); ++parts) {
+  for (const int64_t parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+    if (parts > 1 && up(N, 64) / parts < 4) break;
     int64_t clocks;
     deal_of(h, M, N, K, parts, true, true, &clocks);
     // the parts written and read again, at 3,000 bytes a clock, and a launch
@@ -295,7 +296,7 @@ cudaError_t launch_grad_products(ss_handle *h, const grad_products &g, cudaStrea
   f.sum_rows = g.sum_rows;
   f.sum_cols = g.sum_cols;
   f.sum_to = g.sum_to;
-  const unsigned blocks = (unsigned)(f.blocks_x + (g.sums ? up(g.sum_cols, 1024) : 0));
+  const unsigned blocks = (unsigned)(f.blocks_x + (g.sums ? up(g.sum_cols, 32) : 0));
   *queued += 1;
   auto kernel = g.grad_x.type == SS_VALUES_F32 ? k_finish<float> : g.grad_x.type == SS_VALUES_BF16 ? k_finish<__nv_bfloat16> : k_finish<__half>;
   return launch_beside(kernel, blocks, 256, 0, s, true, f);

@@ -726,54 +726,80 @@ __global__ void __launch_bounds__(32 * kRowWarps, kM == 1 ? 16 : 1) k_rows(const
 // by memory and, with a gelu, by instructions: 8192 x 4096 bf16 36 us (5.5 TB/s).
 template <typename T, int kN, int kAct, bool kKept>
 __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, const ss_kept kept, T *gz, int64_t ld, float *part) {
+  tc::let_next();
   __shared__ float sm[8][32 * kN + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t M = grad_y.n_rows, N = grad_y.n_cols, c = ((int64_t)blockIdx.x * 32 + lane) * kN;
-  const int64_t step = (int64_t)gridDim.y * 8;
-  const T *gp = static_cast<const T *>(grad_y.data) + c, *zp = static_cast<const T *>(pre.data) + c;
+  const int64_t step = (int64_t)gridDim.y * 8, first = (int64_t)blockIdx.y * 8 + warp;
+  const T *gp = static_cast<const T *>(grad_y.data) + first * grad_y.ld + c;
+  const T *zp = static_cast<const T *>(pre.data) + (kAct != SS_ACT_NONE && !kKept ? first * pre.ld + c : 0);
+  const uint8_t *codes = static_cast<const uint8_t *>(kept.codes) + (kKept ? first * kept.ld + c : 0);
+  const uint8_t *scale = kept.scale + (kKept ? first * kept.ld_scale + c / kGroup : 0);
+  T *to = gz ? gz + first * ld + c : nullptr;
+  const int64_t step_g = step * grad_y.ld, step_z = step * pre.ld, step_c = step * kept.ld, step_s = step * kept.ld_scale, step_to = step * ld;
   float sum[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) sum[i] = 0.0f;
   if (c < N)
-    for (int64_t m = (int64_t)blockIdx.y * 8 + warp; m < M; m += 2 * step) {
+    for (int64_t m = first; m < M; m += 2 * step) {
       Pack<T, kN> gv[2], zv[2];
-      float zk[2][kN];
+      Codes<kN> cv[2];
+      uint32_t byte[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         if (m + u * step < M) {
-          gv[u] = load_pack<T, kN>(gp + (m + u * step) * grad_y.ld);
-          if (kKept)
-            load_kept<kN>(kept, m + u * step, c, zk[u]);
-          else if (kAct != SS_ACT_NONE)
-            zv[u] = load_pack<T, kN>(zp + (m + u * step) * pre.ld);
+          gv[u] = load_pack<T, kN>(gp + u * step_g);
+          if (kKept) {
+            cv[u].load(codes + u * step_c);
+            byte[u] = scale[u * step_s];
+          } else if (kAct != SS_ACT_NONE) {
+            zv[u] = load_pack<T, kN>(zp + u * step_z);
+          }
         }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         if (m + u * step < M) {
           float g[kN], z[kN];
           widen(gv[u], g);
-          if (kAct != SS_ACT_NONE) {
-            if (!kKept) widen(zv[u], z);
-            const float *of = kKept ? zk[u] : z;
-            if constexpr (kAct == SS_ACT_GELU && kN > 1) {
-#pragma unroll
-              for (int i = 0; i < kN; i += 2) {
-                const Two zz = two(of[i], of[i + 1]);
-                Two ex;
-                const Two cdf = normal_cdf2(zz, ex);
-                const float2 slope = both(fma_of(zz * two(0.39894228040143268f, 0.39894228040143268f), ex, cdf));
-                g[i] *= slope.x;
-                g[i + 1] *= slope.y;
-              }
+          if (kKept) {
+            const float s = scale_of_byte(byte[u]);
+            if constexpr (kN == 1) {
+              z[0] = cv[u].one() * s;
             } else {
 #pragma unroll
-              for (int i = 0; i < kN; ++i) g[i] *= act_slope<kAct>(of[i]);
+              for (int i = 0; i < kN; i += 2) {
+                const float2 f = cv[u].pair(i / 2), q = both(two(f.x, f.y) * two(s, s));
+                z[i] = q.x;
+                z[i + 1] = q.y;
+              }
             }
+          } else if (kAct != SS_ACT_NONE) {
+            widen(zv[u], z);
           }
-          if (gz) store_pack(gz + (m + u * step) * ld + c, narrow<T, kN>(g));
+          if constexpr (kAct == SS_ACT_GELU && kN > 1) {
+#pragma unroll
+            for (int i = 0; i < kN; i += 2) {
+              const Two zz = two(z[i], z[i + 1]);
+              Two ex;
+              const Two cdf = normal_cdf2(zz, ex);
+              const Two slope = fma_of(zz * two(0.39894228040143268f, 0.39894228040143268f), ex, cdf);
+              const float2 q = both(two(g[i], g[i + 1]) * slope);
+              g[i] = q.x;
+              g[i + 1] = q.y;
+            }
+          } else if constexpr (kAct != SS_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) g[i] *= act_slope<kAct>(z[i]);
+          }
+          if (to) store_pack(to + u * step_to, narrow<T, kN>(g));
 #pragma unroll
           for (int i = 0; i < kN; ++i) sum[i] += g[i];
         }
+      gp += 2 * step_g;
+      zp += 2 * step_z;
+      codes += 2 * step_c;
+      scale += 2 * step_s;
+      if (to) to += 2 * step_to;
     }
   if (!part) return;
 #pragma unroll
@@ -787,41 +813,71 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
   }
 }
 
-// Copies of matrices with rows of ld values, one of them each blockIdx.y.
+// Copies of matrices into rows of ld values that start on 16-byte boundaries,
+// one of them each blockIdx.y.
 struct Copies {
   ss_dense src[2];
   void *dst[2];
   int64_t ld[2];
 };
+// The 16 bytes at p, which lie anywhere, from the two aligned 16-byte units that
+// hold them where these lie in [begin, end), value by value where not, as far as
+// `end`.
 template <typename T>
-__global__ void __launch_bounds__(256) k_copy_rows(const Copies a) {
-  const bool second = blockIdx.y == 1;
-  const ss_dense src = second ? a.src[1] : a.src[0];
-  const int64_t ld = second ? a.ld[1] : a.ld[0];
-  T *dst = static_cast<T *>(second ? a.dst[1] : a.dst[0]);
-  const int n = (int)src.n_cols;
-  for (int64_t r = blockIdx.x; r < src.n_rows; r += gridDim.x) {
-    const T *p = static_cast<const T *>(src.data) + r * src.ld;
-    T *q = dst + r * ld;
-    for (int c = threadIdx.x; c < n; c += 4 * 256) {  // four loads under way at a time
-      T v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c + u * 256 < n) v[u] = p[c + u * 256];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c + u * 256 < n) q[c + u * 256] = v[u];
+__device__ __forceinline__ uint4 read_anywhere(const unsigned char *p, const unsigned char *begin, const unsigned char *end) {
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+  if (p - off >= begin && p - off + 32 <= end) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p - off), b = *reinterpret_cast<const uint4 *>(p - off + 16);
+    const uint32_t bits = 8 * (off & 3);
+    auto shift = [&](uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, uint32_t v4) {
+      return make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits), __funnelshift_r(v2, v3, bits), __funnelshift_r(v3, v4, bits));
+    };
+    switch (off >> 2) {  // the same for a row's threads
+      case 0: return shift(a.x, a.y, a.z, a.w, b.x);
+      case 1: return shift(a.y, a.z, a.w, b.x, b.y);
+      case 2: return shift(a.z, a.w, b.x, b.y, b.z);
+      default: return shift(a.w, b.x, b.y, b.z, b.w);
     }
   }
+  constexpr int kN = 16 / (int)sizeof(T);
+  T v[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = p + (i + 1) * sizeof(T) <= end ? *reinterpret_cast<const T *>(p + i * sizeof(T)) : T(0);
+  uint4 q;
+  memcpy(&q, v, 16);
+  return q;
+}
+template <typename T>
+__global__ void __launch_bounds__(256) k_copy_rows(const Copies a) {
+  tc::let_next();
+  const bool second = blockIdx.y == 1;
+  const ss_dense src = second ? a.src[1] : a.src[0];
+  const int64_t ld = (second ? a.ld[1] : a.ld[0]) * (int64_t)sizeof(T), bytes = src.n_cols * (int64_t)sizeof(T);
+  unsigned char *dst = static_cast<unsigned char *>(second ? a.dst[1] : a.dst[0]);
+  const unsigned char *from = static_cast<const unsigned char *>(src.data);
+  const unsigned char *end = from + ((src.n_rows - 1) * src.ld + src.n_cols) * (int64_t)sizeof(T);
+  // What lies past a row's end within its last 16 bytes goes along: no one reads
+  // it there.  blockDim.x threads along a row, blockDim.y rows
+  for (int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; r < src.n_rows; r += (int64_t)gridDim.x * blockDim.y)
+    for (int64_t c = (int64_t)threadIdx.x * 16; c < bytes; c += 2 * 16 * (int64_t)blockDim.x) {  // two loads under way at a time
+      const int64_t c1 = c + 16 * (int64_t)blockDim.x;
+      const uint4 v0 = read_anywhere<T>(from + r * src.ld * (int64_t)sizeof(T) + c, from, end);
+      uint4 v1;
+      if (c1 < bytes) v1 = read_anywhere<T>(from + r * src.ld * (int64_t)sizeof(T) + c1, from, end);
+      *reinterpret_cast<uint4 *>(dst + r * ld + c) = v0;
+      if (c1 < bytes) *reinterpret_cast<uint4 *>(dst + r * ld + c1) = v1;
+    }
+  tc::wait_before();  // what follows waits for this kernel, and so for the one before it
 }
 
 // ---------------------------------------------------------------- host side
 // Each matrix itself, or its copy with padded rows at *scratch (advanced past
-// it); one launch.
-cudaError_t aligned_rows(ss_handle *h, std::initializer_list<ss_dense *> ms, unsigned char **scratch, cudaStream_t s, int *queued) {
+// it); one launch, beside the end of the one before where `beside`.
+cudaError_t aligned_rows(ss_handle *h, std::initializer_list<ss_dense *> ms, unsigned char **scratch, cudaStream_t s, int *queued,
+                         bool beside = false) {
   Copies a = {};
   int n = 0;
-  int64_t rows = 0;
+  int64_t rows = 0, units = 1;
   bool bytes = false;
   for (ss_dense *m : ms) {
     if (rows_aligned(*m, 16)) continue;
@@ -830,18 +886,26 @@ cudaError_t aligned_rows(ss_handle *h, std::initializer_list<ss_dense *> ms, uns
     a.ld[n] = padded_ld(*m);
     bytes = size_of(m->type) == 1;
     rows = std::max(rows, m->n_rows);
+    units = std::max(units, (m->n_cols * size_of(m->type) + 15) / 16);
     m->data = *scratch;
     m->ld = a.ld[n++];
     *scratch += align_up(m->n_rows * m->ld * size_of(m->type));
   }
   if (n == 0) return cudaSuccess;
-  const dim3 grid((unsigned)std::min<int64_t>(rows, 8 * std::max(1, h->sm_count)), (unsigned)n);
-  if (bytes)
-    k_copy_rows<uint8_t><<<grid, 256, 0, s>>>(a);
-  else
-    k_copy_rows<uint16_t><<<grid, 256, 0, s>>>(a);
+  unsigned x = 8;
+  while (x < 256 && 2 * (int64_t)x < units) x *= 2;
+  const unsigned y = 256 / x;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((rows + y - 1) / y, 16 * (int64_t)std::max(1, h->sm_count)), (unsigned)n);
+  cfg.blockDim = dim3(x, y);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = beside ? 1 : 0;
   *queued += 1;
-  return cudaGetLastError();
+  return bytes ? cudaLaunchKernelEx(&cfg, k_copy_rows<uint8_t>, a) : cudaLaunchKernelEx(&cfg, k_copy_rows<uint16_t>, a);
 }
 
 template <int kBN, int kMajA, int kMajB, bool kF8>
@@ -928,7 +992,7 @@ Cut cut_of(const ss_handle *h, int64_t rows_a, int64_t rows_b, int64_t blocks_k,
       // Blocks at a time: clusters stay within a group of SMs, and of 152 SMs 36
       // of 4 blocks and 15 of 8 run at once (of 456 places 110 and 51).
       const int64_t an_sm = bn <= 32 ? 3 : bn == 64 ? 2 : 1, places = sms * an_sm;
-      const int64_t at_once = split == 8 ? places * (an_sm > 1 ? 17 : 15) / 19 : split == 4 ? places * 18 / 19 : places;
+      const int64_t at_once = std::max<int64_t>(1, split == 8 ? places * (an_sm > 1 ? 17 : 15) / 19 : split == 4 ? places * 18 / 19 : places);
       const int64_t blocks = up(rows_a, kTileM) * up(rows_b, bn) * split;
       const double sharing = (double)std::min(an_sm, up(blocks, sms));
       // a matrix that one row of tiles reads once comes from memory, not L2
@@ -1049,7 +1113,7 @@ bool together(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *part
   int64_t clocks;
   *parts = grad_product_parts(h, M, N, K, &clocks);
   const double apart = cut_of(h, M, K, (N + 63) / 64, 64, true).clocks + cut_of(h, N, K, (M + 63) / 64, 64, true).clocks;
-  return K > 0 && (double)clocks + 18e3 < apart;
+  return K > 0 && (double)clocks + 12e3 < apart;
 }
 int64_t together_bytes(const ss_handle *h, int64_t M, int64_t N, int64_t K) {
   int64_t parts;
@@ -1130,6 +1194,9 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
     gz.data = scratch;
     scratch += align_up(M * gz.ld * (int64_t)sizeof(T));
   }
+  int64_t parts_x;
+  // also where one of the two is left out: the other's bits are the same then
+  const bool joint = together(h, M, N, x.n_cols, &parts_x);
   float *part = reinterpret_cast<float *>(scratch);
   const int64_t parts = grad_parts(h, M, N);
   scratch += align_up(parts * N * (int64_t)sizeof(float));
@@ -1161,11 +1228,11 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
       default: run(std::integral_constant<int, SS_ACT_NONE>()); break;
     }
     *queued += 1;
-    if (sums) {
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (sums && !joint) {
+      if ((e = launch_sum_rows(h, part, parts, N, a.grad_bias, SS_VALUES_F32, s)) != cudaSuccess) return e;
       *queued += 1;
     }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (sums && (e = launch_sum_rows(h, part, parts, N, a.grad_bias, SS_VALUES_F32, s)) != cudaSuccess) return e;
   }
   auto out = [](const ss_dense &m) {
     Epilogue ep = {};
@@ -1173,22 +1240,27 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
     ep.vec = rows_aligned(m, 16);
     return ep;
   };
-  if (a.grad_x.data && (e = aligned_rows(h, {&w}, &scratch, s, queued)) != cudaSuccess) return e;
+  if (a.grad_x.data && (e = aligned_rows(h, {&w}, &scratch, s, queued, joint && *queued > 0)) != cudaSuccess) return e;
   if (a.grad_w.data) {
     if (a.x_kept.codes) {
       x.ld = padded_ld(x);
       x.data = scratch;
       scratch += align_up(x.n_rows * x.ld * (int64_t)sizeof(T));
       int n = 0;
-      if ((e = launch_expand(a.x_kept, x, s, &n)) != cudaSuccess) return e;
+      if ((e = launch_expand(a.x_kept, x, s, &n, joint && *queued > 0)) != cudaSuccess) return e;
       *queued += n;
-    } else if ((e = aligned_rows(h, {&x}, &scratch, s, queued)) != cudaSuccess) {
+    } else if ((e = aligned_rows(h, {&x}, &scratch, s, queued, joint && *queued > 0)) != cudaSuccess) {
       return e;
     }
   }
-  int64_t parts_x;
-  if (a.grad_x.data && a.grad_w.data && together(h, M, N, x.n_cols, &parts_x)) {
+  if (joint) {
     grad_products g = {gz, w, x, a.grad_x, a.grad_w, reinterpret_cast<float *>(scratch), nullptr, (int32_t)parts_x, false, true, *queued > 0};
+    if (a.grad_bias) {
+      g.sums = part;
+      g.sum_rows = parts;
+      g.sum_cols = N;
+      g.sum_to = a.grad_bias;
+    }
     return launch_grad_products(h, g, s, queued);
   }
   if (a.grad_x.data &&

@@ -42,10 +42,35 @@ __device__ __forceinline__ void put_row(uint32_t box, int lane, const float *v) 
                  : "memory");
   }
 }
-// The box's values to rows that start anywhere: row after row, the lanes along it.
+// The box's values to rows that start anywhere: row after row, the lanes along
+// it.  16-bit values go two rows at a time in words, of columns 2 l and 2 l + 1
+// where the row starts on a word, else of 2 l + 1 and 2 l + 2 between its first
+// and its last value; one by one at the matrix's edge.
 template <typename U>
 __device__ __forceinline__ void store_ragged(const ss_dense &out, uint32_t box, int lane, int64_t m0, int64_t n) {
   constexpr int kCols = 64 / (int)sizeof(U), kPer = 16 / (int)sizeof(U);
+  if constexpr (sizeof(U) == 2) {
+    if (n + 32 <= out.n_cols) {
+      const int l = lane % 16;
+      uint16_t *base = static_cast<uint16_t *>(out.data) + m0 * out.ld + n;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = i / 2 * 4 + i % 2 + lane / 16 * 2;  // rows two apart start alike
+        uint16_t *to = base + r * out.ld;
+        const uint32_t w = tc::read_shared<uint32_t>(unit_at(box, r, l / 4) + (uint32_t)(l % 4 * 4));
+        const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1);
+        if (m0 + r >= out.n_rows) continue;
+        if (reinterpret_cast<uintptr_t>(to) & 2) {
+          if (l < 15) *reinterpret_cast<uint32_t *>(to + 2 * l + 1) = __funnelshift_r(w, next, 16);
+          if (l == 0) to[0] = (uint16_t)w;
+          if (l == 15) to[31] = (uint16_t)(w >> 16);
+        } else {
+          *reinterpret_cast<uint32_t *>(to + 2 * l) = w;
+        }
+      }
+      return;
+    }
+  }
   U *to = static_cast<U *>(out.data) + m0 * out.ld + n + lane % kCols;
 #pragma unroll 8
   for (int r = lane / kCols; r < 32; r += 32 / kCols) {
