@@ -164,7 +164,8 @@ struct Codes {
   Codes(const Call &c, int64_t rows, int64_t cols, bool vector) {
     const int64_t ld = (cols + 15) / 16 * 16, groups = (cols + SS_KEPT_GROUP - 1) / SS_KEPT_GROUP;
     codes = c.empty({rows, ld}, at::kFloat8_e4m3fn);
-    if (ld != cols) codes = codes.narrow(1, 0, cols);
+    // the rows' first values (as narrow() gives them, in a fifth of its time)
+    if (ld != cols) codes.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef({rows, cols}), at::IntArrayRef({ld, (int64_t)1}));
     scale = c.empty({rows, groups}, at::kFloat8_e8m0fnu);
     m = {codes.data_ptr(), static_cast<uint8_t *>(scale.data_ptr()), rows, cols, ld, groups};
     if (vector) {

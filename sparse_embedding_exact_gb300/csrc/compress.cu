@@ -34,6 +34,29 @@ struct Unit {
       w[4 * i + 3] = q.w;
     }
   }
+  // From anywhere; zeros after `left` of the values.
+  __device__ __forceinline__ void load_any(const T *p, const void *begin, const void *end, int left) {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      uint32_t q[4];
+      load_anywhere<16, (int)sizeof(T)>(reinterpret_cast<const uint4 *>(p) + i, begin, end, q);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[4 * i + k] = q[k];
+    }
+    if (left < kN) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(T) == 4)
+          w[i] = i < left ? w[i] : 0;
+        else
+          w[i] = 2 * i + 1 < left ? w[i] : 2 * i < left ? w[i] & 0xFFFFu : 0;
+      }
+    }
+  }
+  __device__ __forceinline__ T value(int i) const {
+    const float2 f = pair(i / 2);
+    return Type<T>::down(i % 2 ? f.y : f.x);
+  }
   __device__ __forceinline__ void store(T *p) const {
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i) reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
@@ -83,6 +106,7 @@ struct Unit<T, 1> {
   T v;
   __device__ __forceinline__ void clear() { v = Type<T>::down(0.0f); }
   __device__ __forceinline__ void load(const T *p) { v = *p; }
+  __device__ __forceinline__ void load_any(const T *p, const void *, const void *, int) { v = *p; }
   __device__ __forceinline__ uint32_t most() const { return abs_bits(Type<T>::up(v)); }
 };
 
@@ -116,11 +140,14 @@ struct Place {
   __device__ __forceinline__ int32_t unit_of(int along) const { return unit + along * (int32_t)blockDim.x; }
 };
 
-template <typename T, int kN, int kAlong>
+// kAny: x's rows start anywhere, or end within a unit (codes' rows start on
+// 8-byte boundaries all the same).
+template <typename T, int kN, int kAlong, bool kAny>
 __global__ void __launch_bounds__(kThreads) k_compress(const ss_dense x, const ss_kept out, int least) {
   constexpr int kShare = kGroup / kN;  // threads of a group: neighbours in a warp
   const int32_t units = (int32_t)((x.n_cols + kN - 1) / kN);
   const Place<kAlong> at;
+  const void *end = end_of(x.data, x.n_rows, x.n_cols, x.ld, sizeof(T));
   Unit<T, kN> v[4];
 #pragma unroll
   for (int d = 0; d < at.kDown; ++d) {
@@ -129,7 +156,12 @@ __global__ void __launch_bounds__(kThreads) k_compress(const ss_dense x, const s
 #pragma unroll
     for (int k = 0; k < kAlong; ++k) {
       v[d * kAlong + k].clear();
-      if (there && at.unit_of(k) < units) v[d * kAlong + k].load(p + (int64_t)at.unit_of(k) * kN);
+      if (there && at.unit_of(k) < units) {
+        if (kAny)
+          v[d * kAlong + k].load_any(p + (int64_t)at.unit_of(k) * kN, x.data, end, (int)min((int64_t)kN, x.n_cols - (int64_t)at.unit_of(k) * kN));
+        else
+          v[d * kAlong + k].load(p + (int64_t)at.unit_of(k) * kN);
+      }
     }
   }
 #pragma unroll
@@ -164,7 +196,13 @@ __global__ void __launch_bounds__(kThreads) k_compress(const ss_dense x, const s
 #pragma unroll
           for (int i = 0; i < 4; ++i) q[i] = codes2(scaled_down(f.pair(i).x, down), scaled_down(f.pair(i).y, down));
         }
-        *reinterpret_cast<uint2 *>(codes + (int64_t)u * kN) = make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+        if (kAny && (int64_t)u * kN + kN > x.n_cols) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((int64_t)u * kN + i < x.n_cols) codes[(int64_t)u * kN + i] = (uint8_t)(q[i / 2] >> i % 2 * 8);
+        } else {
+          *reinterpret_cast<uint2 *>(codes + (int64_t)u * kN) = make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+        }
       } else {
         codes[u] = (uint8_t)codes2(scaled_down(Type<T>::up(f.v), down), 0.0f);
       }
@@ -173,10 +211,11 @@ __global__ void __launch_bounds__(kThreads) k_compress(const ss_dense x, const s
   }
 }
 
-template <typename T, int kN, int kAlong>
+template <typename T, int kAlong>
 __global__ void __launch_bounds__(kThreads) k_expand(const ss_kept x, const ss_dense y) {
+  constexpr int kN = 8;
   tc::let_next();
-  const int32_t units = (int32_t)((y.n_cols + kN - 1) / kN);
+  const int32_t units = (int32_t)(y.n_cols / kN);
   const Place<kAlong> at;
   uint2 q[4];
   uint32_t byte[4];
@@ -187,10 +226,7 @@ __global__ void __launch_bounds__(kThreads) k_expand(const ss_kept x, const ss_d
     for (int k = 0; k < kAlong; ++k)
       if (at.row_of(d) < y.n_rows && at.unit_of(k) < units) {
         const int32_t u = at.unit_of(k);
-        if constexpr (kN == 8)
-          q[d * kAlong + k] = *reinterpret_cast<const uint2 *>(codes + (int64_t)u * kN);
-        else
-          q[d * kAlong + k].x = codes[u];
+        q[d * kAlong + k] = *reinterpret_cast<const uint2 *>(codes + (int64_t)u * kN);
         byte[d * kAlong + k] = scale[u / (kGroup / kN)];
       }
   }
@@ -203,27 +239,77 @@ __global__ void __launch_bounds__(kThreads) k_expand(const ss_kept x, const ss_d
       const int32_t u = at.unit_of(k);
       if (at.row_of(d) >= y.n_rows || u >= units) continue;
       const float s = scale_of_byte(byte[i]);
-      if constexpr (kN == 8) {
-        Unit<T, 8> out;
-        float2 f[4];
+      Unit<T, 8> out;
+      float2 f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 c = widen_codes2((j < 2 ? q[i].x : q[i].y) >> j % 2 * 16 & 0xFFFFu);
-          f[j] = both(two(c.x, c.y) * two(s, s));
-        }
-        if (byte[i] > safe_byte<T>()) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = make_float2(within<T>(f[j].x), within<T>(f[j].y));
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) out.set_pair(j, f[j]);
-        out.store(to + (int64_t)u * kN);
-      } else {
-        to[u] = Type<T>::down(within<T>(widen_code((uint8_t)q[i].x) * s));
+      for (int j = 0; j < 4; ++j) {
+        const float2 c = widen_codes2((j < 2 ? q[i].x : q[i].y) >> j % 2 * 16 & 0xFFFFu);
+        f[j] = both(two(c.x, c.y) * two(s, s));
       }
+      if (byte[i] > safe_byte<T>()) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = make_float2(within<T>(f[j].x), within<T>(f[j].y));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out.set_pair(j, f[j]);
+      out.store(to + (int64_t)u * kN);
     }
   }
   tc::wait_before();  // what follows waits for this kernel, and so for the one before it
+}
+
+// The same for rows that start anywhere: a thread's units of 8 values lie from
+// the row's first 16-byte boundary in y on (unit 0 before it), and take their
+// codes from anywhere.
+template <typename T, int kAlong>
+__global__ void __launch_bounds__(kThreads) k_expand_any(const ss_kept x, const ss_dense y) {
+  tc::let_next();
+  const Place<kAlong> at;
+  const void *end = end_of(x.codes, x.n_rows, x.n_cols, x.ld, 1);
+  const int32_t cols = (int32_t)y.n_cols;
+#pragma unroll
+  for (int d = 0; d < at.kDown; ++d) {
+    if (at.row_of(d) >= y.n_rows) break;
+    T *to = static_cast<T *>(y.data) + at.row_of(d) * y.ld;
+    const uint8_t *codes = static_cast<const uint8_t *>(x.codes) + at.row_of(d) * x.ld, *scale = x.scale + at.row_of(d) * x.ld_scale;
+    const int32_t head = (int32_t)((16 - (reinterpret_cast<uintptr_t>(to) & 15)) % 16 / sizeof(T)) - 8;
+#pragma unroll
+    for (int k = 0; k < kAlong; ++k) {
+      const int32_t first = head + 8 * at.unit_of(k), c0 = max(first, 0), c1 = min(first + 8, cols);
+      if (c0 >= c1) continue;
+      uint32_t q[2];
+      load_anywhere<8, 1>(codes + c0, x.codes, end, q);
+      if (first < 0) {  // codes of what lies before the row are none
+        const uint64_t v = ((uint64_t)q[1] << 32 | q[0]) << -8 * first;
+        q[0] = (uint32_t)v;
+        q[1] = (uint32_t)(v >> 32);
+      }
+      const uint32_t b0 = scale[c0 / kGroup], b1 = scale[(c1 - 1) / kGroup];
+      const float s0 = scale_of_byte(b0), s1 = scale_of_byte(b1);
+      const int32_t border = (c0 / kGroup + 1) * kGroup - first;  // values before it have s0
+      Unit<T, 8> out;
+      float2 f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 c = widen_codes2((j < 2 ? q[0] : q[1]) >> j % 2 * 16 & 0xFFFFu);
+        f[j] = make_float2(c.x * (2 * j < border ? s0 : s1), c.y * (2 * j + 1 < border ? s0 : s1));
+      }
+      if (max(b0, b1) > safe_byte<T>()) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = make_float2(within<T>(f[j].x), within<T>(f[j].y));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out.set_pair(j, f[j]);
+      if (c1 - c0 == 8) {
+        out.store(to + first);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (first + j >= c0 && first + j < c1) to[first + j] = out.value(j);
+      }
+    }
+  }
+  tc::wait_before();
 }
 
 // Calls run(kAlong, grid, block) for `rows` rows of `units` units; a block's
@@ -251,13 +337,17 @@ constexpr int64_t kMostCols = (int64_t)65535 * kThreads * 4;
 template <typename T>
 cudaError_t compress_typed(const ss_dense &x, const ss_kept &out, cudaStream_t s) {
   const int least = least_exponent(x.type);
-  if (x.n_cols % 8 == 0 && rows_aligned(x, 16) && kept_aligned(out, 8))
-    laid_out(x.n_rows, x.n_cols / 8, 4, [&](auto along, dim3 grid, dim3 block) {
-      k_compress<T, 8, decltype(along)::value><<<grid, block, 0, s>>>(x, out, least);
+  const bool whole = x.n_cols % 8 == 0 && rows_aligned(x, 16);
+  if (kept_aligned(out, 8))
+    laid_out(x.n_rows, (x.n_cols + 7) / 8, 4, [&](auto along, dim3 grid, dim3 block) {
+      if (whole)
+        k_compress<T, 8, decltype(along)::value, false><<<grid, block, 0, s>>>(x, out, least);
+      else
+        k_compress<T, 8, decltype(along)::value, true><<<grid, block, 0, s>>>(x, out, least);
     });
   else
     laid_out(x.n_rows, x.n_cols, 32, [&](auto along, dim3 grid, dim3 block) {
-      k_compress<T, 1, decltype(along)::value><<<grid, block, 0, s>>>(x, out, least);
+      k_compress<T, 1, decltype(along)::value, false><<<grid, block, 0, s>>>(x, out, least);
     });
   return cudaGetLastError();
 }
@@ -275,13 +365,13 @@ cudaError_t expand_typed(const ss_kept &x, const ss_dense &y, cudaStream_t s, bo
     laid_out(y.n_rows, y.n_cols / 8, 4, [&](auto along, dim3 grid, dim3 block) {
       cfg.gridDim = grid;
       cfg.blockDim = block;
-      e = cudaLaunchKernelEx(&cfg, k_expand<T, 8, decltype(along)::value>, x, y);
+      e = cudaLaunchKernelEx(&cfg, k_expand<T, decltype(along)::value>, x, y);
     });
   else
-    laid_out(y.n_rows, y.n_cols, 32, [&](auto along, dim3 grid, dim3 block) {
+    laid_out(y.n_rows, (y.n_cols + 7) / 8 + 1, 4, [&](auto along, dim3 grid, dim3 block) {
       cfg.gridDim = grid;
       cfg.blockDim = block;
-      e = cudaLaunchKernelEx(&cfg, k_expand<T, 1, decltype(along)::value>, x, y);
+      e = cudaLaunchKernelEx(&cfg, k_expand_any<T, decltype(along)::value>, x, y);
     });
   return e;
 }

@@ -6,8 +6,8 @@
 //   grad_x = gz w,  grad_w = gz^T x,  grad_bias = sum_r gz_r
 //
 // x [M, K] rows, w [V, K] items, 16 bits; sums, statistics and the epilogue
-// float32.  A row without a target, with one that the bias masks (its logit is
-// -inf) or of weight 0 is absent: loss 0 and gradient 0, whatever x holds.
+// float32.  A row without a target, with one that the bias masks (-inf) or of
+// weight 0 is absent: loss 0 and gradient 0, whatever x holds.
 //
 // The loss (k_statistics): tiles of 256 x 256 logits by pairs of blocks
 // (product.cuh) that stay in tensor memory.  A thread of the epilogue owns a row
@@ -322,10 +322,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
 // their order (unless the statistics are given), what gz takes of each row, x
 // with the absent rows' values 0, as 0 times an infinity or NaN there would
 // reach grad_w, and binary16's power of two and its reciprocal.  A block takes
-// 32 rows, 16 threads a row.
+// eight rows, 32 threads a row.
 struct Between {
   const float2 *part;  // or null: stats are given
-  const float *here, *weight, *grad_loss;
+  const float *here, *weight, *grad_loss, *bias;
   const int64_t *targets;
   int64_t M, V;
   int32_t parts, vec;
@@ -340,14 +340,14 @@ struct Between {
   int64_t ld;
   float *factor;       // or null
 };
-constexpr int kBetweenWarps = 16;
-__global__ void __launch_bounds__(32 * kBetweenWarps) k_between(const Between a) {
-  __shared__ float2 sm[kBetweenWarps][32];
-  __shared__ bool there[32];
+constexpr int kBetweenRows = 8, kBetweenThreads = 256;
+__global__ void __launch_bounds__(kBetweenThreads) k_between(const Between a) {
+  __shared__ float2 sm[kBetweenThreads / 32][kBetweenRows];
+  __shared__ bool there[kBetweenRows];
   tc::wait_before();
   tc::let_next();
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int64_t m = (int64_t)blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row0 = (int64_t)blockIdx.x * kBetweenRows, m = row0 + lane % kBetweenRows;
   float most = -INFINITY, sum = 0.0f;
   auto add = [&](float2 p) {
     const float top = fmaxf(most, p.x), b = base_of(top, a.c);
@@ -356,33 +356,35 @@ __global__ void __launch_bounds__(32 * kBetweenWarps) k_between(const Between a)
     most = top;
   };
   if (a.part) {
+    constexpr int kLanes = kBetweenThreads / kBetweenRows;  // threads of a row
     if (m < a.M)
-      for (int p0 = g; p0 < a.parts; p0 += 8 * kBetweenWarps) {
+      for (int p0 = threadIdx.x / kBetweenRows; p0 < a.parts; p0 += 8 * kLanes) {
         float2 v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          v[k] = p0 + k * kBetweenWarps < a.parts ? a.part[(int64_t)(p0 + k * kBetweenWarps) * a.M + m] : make_float2(-INFINITY, 0.0f);
+        for (int k = 0; k < 8; ++k) v[k] = p0 + k * kLanes < a.parts ? a.part[(int64_t)(p0 + k * kLanes) * a.M + m] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) add(v[k]);
+        for (int k = 0; k < 8; ++k)
+          if (p0 + k * kLanes < a.parts) add(v[k]);
       }
-    sm[g][lane] = make_float2(most, sum);
+#pragma unroll
+    for (int o = kBetweenRows; o < 32; o *= 2) {
+      const float2 other = make_float2(__shfl_down_sync(0xFFFFFFFFu, most, o), __shfl_down_sync(0xFFFFFFFFu, sum, o));
+      add(other);
+    }
+    if (lane < kBetweenRows) sm[warp][lane] = make_float2(most, sum);
     __syncthreads();
   }
-  if (g == 0 && m < a.M) {
+  if (threadIdx.x < kBetweenRows && m < a.M) {
     const int64_t target = a.targets[m];
     const float weight = a.weight ? a.weight[m] : 1.0f;
     const bool past = target >= a.V;
     if (past) flag(a.status, DEV_OUT_OF_RANGE);
-    bool live = target >= 0 && !past && weight != 0.0f;
+    bool live = target >= 0 && !past && weight != 0.0f && !(a.bias && a.bias[target] == -INFINITY);
     there[lane] = live;
     if (a.part) {
-      for (int k = 1; k < kBetweenWarps; ++k) add(sm[k][lane]);
+      for (int k = 1; k < kBetweenThreads / 32; ++k) add(sm[k][lane]);
       float loss = 0.0f;
-      if (live) {
-        const float z = a.here[m];
-        live = z != -INFINITY;
-        if (live) loss = weight * (kLn2 * (log2f(sum) - fmaf(z, a.c, -base_of(most, a.c))));
-      }
+      if (live) loss = weight * (kLn2 * (log2f(sum) - fmaf(a.here[m], a.c, -base_of(most, a.c))));
       a.loss[m] = loss;
       if (a.stats) a.stats[m] = make_float2(most, live ? sum : INFINITY);
     } else {
@@ -397,14 +399,15 @@ __global__ void __launch_bounds__(32 * kBetweenWarps) k_between(const Between a)
   }
   if (!a.rows) return;
   __syncthreads();
-  for (int r = g; r < 32; r += kBetweenWarps) {
-    const int64_t row = (int64_t)blockIdx.x * 32 + r;
-    if (row >= a.M) break;
+  static_assert(kBetweenThreads / 32 == kBetweenRows, "a warp a row");
+  const int r = warp;
+  const int64_t row = row0 + r;
+  if (row < a.M) {
     uint16_t *to = static_cast<uint16_t *>(a.to) + row * a.ld;
     const uint16_t *from = static_cast<const uint16_t *>(a.x.data) + row * a.x.ld;
     const bool same = from == to;
-    if (same && there[r]) continue;
-    if (a.vec) {
+    if (same && there[r]) {
+    } else if (a.vec) {
       for (int64_t c = (int64_t)lane * 8; c < a.x.n_cols; c += 256)
         *reinterpret_cast<uint4 *>(to + c) = there[r] ? *reinterpret_cast<const uint4 *>(from + c) : make_uint4(0, 0, 0, 0);
     } else {
@@ -414,16 +417,16 @@ __global__ void __launch_bounds__(32 * kBetweenWarps) k_between(const Between a)
   if (!a.factor || blockIdx.x != 0) return;
   most = 0.0f;
 #pragma unroll 4
-  for (int64_t r = threadIdx.x; r < a.M; r += 32 * kBetweenWarps) {
-    const float v = fabsf((a.weight ? a.weight[r] : 1.0f) * (a.grad_loss ? a.grad_loss[r] : 1.0f) * a.inv_t);
+  for (int64_t k = threadIdx.x; k < a.M; k += kBetweenThreads) {
+    const float v = fabsf((a.weight ? a.weight[k] : 1.0f) * (a.grad_loss ? a.grad_loss[k] : 1.0f) * a.inv_t);
     if (v < INFINITY) most = fmaxf(most, v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-  if (lane == 0) sm[g][0].x = most;
+  if (lane == 0) sm[warp][0].x = most;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int k = 1; k < kBetweenWarps; ++k) most = fmaxf(most, sm[k][0].x);
+    for (int k = 1; k < kBetweenThreads / 32; ++k) most = fmaxf(most, sm[k][0].x);
     const int e = most > 0.0f ? max(-100, min(100, 14 - ilogbf(most))) : 0;
     a.factor[0] = ldexpf(1.0f, e);
     a.factor[1] = ldexpf(1.0f, -e);
@@ -547,6 +550,7 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   Between b = {};
   b.weight = a.weight;
   b.grad_loss = a.grad_loss;
+  b.bias = a.bias;
   b.targets = a.targets;
   b.M = M;
   b.V = V;
@@ -577,7 +581,7 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   }
   const bool first = *queued == 0;
   *queued += 1;
-  if ((e = launch_beside(k_between, (unsigned)up(M, 32), 32 * kBetweenWarps, 0, s, !first, b)) != cudaSuccess || !grad) return e;
+  if ((e = launch_beside(k_between, (unsigned)up(M, kBetweenRows), kBetweenThreads, 0, s, !first, b)) != cudaSuccess || !grad) return e;
   x.data = copy;
   x.ld = b.ld;
   p.rows = b.rows;

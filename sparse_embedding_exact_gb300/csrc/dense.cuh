@@ -9,6 +9,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "internal.cuh"
 
 namespace dense {
@@ -128,6 +130,58 @@ template <typename T, int kN>
 __device__ __forceinline__ void store_pack(T *p, const Pack<T, kN> &v) {
   *reinterpret_cast<Pack<T, kN> *>(p) = v;
 }
+// kBytes (16 or 8) bytes at p, which may lie anywhere that holds the values of
+// kSize bytes whole: from the aligned units that hold them where these lie within
+// [begin, end), the memory of the whole matrix; else value by value, zeros from
+// `end` on.
+template <int kBytes, int kSize>
+__device__ __forceinline__ void load_anywhere(const void *at, const void *begin, const void *end, uint32_t (&v)[kBytes / 4]) {
+  const unsigned char *p = static_cast<const unsigned char *>(at);
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & (kBytes - 1)), bits = 8 * (off & 3);
+  if (p - off >= begin && p - off + 2 * kBytes <= end) {
+    constexpr int kW = kBytes / 4;
+    uint32_t w[2 * kW];
+    if constexpr (kBytes == 16) {
+      const uint4 a = *reinterpret_cast<const uint4 *>(p - off), b = *reinterpret_cast<const uint4 *>(p - off + 16);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2 *>(p - off), b = *reinterpret_cast<const uint2 *>(p - off + 8);
+      w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
+    }
+    auto from = [&](auto first) {
+      constexpr int k = decltype(first)::value;
+#pragma unroll
+      for (int i = 0; i < kW; ++i) v[i] = __funnelshift_r(w[k + i], w[(k + i + 1) % (2 * kW)], bits);
+    };
+    switch (off >> 2) {  // the same for the threads of a row
+      case 0: from(std::integral_constant<int, 0>()); break;
+      case 1: from(std::integral_constant<int, 1>()); break;
+      case 2: from(std::integral_constant<int, kBytes == 16 ? 2 : 0>()); break;
+      default: from(std::integral_constant<int, kBytes == 16 ? 3 : 1>()); break;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i) v[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kBytes; i += kSize) {
+      uint32_t x = 0;
+      if (p + i + kSize <= end) {
+        if constexpr (kSize == 1)
+          x = p[i];
+        else if constexpr (kSize == 2)
+          x = *reinterpret_cast<const uint16_t *>(p + i);
+        else
+          x = *reinterpret_cast<const uint32_t *>(p + i);
+      }
+      v[i / 4] |= x << i % 4 * 8;
+    }
+  }
+}
+// The end of a matrix's memory.
+__device__ __forceinline__ const void *end_of(const void *data, int64_t rows, int64_t cols, int64_t ld, int size) {
+  return static_cast<const unsigned char *>(data) + ((rows - 1) * ld + cols) * size;
+}
+
 // kN values rounded to e4m3 (to the nearest, beyond 448 to 448; NaN kept).
 template <int kN>
 __device__ __forceinline__ void store_f8(uint8_t *p, const float (&f)[kN]) {

@@ -151,7 +151,7 @@ __device__ __forceinline__ float act_slope(float z) {
     return s + z * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
   }
   if (kAct == SS_ACT_SILU) {
-    const float s = 1.0f / (1.0f + __expf(-z));
+    const float s = __fdividef(1.0f, 1.0f + __expf(-z));
     return s * (1.0f + z * (1.0f - s));
   }
   if (kAct == SS_ACT_LOG1P_RELU) return z > 0.0f ? 1.0f / (1.0f + z) : (z == z ? 0.0f : z);
@@ -724,8 +724,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, kM == 1 ? 16 : 1) k_rows(const
 // columns over the block's rows into part[blockIdx.y][N] (or nowhere).  A warp
 // takes every eighth row of the block's share, two of them at a time.  Bound
 // by memory and, with a gelu, by instructions: 8192 x 4096 bf16 36 us (5.5 TB/s).
-template <typename T, int kN, int kAct, bool kKept>
+// kAny: rows that start anywhere, or end within a unit of kN values.
+template <typename T, int kAct, bool kKept, bool kAny>
 __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, const ss_kept kept, T *gz, int64_t ld, float *part) {
+  constexpr int kN = 8;
   tc::let_next();
   __shared__ float sm[8][32 * kN + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -735,6 +737,9 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
   const T *zp = static_cast<const T *>(pre.data) + (kAct != SS_ACT_NONE && !kKept ? first * pre.ld + c : 0);
   const uint8_t *codes = static_cast<const uint8_t *>(kept.codes) + (kKept ? first * kept.ld + c : 0);
   const uint8_t *scale = kept.scale + (kKept ? first * kept.ld_scale + c / kGroup : 0);
+  const void *end_g = end_of(grad_y.data, M, N, grad_y.ld, sizeof(T)), *end_z = end_of(pre.data, M, N, pre.ld, sizeof(T));
+  const void *end_c = end_of(kept.codes, M, N, kept.ld, 1);
+  const int left = (int)min((int64_t)kN, N - c);
   T *to = gz ? gz + first * ld + c : nullptr;
   const int64_t step_g = step * grad_y.ld, step_z = step * pre.ld, step_c = step * kept.ld, step_s = step * kept.ld_scale, step_to = step * ld;
   float sum[kN];
@@ -748,12 +753,21 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         if (m + u * step < M) {
-          gv[u] = load_pack<T, kN>(gp + u * step_g);
+          if (kAny)
+            load_anywhere<16, 2>(gp + u * step_g, grad_y.data, end_g, gv[u].w);
+          else
+            gv[u] = load_pack<T, kN>(gp + u * step_g);
           if (kKept) {
-            cv[u].load(codes + u * step_c);
+            if (kAny)
+              load_anywhere<8, 1>(codes + u * step_c, kept.codes, end_c, cv[u].w);
+            else
+              cv[u].load(codes + u * step_c);
             byte[u] = scale[u * step_s];
           } else if (kAct != SS_ACT_NONE) {
-            zv[u] = load_pack<T, kN>(zp + u * step_z);
+            if (kAny)
+              load_anywhere<16, 2>(zp + u * step_z, pre.data, end_z, zv[u].w);
+            else
+              zv[u] = load_pack<T, kN>(zp + u * step_z);
           }
         }
 #pragma unroll
@@ -763,20 +777,21 @@ __global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const s
           widen(gv[u], g);
           if (kKept) {
             const float s = scale_of_byte(byte[u]);
-            if constexpr (kN == 1) {
-              z[0] = cv[u].one() * s;
-            } else {
 #pragma unroll
-              for (int i = 0; i < kN; i += 2) {
-                const float2 f = cv[u].pair(i / 2), q = both(two(f.x, f.y) * two(s, s));
-                z[i] = q.x;
-                z[i + 1] = q.y;
-              }
+            for (int i = 0; i < kN; i += 2) {
+              const float2 f = cv[u].pair(i / 2), q = both(two(f.x, f.y) * two(s, s));
+              z[i] = q.x;
+              z[i + 1] = q.y;
             }
           } else if (kAct != SS_ACT_NONE) {
             widen(zv[u], z);
           }
-          if constexpr (kAct == SS_ACT_GELU && kN > 1) {
+          if (kAny && left < kN) {  // what lies past the row's end
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (i >= left) g[i] = z[i] = 0.0f;
+          }
+          if constexpr (kAct == SS_ACT_GELU) {
 #pragma unroll
             for (int i = 0; i < kN; i += 2) {
               const Two zz = two(z[i], z[i + 1]);
@@ -820,33 +835,6 @@ struct Copies {
   void *dst[2];
   int64_t ld[2];
 };
-// The 16 bytes at p, which lie anywhere, from the two aligned 16-byte units that
-// hold them where these lie in [begin, end), value by value where not, as far as
-// `end`.
-template <typename T>
-__device__ __forceinline__ uint4 read_anywhere(const unsigned char *p, const unsigned char *begin, const unsigned char *end) {
-  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
-  if (p - off >= begin && p - off + 32 <= end) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p - off), b = *reinterpret_cast<const uint4 *>(p - off + 16);
-    const uint32_t bits = 8 * (off & 3);
-    auto shift = [&](uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, uint32_t v4) {
-      return make_uint4(__funnelshift_r(v0, v1, bits), __funnelshift_r(v1, v2, bits), __funnelshift_r(v2, v3, bits), __funnelshift_r(v3, v4, bits));
-    };
-    switch (off >> 2) {  // the same for a row's threads
-      case 0: return shift(a.x, a.y, a.z, a.w, b.x);
-      case 1: return shift(a.y, a.z, a.w, b.x, b.y);
-      case 2: return shift(a.z, a.w, b.x, b.y, b.z);
-      default: return shift(a.w, b.x, b.y, b.z, b.w);
-    }
-  }
-  constexpr int kN = 16 / (int)sizeof(T);
-  T v[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = p + (i + 1) * sizeof(T) <= end ? *reinterpret_cast<const T *>(p + i * sizeof(T)) : T(0);
-  uint4 q;
-  memcpy(&q, v, 16);
-  return q;
-}
 template <typename T>
 __global__ void __launch_bounds__(256) k_copy_rows(const Copies a) {
   tc::let_next();
@@ -855,15 +843,20 @@ __global__ void __launch_bounds__(256) k_copy_rows(const Copies a) {
   const int64_t ld = (second ? a.ld[1] : a.ld[0]) * (int64_t)sizeof(T), bytes = src.n_cols * (int64_t)sizeof(T);
   unsigned char *dst = static_cast<unsigned char *>(second ? a.dst[1] : a.dst[0]);
   const unsigned char *from = static_cast<const unsigned char *>(src.data);
-  const unsigned char *end = from + ((src.n_rows - 1) * src.ld + src.n_cols) * (int64_t)sizeof(T);
+  const void *end = end_of(from, src.n_rows, src.n_cols, src.ld, sizeof(T));
+  auto read = [&](int64_t r, int64_t c) {
+    uint32_t v[4];
+    load_anywhere<16, (int)sizeof(T)>(from + r * src.ld * (int64_t)sizeof(T) + c, from, end, v);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  };
   // What lies past a row's end within its last 16 bytes goes along: no one reads
   // it there.  blockDim.x threads along a row, blockDim.y rows
   for (int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; r < src.n_rows; r += (int64_t)gridDim.x * blockDim.y)
     for (int64_t c = (int64_t)threadIdx.x * 16; c < bytes; c += 2 * 16 * (int64_t)blockDim.x) {  // two loads under way at a time
       const int64_t c1 = c + 16 * (int64_t)blockDim.x;
-      const uint4 v0 = read_anywhere<T>(from + r * src.ld * (int64_t)sizeof(T) + c, from, end);
+      const uint4 v0 = read(r, c);
       uint4 v1;
-      if (c1 < bytes) v1 = read_anywhere<T>(from + r * src.ld * (int64_t)sizeof(T) + c1, from, end);
+      if (c1 < bytes) v1 = read(r, c1);
       *reinterpret_cast<uint4 *>(dst + r * ld + c) = v0;
       if (c1 < bytes) *reinterpret_cast<uint4 *>(dst + r * ld + c1) = v1;
     }
@@ -1104,7 +1097,7 @@ bool few_rows(const ss_dense &x) { return x.n_rows <= few_rows_of(x) || x.n_cols
 
 int64_t grad_parts(const ss_handle *h, int64_t M, int64_t N) {
   const int64_t slabs = std::max<int64_t>(1, (N + 255) / 256);
-  return std::max<int64_t>(1, std::min<int64_t>((M + 63) / 64, 8 * (int64_t)std::max(1, h->sm_count) / slabs));
+  return std::max<int64_t>(1, std::min<int64_t>((M + 31) / 32, 8 * (int64_t)std::max(1, h->sm_count) / slabs));
 }
 
 // Whether a gradient's products take less time as one launch (gradients.cu) than
@@ -1208,10 +1201,11 @@ cudaError_t grad_typed(ss_handle *h, const linear_grad_args &a, cudaStream_t s, 
     auto run_of = [&](auto act, auto is_kept) {
       constexpr int kAct = decltype(act)::value;
       constexpr bool kKept = decltype(is_kept)::value;
+      const dim3 grid((unsigned)((N + 255) / 256), (unsigned)parts);
       if (vec)
-        k_act_grad<T, 8, kAct, kKept><<<dim3((unsigned)((N + 255) / 256), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, a.pre_kept, to, gz.ld, sums);
+        k_act_grad<T, kAct, kKept, false><<<grid, 256, 0, s>>>(a.grad_y, a.pre, a.pre_kept, to, gz.ld, sums);
       else
-        k_act_grad<T, 1, kAct, kKept><<<dim3((unsigned)((N + 31) / 32), (unsigned)parts), 256, 0, s>>>(a.grad_y, a.pre, a.pre_kept, to, gz.ld, sums);
+        k_act_grad<T, kAct, kKept, true><<<grid, 256, 0, s>>>(a.grad_y, a.pre, a.pre_kept, to, gz.ld, sums);
     };
     auto run = [&](auto act) {
       if constexpr (decltype(act)::value != SS_ACT_NONE) {

@@ -127,6 +127,19 @@ def test_absent_rows_and_masked_items(h):
         assert not gw[masked].any() and not gb[masked].any()
 
 
+def test_rows_of_masked_targets_hold_anything(h):
+    for dtype in HALVES:
+        x, w, t, b, wt, gl = _case(70, 600, 64, dtype)
+        b[77] = -math.inf
+        t[[4, 40, 69]] = 77
+        b[t[:3]] = 0.0
+        clean = x.clone()
+        clean[[4, 40, 69]] = 0.0
+        x[4], x[40, 5], x[69] = math.nan, math.inf, -math.inf
+        _, (loss, _, gx, _, _) = _check(h, x, w, t, gl, b, wt, plain=(clean, w))
+        assert not loss[[4, 40, 69]].any() and not gx[[4, 40, 69]].any()
+
+
 def test_everything_masked(h):
     x, w, t, b, wt, gl = _case(40, 300, 32, torch.bfloat16)
     loss, stats = h.cross_entropy(x, w, t, bias=torch.full_like(b, -math.inf))
