@@ -66,6 +66,12 @@ struct Codes {
       w[0] = *p;
     }
   }
+  __device__ __forceinline__ void load_shared(uint32_t at) {
+    if constexpr (kN == 8)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    else
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+  }
   // Codes 2 i and 2 i + 1.
   __device__ __forceinline__ float2 pair(int i) const { return widen_codes2(w[i / 2] >> i % 2 * 16 & 0xFFFFu); }
   __device__ __forceinline__ float one() const { return widen_code((uint8_t)w[0]); }

@@ -572,6 +572,25 @@ struct KeptScales {
   uint8_t byte[kPer];
 };
 
+// The sum of a over the group, in every thread: a warp's by shuffles, the warps'
+// read back by all (eight of them in two loads).  sm as in group_reduce.
+__device__ __forceinline__ float group_sum(const Group &gr, float a, float *sm) {
+  a = warp_sum(a);
+  const int n_warps = gr.threads >> 5;
+  if (n_warps == 1) {
+    __syncwarp();
+    return a;
+  }
+  const int lane = threadIdx.x & 31, first = gr.index * n_warps;
+  if (lane == 0) sm[threadIdx.x >> 5] = a;
+  gr.sync();
+  if (n_warps == 8) {
+    const float4 p = reinterpret_cast<const float4 *>(sm + first)[0], q = reinterpret_cast<const float4 *>(sm + first)[1];
+    return ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+  }
+  return warp_sum(lane < n_warps ? sm[first + lane] : 0.0f);
+}
+
 constexpr int kKeptThreads = 256;  // of a block, or a row's own where it has more
 constexpr int kKeptSlots = 4;
 template <typename T, int kN, int kPer, int kThreads>
@@ -579,92 +598,92 @@ __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_
   using W = Work<T, kN>;
   constexpr bool kAsync = kN > 1;
   extern __shared__ __align__(16) unsigned char raw[];
-  __shared__ float2 sm[2][32];
+  __shared__ __align__(16) float sm[2][32];
   const Group gr(threads);
-  const int D = (int)a.total.n_cols;
-  const int64_t R = a.total.n_rows, step = (int64_t)gridDim.x * (blockDim.x / threads);
+  const int D = (int)a.total.n_cols, R = (int)a.total.n_rows, step = (int)gridDim.x * ((int)blockDim.x / threads);
   const float inv_d = 1.0f / (float)D;
   const bool past = a.grad_total.data != nullptr;
+  // A thread past the row's end works on the last unit again, without branches,
+  // and keeps it to itself.
   int at[kPer];
+  bool in[kPer];
   typename W::V w[kPer][W::kM], gw[kPer][W::kM];
 #pragma unroll
   for (int p = 0; p < kPer; ++p) {
-    at[p] = (p * threads + gr.lane) * kN;
+    const int c = (p * threads + gr.lane) * kN;
+    in[p] = c < D;
+    at[p] = min(c, D - kN);
     float f[kN];
-    load_weights<kN>(a.weight, min(at[p], D), f);
+    load_weights<kN>(a.weight, at[p], f);
 #pragma unroll
     for (int i = 0; i < W::kM; ++i) {
       w[p][i] = W::of(f, i);
       gw[p][i] = W::all(0.0f);
     }
   }
-  const int64_t first = (int64_t)gr.index * gridDim.x + blockIdx.x;
-  const int apart = threads * kN;  // from one unit of this thread to the next
-  // What is read next, and written: at this thread's first unit, a step of rows
-  // further every turn
-  const T *gy = static_cast<const T *>(a.grad_y.data) + first * a.grad_y.ld + at[0];
-  const T *gt = static_cast<const T *>(a.grad_total.data) + (past ? first * a.grad_total.ld + at[0] : 0);
-  const uint8_t *codes = static_cast<const uint8_t *>(a.total_kept.codes) + first * a.total_kept.ld + at[0];
+  const int first = gr.index * (int)gridDim.x + (int)blockIdx.x;
+  // What is read next, and written: a step of rows further every turn
+  const T *gy = static_cast<const T *>(a.grad_y.data) + first * a.grad_y.ld;
+  const T *gt = static_cast<const T *>(a.grad_total.data) + (past ? first * a.grad_total.ld : 0);
+  const uint8_t *codes = static_cast<const uint8_t *>(a.total_kept.codes) + first * a.total_kept.ld;
   const uint8_t *scale = a.total_kept.scale + first * a.total_kept.ld_scale;
-  T *gx = static_cast<T *>(a.grad_x.data) + first * a.grad_x.ld + at[0];
+  T *gx = static_cast<T *>(a.grad_x.data) + first * a.grad_x.ld;
   const int64_t step_g = step * a.grad_y.ld, step_t = step * a.grad_total.ld, step_c = step * a.total_kept.ld;
   const int64_t step_s = step * a.total_kept.ld_scale, step_x = step * a.grad_x.ld;
-  // This thread's units of a slot: 16 bytes of g and of t, kN of codes
-  auto unit = [&](int slot, int p) { return (uint32_t)((slot * kPer + p) * (int)blockDim.x + (int)threadIdx.x); };
-  const uint32_t base = tc::smem_u32(raw), units = (uint32_t)(kKeptSlots * kPer) * blockDim.x;
-  auto fetch = [&](int slot, int64_t row) {
+  // A slot: 16 bytes of g and of t and kN of codes for every unit of the block
+  const uint32_t units = kPer * blockDim.x, slot_bytes = units * (32 + kN), base = tc::smem_u32(raw), base_end = base + kKeptSlots * slot_bytes;
+  auto fetch = [&](uint32_t slot, int row) {
     if (row < R) {
 #pragma unroll
-      for (int p = 0; p < kPer; ++p)
-        if (at[p] < D) {
-          const uint32_t u = unit(slot, p);
-          copy_async<16>(base + 16 * u, gy + p * apart);
-          if (past) copy_async<16>(base + 16 * (units + u), gt + p * apart);
-          copy_async<kN == 1 ? 4 : kN>(base + 32 * units + kN * u, codes + p * apart);
-        }
+      for (int p = 0; p < kPer; ++p) {
+        const uint32_t u = p * blockDim.x + threadIdx.x;
+        copy_async<16>(slot + 16 * u, gy + at[p]);
+        if (past) copy_async<16>(slot + 16 * units + 16 * u, gt + at[p]);
+        copy_async<kN == 1 ? 4 : kN>(slot + 32 * units + kN * u, codes + at[p]);
+      }
       gy += step_g;
       gt += step_t;
       codes += step_c;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto scales = [&](int64_t row) {
+  auto scales = [&](int row) {
     KeptScales<kPer> s = {};
     if (row < R) {
       s.rstd = a.rstd[row];
 #pragma unroll
-      for (int p = 0; p < kPer; ++p)
-        if (at[p] < D) s.byte[p] = scale[at[p] / kGroup];
+      for (int p = 0; p < kPer; ++p) s.byte[p] = scale[at[p] / kGroup];
       scale += step_s;
     }
     return s;
   };
-  int set = 0, slot = 0;
+  int set = 0;
+  uint32_t now = base, fill = base + (kKeptSlots - 1) * slot_bytes;  // the slots of this row, and of the next to be fetched
   KeptScales<kPer> s0 = scales(first), s1 = scales(first + step), s2;
   if (kAsync)
-    for (int i = 0; i < kKeptSlots - 1; ++i) fetch(i, first + i * step);
-  for (int64_t row = first; row < R; row += step, set ^= 1) {
+    for (int i = 0; i < kKeptSlots - 1; ++i) fetch(base + i * slot_bytes, first + i * step);
+  for (int row = first; row < R; row += step, set ^= 1) {
     KeptRow<T, kN, kPer> v;
     if constexpr (kAsync) {
-      fetch(slot == 0 ? kKeptSlots - 1 : slot - 1, row + (kKeptSlots - 1) * step);  // the slot of the row before
+      fetch(fill, row + (kKeptSlots - 1) * step);  // into the slot of the row before
+      fill = now;
       asm volatile("cp.async.wait_group %0;" ::"n"(kKeptSlots - 1) : "memory");
 #pragma unroll
-      for (int p = 0; p < kPer; ++p)
-        if (at[p] < D) {
-          const uint32_t u = unit(slot, p);
-          v.g[p] = *reinterpret_cast<const Pack<T, kN> *>(raw + 16 * u);
-          if (past) v.t[p] = *reinterpret_cast<const Pack<T, kN> *>(raw + 16 * (units + u));
-          v.c[p].load(raw + 32 * units + kN * u);
-        }
-      if (++slot == kKeptSlots) slot = 0;
+      for (int p = 0; p < kPer; ++p) {
+        const uint32_t u = p * blockDim.x + threadIdx.x;
+        v.g[p] = tc::read_shared<Pack<T, kN>>(now + 16 * u);
+        if (past) v.t[p] = tc::read_shared<Pack<T, kN>>(now + 16 * units + 16 * u);
+        v.c[p].load_shared(now + 32 * units + kN * u);
+      }
+      now += slot_bytes;
+      if (now == base_end) now = base;
     } else {
 #pragma unroll
-      for (int p = 0; p < kPer; ++p)
-        if (at[p] < D) {
-          v.g[p] = load_pack<T, kN>(gy + p * apart);
-          if (past) v.t[p] = load_pack<T, kN>(gt + p * apart);
-          v.c[p].load(codes + p * apart);
-        }
+      for (int p = 0; p < kPer; ++p) {
+        v.g[p] = load_pack<T, kN>(gy + at[p]);
+        if (past) v.t[p] = load_pack<T, kN>(gt + at[p]);
+        v.c[p].load(codes + at[p]);
+      }
       gy += step_g;
       gt += step_t;
       codes += step_c;
@@ -678,31 +697,35 @@ __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_
         return two(f.x, f.y);
       }
     };
-    typename W::V dot = W::all(0.0f);
+    float dot = 0.0f;
+    typename W::V weighed[kPer][W::kM], scaled[kPer][W::kM];  // g w and x, for both passes
 #pragma unroll
-    for (int p = 0; p < kPer; ++p)
-      if (at[p] < D) {
-        const typename W::V s = W::all(scale_of_byte(s0.byte[p]) * s0.rstd);
+    for (int p = 0; p < kPer; ++p) {
+      const typename W::V s = W::all(scale_of_byte(s0.byte[p])), r = W::all(s0.rstd);
+      typename W::V sum = W::all(0.0f);
 #pragma unroll
-        for (int i = 0; i < W::kM; ++i) {
-          const typename W::V g = W::get(v.g[p], i), xh = code(p, i) * s;
-          gw[p][i] = fma_of(g, xh, gw[p][i]);
-          dot = fma_of(g * w[p][i], xh, dot);
-        }
+      for (int i = 0; i < W::kM; ++i) {
+        const typename W::V g = W::get(v.g[p], i);
+        scaled[p][i] = code(p, i) * s;
+        weighed[p][i] = g * w[p][i];
+        const typename W::V xh = scaled[p][i] * r;
+        gw[p][i] = fma_of(g, xh, gw[p][i]);
+        sum = fma_of(weighed[p][i], xh, sum);
       }
-    const float mean = group_reduce<false>(gr, W::sum(dot), 0.0f, sm, set).x * inv_d;
+      dot += in[p] ? W::sum(sum) : 0.0f;
+    }
+    const float mean = group_sum(gr, dot, sm[set]) * inv_d;
+    const typename W::V fx = W::all(-s0.rstd * s0.rstd * mean), fg = W::all(s0.rstd);
 #pragma unroll
-    for (int p = 0; p < kPer; ++p)
-      if (at[p] < D) {
-        const typename W::V fx = W::all(-s0.rstd * s0.rstd * mean), fg = W::all(s0.rstd), s = W::all(scale_of_byte(s0.byte[p]));
-        float y[kN];
+    for (int p = 0; p < kPer; ++p) {
+      float y[kN];
 #pragma unroll
-        for (int i = 0; i < W::kM; ++i) {
-          const typename W::V t = past ? W::get(v.t[p], i) : W::all(0.0f);
-          W::put(y, i, fma_of(W::get(v.g[p], i) * w[p][i], fg, fma_of(code(p, i) * s, fx, t)));
-        }
-        store_pack(gx + p * apart, narrow<T, kN>(y));
+      for (int i = 0; i < W::kM; ++i) {
+        const typename W::V t = past ? W::get(v.t[p], i) : W::all(0.0f);
+        W::put(y, i, fma_of(weighed[p][i], fg, fma_of(scaled[p][i], fx, t)));
       }
+      if (in[p]) store_pack(gx + at[p], narrow<T, kN>(y));
+    }
     gx += step_x;
     s0 = s1;
     s1 = s2;
@@ -719,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_
     for (int i = 0; i < W::kM; ++i) W::put(f, i, gw[p][i]);
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      if (at[p] + i < D) mine[at[p] + i] = f[i];
+      if (in[p]) mine[at[p] + i] = f[i];
   }
   if (groups > 1) {
     __syncthreads();
