@@ -107,6 +107,15 @@ def test_strides(h, dtype, pad, shift):
     _check(h, _strided(x, pad, shift), _strided(w, 2 * pad, shift), t, gl, b, wt, plain=(x, w))
 
 
+@pytest.mark.parametrize("which", ["x", "w"])
+def test_one_of_two_needs_a_copy(h, which):
+    # one matrix's rows start on 16-byte boundaries, the other's do not
+    for dtype in HALVES:
+        x, w, t, b, wt, gl = _case(70, 400, 72, dtype)
+        xs, ws = (_strided(x, 3), w) if which == "x" else (x, _strided(w, 3))
+        _check(h, xs, ws, t, gl, b, wt, plain=(x, w))
+
+
 def test_absent_rows_and_masked_items(h):
     for dtype in HALVES:
         x, w, t, b, wt, gl = _case(300, 600, 64, dtype)
@@ -241,6 +250,33 @@ def test_streams_and_graphs(h):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, fresh))
+
+
+def test_two_streams_at_once(h):
+    cases = [_case(500, 6000, 200, dtype, seed=10 * i) for i, dtype in enumerate(HALVES)]
+    want = [h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt) for x, w, t, b, wt, gl in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for s, (x, w, t, b, wt, gl) in zip(streams, cases):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append([h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt) for _ in range(8)])
+    torch.cuda.synchronize()
+    for outs, one in zip(got, want):
+        for out in outs:
+            assert all(torch.equal(p, q) for p, q in zip(out, one))
+
+
+def test_calls_in_a_row_share_memory(h):
+    # each call's scratch is the one before's, freed and taken again: no kernel
+    # of a call starts on it early
+    cases = [_case(m, v, k, torch.bfloat16, seed=m) for m, v, k in ((600, 9000, 96), (40, 20_000, 72), (1500, 3000, 260))]
+    want = [h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt) for x, w, t, b, wt, gl in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (x, w, t, b, wt, gl), one in zip(cases, want):
+            out = h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt)
+            assert all(torch.equal(p, q) for p, q in zip(out, one))
 
 
 def test_refusals(h):
