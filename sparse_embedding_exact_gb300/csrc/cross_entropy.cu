@@ -91,6 +91,7 @@ struct Logits {
   const float *bias;     // of the piece, or null
   int32_t bias_pairs;    // it starts on an 8-byte boundary
   float c;               // log2(e) / T
+  float cut;             // cut_share(K)
   // statistics
   const int64_t *targets;
   float2 *part;          // [units * 4][M]
@@ -154,7 +155,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_s
             tc::load_acc_wait();
             if (half == 1) release();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            for (int i = 0; i < 32; i += 2) {
+              const Two z = two(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+              const float2 f = both(fma_of(z, two(a.cut, a.cut), z));
+              v[i] = f.x;
+              v[i + 1] = f.y;
+            }
           }
           if (m0 >= a.M || n0 >= a.V) continue;
           if (a.bias) along32(a.bias + n0, a.V - n0, [&](int i, float f) { v[i] += f; });
@@ -265,6 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
               for (int k = 0; k < 4; ++k) {
                 const uint32_t *f = r + 16 * (k / 2) + 4 * i + 2 * (k % 2);
                 Two z = two(__uint_as_float(f[0]), __uint_as_float(f[1]));
+                z = fma_of(z, two(a.cut, a.cut), z);
                 if (a.bias) z = z + bias[i];
                 const float2 e = both(fma_of(z, c2, two(-row[k].base, -row[k].base)));
                 Two g = two(exp2_fast(e.x), exp2_fast(e.y)) * two(row[k].share, row[k].share);
@@ -496,6 +503,7 @@ cudaError_t run_logits(ss_handle *h, Logits &p, const ss_dense &x, const ss_dens
   p.status = h->d_status;
   p.M = x.n_rows;
   p.V = w.n_rows;
+  p.cut = cut_share(x.n_cols);
   p.bias_pairs = reinterpret_cast<uintptr_t>(p.bias) % 8 == 0;
   auto kernel = !gradient ? k_statistics : x.type == SS_VALUES_BF16 ? k_logit_gradient<__nv_bfloat16> : k_logit_gradient<__half>;
   const size_t smem = gradient ? PairRing<kBN, 2>::kSmem : PairRing<kBN, 0>::kSmem;
