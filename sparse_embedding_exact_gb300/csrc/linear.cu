@@ -15,9 +15,10 @@
 // tensor copies in the 128-byte swizzle through a ring of stages; one warp
 // copies, one thread issues the products, sixteen warps run the epilogue and
 // store by tensor copies.  Measured, 8192 x 4096 x 4096 bf16, ten calls after a
-// pause: 159 us alone (1,730 TFLOP/s; cuBLAS on the same card 144), 202 us with
+// pause: 156 us alone (1,760 TFLOP/s; cuBLAS on the same card 144), 184 us with
 // bias, gelu, residual and kept pre-activation (the last tiles' epilogue and the
-// 200 MB of it); 5000 x 10000 x 2048 e4m3: 87 us.
+// 200 MB of it); 5000 x 10000 x 2048 e4m3: 84 us.  8192 x 4096 x 1024 with bias
+// and gelu 64 us, 71 with the pre-activation kept in 16 bits and 75 in 8.
 //
 // Fewer tiles than that fills (k_product): blocks on their own with tiles of
 // 128 x kBN, the summed dimension split over a cluster of up to 8 of them
@@ -31,7 +32,9 @@
 // The three products of a layer differ in which operand runs along the summed
 // dimension: x w^T has both rows contiguous in it (K-major), gz w has w
 // contiguous across it, and gz^T x both (MN-major); the copies and descriptors
-// take either, so nothing is transposed in memory.
+// take either, so nothing is transposed in memory.  A gradient's two products go
+// into one launch (gradients.cu) where that is estimated to end sooner: 8192 x
+// 4096 x 1024 bf16 95 us, where one after the other they took 56 and 52.
 //
 // One row, two of 16 bits (k_rows): a warp takes whole rows of w with 16-byte loads and
 // ordinary multiply-adds, no tile to fill.  One row, 65,536 features of 1024
@@ -728,10 +731,11 @@ __global__ void __launch_bounds__(32 * kRowWarps, kM == 1 ? 16 : 1) k_rows(const
 // gz = grad_y act'(pre) into gz[M][ld] (or nowhere), and the sums of its
 // columns over the block's rows into part[blockIdx.y][N] (or nowhere).  A warp
 // takes every eighth row of the block's share, two of them at a time.  Bound
-// by memory and, with a gelu, by instructions: 8192 x 4096 bf16 36 us (5.5 TB/s).
+// by memory and, with a gelu, by instructions: 8192 x 4096 bf16 36 us (5.5 TB/s),
+// from codes 38 at four blocks an SM (42 at three).
 // kAny: rows that start anywhere, or end within a unit of kN values.
 template <typename T, int kAct, bool kKept, bool kAny>
-__global__ void __launch_bounds__(256) k_act_grad(const ss_dense grad_y, const ss_dense pre, const ss_kept kept, T *gz, int64_t ld, float *part) {
+__global__ void __launch_bounds__(256, kAny ? 1 : 4) k_act_grad(const ss_dense grad_y, const ss_dense pre, const ss_kept kept, T *gz, int64_t ld, float *part) {
   constexpr int kN = 8;
   tc::let_next();
   __shared__ float sm[8][32 * kN + 1];
@@ -894,7 +898,7 @@ cudaError_t aligned_rows(ss_handle *h, std::initializer_list<ss_dense *> ms, uns
   while (x < 256 && 2 * (int64_t)x < units) x *= 2;
   const unsigned y = 256 / x;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>((rows + y - 1) / y, 16 * (int64_t)std::max(1, h->sm_count)), (unsigned)n);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((rows + y - 1) / y, 8 * (int64_t)std::max(1, h->sm_count)), (unsigned)n);
   cfg.blockDim = dim3(x, y);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
