@@ -241,7 +241,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
           tc::load_acc16x32(acc + (uint32_t)col + (16u << 16), r + 16);
           tc::load_acc_wait();
           if (half == 1) release();
-          if (n0 >= a.V) continue;
+          if (n0 >= a.V) {
+            if (a.sums && half == 1) tc::named_sync(1 + quarter, 128);  // the first half's place has been read
+            continue;
+          }
           const int64_t left = a.V - n0;
           float sums[8];
           if (m0 < a.M) {
@@ -311,7 +314,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
             const uint32_t mine = boxes + kStaging + (uint32_t)(half * 128);
             tc::write_shared(mine + 4 * (uint32_t)(lane / 8 * 8 + lane % 4 * 2 + (lane / 4 & 1)), total);
             // the four warps of these columns; a half's place is written again
-            // only after the other half's barrier, when all have read it
+            // only after the other half's barrier, when it has been read (the
+            // second half's barrier comes in every tile)
             tc::named_sync(1 + quarter, 128);
             if (q == half) {
               const int warp = (int)(threadIdx.x >> 5) - 2;

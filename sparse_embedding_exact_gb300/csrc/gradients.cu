@@ -275,6 +275,8 @@ cudaError_t launch_grad_products(ss_handle *h, const grad_products &g, cudaStrea
     if (e == cudaSuccess && p.vec[1]) e = encode_out(&p.out[1], p.y[1]);
     p.idesc[1] = idesc_of(g.gz, kMajorMN, kMajorMN, 2 * kTileM, kBN);
   }
+  if (!with_w) p.a[1] = p.a[0], p.b[1] = p.b[0];  // no tile of that kind, but the maps are fetched
+  if (!with_x) p.a[0] = p.a[1], p.b[0] = p.b[1];
   constexpr int kSmem = PairRing<kBN, 1>::kSmem;
   if (e == cudaSuccess) e = ensure_dyn_smem(k_grad_products, kSmem);
   if (e != cudaSuccess) return e;

@@ -279,6 +279,48 @@ def test_calls_in_a_row_share_memory(h):
             assert all(torch.equal(p, q) for p, q in zip(out, one))
 
 
+@pytest.mark.parametrize("v", [2561, 2592, 2593, 2624, 2625])
+def test_last_columns_over_many_tiles(h, v):
+    # tiles whose last quarter, or half of one, has no columns, many a pair of blocks
+    x, w, t, b, wt, gl = _case(5000, v, 64, torch.bfloat16)
+    _, (_, _, gx, gw, gb) = _check(h, x, w, t, gl, b, wt)
+    for _ in range(5):
+        again = h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt)
+        assert all(torch.equal(p, q) for p, q in zip(again[1:], (gx, gw, gb)))
+
+
+def test_gradients_left_out(h):
+    # the C calls' NULL gradients: the others' bits stay, and what is left out is not written
+    import ctypes
+
+    from sparse_embedding_exact_gb300 import _abi
+
+    x, w, t, b, wt, gl = _case(300, 2000, 136, torch.float16)
+    want = h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt)
+
+    def record(m):
+        return _abi.ss_dense(m.data_ptr(), m.shape[0], m.shape[1], m.stride(0), _abi.SS_VALUES_F16)
+
+    for asked in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 0, 1), (0, 1, 1), (0, 0, 0)):
+        got = [torch.full_like(g, 7) for g in want]
+        keep = [record(m) for m in (x, w, got[1], got[2])]
+        at = [ctypes.addressof(r) for r in keep]
+        need = h._lib.ss_cross_entropy_step_scratch(h._h, at[0], at[1])
+        room = torch.empty(need, dtype=torch.uint8, device="cuda")
+        st = h._lib.ss_cross_entropy_step(h._h, gl.data_ptr(), at[0], at[1], b.data_ptr(), t.data_ptr(), 1.0, wt.data_ptr(),
+                                          got[0].data_ptr(), at[2] if asked[0] else None, at[3] if asked[1] else None,
+                                          got[3].data_ptr() if asked[2] else None, room.data_ptr(), need,
+                                          torch.cuda.current_stream().cuda_stream)
+        assert st == _abi.SS_OK
+        assert torch.equal(got[0], want[0])
+        for a, g, one in zip(asked, got[1:], want[1:]):
+            assert torch.equal(g, one if a else torch.full_like(g, 7))
+        st = h._lib.ss_cross_entropy_step(h._h, gl.data_ptr(), at[0], at[1], b.data_ptr(), t.data_ptr(), 1.0, wt.data_ptr(),
+                                          got[0].data_ptr(), at[2], at[3], got[3].data_ptr(), room.data_ptr(), need - 1,
+                                          torch.cuda.current_stream().cuda_stream)
+        assert st == _abi.SS_ERR_INVALID_ARG
+
+
 def test_refusals(h):
     from sparse_embedding_exact_gb300 import SparseCosError
 
