@@ -290,8 +290,10 @@ cudaError_t launch_compress(const ss_dense &x, const ss_kept &out, cudaStream_t 
 cudaError_t launch_expand(const ss_kept &x, const ss_dense &y, cudaStream_t s, int *queued, bool beside = false);
 
 // out[c] = the sum of column c over the n rows of part (one kernel; a fixed
-// order), rounded to `type`.
-cudaError_t launch_sum_rows(const ss_handle *h, const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s);
+// order), rounded to `type`; beside: at the end of the kernel before, which is of
+// the same call.
+cudaError_t launch_sum_rows(const ss_handle *h, const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s,
+                            bool beside = false);
 
 struct distill_args {
   ss_dense logits, grad_logits;

@@ -845,7 +845,7 @@ struct Copies {
   int64_t ld[2];
 };
 template <typename T>
-__global__ void __launch_bounds__(256) k_copy_rows(const Copies a) {
+__global__ void __launch_bounds__(256, 6) k_copy_rows(const Copies a) {
   tc::let_next();
   const bool second = blockIdx.y == 1;
   const ss_dense src = second ? a.src[1] : a.src[0];
@@ -898,7 +898,8 @@ cudaError_t aligned_rows(ss_handle *h, std::initializer_list<ss_dense *> ms, uns
   while (x < 256 && 2 * (int64_t)x < units) x *= 2;
   const unsigned y = 256 / x;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>((rows + y - 1) / y, 8 * (int64_t)std::max(1, h->sm_count)), (unsigned)n);
+  // as many blocks as run at once: with 16 an SM the copy took half as long again
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((rows + y - 1) / y, 6 * (int64_t)std::max(1, h->sm_count)), (unsigned)n);
   cfg.blockDim = dim3(x, y);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

@@ -72,8 +72,7 @@ __device__ __forceinline__ void store_ragged(const ss_dense &out, uint32_t box, 
         if (m0 + r >= out.n_rows) continue;
         if (reinterpret_cast<uintptr_t>(to) & 2) {
           if (l < 15) *reinterpret_cast<uint32_t *>(to + 2 * l + 1) = __funnelshift_r(w, next, 16);
-          if (l == 0) to[0] = (uint16_t)w;
-          if (l == 15) to[31] = (uint16_t)(w >> 16);
+          if (l % 15 == 0) to[l == 0 ? 0 : 31] = (uint16_t)(l == 0 ? w : w >> 16);
         } else {
           *reinterpret_cast<uint32_t *>(to + 2 * l) = w;
         }

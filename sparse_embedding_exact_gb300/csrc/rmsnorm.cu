@@ -32,7 +32,7 @@
 #include <initializer_list>
 
 #include "kept.cuh"
-#include "tc.cuh"
+#include "product.cuh"
 
 namespace {
 
@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_
   constexpr bool kAsync = kN > 1;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ __align__(16) float sm[2][32];
+  tc::let_next();
   const Group gr(threads);
   const int D = (int)a.total.n_cols, R = (int)a.total.n_rows, step = (int)gridDim.x * ((int)blockDim.x / threads);
   const float inv_d = 1.0f / (float)D;
@@ -824,6 +825,7 @@ __global__ void __launch_bounds__(256) k_rms_grad_cols(const rms_grad_args a) {
 // rows of 1001: 5 us with 32, 3 with 8), else 32, a line a warp.
 template <int kCols>
 __global__ void __launch_bounds__(1024) k_sum_rows(const float *part, int64_t n, int64_t D, void *out, int32_t type) {
+  tc::wait_before();
   constexpr int kLanes = 1024 / kCols;
   __shared__ float sm[kLanes][kCols + 1];
   const int col = threadIdx.x % kCols, lane = threadIdx.x / kCols;
@@ -985,7 +987,7 @@ cudaError_t rms_grad_kept_typed(ss_handle *h, const rms_grad_args &a, cudaStream
     kernel<<<(unsigned)n, groups * threads, smem, s>>>(a, threads);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     *queued += 2;
-    return launch_sum_rows(h, a.scratch, n, D, a.grad_weight.data, a.grad_weight.type, s);
+    return launch_sum_rows(h, a.scratch, n, D, a.grad_weight.data, a.grad_weight.type, s, true);
   };
   const bool small = threads * groups <= kKeptThreads;
   if (vec) {
@@ -1062,12 +1064,10 @@ cudaError_t launch_rms_norm(ss_handle *h, const rms_args &a, cudaStream_t s, int
   }
 }
 
-cudaError_t launch_sum_rows(const ss_handle *h, const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s) {
-  if (cols / 32 >= h->sm_count / 2)
-    k_sum_rows<32><<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(part, n, cols, out, type);
-  else
-    k_sum_rows<8><<<(unsigned)((cols + 7) / 8), 1024, 0, s>>>(part, n, cols, out, type);
-  return cudaGetLastError();
+cudaError_t launch_sum_rows(const ss_handle *h, const float *part, int64_t n, int64_t cols, void *out, int32_t type, cudaStream_t s,
+                            bool beside) {
+  if (cols / 32 >= h->sm_count / 2) return launch_beside(k_sum_rows<32>, (unsigned)((cols + 31) / 32), 1024, 0, s, beside, part, n, cols, out, type);
+  return launch_beside(k_sum_rows<8>, (unsigned)((cols + 7) / 8), 1024, 0, s, beside, part, n, cols, out, type);
 }
 
 int64_t rms_grad_scratch(const ss_handle *h, int64_t R, int64_t D) {
