@@ -743,9 +743,10 @@ ss_status ss_rms_norm_kept_backward(ss_handle *h, const ss_dense *grad_y, const 
  * exp((x w^T + bias - it) / temperature); INFINITY for an absent row) for
  * ss_cross_entropy_backward, which takes the same arguments.  grad_x (M x K)
  * and grad_w (V x K): of x's type or float32; grad_bias: float[V]; each may
- * be NULL.  The gradients are computed in pieces of the items, a piece's gz
- * in scratch and rounded to x's type (float16: scaled by a power of two, so
- * that the largest |weight grad_loss / temperature| is near 2^15).
+ * be NULL.  The gradients are computed in pieces of the items, a piece's
+ * softmax less its targets in scratch and rounded to x's type, as are the rows
+ * of x times grad_loss * weight / temperature that grad_w is computed from
+ * (float16: both scaled by powers of two, the latter by one for the call).
  * A softmax below 2^-126 of the largest counts as 0.  grad_bias sums gz
  * unrounded.  ss_cross_entropy_step gives loss and
  * gradients in one call.  scratch: bytes of the call's _scratch.

@@ -25,10 +25,15 @@
 // pieces in float32 (gradients.cu).  Nothing of the size of the logits is ever
 // held; the price are the logits' flops once more (8 M V K in place of 6).
 //
-// gz of binary16 is held times a power of two that brings the largest |weight
-// grad_loss / T| below 2^15, as a softmax over many items lies below binary16's
-// smallest values; the products' epilogues take it out again.  bfloat16 has
-// float32's exponents and needs none.
+// gz is held without its row's factor weight grad_loss / T, between -1 and 1:
+// the target's value, p - 1, is most of a row and near -1 as a rule, where it
+// rounds to next to nothing.  grad_x's rows take the factor in the epilogue,
+// grad_w takes rows of x times it, rounded to x's type.  (With the factor in gz
+// the target's value lost up to half a step, the whole row of grad_x with it:
+// 1.6 times the final rounding's error with few rows.)  binary16's gz is held
+// times 2^14, as most of a softmax over many items lies below its smallest
+// values, and its rows of x times one power of two that brings the largest
+// factor near 1; the epilogues take both out again.
 #include <math.h>
 
 #include <algorithm>
@@ -76,11 +81,13 @@ struct UnitWalk {
 };
 
 // What the gradient of a row's logits takes: gz_v = exp2(c z_v - base) share,
-// less `scale` at the target.
+// less `hot` at the target, and the row's factor over `hot`.  hot, what 1 stands
+// for in gz: 1, binary16 2^14.
 struct alignas(16) Row {
   float base, share, scale;
   int32_t target;
 };
+constexpr int kHalfBits = 14;
 __device__ __forceinline__ Row absent_row() { return {INFINITY, 0.0f, 0.0f, -1}; }  // exp2(-inf) 0
 
 struct Logits {
@@ -100,7 +107,7 @@ struct Logits {
   float *here;           // [M]: the target's logit
   // gradient
   const Row *rows;
-  const float *factor;   // gz's power of two, or null: 1
+  float hot;
   ss_dense out;
   float *sums;           // [tiles_a * 2][ld_sums] or null: columns' sums over 128 rows
   int64_t ld_sums;
@@ -222,14 +229,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
       &a.a, &a.b, &a.idesc, a.status, walk,
       [&](const UnitWalk &, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
         const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32;
-        const float factor = a.factor ? a.factor[0] : 1.0f;
         Row row[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int64_t m = m0 + lane / 4 + 8 * k;
           row[k] = m < a.M ? a.rows[m] : absent_row();
-          row[k].share *= factor;
-          row[k].scale *= factor;
         }
         const Two c2 = two(a.c, a.c);
 #pragma unroll 1
@@ -282,9 +286,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
                 Two g = two(exp2_fast(e.x), exp2_fast(e.y)) * two(row[k].share, row[k].share);
                 if (any_hot) {
                   const int64_t at = row[k].target - (a.first + n0) - (8 * i + 2 * (lane % 4));
-                  g = g + two(at == 0 ? -row[k].scale : 0.0f, at == 1 ? -row[k].scale : 0.0f);
+                  g = g + two(at == 0 ? -a.hot : 0.0f, at == 1 ? -a.hot : 0.0f);
                 }
-                sum = sum + g;
+                sum = fma_of(g, two(row[k].scale, row[k].scale), sum);
                 const float2 h = both(g);
                 packed[k][i] = narrow2(T(), h.x, h.y);
               }
@@ -323,7 +327,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
               total = 0.0f;
 #pragma unroll
               for (int k = 0; k < 4; ++k) total += tc::read_shared<float>(firsts + (uint32_t)(k * 2 * kStaging) + 4 * (uint32_t)lane);
-              if (a.factor) total *= a.factor[1];
               if (lane < left) a.sums[(m0 / kTileM) * a.ld_sums + n0 + lane] = total;
             }
           }
@@ -332,9 +335,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
 }
 
 // Between the two: the rows' losses and statistics from the units' pairs, in
-// their order (unless the statistics are given), what gz takes of each row, x
-// with the absent rows' values 0, as 0 times an infinity or NaN there would
-// reach grad_w, and binary16's power of two and its reciprocal.  A block takes
+// their order (unless the statistics are given), what gz takes of each row, and
+// x with the absent rows' values 0, as 0 times an infinity or NaN there would
+// reach grad_w, once as it is and once times the rows' factors.  A block takes
 // eight rows, 32 threads a row.
 struct Between {
   const float2 *part;  // or null: stats are given
@@ -351,12 +354,52 @@ struct Between {
   ss_dense x;
   void *to;            // x's copy, or x's own data: absent rows alone are written then
   int64_t ld;
-  float *factor;       // or null
+  void *scaled;         // x times the rows' factors (and the power of two)
+  float hot;
+  const float *factor;  // binary16's power of two, or null: 1
+  int32_t type;
 };
+// binary16's power of two, which brings the largest |factor of a row| to 1/2 at
+// least and below 1, and what takes it and gz's out of their products.
+__global__ void __launch_bounds__(1024) k_factor(const float *weight, const float *grad_loss, float inv_t, int64_t M, float *factor) {
+  __shared__ float sm[32];
+  tc::let_next();
+  float most = 0.0f;
+#pragma unroll 4
+  for (int64_t k = threadIdx.x; k < M; k += 1024) {
+    const float v = fabsf((weight ? weight[k] : 1.0f) * (grad_loss ? grad_loss[k] : 1.0f) * inv_t);
+    if (v < INFINITY) most = fmaxf(most, v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = most;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 32; ++k) most = fmaxf(most, sm[k]);
+    const int e = most > 0.0f ? max(-100, min(100, -1 - ilogbf(most))) : 0;
+    factor[0] = ldexpf(1.0f, e);
+    factor[1] = ldexpf(1.0f, -e - kHalfBits);
+  }
+  tc::wait_before();  // what follows waits for this kernel, and so for the one before it
+}
+// 8 values, or one, of T times f.
+template <typename T>
+__device__ __forceinline__ uint4 times(uint4 v, float f) {
+  Pack<T, 8> p;
+  memcpy(&p, &v, 16);
+  float x[8];
+  widen(p, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= f;
+  p = narrow<T, 8>(x);
+  memcpy(&v, &p, 16);
+  return v;
+}
 constexpr int kBetweenRows = 8, kBetweenThreads = 256;
 __global__ void __launch_bounds__(kBetweenThreads) k_between(const Between a) {
   __shared__ float2 sm[kBetweenThreads / 32][kBetweenRows];
   __shared__ bool there[kBetweenRows];
+  __shared__ float scales[kBetweenRows];
   tc::wait_before();
   tc::let_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -407,7 +450,8 @@ __global__ void __launch_bounds__(kBetweenThreads) k_between(const Between a) {
     }
     if (a.rows) {
       const float scale = weight * (a.grad_loss ? a.grad_loss[m] : 1.0f) * a.inv_t;
-      a.rows[m] = live ? Row{base_of(most, a.c), scale / sum, scale, (int32_t)target} : absent_row();
+      a.rows[m] = live ? Row{base_of(most, a.c), a.hot / sum, scale / a.hot, (int32_t)target} : absent_row();
+      scales[lane] = live ? (a.factor ? scale * a.factor[0] : scale) : 0.0f;
     }
   }
   if (!a.rows) return;
@@ -416,33 +460,25 @@ __global__ void __launch_bounds__(kBetweenThreads) k_between(const Between a) {
   const int r = warp;
   const int64_t row = row0 + r;
   if (row < a.M) {
-    uint16_t *to = static_cast<uint16_t *>(a.to) + row * a.ld;
+    uint16_t *to = static_cast<uint16_t *>(a.to) + row * a.ld, *scaled = static_cast<uint16_t *>(a.scaled) + row * a.ld;
     const uint16_t *from = static_cast<const uint16_t *>(a.x.data) + row * a.x.ld;
-    const bool same = from == to;
-    if (same && there[r]) {
-    } else if (a.vec) {
-      for (int64_t c = (int64_t)lane * 8; c < a.x.n_cols; c += 256)
-        *reinterpret_cast<uint4 *>(to + c) = there[r] ? *reinterpret_cast<const uint4 *>(from + c) : make_uint4(0, 0, 0, 0);
+    const float f = scales[r];
+    const bool bf16 = a.type == SS_VALUES_BF16;
+    if (a.vec) {
+      for (int64_t c = (int64_t)lane * 8; c < a.x.n_cols; c += 256) {
+        const uint4 v = there[r] ? *reinterpret_cast<const uint4 *>(from + c) : make_uint4(0, 0, 0, 0);
+        if (from != to || !there[r]) *reinterpret_cast<uint4 *>(to + c) = v;
+        *reinterpret_cast<uint4 *>(scaled + c) = bf16 ? times<__nv_bfloat16>(v, f) : times<__half>(v, f);
+      }
     } else {
-      for (int64_t c = lane; c < a.x.n_cols; c += 32) to[c] = there[r] ? from[c] : (uint16_t)0;
+      for (int64_t c = lane; c < a.x.n_cols; c += 32) {
+        const uint16_t v = there[r] ? from[c] : (uint16_t)0;
+        to[c] = v;
+        const uint32_t w = bf16 ? narrow2(__nv_bfloat16(), __uint_as_float((uint32_t)v << 16) * f, 0.0f)
+                                : narrow2(__half(), __half2float(__ushort_as_half(v)) * f, 0.0f);
+        scaled[c] = (uint16_t)w;
+      }
     }
-  }
-  if (!a.factor || blockIdx.x != 0) return;
-  most = 0.0f;
-#pragma unroll 4
-  for (int64_t k = threadIdx.x; k < a.M; k += kBetweenThreads) {
-    const float v = fabsf((a.weight ? a.weight[k] : 1.0f) * (a.grad_loss ? a.grad_loss[k] : 1.0f) * a.inv_t);
-    if (v < INFINITY) most = fmaxf(most, v);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-  if (lane == 0) sm[warp][0].x = most;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < kBetweenThreads / 32; ++k) most = fmaxf(most, sm[k][0].x);
-    const int e = most > 0.0f ? max(-100, min(100, 14 - ilogbf(most))) : 0;
-    a.factor[0] = ldexpf(1.0f, e);
-    a.factor[1] = ldexpf(1.0f, -e);
   }
 }
 
@@ -467,7 +503,7 @@ int64_t units_of(const ss_handle *h, int64_t tiles_a, int64_t tiles_b) {
 
 // The scratch of a call, in this order.
 struct Room {
-  int64_t V, K, piece, x, w, factor, part, here, rows, gz, acc, sums;
+  int64_t V, K, piece, x, scaled, w, factor, part, here, rows, gz, acc, sums;
   int64_t units, parts;
   bool whole_sums;  // the columns' sums of all pieces at once
   Room(const ss_handle *h, const ss_dense &x_, const ss_dense &w_, int32_t mode) {
@@ -480,6 +516,7 @@ struct Room {
     const int64_t most = std::max<int64_t>(2048, ((int64_t)1 << 27) / std::max<int64_t>(1, M)), pieces = up(V, most);
     piece = up(up(V, pieces), kBN) * kBN;
     x = grad ? align_up(M * padded_ld(x_) * 2) : copy_bytes(x_);
+    scaled = grad ? x : 0;
     w = copy_bytes(w_);
     factor = grad ? SS_SCRATCH_ALIGN : 0;
     part = loss ? align_up(units * 4 * M * (int64_t)sizeof(float2)) : 0;
@@ -491,7 +528,7 @@ struct Room {
     whole_sums = tiles_a * 2 * V <= (int64_t)1 << 26;
     sums = grad ? align_up(tiles_a * 2 * (whole_sums ? V : piece) * 4) : 0;
   }
-  int64_t bytes() const { return x + w + factor + part + here + rows + gz + acc + sums; }
+  int64_t bytes() const { return x + scaled + w + factor + part + here + rows + gz + acc + sums; }
 };
 
 ss_dense rows_from(const ss_dense &m, int64_t first, int64_t n) {
@@ -550,17 +587,19 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   };
   ss_dense x = a.x, w = a.w;
   void *copy = grad ? take(room.x) : nullptr;
+  void *scaled = nullptr;
   if (grad) {
     unsigned char *to = rows_aligned(x, 16) ? at : static_cast<unsigned char *>(copy);  // w's copy follows x's place
     // rows that start anywhere are copied here, the absent ones cleared later
     if ((e = launch_aligned_rows(h, &x, &w, &to, s, queued)) != cudaSuccess) return e;
     at += room.w;
+    scaled = take(room.scaled);
   } else if ((e = launch_aligned_rows(h, &x, &w, &at, s, queued)) != cudaSuccess) {
     return e;
   }
   Logits p = {};
   p.c = kLog2e / a.temperature;
-  p.factor = nullptr;
+  p.hot = a.x.type == SS_VALUES_F16 ? (float)(1 << kHalfBits) : 1.0f;
   Between b = {};
   b.weight = a.weight;
   b.grad_loss = a.grad_loss;
@@ -574,6 +613,11 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   b.stats = reinterpret_cast<float2 *>(a.stats);
   b.status = h->d_status;
   float *factor = reinterpret_cast<float *>(take(room.factor));
+  if (grad && a.x.type == SS_VALUES_F16) {
+    if ((e = launch_beside(k_factor, 1, 1024, 0, s, *queued > 0, a.weight, a.grad_loss, b.inv_t, M, factor)) != cudaSuccess) return e;
+    *queued += 1;
+    b.factor = factor;
+  }
   if (loss) {
     p.targets = a.targets;
     p.part = reinterpret_cast<float2 *>(take(room.part));
@@ -591,7 +635,9 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
     b.to = copy;
     b.ld = padded_ld(a.x);
     b.vec = K % 8 == 0 && rows_aligned(x, 16);
-    b.factor = a.x.type == SS_VALUES_F16 ? factor : nullptr;
+    b.scaled = scaled;
+    b.hot = p.hot;
+    b.type = a.x.type;
   }
   const bool first = *queued == 0;
   *queued += 1;
@@ -599,15 +645,17 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   x.data = copy;
   x.ld = b.ld;
   p.rows = b.rows;
-  p.factor = b.factor;
   void *gz = take(room.gz);
   grad_products g = {};
   g.x = x;
+  g.x.data = scaled;
   g.grad_x = a.grad_x;
   g.acc = reinterpret_cast<float *>(take(room.acc));
   g.parts = (int32_t)room.parts;
   g.beside = true;
   g.factor = b.factor ? b.factor + 1 : nullptr;
+  g.row_factor = &b.rows->scale;
+  g.row_step = sizeof(Row) / sizeof(float);
   float *sums = reinterpret_cast<float *>(take(room.sums));
   const int64_t tiles_a = up(M, 2 * kTileM);
   for (int64_t first = 0; first < V; first += room.piece) {

@@ -336,7 +336,7 @@ cudaError_t launch_aligned_rows(ss_handle *h, ss_dense *m, ss_dense *other, unsi
 
 // A layer's two gradient products in one launch, all matrices of 16 bits with
 // 16-byte aligned rows:
-//   grad_x (+)= factor gz wide  and  grad_w = factor gz^T x
+//   grad_x (+)= diag(row_factor) gz wide  and  grad_w = factor gz^T x
 // grad_x may come in several calls (`begun`: an earlier one added to acc;
 // `ends`: grad_x is written), each of another gz and wide of the same sizes or
 // less.  Its sum is split over `parts` (grad_product_parts of the largest gz)
@@ -354,6 +354,8 @@ struct grad_products {
   const float *sums;
   int64_t sum_rows, sum_cols;
   float *sum_to;
+  const float *row_factor;  // float r row_step of it for row r, or null: 1
+  int32_t row_step;
 };
 int64_t grad_product_parts(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *clocks = nullptr);
 int64_t grad_part_bytes(int64_t M, int64_t K);

@@ -79,7 +79,8 @@ struct Products {
   int32_t vec[2];       // their rows start on 16-byte boundaries
   const float *before;  // what earlier calls added up, or null
   int64_t ld_before, part_rows;
-  const float *factor;
+  const float *factor, *row_factor;
+  int32_t row_step;
   int32_t *status;
 };
 
@@ -90,7 +91,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_g
   pair_products<kBN, kMajorByKind, kMajorMN, false, 1>(
       a.a, a.b, a.idesc, a.status, DealWalk{a.deal, pair, 0, 0},
       [&](const DealWalk &w, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
-        const float factor = a.factor ? *a.factor : 1.0f;
         ss_dense y = a.y[t.kind];
         int64_t under = 0;  // rows of the parts before this one
         if (t.kind == 0 && a.part_rows) {
@@ -99,6 +99,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_g
         }
         const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32, row = under + m0;
         const bool there = row < y.n_rows;
+        float factor = 1.0f;
+        if (t.kind == 0 && a.row_factor && row + lane < y.n_rows) factor = a.row_factor[(m0 + lane) * a.row_step];
+        if (t.kind == 1 && a.factor) factor = *a.factor;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int col = quarter * (kBN / 4) + half * 32;
@@ -252,6 +255,8 @@ cudaError_t launch_grad_products(ss_handle *h, const grad_products &g, cudaStrea
   const int64_t parts = std::min<int64_t>(g.parts, up(N, 64));
   p.deal = deal_of(h, M, N, K, parts, with_x, with_w, nullptr);
   p.factor = g.factor;
+  p.row_factor = g.row_factor;
+  p.row_step = g.row_step;
   p.status = h->d_status;
   cudaError_t e = cudaSuccess;
   if (with_x) {

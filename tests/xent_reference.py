@@ -52,8 +52,10 @@ def bounds(r, x, w, bias=None, weight=None, grad_loss=None, temperature=1.0, dty
     (log2 e / T times logit minus base) is off by three roundings relative to
     itself, ex2 by 2^-22; a row's sum of V of them is added up in chains of at
     most V / 7 + 64 roundings, rescalings included; the softmax has both twice.
-    gz is then rounded to x's type, or that of binary16 times a power of two
-    that brings the largest to 2^14 at least (half a step 2^-25 there)."""
+    The softmax less its target is then rounded to x's type (that of binary16
+    times 2^14: half a step 2^-39), and for grad_w x times its row's factor
+    (that of binary16 times a power of two that brings the largest factor to
+    1/2 at least: half a step at most 2^-24 of that)."""
     V, K = w.shape
     size = r["x"].abs() @ w.to(F64).abs().t()
     if bias is not None:
@@ -74,14 +76,18 @@ def bounds(r, x, w, bias=None, weight=None, grad_loss=None, temperature=1.0, dty
     # of 1 at least: 2^-126 |scale| more
     soft = s * r["p"] * rel + 4 * E * s * (r["p"] + r["hot"]) + s * 2.0 ** -126
     top = float(s.max()) if s.numel() else 0.0
-    half = 2.0 ** -39 * top if x.dtype == torch.float16 else STEP[x.dtype]
-    off = soft + ROUND[x.dtype] * (r["gz"].abs() + soft) + torch.where(r["live"][:, None], half, 0.0)
+    half = s * (2.0 ** -39 if x.dtype == torch.float16 else STEP[x.dtype])
+    off = soft + ROUND[x.dtype] * (r["gz"].abs() + soft) + torch.where(r["live"][:, None], half, torch.zeros_like(half))
     full = r["gz"].abs() + off
     M = x.shape[0]
     wa, xa = w.to(F64).abs(), r["x"].abs()
+    # the rounding of a row of x times its factor, in that product's terms
+    unit = torch.where(s > 0, full / s.clamp_min(1e-300), torch.zeros_like(full))
+    step_x = 2.0 ** -24 * top if x.dtype == torch.float16 else STEP[x.dtype]
+    off_x = ROUND[x.dtype] * full.t() @ xa + unit.t() @ torch.full_like(xa, step_x)
     out = dtype or x.dtype
     close = lambda want, extra: ROUND[out] * (want.abs() + extra) + extra + STEP[out]  # noqa: E731
     gx = close(r["grad_x"], off @ wa + sum_bound(full @ wa, V) + pieces * E * (full @ wa))
-    gw = close(r["grad_w"], off.t() @ xa + sum_bound(full.t() @ xa, M))
+    gw = close(r["grad_w"], (1 + ROUND[x.dtype]) * (off.t() @ xa) + off_x + sum_bound(full.t() @ xa + off_x, M))
     gb = soft.sum(0) + (64 + M / 8) * E * full.sum(0) + 2.0 ** -149
     return {"loss": loss + 2.0 ** -149, "grad_x": gx, "grad_w": gw, "grad_bias": gb}
