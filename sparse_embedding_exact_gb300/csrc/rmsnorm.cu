@@ -992,7 +992,9 @@ cudaError_t rms_grad_kept_typed(ss_handle *h, const rms_grad_args &a, cudaStream
   const bool small = threads * groups <= kKeptThreads;
   if (vec) {
     if (per == 1) return run(k_rms_grad_kept<T, kV, 1, kKeptThreads>, 3);
-    if (per == 2) return small ? run(k_rms_grad_kept<T, kV, 2, kKeptThreads>, 3) : run(k_rms_grad_kept<T, kV, 2, kMostThreads>, 1);
+    // two units want more registers than three blocks an SM leave (4096 x 4096
+    // bf16 with them 65 us)
+    if (per == 2) return run(k_rms_grad_kept<T, kV, 2, kMostThreads>, small ? 2 : 1);
     if constexpr (kV == 4) return run(k_rms_grad_kept<T, kV, 4, kMostThreads>, 1);
   }
   if (per == 4) return small ? run(k_rms_grad_kept<T, 1, 4, kKeptThreads>, 3) : run(k_rms_grad_kept<T, 1, 4, kMostThreads>, 1);
