@@ -746,7 +746,9 @@ ss_status ss_rms_norm_kept_backward(ss_handle *h, const ss_dense *grad_y, const 
  * be NULL.  The gradients are computed in pieces of the items, a piece's
  * softmax less its targets in scratch and rounded to x's type, as are the rows
  * of x times grad_loss * weight / temperature that grad_w is computed from
- * (float16: both scaled by powers of two, the latter by one for the call).
+ * (float16: both scaled by powers of two, the latter by one for the call that
+ * brings the largest factor of a row that takes part near 1: values that are
+ * then below 2^-14 lose bits).
  * A softmax below 2^-126 of the largest counts as 0.  grad_bias sums gz
  * unrounded.  ss_cross_entropy_step gives loss and
  * gradients in one call.  scratch: bytes of the call's _scratch.

@@ -360,15 +360,18 @@ struct Between {
   int32_t type;
 };
 // binary16's power of two, which brings the largest |factor of a row| to 1/2 at
-// least and below 1, and what takes it and gz's out of their products.
-__global__ void __launch_bounds__(1024) k_factor(const float *weight, const float *grad_loss, float inv_t, int64_t M, float *factor) {
+// least and below 1, and what takes it and gz's out of their products.  Of the
+// rows that take part: a padded one's weight and gradient may be anything.
+__global__ void __launch_bounds__(1024) k_factor(const int64_t *targets, const float *bias, const float *weight, const float *grad_loss, float inv_t,
+                                                 int64_t M, int64_t V, float *factor) {
   __shared__ float sm[32];
   tc::let_next();
   float most = 0.0f;
 #pragma unroll 4
   for (int64_t k = threadIdx.x; k < M; k += 1024) {
+    const int64_t target = targets[k];
     const float v = fabsf((weight ? weight[k] : 1.0f) * (grad_loss ? grad_loss[k] : 1.0f) * inv_t);
-    if (v < INFINITY) most = fmaxf(most, v);
+    if (target >= 0 && target < V && v < INFINITY && !(bias && bias[target] == -INFINITY)) most = fmaxf(most, v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
@@ -614,7 +617,8 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   b.status = h->d_status;
   float *factor = reinterpret_cast<float *>(take(room.factor));
   if (grad && a.x.type == SS_VALUES_F16) {
-    if ((e = launch_beside(k_factor, 1, 1024, 0, s, *queued > 0, a.weight, a.grad_loss, b.inv_t, M, factor)) != cudaSuccess) return e;
+    if ((e = launch_beside(k_factor, 1, 1024, 0, s, *queued > 0, a.targets, a.bias, a.weight, a.grad_loss, b.inv_t, M,
+                           V, factor)) != cudaSuccess) return e;
     *queued += 1;
     b.factor = factor;
   }

@@ -149,6 +149,28 @@ def test_rows_of_masked_targets_hold_anything(h):
         assert not loss[[4, 40, 69]].any() and not gx[[4, 40, 69]].any()
 
 
+def test_padded_rows_have_any_weight_and_gradient(h):
+    # rows that take no part do not set the scale of those that do
+    for dtype in HALVES:
+        x, w, t, b, wt, gl = _case(70, 600, 64, dtype)
+        b[77] = -math.inf
+        t[[4, 40]] = -1
+        t[[5, 69]] = 77
+        wt[50] = 0.0
+        b[t[:3]] = 0.0
+        plain = [v.clone() for v in (wt, gl)]
+        r = ref.cross_entropy(x, w, t, plain[1], b, plain[0])
+        room = ref.bounds(r, x, w, b, plain[0], plain[1])
+        wt[[4, 5]], gl[[4, 69]], gl[50] = 1e30, 1e25, 1e35
+        wt[40], gl[40] = math.nan, math.inf
+        got = h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt)
+        for name, one in zip(NAMES, got):
+            _compare(one, r[name], room[name], name)
+        _, stats = h.cross_entropy(x, w, t, bias=b, weight=wt)
+        for name, one in zip(NAMES[1:], h.cross_entropy_backward(gl, x, w, t, stats, bias=b, weight=wt)):
+            _compare(one, r[name], room[name], name)
+
+
 def test_everything_masked(h):
     x, w, t, b, wt, gl = _case(40, 300, 32, torch.bfloat16)
     loss, stats = h.cross_entropy(x, w, t, bias=torch.full_like(b, -math.inf))
