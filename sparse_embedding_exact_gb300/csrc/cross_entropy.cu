@@ -6,7 +6,7 @@
 //   grad_x = gz w,  grad_w = gz^T x,  grad_bias = sum_r gz_r
 //
 // x [M, K] rows, w [V, K] items, 16 bits; sums, statistics and the epilogue
-// float32.  A row without a target, with one that the bias masks (-inf) or of
+// float32.  A row without a target, with one that the bias masks or of
 // weight 0 is absent: loss 0 and gradient 0, whatever x holds.
 //
 // The loss (k_statistics): tiles of 256 x 256 logits by pairs of blocks
@@ -53,8 +53,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 // The exponent of a logit is fma(z, c, -base_of(largest z)), c = log2(e) / T:
-// the same rounded base everywhere, so that it cancels.
-__device__ __forceinline__ float base_of(float most, float c) { return most == -INFINITY ? 0.0f : most * c; }
+// the same rounded base everywhere, so that it cancels.  A value at or below
+// `low` is masked, as -infinity is: times c it may be past float32's lowest, and
+// as the base of a range of items that are all masked it would give inf - inf.
+// With the base 0 their exponentials are 0.
+__device__ __forceinline__ float base_of(float most, float c, float low) { return most <= low ? 0.0f : most * c; }
 
 // Units of consecutive tiles of one row of tiles; units that share their items
 // follow one another, so that the tiles in flight share w's rows in L2.
@@ -100,6 +103,7 @@ struct Logits {
   const float *bias;     // of the piece, or null
   int32_t bias_pairs;    // it starts on an 8-byte boundary
   float c;               // log2(e) / T
+  float low;             // masked from here down
   float cut;             // cut_share(K)
   // statistics
   const int64_t *targets;
@@ -117,12 +121,12 @@ struct Logits {
 // exponentials, over its columns of a unit.
 struct Running {
   float most, sum;
-  __device__ __forceinline__ void add32(float (&v)[32], float c) {
+  __device__ __forceinline__ void add32(float (&v)[32], float c, float low) {
     float top = most;
 #pragma unroll
     for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
-    const float b = base_of(top, c);
-    sum = most == -INFINITY ? 0.0f : sum * exp2_fast(base_of(most, c) - b);
+    const float b = base_of(top, c, low);
+    sum = most <= low ? 0.0f : sum * exp2_fast(base_of(most, c, low) - b);
     most = top;
     const Two c2 = two(c, c), b2 = two(-b, -b);
     Two s = two(0.0f, 0.0f);
@@ -188,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_s
               if (bit & (1u << i)) z = v[i];
             if (target < a.V) a.here[m] = z;
           }
-          run.add32(v, a.c);
+          run.add32(v, a.c, a.low);
         }
         if (w.last() && m < a.M) a.part[(w.number * 4 + quarter) * a.M + m] = make_float2(run.most, run.sum);
       });
@@ -345,7 +349,7 @@ struct Between {
   const int64_t *targets;
   int64_t M, V;
   int32_t parts, vec;
-  float c, inv_t;
+  float c, low, inv_t;
   float *loss;
   float2 *stats;
   int32_t *status;
@@ -362,8 +366,8 @@ struct Between {
 // binary16's power of two, which brings the largest |factor of a row| to 1/2 at
 // least and below 1, and what takes it and gz's out of their products.  Of the
 // rows that take part: a padded one's weight and gradient may be anything.
-__global__ void __launch_bounds__(1024) k_factor(const int64_t *targets, const float *bias, const float *weight, const float *grad_loss, float inv_t,
-                                                 int64_t M, int64_t V, float *factor) {
+__global__ void __launch_bounds__(1024) k_factor(const int64_t *targets, const float *bias, float low, const float *weight, const float *grad_loss,
+                                                 float inv_t, int64_t M, int64_t V, float *factor) {
   __shared__ float sm[32];
   tc::let_next();
   float most = 0.0f;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(1024) k_factor(const int64_t *targets, const f
   for (int64_t k = threadIdx.x; k < M; k += 1024) {
     const int64_t target = targets[k];
     const float v = fabsf((weight ? weight[k] : 1.0f) * (grad_loss ? grad_loss[k] : 1.0f) * inv_t);
-    if (target >= 0 && target < V && v < INFINITY && !(bias && bias[target] == -INFINITY)) most = fmaxf(most, v);
+    if (target >= 0 && target < V && v < INFINITY && !(bias && bias[target] <= low)) most = fmaxf(most, v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
@@ -409,9 +413,9 @@ __global__ void __launch_bounds__(kBetweenThreads) k_between(const Between a) {
   const int64_t row0 = (int64_t)blockIdx.x * kBetweenRows, m = row0 + lane % kBetweenRows;
   float most = -INFINITY, sum = 0.0f;
   auto add = [&](float2 p) {
-    const float top = fmaxf(most, p.x), b = base_of(top, a.c);
-    sum = (most == -INFINITY ? 0.0f : sum * exp2_fast(base_of(most, a.c) - b)) +
-          (p.x == -INFINITY && p.y == 0.0f ? 0.0f : p.y * exp2_fast(base_of(p.x, a.c) - b));
+    const float top = fmaxf(most, p.x), b = base_of(top, a.c, a.low);
+    sum = (most <= a.low ? 0.0f : sum * exp2_fast(base_of(most, a.c, a.low) - b)) +
+          (p.x <= a.low && p.y == 0.0f ? 0.0f : p.y * exp2_fast(base_of(p.x, a.c, a.low) - b));
     most = top;
   };
   if (a.part) {
@@ -438,12 +442,12 @@ __global__ void __launch_bounds__(kBetweenThreads) k_between(const Between a) {
     const float weight = a.weight ? a.weight[m] : 1.0f;
     const bool past = target >= a.V;
     if (past) flag(a.status, DEV_OUT_OF_RANGE);
-    bool live = target >= 0 && !past && weight != 0.0f && !(a.bias && a.bias[target] == -INFINITY);
+    bool live = target >= 0 && !past && weight != 0.0f && !(a.bias && a.bias[target] <= a.low);
     there[lane] = live;
     if (a.part) {
       for (int k = 1; k < kBetweenThreads / 32; ++k) add(sm[k][lane]);
       float loss = 0.0f;
-      if (live) loss = weight * (kLn2 * (log2f(sum) - fmaf(a.here[m], a.c, -base_of(most, a.c))));
+      if (live) loss = weight * (kLn2 * (log2f(sum) - fmaf(a.here[m], a.c, -base_of(most, a.c, a.low))));
       a.loss[m] = loss;
       if (a.stats) a.stats[m] = make_float2(most, live ? sum : INFINITY);
     } else {
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kBetweenThreads) k_between(const Between a) {
     }
     if (a.rows) {
       const float scale = weight * (a.grad_loss ? a.grad_loss[m] : 1.0f) * a.inv_t;
-      a.rows[m] = live ? Row{base_of(most, a.c), a.hot / sum, scale / a.hot, (int32_t)target} : absent_row();
+      a.rows[m] = live ? Row{base_of(most, a.c, a.low), a.hot / sum, scale / a.hot, (int32_t)target} : absent_row();
       scales[lane] = live ? (a.factor ? scale * a.factor[0] : scale) : 0.0f;
     }
   }
@@ -602,6 +606,7 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   }
   Logits p = {};
   p.c = kLog2e / a.temperature;
+  p.low = -1e38f * std::min(1.0f, a.temperature);
   p.hot = a.x.type == SS_VALUES_F16 ? (float)(1 << kHalfBits) : 1.0f;
   Between b = {};
   b.weight = a.weight;
@@ -611,14 +616,15 @@ cudaError_t launch_xent(ss_handle *h, const xent_args &a, int32_t mode, cudaStre
   b.M = M;
   b.V = V;
   b.c = p.c;
+  b.low = p.low;
   b.inv_t = 1.0f / a.temperature;
   b.loss = a.loss;
   b.stats = reinterpret_cast<float2 *>(a.stats);
   b.status = h->d_status;
   float *factor = reinterpret_cast<float *>(take(room.factor));
   if (grad && a.x.type == SS_VALUES_F16) {
-    if ((e = launch_beside(k_factor, 1, 1024, 0, s, *queued > 0, a.targets, a.bias, a.weight, a.grad_loss, b.inv_t, M,
-                           V, factor)) != cudaSuccess) return e;
+    if ((e = launch_beside(k_factor, 1, 1024, 0, s, *queued > 0, a.targets, a.bias, p.low, a.weight, a.grad_loss,
+                           b.inv_t, M, V, factor)) != cudaSuccess) return e;
     *queued += 1;
     b.factor = factor;
   }

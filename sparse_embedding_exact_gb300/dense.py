@@ -173,10 +173,11 @@ class DenseOperators:
                       temperature: float = 1.0, stream=None):
         """(loss, stats): per row weight * -log softmax((x w^T + bias) / T) at
         its target, over every item, without the logits; x (M, K) and w (V, K)
-        in bfloat16 or float16, targets int64 (M,).  A row of a negative
-        target, of one whose bias is -inf, or of weight 0 has loss 0; a target
-        past the last item too, and ``check_device`` reports it.  stats are
-        what ``cross_entropy_backward`` takes."""
+        in bfloat16 or float16, targets int64 (M,).  A bias of -inf, or of at
+        most -1e38 min(1, T), masks an item.  A row of a negative target, of a
+        masked one, or of weight 0 has loss 0; a target past the last item too,
+        and ``check_device`` reports it.  stats are what
+        ``cross_entropy_backward`` takes."""
         return self._run("cross_entropy", stream, x, w, targets, bias, weight, temperature)
 
     def cross_entropy_backward(self, grad_loss: Optional[torch.Tensor], x: torch.Tensor, w: torch.Tensor,

@@ -171,6 +171,28 @@ def test_padded_rows_have_any_weight_and_gradient(h):
             _compare(one, r[name], room[name], name)
 
 
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("T,mask", [(1.0, torch.finfo(torch.float32).min), (4.0, torch.finfo(torch.bfloat16).min), (0.05, -5e36), (0.05, -3e38)])
+def test_masks_of_the_lowest_value(h, dtype, T, mask):
+    # whole units, tiles and halves of tiles of masked items, and a row's target among them
+    x, w, t, b, wt, gl = _case(300, 3000, 64, dtype)
+    b[300:1700], b[1800:1835], b[2990:] = -math.inf, -math.inf, -math.inf
+    t[:] = t % 250
+    t[7], t[200] = 301, 2995
+    low = torch.where(torch.isinf(b), torch.full_like(b, mask), b)
+    b[::5], low[::5] = -math.inf, -math.inf
+    _, want = _check(h, x, w, t, gl, b, wt, T=T)
+    loss, stats = h.cross_entropy(x, w, t, bias=low, weight=wt, temperature=T)
+    got = (loss, stats) + tuple(h.cross_entropy_backward(gl, x, w, t, stats, bias=low, weight=wt, temperature=T))
+    assert not loss[[7, 200]].any() and loss.count_nonzero() > 200
+    for a, one in zip(want, got):
+        assert torch.equal(a, one)
+    for a, one in zip((want[0],) + tuple(want[2:]), h.cross_entropy_step(x, w, t, gl, bias=low, weight=wt, temperature=T)):
+        assert torch.equal(a, one)
+    everything = torch.full_like(b, mask)
+    assert not any(o.any() for o in h.cross_entropy_step(x, w, t, gl, bias=everything, weight=wt, temperature=T))
+
+
 def test_everything_masked(h):
     x, w, t, b, wt, gl = _case(40, 300, 32, torch.bfloat16)
     loss, stats = h.cross_entropy(x, w, t, bias=torch.full_like(b, -math.inf))
