@@ -15,8 +15,8 @@
 // and sum of exponentials in registers over a unit of consecutive tiles of one
 // row of tiles, and writes one pair a unit.  k_between adds the pairs up in a
 // fixed order.  Bound by the tensor cores where rows are many: 5000 x 200,000 x
-// 1024 bf16 1.29 ms (1,590 TFLOP/s; the card is at its power cap).  A step of
-// half the rows takes 2.78 ms: 0.59 of it this, 0.18 and 0.29 a piece of 50,176
+// 1024 bf16 1.26 to 1.30 ms (1,600 TFLOP/s; the card is at its power cap).  A step of
+// half the rows takes 2.7 to 2.8 ms: 0.59 of it this, 0.18 and 0.29 a piece of 50,176
 // items for gz and for the two products.
 //
 // The gradients, in pieces of the items: k_logit_gradient computes a piece's
