@@ -594,11 +594,14 @@ __device__ __forceinline__ float group_sum(const Group &gr, float a, float *sm) 
 }
 
 constexpr int kKeptThreads = 256;  // of a block, or a row's own where it has more
-constexpr int kKeptSlots = 4;
+// Rows under way: four, three where 512 threads' units would not fit 227 KB.
+constexpr int kept_slots(int n, int per) { return kMostThreads * per * (32 + n) * 4 <= 220 * 1024 ? 4 : 3; }
+static_assert(kMostThreads * 4 * (32 + 4) * kept_slots(4, 4) <= 220 * 1024 && kMostThreads * 2 * (32 + 8) * kept_slots(8, 2) <= 220 * 1024, "too large");
 template <typename T, int kN, int kPer, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_rms_grad_kept(const rms_grad_args a, int threads) {
   using W = Work<T, kN>;
   constexpr bool kAsync = kN > 1;
+  constexpr int kSlots = kept_slots(kN, kPer);
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ __align__(16) float sm[2][32];
   tc::let_next();
@@ -634,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_
   const int64_t step_g = step * a.grad_y.ld, step_t = step * a.grad_total.ld, step_c = step * a.total_kept.ld;
   const int64_t step_s = step * a.total_kept.ld_scale, step_x = step * a.grad_x.ld;
   // A slot: 16 bytes of g and of t and kN of codes for every unit of the block
-  const uint32_t units = kPer * blockDim.x, slot_bytes = units * (32 + kN), base = tc::smem_u32(raw), base_end = base + kKeptSlots * slot_bytes;
+  const uint32_t units = kPer * blockDim.x, slot_bytes = units * (32 + kN), base = tc::smem_u32(raw), base_end = base + kSlots * slot_bytes;
   auto fetch = [&](uint32_t slot, int row) {
     if (row < R) {
 #pragma unroll
@@ -661,16 +664,16 @@ __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_
     return s;
   };
   int set = 0;
-  uint32_t now = base, fill = base + (kKeptSlots - 1) * slot_bytes;  // the slots of this row, and of the next to be fetched
+  uint32_t now = base, fill = base + (kSlots - 1) * slot_bytes;  // the slots of this row, and of the next to be fetched
   KeptScales<kPer> s0 = scales(first), s1 = scales(first + step), s2;
   if (kAsync)
-    for (int i = 0; i < kKeptSlots - 1; ++i) fetch(base + i * slot_bytes, first + i * step);
+    for (int i = 0; i < kSlots - 1; ++i) fetch(base + i * slot_bytes, first + i * step);
   for (int row = first; row < R; row += step, set ^= 1) {
     KeptRow<T, kN, kPer> v;
     if constexpr (kAsync) {
-      fetch(fill, row + (kKeptSlots - 1) * step);  // into the slot of the row before
+      fetch(fill, row + (kSlots - 1) * step);  // into the slot of the row before
       fill = now;
-      asm volatile("cp.async.wait_group %0;" ::"n"(kKeptSlots - 1) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
 #pragma unroll
       for (int p = 0; p < kPer; ++p) {
         const uint32_t u = p * blockDim.x + threadIdx.x;
@@ -982,7 +985,7 @@ cudaError_t rms_grad_kept_typed(ss_handle *h, const rms_grad_args &a, cudaStream
   int64_t per = vec ? (units > 128 ? 2 : 1) : 4;
   while ((units + per - 1) / per > (per == 1 ? kKeptThreads : kMostThreads)) per *= 2;
   const int threads = (int)(((units + per - 1) / per + 31) / 32 * 32), groups = std::max(1, kKeptThreads / threads);
-  const size_t slots = vec ? (size_t)kKeptSlots * per * (threads * groups) * (32 + kV) : 0;
+  const size_t slots = vec ? (size_t)kept_slots(kV, (int)per) * per * (threads * groups) * (32 + kV) : 0;
   const size_t smem = std::max(slots, groups > 1 ? (size_t)groups * D * sizeof(float) : 0);
   auto run = [&](auto kernel, int an_sm) -> cudaError_t {
     cudaError_t e = ensure_dyn_smem(kernel, smem);

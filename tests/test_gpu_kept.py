@@ -247,6 +247,12 @@ def test_norm_backward(h, dtype, rows, cols, more):
     assert torch.equal(again[0], gx) and torch.equal(again[1], gw)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(40, 1032), (700, 2056), (9, 4104), (700, 5000), (5, 6152), (333, 7000), (700, 8192), (5, 8200)])
+def test_norm_backward_of_wide_rows(h, dtype, rows, cols):
+    test_norm_backward(h, dtype, rows, cols, True)
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (3, 0), (0, 1), (5, 3)])
 def test_norm_backward_strides(h, pad, shift):
     for dtype in TYPES:
