@@ -169,7 +169,6 @@ struct Epilogue {
   int32_t act;
   int32_t vec;  // y, pre and residual rows start on 16-byte boundaries
   ss_kept keep;   // in pre's place, or null codes; by kernels of their own (their code cost the others registers)
-  float cut;      // with it: cut_share(K), 0 for 8-bit inputs
 };
 __device__ __forceinline__ float read_any(const ss_dense &m, int64_t i) {
   return m.type == SS_VALUES_F32    ? static_cast<const float *>(m.data)[i]
@@ -299,9 +298,8 @@ __device__ __forceinline__ void add_box(const Box &b, bool whole, uint32_t box, 
   }
   __syncwarp();
 }
-// A group of 32 values of each lane's row to codes and a scale, with the share
-// that the tensor cores cut: near a border between two codes it decides.  y is
-// computed from the values as they are, as without it.
+// A group of 32 values of each lane's row to codes and a scale, as compress has
+// them of the float32 values.
 __device__ __forceinline__ void keep32(const Epilogue &ep, int64_t m, int64_t n0, const float (&v)[32]) {
   const ss_kept &k = ep.keep;
   if (m >= k.n_rows) return;
@@ -316,7 +314,7 @@ __device__ __forceinline__ void keep32(const Epilogue &ep, int64_t m, int64_t n0
       if (n0 + i < k.n_cols) top = fmaxf(top, fabsf(v[i]));
   }
   const bool odd = top == INFINITY;
-  uint32_t most = __float_as_uint(fmaf(top, ep.cut, top));
+  uint32_t most = __float_as_uint(top);
   if (odd) {
     most = 0;
 #pragma unroll
@@ -333,8 +331,7 @@ __device__ __forceinline__ void keep32(const Epilogue &ep, int64_t m, int64_t n0
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float *f = v + 16 * part + 4 * j;
-      auto of = [&](int i) { return fmaf(f[i], ep.cut, f[i]) * down; };
-      w[j] = codes2(of(0), of(1)) | codes2(of(2), of(3)) << 16;
+      w[j] = codes2(f[0] * down, f[1] * down) | codes2(f[2] * down, f[3] * down) << 16;
     }
     if (odd) {
 #pragma unroll
@@ -1155,10 +1152,7 @@ cudaError_t launch_linear(ss_handle *h, const linear_args &a, cudaStream_t s, in
   Epilogue ep = {a.y, a.pre, a.residual, a.x_scale, a.w_scale, a.bias, a.activation, 0};
   auto aligned = [](const ss_dense &m) { return !m.data || rows_aligned(m, 16); };
   ep.vec = aligned(a.y) && aligned(a.pre) && aligned(a.residual);
-  if (a.keep.codes) {
-    ep.keep = a.keep;
-    ep.cut = a.x.type == SS_VALUES_F8 ? 0.0f : cut_share(a.x.n_cols);
-  }
+  if (a.keep.codes) ep.keep = a.keep;
   if (few_rows(a.x) && !a.keep.codes) {
     *queued = 1;
     const int v = a.x.type == SS_VALUES_F8 ? 16 : 8;

@@ -22,8 +22,8 @@ enum : int { kMajorK = 0, kMajorMN = 1, kMajorByKind = 2 };  // by a tile's kind
 // the average k / K of the whole, so that what is cut is a share of the sum that
 // grows with K: over normal values 7.0, 7.1, 8.1 and 9.1e-10 K for K = 64, 256,
 // 1024 and 4096 (the same in bf16 products of another library).  Where a sum's
-// last bits count, in a loss and in what is rounded to codes, this share is
-// added back: of 1e-6 at K = 1024 half is left, the cuts' own scatter.
+// last bits count, in a loss, this share is added back: of 1e-6 at K = 1024 half
+// is left, the cuts' own scatter.
 constexpr float kCut = 8e-10f;
 inline float cut_share(int64_t K) { return kCut * (float)K; }
 
