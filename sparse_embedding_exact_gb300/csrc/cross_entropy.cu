@@ -6,7 +6,9 @@
 //   grad_x = gz w,  grad_w = gz^T x,  grad_bias = sum_r gz_r
 //
 // x [M, K] rows, w [V, K] items, 16 bits; sums, statistics and the epilogue
-// float32.  A row without a target, with one that the bias masks or of
+// float32.  The sums are the tensor cores': of 16 products at a time, each partial
+// sum cut toward zero (at most 2^-23 of it; over normal values 8e-10 K of the
+// whole).  Sums that are exact stay so.  A row without a target, with one that the bias masks or of
 // weight 0 is absent: loss 0 and gradient 0, whatever x holds.
 //
 // The loss (k_statistics): tiles of 256 x 256 logits by pairs of blocks
@@ -104,7 +106,6 @@ struct Logits {
   int32_t bias_pairs;    // it starts on an 8-byte boundary
   float c;               // log2(e) / T
   float low;             // masked from here down
-  float cut;             // cut_share(K)
   // statistics
   const int64_t *targets;
   float2 *part;          // [units * 4][M]
@@ -168,12 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_s
             tc::load_acc_wait();
             if (half == 1) release();
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const Two z = two(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-              const float2 f = both(fma_of(z, two(a.cut, a.cut), z));
-              v[i] = f.x;
-              v[i + 1] = f.y;
-            }
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
           }
           if (m0 >= a.M || n0 >= a.V) continue;
           if (a.bias) along32(a.bias + n0, a.V - n0, [&](int i, float f) { v[i] += f; });
@@ -284,7 +280,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_l
               for (int k = 0; k < 4; ++k) {
                 const uint32_t *f = r + 16 * (k / 2) + 4 * i + 2 * (k % 2);
                 Two z = two(__uint_as_float(f[0]), __uint_as_float(f[1]));
-                z = fma_of(z, two(a.cut, a.cut), z);
                 if (a.bias) z = z + bias[i];
                 const float2 e = both(fma_of(z, c2, two(-row[k].base, -row[k].base)));
                 Two g = two(exp2_fast(e.x), exp2_fast(e.y)) * two(row[k].share, row[k].share);
@@ -554,7 +549,6 @@ cudaError_t run_logits(ss_handle *h, Logits &p, const ss_dense &x, const ss_dens
   p.status = h->d_status;
   p.M = x.n_rows;
   p.V = w.n_rows;
-  p.cut = cut_share(x.n_cols);
   p.bias_pairs = reinterpret_cast<uintptr_t>(p.bias) % 8 == 0;
   auto kernel = !gradient ? k_statistics : x.type == SS_VALUES_BF16 ? k_logit_gradient<__nv_bfloat16> : k_logit_gradient<__half>;
   const size_t smem = gradient ? PairRing<kBN, 2>::kSmem : PairRing<kBN, 0>::kSmem;

@@ -17,16 +17,6 @@ constexpr int kStaging = 32 * 64;  // an epilogue warp's box: 32 rows of 64 byte
 
 enum : int { kMajorK = 0, kMajorMN = 1, kMajorByKind = 2 };  // by a tile's kind: 0 along the sum, 1 across it
 
-// The tensor cores cut a sum toward zero each time they add 16 products of 16
-// bits to it.  Where products come in any order, a partial sum of k of them is on
-// the average k / K of the whole, so that what is cut is a share of the sum that
-// grows with K: over normal values 7.0, 7.1, 8.1 and 9.1e-10 K for K = 64, 256,
-// 1024 and 4096 (the same in bf16 products of another library).  Where a sum's
-// last bits count, in a loss, this share is added back: of 1e-6 at K = 1024 half
-// is left, the cuts' own scatter.
-constexpr float kCut = 8e-10f;
-inline float cut_share(int64_t K) { return kCut * (float)K; }
-
 // ---------------------------------------------------------------- boxes
 // An epilogue warp takes 32 rows x 32 columns at a time.  Its boxes in shared
 // memory have 32 rows of 64 bytes in the 64-byte swizzle of tensor copies
