@@ -731,7 +731,8 @@ ss_status ss_rms_norm_kept_backward(ss_handle *h, const ss_dense *grad_y, const 
  *   gz_v = grad_loss * weight / temperature * (softmax(z)_v - [v = target])
  *   grad_x = gz w,  grad_w = gz^T x,  grad_bias = sum over rows of gz
  * x: M x K rows and w: V x K items (K, V >= 1), both bfloat16 or both float16,
- * finite (an item masked by its bias included).  bias: float[V] or NULL; one
+ * finite (an item masked by its bias included; a NaN logit makes a row's loss
+ * and gradient NaN).  bias: float[V] or NULL; one
  * of at most -1e38 min(1, temperature), as -INFINITY and the lowest float32
  * and bfloat16 are, masks an item: its softmax and gradients are 0.  Other
  * logits lie within that size.  targets: int64[M].  A row of a negative target, of a masked one or of weight 0 is

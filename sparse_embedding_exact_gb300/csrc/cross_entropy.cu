@@ -127,7 +127,9 @@ struct Running {
 #pragma unroll
     for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
     const float b = base_of(top, c, low);
-    sum = most <= low ? 0.0f : sum * exp2_fast(base_of(most, c, low) - b);
+    // of masked logits alone it is 0, or NaN where one among them is: fmaxf leaves
+    // NaN out of `most`, the sum keeps it
+    if (most > low) sum *= exp2_fast(base_of(most, c, low) - b);
     most = top;
     const Two c2 = two(c, c), b2 = two(-b, -b);
     Two s = two(0.0f, 0.0f);
@@ -409,8 +411,9 @@ __global__ void __launch_bounds__(kBetweenThreads) k_between(const Between a) {
   float most = -INFINITY, sum = 0.0f;
   auto add = [&](float2 p) {
     const float top = fmaxf(most, p.x), b = base_of(top, a.c, a.low);
-    sum = (most <= a.low ? 0.0f : sum * exp2_fast(base_of(most, a.c, a.low) - b)) +
-          (p.x <= a.low && p.y == 0.0f ? 0.0f : p.y * exp2_fast(base_of(p.x, a.c, a.low) - b));
+    // of masked logits alone a sum is 0, or NaN
+    sum = (most <= a.low ? sum : sum * exp2_fast(base_of(most, a.c, a.low) - b)) +
+          (p.x <= a.low ? p.y : p.y * exp2_fast(base_of(p.x, a.c, a.low) - b));
     most = top;
   };
   if (a.part) {

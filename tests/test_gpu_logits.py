@@ -97,3 +97,33 @@ def test_wide_sums(h, dtype, m, v, k, T):
     got = h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt, temperature=T)
     for name, one in zip(NAMES, got):
         _compare(one, r[name], room[name], name)
+
+
+# Items whose logits are not numbers, alone or among masked ones: where a thread's
+# first 32 columns, a block's or a unit's have no other, and in a last, short block.
+NOT_NUMBERS = [(1000, range(0, 32)), (1000, range(32, 64)), (1000, range(0, 64)), (1000, range(256, 512)), (3000, range(0, 2816)),
+               (33, [32]), (257, [256]), (1, [0]), (700, [699]), (700, [300])]
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("m", [1, 300])
+@pytest.mark.parametrize("v,items", NOT_NUMBERS)
+def test_a_nan_shows(h, m, v, items, masked):
+    for dtype in HALVES:
+        x, w, t = _randn(m, 64, dtype=dtype), _randn(v, 64, std=0.3, dtype=dtype, seed=1), _ints(0, v, m, seed=2)
+        b, wt = torch.zeros(v, device="cuda"), torch.ones(m, device="cuda")
+        items = list(items)
+        if masked and len(items) > 1:  # all but one of them
+            b[items[1:]] = -math.inf
+        w[items[:1] if masked else items] = math.nan
+        live = torch.ones(m, dtype=torch.bool, device="cuda")
+        if m > 8:
+            t[3], wt[5] = -1, 0.0
+            live[[3, 5]] = False
+        live &= ~torch.isinf(b[t.clamp_min(0)])
+        loss, stats = h.cross_entropy(x, w, t, bias=b, weight=wt)
+        step = h.cross_entropy_step(x, w, t, bias=b, weight=wt)
+        assert torch.equal(torch.isnan(loss), live) and not loss[~live].any()
+        assert torch.equal(torch.isnan(step[0]), live) and not step[0][~live].any()
+        for gx in (step[1], h.cross_entropy_backward(None, x, w, t, stats, bias=b, weight=wt)[0]):
+            assert torch.isnan(gx[live]).all()
