@@ -154,7 +154,7 @@ __device__ __forceinline__ float act_slope(float z) {
     return s + z * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
   }
   if (kAct == SS_ACT_SILU) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+    const float s = 1.0f / (1.0f + __expf(-z));  // __fdividef gives 0 where the sum is past 2^126
     return s * (1.0f + z * (1.0f - s));
   }
   if (kAct == SS_ACT_LOG1P_RELU) return z > 0.0f ? 1.0f / (1.0f + z) : (z == z ? 0.0f : z);
