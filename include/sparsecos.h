@@ -682,6 +682,10 @@ ss_status ss_distill_step(ss_handle *h, const float *grad_loss, const ss_dense *
  * A value is off by at most 2^-4 of itself, or 2^(e - 10); one of 16 bits is
  * exact in its type (beyond the type's largest: that).  An infinity or a NaN
  * becomes NaN and leaves the others of its group as they are.
+ *
+ * Kept values enter a gradient's call as ss_expand gives them in the type of
+ * its other matrices: to the nearest, beyond its largest to that (values that
+ * were kept from that type are exact).
  */
 #define SS_KEPT_GROUP 32
 typedef struct ss_kept {
@@ -717,7 +721,7 @@ ss_status ss_linear_kept_backward(ss_handle *h, const ss_dense *grad_y, const ss
                                   int64_t scratch_bytes, void *stream);
 
 /* ss_rms_norm_backward from the kept total; grad_y, grad_total and grad_x of
- * one type, to which total's values are rounded.  scratch:
+ * one type, total's values too.  scratch:
  * ss_rms_norm_kept_backward_scratch bytes. */
 int64_t ss_rms_norm_kept_backward_scratch(const ss_handle *h, int64_t n_rows, int64_t n_cols, int32_t type);
 ss_status ss_rms_norm_kept_backward(ss_handle *h, const ss_dense *grad_y, const ss_kept *total, const ss_dense *weight,

@@ -110,21 +110,6 @@ struct Unit<T, 1> {
   __device__ __forceinline__ uint32_t most() const { return abs_bits(Type<T>::up(v)); }
 };
 
-// A type's largest value: what stands for more becomes that.
-template <typename T>
-__device__ __forceinline__ constexpr float largest() {
-  return sizeof(T) == 4 ? 3.40282347e38f : std::is_same<T, __half>::value ? 65504.0f : 3.38953139e38f;
-}
-template <typename T>
-__device__ __forceinline__ float within(float v) {
-  return v > largest<T>() ? largest<T>() : v < -largest<T>() ? -largest<T>() : v;
-}
-// Bytes of scales up to which no code reaches beyond the type: 448 2^e = 1.75 2^(e + 8).
-template <typename T>
-__device__ __forceinline__ constexpr uint32_t safe_byte() {
-  return std::is_same<T, __half>::value ? 127 + 6 : 127 + 118;
-}
-
 // Where a thread's four units of kN values lie: kAlong of them along a row, a
 // block's width apart, in each of kDown rows, a block's rows apart.  All four
 // are asked for before the first is used: with one at a time too few bytes were

@@ -50,6 +50,35 @@ __device__ __forceinline__ float scaled_down(float x, float down) {
   return abs_bits(x) == kInfBits ? __uint_as_float(0x7FC00000u) : x * down;
 }
 
+// A type's largest value: what stands for more becomes that.
+template <typename T>
+__device__ __forceinline__ constexpr float largest() {
+  return sizeof(T) == 4 ? 3.40282347e38f : std::is_same<T, __half>::value ? 65504.0f : 3.38953139e38f;
+}
+template <typename T>
+__device__ __forceinline__ float within(float v) {
+  return v > largest<T>() ? largest<T>() : v < -largest<T>() ? -largest<T>() : v;
+}
+// Bytes of scales up to which no code reaches beyond the type: 448 2^e = 1.75 2^(e + 8).
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t safe_byte() {
+  return std::is_same<T, __half>::value ? 127 + 6 : 127 + 118;
+}
+
+// Of these bytes every code stands for a value of the type: none is beyond its
+// largest, or between two of its smallest.
+template <typename T>
+__device__ __forceinline__ constexpr bool exact_byte(uint32_t b) {
+  constexpr uint32_t low = sizeof(T) == 4 ? 0 : 127 + least_exponent(std::is_same<T, __half>::value ? SS_VALUES_F16 : SS_VALUES_BF16);
+  return b - low <= safe_byte<T>() - low;
+}
+// What a kept value is to the gradients: the type's nearest, as expand has it.
+// Only of a scale that is not exact_byte is that another value.
+template <typename T>
+__device__ __forceinline__ float as_type(float v) {
+  return Type<T>::up(Type<T>::down(within<T>(v)));
+}
+
 // kN codes of a row (8, 4 or 1) as a load leaves them.
 template <int kN>
 struct Codes {
@@ -76,23 +105,6 @@ struct Codes {
   __device__ __forceinline__ float2 pair(int i) const { return widen_codes2(w[i / 2] >> i % 2 * 16 & 0xFFFFu); }
   __device__ __forceinline__ float one() const { return widen_code((uint8_t)w[0]); }
 };
-// kN values of a row from column c on, in float32, before their type's largest.
-template <int kN>
-__device__ __forceinline__ void load_kept(const ss_kept &m, int64_t row, int64_t c, float (&f)[kN]) {
-  Codes<kN> q;
-  q.load(static_cast<const uint8_t *>(m.codes) + row * m.ld + c);
-  const float s = scale_of_byte(m.scale[row * m.ld_scale + c / kGroup]);
-  if constexpr (kN == 1) {
-    f[0] = q.one() * s;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kN / 2; ++i) {
-      const float2 v = q.pair(i);
-      f[2 * i] = v.x * s;
-      f[2 * i + 1] = v.y * s;
-    }
-  }
-}
 inline bool kept_aligned(const ss_kept &m, int64_t unit) {
   return reinterpret_cast<uintptr_t>(m.codes) % (uintptr_t)unit == 0 && (m.n_rows <= 1 || m.ld % unit == 0);
 }

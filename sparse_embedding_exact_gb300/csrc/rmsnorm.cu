@@ -234,6 +234,11 @@ struct Work {
     const float2 q = both(v);
     return max_nan(m, max_nan(fabsf(q.x), fabsf(q.y)));
   }
+  template <typename F>
+  static __device__ __forceinline__ V each(V v, F f) {
+    const float2 q = both(v);
+    return two(f(q.x), f(q.y));
+  }
 };
 __device__ __forceinline__ float fma_of(float a, float b, float c) { return fmaf(a, b, c); }
 using dense::fma_of;
@@ -247,6 +252,8 @@ struct Work<T, 1> {
   static __device__ __forceinline__ void put(float (&f)[1], int, V v) { f[0] = v; }
   static __device__ __forceinline__ float sum(V v) { return v; }
   static __device__ __forceinline__ float most(float m, V v) { return max_nan(m, fabsf(v)); }
+  template <typename F>
+  static __device__ __forceinline__ V each(V v, F f) { return f(v); }
 };
 
 // Barriers and place of this group's ring in dynamic shared memory (the
@@ -713,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_
       for (int i = 0; i < W::kM; ++i) {
         const typename W::V g = W::get(v.g[p], i);
         scaled[p][i] = code(p, i) * s;
+        if (!exact_byte<T>(s0.byte[p])) scaled[p][i] = W::each(scaled[p][i], [](float v) { return as_type<T>(v); });
         weighed[p][i] = g * w[p][i];
         const typename W::V xh = scaled[p][i] * r;
         gw[p][i] = fma_of(g, xh, gw[p][i]);
