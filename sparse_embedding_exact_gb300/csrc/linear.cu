@@ -789,6 +789,10 @@ __global__ void __launch_bounds__(256, kAny ? 1 : 4) k_act_grad(const ss_dense g
               z[i] = q.x;
               z[i + 1] = q.y;
             }
+            if (!exact_byte<T>(byte[u])) {
+#pragma unroll
+              for (int i = 0; i < kN; ++i) z[i] = as_type<T>(z[i]);
+            }
           } else if (kAct != SS_ACT_NONE) {
             widen(zv[u], z);
           }

@@ -84,3 +84,35 @@ def test_a_norms_total(h, dtype, kept, rows, cols):
         _near(gx, wx, _out(wx, dtype, 64 * E * size + 2.0 ** -120), dtype)
         wsize = (gy.to(F64).abs() * xh).sum(0)
         _near(gw, ww, _out(ww, torch.float32, (64 + rows / 8) * E * wsize + 2.0 ** -120), torch.float32)
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("kept", TYPES)
+@pytest.mark.parametrize("name", ["relu", "gelu", "gelu_tanh", "silu", "log1p_relu"])
+@pytest.mark.parametrize("n", [256, 333])
+def test_a_layers_pre_activation(h, dtype, kept, name, n):
+    """The gradients from the codes are those from the values that expand gives."""
+    m, k = 70, 64
+    top = torch.finfo(kept).max
+    pre = torch.cat([_values(14, n, low, high) for low, high, _ in SIZES] + [_randn(14, n, std=3.0, seed=4)]).clamp(-top, top).to(kept)
+    x, w, gy = _randn(m, k, dtype=dtype), _randn(n, k, dtype=dtype, seed=1), _randn(m, n, dtype=dtype, seed=2)
+    q, s = h.compress(pre)
+    got = h.linear_backward(gy, x, w, q, name, pre_scale=s)
+    want = h.linear_backward(gy, x, w, h.expand(q, s, dtype), name)
+    for a, b in zip(got, want):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["gelu", "log1p_relu", "silu"])
+def test_pre_activations_past_float16(h, name):
+    """A layer's z beyond float16's largest is kept as that."""
+    m, k, n, dtype = 40, 64, 96, torch.float16
+    x, w = torch.full((m, k), 64.0, device="cuda", dtype=dtype), torch.ones(n, k, device="cuda", dtype=dtype)
+    b = torch.linspace(-9e4, 9e4, n, device="cuda")
+    _, q, s = h.linear(x, w, bias=b, activation=name, compress_pre=True)
+    gy = _randn(m, n, dtype=dtype, seed=2)
+    got = h.linear_backward(gy, x, w, q, name, pre_scale=s)
+    v = h.expand(q, s, dtype)
+    assert float(v.abs().max()) == 65504
+    for a, c in zip(got, h.linear_backward(gy, x, w, v, name)):
+        assert torch.equal(a, c)
