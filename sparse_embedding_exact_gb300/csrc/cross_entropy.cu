@@ -79,7 +79,7 @@ struct UnitWalk {
       end = tiles_b * (number + 1) / units;
       unit += step;
     }
-    t = {ta, tb++, 0, kb, 0};
+    t = {(int32_t)ta, (int32_t)tb++, 0, kb, 0};
     return true;
   }
   __device__ __forceinline__ bool last() const { return tb == end; }

@@ -60,7 +60,7 @@ struct DealWalk {
     while (turn_w < (pair < d.more ? d.w_more : d.w_less)) {
       const int64_t tile = number(turn_w++, d.w_more, d.w_less);
       if (tile >= d.tiles_w) continue;
-      t = {tile / d.tiles_k, tile % d.tiles_k, 0, d.stages_m, 1};
+      t = {(int32_t)tile / d.tiles_k, (int32_t)tile % d.tiles_k, 0, d.stages_m, 1};
       return true;
     }
     return false;
@@ -134,7 +134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_g
               for (int j = 0; j < 8; ++j) reinterpret_cast<float4 *>(p)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             }
           } else {
-            put32(y, &a.out[t.kind], a.vec[t.kind], boxes, lane, m0, n0, v);
+            put32<false>(y, &a.out[t.kind], a.vec[t.kind], boxes, lane, m0, n0, v);
           }
         }
       });

@@ -15,10 +15,10 @@
 // tensor copies in the 128-byte swizzle through a ring of stages; one warp
 // copies, one thread issues the products, sixteen warps run the epilogue and
 // store by tensor copies.  Measured, 8192 x 4096 x 4096 bf16, ten calls after a
-// pause: 156 us alone (1,760 TFLOP/s; cuBLAS on the same card 144), 184 us with
+// pause: 151 us alone (1,820 TFLOP/s; cuBLAS on the same card 144), 173 us with
 // bias, gelu, residual and kept pre-activation (the last tiles' epilogue and the
-// 200 MB of it); 5000 x 10000 x 2048 e4m3: 84 us.  8192 x 4096 x 1024 with bias
-// and gelu 64 us, 71 with the pre-activation kept in 16 bits and 75 in 8.
+// 200 MB of it); 5000 x 10000 x 2048 e4m3: 86 us.  8192 x 4096 x 1024 with bias
+// and gelu 56 us, 63 with the pre-activation kept in 16 bits and 71 in 8.
 //
 // Fewer tiles than that fills (k_product): blocks on their own with tiles of
 // 128 x kBN, the summed dimension split over a cluster of up to 8 of them
@@ -242,52 +242,31 @@ __device__ __forceinline__ void finish16(const Epilogue &ep, int64_t m, int64_t 
 
 // A box of 16-bit values, rows m0 .. m0 + 31 and columns n0 .. n0 + 31 of m, by
 // loads of 16 bytes, four lanes along a row, or of one value, a row at a time,
-// for rows that start anywhere or end in the box.  (A row a lane, though it
-// needs no shared memory to change over, reads 16 bytes of each of 32 lines at
-// a time: a residual then cost 13 us of 170 at 8192 x 4096 x 4096.)
-struct Box {
-  uint4 q[4];
-};
-__device__ __forceinline__ Box load_box(const ss_dense &m, bool whole, int64_t m0, int64_t n0, int lane) {
-  Box b;
+// for rows that start anywhere or end in the box, into shared memory (box), by
+// asynchronous copies where they are of 16 bytes: held in registers until it is
+// added, it left too few for the rest (8192 x 4096 x 1024 bf16, gelu, residual and
+// kept pre-activation: 87 us, so 70).  (A row a lane reads 16 bytes of each of 32
+// lines at a time: a residual then cost 13 us of 170 at 8192 x 4096 x 4096.)
+__device__ __forceinline__ void fetch_box(const ss_dense &m, bool whole, uint32_t box, int64_t m0, int64_t n0, int lane) {
   const uint16_t *p = static_cast<const uint16_t *>(m.data) + n0;
   if (whole) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t row = min(m0 + 8 * j + lane / 4, m.n_rows - 1);  // rows past the end are not used
-      b.q[j] = *reinterpret_cast<const uint4 *>(p + row * m.ld + lane % 4 * 8);
+      tc::copy_async<16>(unit_at(box, 8 * j + lane / 4, lane % 4), p + row * m.ld + lane % 4 * 8);
     }
   } else {
-    uint32_t w[16];
+    uint16_t w[32];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const bool in = n0 + lane < m.n_cols;
-      const uint32_t lo = in && m0 + 2 * k < m.n_rows ? p[(m0 + 2 * k) * m.ld + lane] : 0;
-      const uint32_t hi = in && m0 + 2 * k + 1 < m.n_rows ? p[(m0 + 2 * k + 1) * m.ld + lane] : 0;
-      w[k] = lo | hi << 16;  // column `lane` of rows 2 k and 2 k + 1
-    }
-    memcpy(b.q, w, sizeof(w));
+    for (int r = 0; r < 32; ++r) w[r] = n0 + lane < m.n_cols && m0 + r < m.n_rows ? p[(m0 + r) * m.ld + lane] : (uint16_t)0;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) tc::write_shared(unit_at(box, r, lane / 8) + (uint32_t)(lane % 8 * 2), w[r]);
   }
-  return b;
 }
-// Adds the box's row `lane` to v, through shared memory.
+// Adds the box's row `lane` to v.
 template <typename T>
-__device__ __forceinline__ void add_box(const Box &b, bool whole, uint32_t box, int lane, float (&v)[32]) {
-  if (whole) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(unit_at(box, 8 * j + lane / 4, lane % 4)), "r"(b.q[j].x),
-                   "r"(b.q[j].y), "r"(b.q[j].z), "r"(b.q[j].w)
-                   : "memory");
-  } else {
-    uint32_t w[16];
-    memcpy(w, b.q, sizeof(w));
-#pragma unroll
-    for (int r = 0; r < 32; ++r)
-      asm volatile("st.shared.b16 [%0], %1;" ::"r"(unit_at(box, r, lane / 8) + (uint32_t)(lane % 8 * 2)),
-                   "h"((uint16_t)(w[r / 2] >> r % 2 * 16))
-                   : "memory");
-  }
+__device__ __forceinline__ void add_box(uint32_t box, int lane, float (&v)[32]) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -370,21 +349,20 @@ __device__ __forceinline__ void act32(float (&v)[32]) {
 
 // 32 columns n0 .. of rows m0 + lane: everything that follows the product,
 // from the accumulators at `acc`; `done` is called once they are read.  The
-// warp's boxes: one for what goes out, one for the residual.
-template <bool kKeep, typename F>
+// warp's boxes: one for what goes out, one for the residual.  kFull: there may be
+// a residual or a pre-activation to write; a kernel of its own for neither has
+// the registers (8192 x 4096 x 1024 bf16, gelu: 57 us, in one for all 62).
+template <bool kKeep, bool kFull, typename F>
 __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *map_y, const CUtensorMap *map_pre, uint32_t boxes,
                                          int lane, int64_t m0, int64_t n0, uint32_t acc, F done) {
   const int64_t m = m0 + lane, M = ep.y.n_rows, N = ep.y.n_cols;
   const bool there = m0 < M && n0 < N, whole = ep.vec && n0 + 32 <= N;
-  const bool by_box = there && ep.residual.data && ep.residual.type != SS_VALUES_F32;
-  Box res;
-  // asked for early, the rest hides the wait; where z is kept in 8 bits late, as
-  // its 16 registers would be spilled
-  if (!kKeep && by_box) res = load_box(ep.residual, whole, m0, n0, lane);
+  const bool by_box = kFull && there && ep.residual.data && ep.residual.type != SS_VALUES_F32;
   float v[32];
   {
     uint32_t r[32];
     tc::load_acc32(acc, r);
+    if (by_box) fetch_box(ep.residual, whole, boxes + kStaging, m0, n0, lane);  // the rest hides the wait
     tc::load_acc_wait();
     done();
 #pragma unroll
@@ -399,8 +377,8 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *
   if (ep.bias) along32(ep.bias + n0, N - n0, [&](int i, float f) { v[i] += f; });
   if (kKeep)
     keep32(ep, m, n0, v);
-  else if (ep.pre.data)
-    put32(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);
+  else if (kFull && ep.pre.data)
+    put32<!kFull>(ep.pre, map_pre, ep.vec, boxes, lane, m0, n0, v);
   switch (ep.act) {
     case SS_ACT_RELU: act32<SS_ACT_RELU>(v); break;
     case SS_ACT_GELU: act32<SS_ACT_GELU>(v); break;
@@ -410,17 +388,16 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, const CUtensorMap *
     default: break;
   }
   if (by_box) {
-    if (kKeep) res = load_box(ep.residual, whole, m0, n0, lane);
     if (ep.residual.type == SS_VALUES_BF16)
-      add_box<__nv_bfloat16>(res, whole, boxes + kStaging, lane, v);
+      add_box<__nv_bfloat16>(boxes + kStaging, lane, v);
     else
-      add_box<__half>(res, whole, boxes + kStaging, lane, v);
-  } else if (ep.residual.data && m < M) {
+      add_box<__half>(boxes + kStaging, lane, v);
+  } else if (kFull && ep.residual.data && m < M) {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (n0 + i < N) v[i] += read_any(ep.residual, m * ep.residual.ld + n0 + i);
   }
-  put32(ep.y, map_y, ep.vec, boxes, lane, m0, n0, v);
+  put32<!kFull>(ep.y, map_y, ep.vec, boxes, lane, m0, n0, v);
 }
 
 // ---------------------------------------------------------------- products
@@ -572,7 +549,7 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Pr
         const uint32_t boxes = ring + (uint32_t)((warp - 2) * 2 * kStaging);
 #pragma unroll 1
         for (int c = slice0; c < slice1; c += 32)
-          finish32<kKeep>(a.ep, &a.y, &a.pre, boxes, lane, (int64_t)row_a + q * 32, (int64_t)row_b + c, lanes + (uint32_t)c, [] {});
+          finish32<kKeep, true>(a.ep, &a.y, &a.pre, boxes, lane, (int64_t)row_a + q * 32, (int64_t)row_b + c, lanes + (uint32_t)c, [] {});
         if (lane == 0) tc::store_wait_all();
       }
     }
@@ -636,19 +613,19 @@ struct PairProduct {
 };
 
 // Persistent: each pair of blocks takes every n-th tile of 256 x kBN.
-template <int kBN, int kMajA, int kMajB, bool kF8, bool kKeep>
+template <int kBN, int kMajA, int kMajB, bool kF8, bool kKeep, bool kFull>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_product_pair(const __grid_constant__ PairProduct a) {
   const int lane = threadIdx.x & 31;
   const int64_t rank_rows = (int64_t)tc::cluster_rank() * kTileM;
   pair_products<kBN, kMajA, kMajB, kF8, 2>(
-      &a.a, &a.b, &a.idesc, a.status, TileWalk{blockIdx.x / 2, gridDim.x / 2, a.tiles_a, a.tiles_b, a.blocks_k},
-      [&](const TileWalk &, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
-        const int64_t m0 = t.ta * 2 * kTileM + rank_rows + q * 32;
+      &a.a, &a.b, &a.idesc, a.status, TileWalk<PairProduct>{a, (int32_t)(blockIdx.x / 2)},
+      [&](const TileWalk<PairProduct> &, const Tile &t, int q, int quarter, uint32_t acc, uint32_t boxes, auto release) {
+        const int64_t m0 = (int64_t)t.ta * 2 * kTileM + rank_rows + q * 32;
 #pragma unroll 1
         for (int c = quarter * (kBN / 4); c < (quarter + 1) * (kBN / 4); c += 32) {
           const bool last = c + 32 == (quarter + 1) * (kBN / 4);
-          finish32<kKeep>(a.ep, &a.y, &a.pre, boxes, lane, m0, t.tb * kBN + c, acc + (uint32_t)c, [&] {
+          finish32<kKeep, kFull>(a.ep, &a.y, &a.pre, boxes, lane, m0, (int64_t)t.tb * kBN + c, acc + (uint32_t)c, [&] {
             if (last) release();
           });
         }
@@ -935,9 +912,13 @@ cudaError_t run_product(Product &p, int split, cudaStream_t s) {
 
 template <int kBN, int kMajA, int kMajB, bool kF8>
 cudaError_t run_pair(ss_handle *h, PairProduct &p, cudaStream_t s) {
-  auto kernel = k_product_pair<kBN, kMajA, kMajB, kF8, false>;
-  if constexpr (kMajA == kMajorK && kMajB == kMajorK)
-    if (p.ep.keep.codes) kernel = k_product_pair<kBN, kMajA, kMajB, kF8, true>;
+  auto kernel = k_product_pair<kBN, kMajA, kMajB, kF8, false, false>;
+  if constexpr (kMajA == kMajorK && kMajB == kMajorK) {
+    if (p.ep.keep.codes)
+      kernel = k_product_pair<kBN, kMajA, kMajB, kF8, true, true>;
+    else if (p.ep.pre.data || p.ep.residual.data)
+      kernel = k_product_pair<kBN, kMajA, kMajB, kF8, false, true>;
+  }
   cudaError_t e = ensure_dyn_smem(kernel, PairRing<kBN, 2>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)p.tiles_a * p.tiles_b;

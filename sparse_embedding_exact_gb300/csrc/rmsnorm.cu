@@ -562,13 +562,6 @@ __global__ void __launch_bounds__(grad_threads(kN, kPer), kN * kPer == 16 ? 3 : 
 // room for half the warps.)  Other rows are loaded value by value.  16,384 x 2048
 // bf16 47 us (5.0 TB/s, 7 of it the sums; by way of a widened copy 94), 4096 x
 // 4096 29 (from 16 bits 38); 5000 x 1001 float32 25.
-template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kBytes) : "memory");
-}
 template <typename T, int kN, int kPer>
 struct KeptRow {
   Pack<T, kN> g[kPer], t[kPer];
@@ -650,9 +643,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == kKeptThreads ? 3 : 1) k_
 #pragma unroll
       for (int p = 0; p < kPer; ++p) {
         const uint32_t u = p * blockDim.x + threadIdx.x;
-        copy_async<16>(slot + 16 * u, gy + at[p]);
-        if (past) copy_async<16>(slot + 16 * units + 16 * u, gt + at[p]);
-        copy_async<kN == 1 ? 4 : kN>(slot + 32 * units + kN * u, codes + at[p]);
+        tc::copy_async<16>(slot + 16 * u, gy + at[p]);
+        if (past) tc::copy_async<16>(slot + 16 * units + 16 * u, gt + at[p]);
+        tc::copy_async<kN == 1 ? 4 : kN>(slot + 32 * units + kN * u, codes + at[p]);
       }
       gy += step_g;
       gt += step_t;

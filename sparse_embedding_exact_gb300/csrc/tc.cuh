@@ -115,6 +115,14 @@ __device__ __forceinline__ void load_bulk(uint32_t dst, const void *src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
+// kBytes (4, 8 or 16) from one thread, both addresses aligned to them.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kBytes) : "memory");
+}
 // A value of 2, 4 or 16 bytes at a shared address aligned to its size.
 template <typename P>
 __device__ __forceinline__ P read_shared(uint32_t at) {
