@@ -80,3 +80,17 @@ def test_residual_changes_with_every_call(h):
         y, pre = h.linear(x, w, residual=r, save_pre=True, stream=side)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(y, want) and torch.equal(pre, z.float().to(dtype))
+
+
+# Few rows and many features, whose sums go by shares; one and many slices of
+# 256 columns; odd widths.
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("m,k,n", [(1, 1024, 4096), (16, 4096, 4096), (70, 1000, 3000), (200, 257, 10_000), (65, 777, 2049), (600, 512, 1000)])
+def test_gradients_of_exact_sums(h, dtype, m, k, n):
+    x, w, gy = _ints(-2, 3, m, k).to(dtype), _ints(-2, 3, n, k, seed=1).to(dtype), _ints(-2, 3, m, n, seed=2).to(dtype)
+    pre = _ints(-1, 2, m, n, seed=3).to(dtype)
+    for act, gz in (("none", gy.to(F64)), ("relu", gy.to(F64) * (pre > 0))):
+        gx, gw, gb = h.linear_backward(gy, x, w, None if act == "none" else pre, act, grad_dtype=torch.float32)
+        assert torch.equal(gx.to(F64), gz @ w.to(F64)) and torch.equal(gw.to(F64), gz.t() @ x.to(F64)) and torch.equal(gb.to(F64), gz.sum(0))
+        gx, gw, _ = h.linear_backward(gy, x, w, None if act == "none" else pre, act)
+        assert torch.equal(gx, (gz @ w.to(F64)).float().to(dtype)) and torch.equal(gw, (gz.t() @ x.to(F64)).float().to(dtype))
