@@ -1093,12 +1093,16 @@ int64_t grad_parts(const ss_handle *h, int64_t M, int64_t N) {
 }
 
 // Whether a gradient's products take less time as one launch (gradients.cu) than
-// as two, by their estimates, and that launch's scratch.
+// as two, by their estimates, and that launch's scratch.  A tenth less is asked
+// for: over 240 sizes the joint launch was then never 2% behind what two launches
+// had taken, as it was, for its longer stages under the power cap, with 12,000 x
+// 4096 x 4096 bf16 (0.915 of the estimate: 576 us, 526 apart) and 6000 x 8192 x
+// 8192 (0.967: 1106 and 1036).
 bool together(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *parts) {
   int64_t clocks;
   *parts = grad_product_parts(h, M, N, K, &clocks);
   const double apart = cut_of(h, M, K, (N + 63) / 64, 64, true).clocks + cut_of(h, N, K, (M + 63) / 64, 64, true).clocks;
-  return K > 0 && (double)clocks + 12e3 < apart;
+  return K > 0 && (double)clocks < 0.9 * apart;
 }
 int64_t together_bytes(const ss_handle *h, int64_t M, int64_t N, int64_t K) {
   int64_t parts;
