@@ -141,16 +141,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1) k_g
 }
 
 // What is left to add up: grad_x of its parts, and the sums of columns (a
-// bias's gradient), each in a fixed order.  Blocks of the first kind take 256
-// columns of a row of grad_x at a time (whole rows left few rows to few blocks: 16
-// x 4096 x 4096 bf16's gradients 44 us, so 34), then come those of 32 columns, eight
-// threads a column.
+// bias's gradient), each in a fixed order.  Blocks of the first kind take rows of
+// grad_x, 2^an_x of them one (whole rows left few rows to few blocks: 16 x 4096 x
+// 4096 bf16's gradients 44 us, so 31), then come those of 32 columns, eight threads
+// a column.
 struct Finish {
   const float *parts;
   int64_t ld;
   int32_t n;
   ss_dense out;
-  int32_t blocks_x;
+  int32_t blocks_x, an_x;
   const float *sums;
   int64_t sum_rows, sum_cols;
   float *sum_to;
@@ -160,15 +160,13 @@ __global__ void __launch_bounds__(256) k_finish(const Finish a) {
   tc::wait_before();
   tc::let_next();
   if ((int)blockIdx.x < a.blocks_x) {
-    const uint32_t slices = (uint32_t)((a.out.n_cols + 255) / 256), units = (uint32_t)a.out.n_rows * slices;  // fewer than 2^31, as out is in memory
-    for (uint32_t unit = blockIdx.x; unit < units; unit += (uint32_t)a.blocks_x) {
-      const int64_t row = unit / slices, c = unit % slices * 256 + threadIdx.x;
-      if (c >= a.out.n_cols) continue;
-      float v = 0.0f;
+    for (int64_t row = blockIdx.x >> a.an_x; row < a.out.n_rows; row += a.blocks_x >> a.an_x)
+      for (int64_t c = (int64_t)(blockIdx.x & ((1u << a.an_x) - 1)) * 256 + threadIdx.x; c < a.out.n_cols; c += (int64_t)256 << a.an_x) {
+        float v = 0.0f;
 #pragma unroll 4
-      for (int p = 0; p < a.n; ++p) v += a.parts[((int64_t)p * a.out.n_rows + row) * a.ld + c];
-      static_cast<T *>(a.out.data)[row * a.out.ld + c] = Type<T>::down(v);
-    }
+        for (int p = 0; p < a.n; ++p) v += a.parts[((int64_t)p * a.out.n_rows + row) * a.ld + c];
+        static_cast<T *>(a.out.data)[row * a.out.ld + c] = Type<T>::down(v);
+      }
     return;
   }
   __shared__ float sm[8][33];
@@ -300,7 +298,9 @@ cudaError_t launch_grad_products(ss_handle *h, const grad_products &g, cudaStrea
     f.ld = part_ld(K);
     f.n = g.parts;
     f.out = g.grad_x;
-    f.blocks_x = (int32_t)std::min<int64_t>(M * up(K, 256), 8 * (int64_t)std::max(1, h->sm_count));
+    const int64_t most = 8 * (int64_t)std::max(1, h->sm_count);
+    while ((M << (f.an_x + 1)) <= most && ((int64_t)256 << f.an_x) < K) ++f.an_x;
+    f.blocks_x = (int32_t)std::min<int64_t>(M << f.an_x, most >> f.an_x << f.an_x);
   }
   f.sums = g.sums;
   f.sum_rows = g.sum_rows;
