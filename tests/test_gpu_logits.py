@@ -127,3 +127,16 @@ def test_a_nan_shows(h, m, v, items, masked):
         assert torch.equal(torch.isnan(step[0]), live) and not step[0][~live].any()
         for gx in (step[1], h.cross_entropy_backward(None, x, w, t, stats, bias=b, weight=wt)[0]):
             assert torch.isnan(gx[live]).all()
+
+
+def test_rows_past_a_piece(h):
+    """More rows than 2^27 values of the least piece of items have."""
+    m, v, k, dtype = 70_000, 4500, 40, torch.bfloat16
+    x, w = _randn(m, k, dtype=dtype), _randn(v, k, std=2.5 * k ** -0.5, dtype=dtype, seed=1)
+    b, t, wt, gl = _randn(v, std=0.5, seed=2), _ints(0, v, m, seed=3), _randn(m, seed=4).abs() + 0.5, _randn(m, seed=5)
+    t[::1000], wt[7::900] = -1, 0.0
+    r = ref.cross_entropy(x, w, t, gl, b, wt)
+    room = ref.bounds(r, x, w, b, wt, gl, pieces=3)
+    got = h.cross_entropy_step(x, w, t, gl, bias=b, weight=wt)
+    for name, one in zip(NAMES, got):
+        _compare(one, r[name], room[name], name)
