@@ -758,7 +758,9 @@ ss_status ss_rms_norm_kept_backward(ss_handle *h, const ss_dense *grad_y, const 
  * steps of 2^-23 of its terms' sizes (an exact sum by none), then the bias.
  * A softmax below 2^-126 of the largest counts as 0.  grad_bias sums gz
  * unrounded.  ss_cross_entropy_step gives loss and
- * gradients in one call.  scratch: bytes of the call's _scratch.
+ * gradients in one call.  scratch: bytes of the call's _scratch (the gradients'
+ * is two copies of x and a piece of M x V of at most 2^27 values, or of 2048
+ * items, for the most part).
  */
 int64_t ss_cross_entropy_scratch(const ss_handle *h, const ss_dense *x, const ss_dense *w);
 ss_status ss_cross_entropy(ss_handle *h, const ss_dense *x, const ss_dense *w, const float *bias, const int64_t *targets,

@@ -17,7 +17,7 @@
 // and sum of exponentials in registers over a unit of consecutive tiles of one
 // row of tiles, and writes one pair a unit.  k_between adds the pairs up in a
 // fixed order.  Bound by the tensor cores where rows are many: 5000 x 200,000 x
-// 1024 bf16 1.26 to 1.30 ms (1,600 TFLOP/s; the card is at its power cap).  A step of
+// 1024 bf16 1.26 to 1.31 ms (1,600 TFLOP/s; the card is at its power cap).  A step of
 // half the rows takes 2.7 to 2.8 ms: 0.59 of it this, 0.18 and 0.29 a piece of 50,176
 // items for gz and for the two products.
 //
@@ -518,7 +518,8 @@ struct Room {
     K = x_.n_cols;
     const bool loss = mode != XENT_BACKWARD, grad = mode != XENT_LOSS;
     units = units_of(h, tiles_a, up(V, kBN));
-    // pieces of at most 2^27 values of gz, of whole tiles and equal sizes
+    // pieces of at most 2^27 values of gz (of 2048 items, where rows are 65,536 or
+    // more), of whole tiles and equal sizes
     const int64_t most = std::max<int64_t>(2048, ((int64_t)1 << 27) / std::max<int64_t>(1, M)), pieces = up(V, most);
     piece = up(up(V, pieces), kBN) * kBN;
     x = grad ? align_up(M * padded_ld(x_) * 2) : copy_bytes(x_);

@@ -188,7 +188,9 @@ int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t part_ld(int64_t K) { return up(K, 32) * 32; }
 
 // Clocks of a tile: 590 a stage (512 are the tensor cores' own) and 3,500, or its
-// epilogue, as measured over 16 and 64 stages.
+// epilogue, as measured over 16 and 64 stages.  (The estimate of a layer's kernel,
+// linear.cu, has 600 and 7,000, as its tiles come one after the other without the
+// 3,500 and its epilogue does more.)
 int64_t clocks_of(int64_t stages) { return std::max<int64_t>(590 * stages + 3500, 6500); }
 // The deal for grad_x in `parts` shares, and the clocks until its last pair is
 // done.  One product's tiles are spread evenly, the other's go where there is

@@ -706,7 +706,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, kM == 1 ? 16 : 1) k_rows(const
 // columns over the block's rows into part[blockIdx.y][N] (or nowhere).  A warp
 // takes every eighth row of the block's share, two of them at a time.  Bound
 // by memory and, with a gelu, by instructions: 8192 x 4096 bf16 36 us (5.5 TB/s),
-// from codes 38 at four blocks an SM (42 at three).
+// from codes 40, at four blocks an SM: some activations spill 4 to 36 bytes of a
+// thread's then, which costs less than three blocks do (the whole gradient of 8192
+// x 4096 x 1024 fp16 with gelu_tanh or log1p_relu 140 us, at three 145 and 147).
 // kAny: rows that start anywhere, or end within a unit of kN values.
 template <typename T, int kAct, bool kKept, bool kAny>
 __global__ void __launch_bounds__(256, kAny ? 1 : 4) k_act_grad(const ss_dense grad_y, const ss_dense pre, const ss_kept kept, T *gz, int64_t ld, float *part) {

@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(grad_threads(kN, kPer), kN * kPer == 16 ? 3 : 
 // registers for what is under way.  (Loads one row ahead into registers left
 // room for half the warps.)  Other rows are loaded value by value.  16,384 x 2048
 // bf16 47 us (5.0 TB/s, 7 of it the sums; by way of a widened copy 94), 4096 x
-// 4096 29 (from 16 bits 38); 5000 x 1001 float32 25.
+// 4096 31 (from 16 bits 38); 5000 x 1001 float32 25.
 template <typename T, int kN, int kPer>
 struct KeptRow {
   Pack<T, kN> g[kPer], t[kPer];
@@ -994,8 +994,9 @@ cudaError_t rms_grad_kept_typed(ss_handle *h, const rms_grad_args &a, cudaStream
   bool vec = D % kV == 0 && kept_aligned(a.total_kept, kV);
   for (const ss_dense *m : {&a.grad_y, &a.grad_total, &a.grad_x}) vec = vec && (!m->data || rows_aligned(*m, 16));
   // units a thread: two, one for short rows, more where a row's threads would be
-  // more than a block has (one unit, 16,384 x 2048 bf16: 51 us); values one by one
-  // four
+  // more than a block has (one unit, 16,384 x 2048 bf16: 51 us; float32 by the same
+  // rule 76, 86% of the memory's rate); values one by one four, up to sixteen, of
+  // which 600 bytes are spilled (2000 x 4095 bf16 37 us, 2000 x 7001 164)
   const int64_t units = vec ? D / kV : D;
   int64_t per = vec ? (units > 128 ? 2 : 1) : 4;
   while ((units + per - 1) / per > (per == 1 ? kKeptThreads : kMostThreads)) per *= 2;
