@@ -754,8 +754,9 @@ ss_status ss_rms_norm_kept_backward(ss_handle *h, const ss_dense *grad_y, const 
  * (float16: both scaled by powers of two, the latter by one for the call that
  * brings the largest factor of a row that takes part near 1: values that are
  * then below 2^-14 lose bits).
- * The logits are float32 sums of exact products, each cut by at most K / 16 + 1
- * steps of 2^-23 of its terms' sizes (an exact sum by none), then the bias.
+ * The logits are the tensor cores' float32 sums of exact products, a partial sum
+ * cut toward zero for every 16 of them (over normal values 8e-10 K of a logit in
+ * all; sums that float32 holds are not cut), and the bias.
  * A softmax below 2^-126 of the largest counts as 0.  grad_bias sums gz
  * unrounded.  ss_cross_entropy_step gives loss and
  * gradients in one call.  scratch: bytes of the call's _scratch (the gradients'

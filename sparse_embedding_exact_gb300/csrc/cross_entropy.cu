@@ -6,9 +6,9 @@
 //   grad_x = gz w,  grad_w = gz^T x,  grad_bias = sum_r gz_r
 //
 // x [M, K] rows, w [V, K] items, 16 bits; sums, statistics and the epilogue
-// float32.  The sums are the tensor cores': of 16 products at a time, each partial
-// sum cut toward zero (at most 2^-23 of it; over normal values 8e-10 K of the
-// whole).  Sums that are exact stay so.  A row without a target, with one that the bias masks or of
+// float32.  The sums are the tensor cores': a partial sum is cut toward zero for
+// every 16 products (over normal values 8e-10 K of the whole in all); sums that
+// float32 holds are not.  A row without a target, with one that the bias masks or of
 // weight 0 is absent: loss 0 and gradient 0, whatever x holds.
 //
 // The loss (k_statistics): tiles of 256 x 256 logits by pairs of blocks

@@ -1096,10 +1096,9 @@ int64_t grad_parts(const ss_handle *h, int64_t M, int64_t N) {
 
 // Whether a gradient's products take less time as one launch (gradients.cu) than
 // as two, by their estimates, and that launch's scratch.  A tenth less is asked
-// for: over 240 sizes the joint launch was then never 2% behind what two launches
-// had taken, as it was, for its longer stages under the power cap, with 12,000 x
-// 4096 x 4096 bf16 (0.915 of the estimate: 576 us, 526 apart) and 6000 x 8192 x
-// 8192 (0.967: 1106 and 1036).
+// for, as large products at the power cap take longer together than estimated:
+// 12,000 x 4096 x 4096 bf16 (estimates 0.915 to 1) 576 us and 526 apart, 6000 x 8192
+// x 8192 (0.967) 1106 and 1036, where 8192 x 4096 x 1024 (0.87) takes 95 and 108.
 bool together(const ss_handle *h, int64_t M, int64_t N, int64_t K, int64_t *parts) {
   int64_t clocks;
   *parts = grad_product_parts(h, M, N, K, &clocks);
