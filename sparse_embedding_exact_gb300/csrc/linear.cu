@@ -17,7 +17,7 @@
 // store by tensor copies.  Measured, 8192 x 4096 x 4096 bf16, ten calls after a
 // pause: 151 us alone (1,820 TFLOP/s; cuBLAS on the same card 144), 173 us with
 // bias, gelu, residual and kept pre-activation (the last tiles' epilogue and the
-// 200 MB of it); 5000 x 10000 x 2048 e4m3: 86 us.  8192 x 4096 x 1024 with bias
+// 200 MB of it); 5000 x 10000 x 2048 e4m3: 84 us.  8192 x 4096 x 1024 with bias
 // and gelu 56 us, 63 with the pre-activation kept in 16 bits and 71 in 8.
 //
 // Fewer tiles than that fills (k_product): blocks on their own with tiles of
